@@ -11,6 +11,7 @@ or no GPU is visible, the compute calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -96,6 +97,14 @@ SIGNATURES = {
     "qlora_linear_bwd_timed": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _F,
                                     _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P,
                                     ctypes.POINTER(TimingC)]),
+    "lora_adapter_tiles": (_I64, [_I64, _I]),
+    "lora_adapter_plan": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _P, _P, _P]),
+    "lora_adapters_workspace_bytes": (ctypes.c_size_t, [_I64, _I, _I]),
+    "lora_adapters_fwd": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _P, _P, _P, _P,
+                               ctypes.c_double, ctypes.c_uint64, _P, _P, _P, ctypes.c_size_t, _P]),
+    "lora_adapters_bwd": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P,
+                               ctypes.c_double, ctypes.c_uint64, _P, _P, _P, _P, ctypes.c_size_t,
+                               _P]),
 }
 
 _lib = None
@@ -527,6 +536,162 @@ def dropout(X, p: float, seed: int, Xd_out=None, mask_out=None):
     _check("lora_dropout", load_library().lora_dropout(
         _ptr(X), M, K, float(p), int(seed) & (2**64 - 1), _ptr(Xd), _ptr(mask), _stream(dev)))
     return Xd, mask[:nw]
+
+
+# ---------------------------------------------------------------------------
+# adapters of many requests beside one shared projection
+# ---------------------------------------------------------------------------
+
+class AdapterPlan(NamedTuple):
+    """Which adapter each token of a batch uses (lora_adapter_plan), int32 on
+    the device; built once per batch, used for all its projections."""
+    token_slot: "object"   # [M]      slot of each token, -1 without an adapter
+    order: "object"        # [M]      tokens by slot, those without one last
+    start: "object"        # [S + 2]  where each slot starts in order; M at the end
+    tiles: "object"        # [tiles, 3]  (slot, first, count), up to 64 tokens each
+    S: int
+
+
+@contextlib.contextmanager
+def _on_device(dev):
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        yield
+    else:
+        with torch.cuda.device(dev):
+            yield
+
+
+def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> AdapterPlan:
+    """The plan of a batch of requests: slots int32 [Q], each request's adapter
+    slot (outside [0, S): none), lengths int32 [Q], its token rows (None: one
+    each).  `tokens` is the batch's number of rows M (default, without lengths:
+    Q); rows behind the last request have no adapter."""
+    torch = _torch()
+    chk = _Checker()
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots: a 1-D int32 tensor")
+    Q = slots.shape[0]
+    chk("slots", slots, torch.int32, (Q,))
+    chk.opt("lengths", lengths, torch.int32, (Q,))
+    if tokens is None:
+        if lengths is not None:
+            raise ValueError("tokens: the batch's number of rows, where lengths are given")
+        tokens = Q
+    dev = chk.device()
+    M, S = int(tokens), int(S)
+    lib = load_library()
+    nt = lib.lora_adapter_tiles(M, S) if abs(M) < 2**62 and abs(S) < 2**31 else 0
+    if nt <= 0:
+        raise QLoRAError("lora_adapter_plan", ERR_SHAPE)
+    # one allocation, each array at a multiple of 16 bytes
+    mp, sp = (M + 3) & ~3, (S + 5) & ~3
+    buf = torch.empty(2 * mp + sp + 3 * nt, dtype=torch.int32, device=dev)
+    plan = AdapterPlan(buf[:M], buf[mp:mp + M], buf[2 * mp:2 * mp + S + 2],
+                       buf[2 * mp + sp:].view(nt, 3), S)
+    with _on_device(dev):
+        _check("lora_adapter_plan", lib.lora_adapter_plan(
+            _ptr(lengths), _ptr(slots) if Q else None, Q, M, S, _ptr(plan.token_slot),
+            _ptr(plan.order), _ptr(plan.start), _ptr(plan.tiles), _stream(dev)))
+    return plan
+
+
+def _batch_adapters(chk, A, B, scale, plan, M, K, N):
+    """Checks the bank and the plan; returns (r, S)."""
+    torch = _torch()
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        raise ValueError("A: a bf16 [S, r, K] tensor")
+    if not isinstance(plan, AdapterPlan):
+        raise ValueError("plan: an AdapterPlan")
+    S, r = A.shape[0], A.shape[1]
+    if plan.S != S:
+        raise ValueError(f"plan: built for {plan.S} slots, the adapters have {S}")
+    chk("A", A, torch.bfloat16, (S, r, K))
+    chk("B", B, torch.bfloat16, (S, N, r))
+    chk("scale", scale, torch.float32, (S,))
+    chk("order", plan.order, torch.int32, (M,))
+    chk("start", plan.start, torch.int32, (S + 2,))
+    chk("tiles", plan.tiles, torch.int32,
+        (load_library().lora_adapter_tiles(M, S), 3))
+    return r, S
+
+
+def _dropout_args(dropout):
+    if dropout is None:
+        return 0.0, 0
+    p, seed = dropout
+    return float(p), int(seed) & (2**64 - 1)
+
+
+def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: bool = True,
+                 out=None, T_out=None, workspace=None):
+    """out = Y + scale (drop(X) A^T) B^T, every token with its slot's A [S, r,
+    K], B [S, N, r] and scale [S].  Y bf16 [M, N] is the shared projection's
+    output (None: the adapters' term alone; out may be Y).  dropout: None or
+    (p, seed), lora_dropout's mask, regenerated where it is needed.  Returns
+    (out bf16 [M, N], T fp32 [M, r] or None)."""
+    torch = _torch()
+    chk = _Checker()
+    M, K = chk.mat("X", X, torch.bfloat16)
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B: a bf16 [S, N, r] tensor")
+    N = B.shape[1]
+    r, S = _batch_adapters(chk, A, B, scale, plan, M, K, N)
+    chk.opt("Y", Y, torch.bfloat16, (M, N))
+    chk.opt("out", out, torch.bfloat16, (M, N))
+    chk.opt("T_out", T_out, torch.float32, (M, r))
+    p, seed = _dropout_args(dropout)
+    dev = chk.device()
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    T = T_out if T_out is not None else (
+        torch.empty(M, r, dtype=torch.float32, device=dev) if save_T else None)
+    lib = load_library()
+    with _on_device(dev):
+        ws, wsb = _ws(dev, lib.lora_adapters_workspace_bytes(M, r, 0), workspace)
+        _check("lora_adapters_fwd", lib.lora_adapters_fwd(
+            _ptr(X), M, K, N, _ptr(A), _ptr(B), _ptr(scale), r, S, _ptr(plan.order),
+            _ptr(plan.start), _ptr(plan.tiles), _ptr(Y), p, seed, _ptr(out), _ptr(T), _ptr(ws),
+            wsb, _stream(dev)))
+    return out, T
+
+
+def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout=None,
+                 need_dX: bool = True, dX_out=None, dA_out=None, dB_out=None, workspace=None):
+    """Backward of adapters_fwd: (dX bf16 [M, K] or None, dA fp32 [S, r, K],
+    dB fp32 [S, N, r]).  dX, if given, is what the shared projection's backward
+    gave: the adapters' term is added to it (dX_out may be the same tensor).
+    T from the forward (None: computed again); dropout as in the forward."""
+    torch = _torch()
+    chk = _Checker()
+    M, K = chk.mat("X", X, torch.bfloat16)
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B: a bf16 [S, N, r] tensor")
+    N = B.shape[1]
+    r, S = _batch_adapters(chk, A, B, scale, plan, M, K, N)
+    chk("dY", dY, torch.bfloat16, (M, N))
+    chk.opt("T", T, torch.float32, (M, r))
+    chk.opt("dX", dX, torch.bfloat16, (M, K))
+    chk.opt("dX_out", dX_out, torch.bfloat16, (M, K))
+    chk.opt("dA", dA_out, torch.float32, (S, r, K))
+    chk.opt("dB", dB_out, torch.float32, (S, N, r))
+    p, seed = _dropout_args(dropout)
+    dev = chk.device()
+    if not need_dX:
+        if dX is not None or dX_out is not None:
+            raise ValueError("dX: given, but need_dX is False")
+    elif dX_out is None:
+        dX_out = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    dA = dA_out if dA_out is not None else torch.empty(S, r, K, dtype=torch.float32, device=dev)
+    dB = dB_out if dB_out is not None else torch.empty(S, N, r, dtype=torch.float32, device=dev)
+    lib = load_library()
+    with _on_device(dev):
+        ws, wsb = _ws(dev, lib.lora_adapters_workspace_bytes(M, r, 1), workspace)
+        _check("lora_adapters_bwd", lib.lora_adapters_bwd(
+            _ptr(dY), _ptr(X), M, K, N, _ptr(A), _ptr(B), _ptr(scale), r, S, _ptr(plan.order),
+            _ptr(plan.start), _ptr(plan.tiles), _ptr(T), _ptr(dX), p, seed, _ptr(dX_out),
+            _ptr(dA), _ptr(dB), _ptr(ws), wsb, _stream(dev)))
+    return dX_out, dA, dB
 
 
 def linear_fwd_dropout(X, Xd, qw: QuantizedWeight, A, B, alpha: float, save_T: bool = True,

@@ -14,25 +14,9 @@
 // when its word is >= floor(p 2^32) (computed on the host).
 #include "device_common.h"
 #include "kernels.h"
+#include "philox.h"
 
 namespace qlk {
-
-// One Philox4x32 block: ten rounds of two 32 x 32 -> 64-bit products with the
-// published multipliers, the key bumped by the Weyl constants between rounds.
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
-#pragma unroll
-  for (int rnd = 0; rnd < 10; ++rnd) {
-    if (rnd) {
-      k0 += 0x9E3779B9u;
-      k1 += 0xBB67AE85u;
-    }
-    const uint64_t p0 = (uint64_t)0xD2511F53u * c.x;
-    const uint64_t p1 = (uint64_t)0xCD9E8D57u * c.z;
-    c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ k0, (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ k1,
-                   (uint32_t)p0);
-  }
-  return c;
-}
 
 // One thread per 32 consecutive elements (one mask word): eight Philox
 // blocks, four 16-byte loads and stores of the bf16 data.  Kept elements are

@@ -252,4 +252,46 @@ hipError_t launch_silu_mul_fwd(const uint16_t* G, const uint16_t* U, int64_t n, 
 hipError_t launch_silu_mul_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
                                int64_t n, uint16_t* dG, uint16_t* dU, hipStream_t st);
 
+// ---- adapters of many requests beside one shared projection ----------------
+
+constexpr int kPlanTile = 64;     // positions of the order in a tile of the plan
+constexpr int kMaxSlots = 1024;
+// Rows of the plan's tiles (an upper bound on the tiles in use).
+int64_t adapter_plan_tiles(int64_t M, int S);
+// lengths may be null (one token per request).
+hipError_t launch_adapter_plan(const int* lengths, const int* slots, int64_t Q, int64_t M, int S,
+                               int* token_slot, int* order, int* start, int* tiles, hipStream_t st);
+
+// The adapters of S slots (A [S, r, K], B [S, N, r], scale [S]) and the
+// batch's plan; r is a multiple of 8.
+struct BatchAdapters {
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* scale;
+  int r, slots;
+  const int* order;
+  const int* start;
+  const int* tiles;
+};
+struct BatchDropout {
+  bool on;
+  uint32_t threshold, k0, k1;
+  float scale;
+};
+struct BatchWorkspace {
+  size_t off_T, off_U, off_Up, off_Tp, bytes;
+};
+BatchWorkspace batch_workspace(int64_t M, int r, bool backward);
+// out = Y + c T B^T (Y null: zeros; out may be Y), T = drop(X) A^T to T_out
+// (null: kept in ws).
+hipError_t launch_batch_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                            const BatchAdapters& a, const uint16_t* Y, const BatchDropout& d,
+                            uint16_t* out, float* T_out, void* ws, hipStream_t st);
+// dX = dX0 + drop(c U A) (skipped if dX is null; dX0 null: zeros; dX may be
+// dX0), dA and dB of every slot; T null: computed again.
+hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                            const BatchAdapters& a, const float* T, const uint16_t* dX0,
+                            const BatchDropout& d, uint16_t* dX, float* dA, float* dB, void* ws,
+                            hipStream_t st);
+
 }  // namespace qlk

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/qlora.h"
@@ -17,6 +18,7 @@ constexpr int64_t kMaxDim = (int64_t)1 << 30;   // keeps every tile index in int
 constexpr int64_t kMaxBufferBytes = (int64_t)1 << 31;
 
 constexpr int kMaxRank = 256;
+constexpr int64_t kMaxBatchDim = (int64_t)1 << 23;   // batched adapters: column blocks fit the grid
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -251,6 +253,31 @@ bool valid_p(double p) { return p >= 0.0 && p < 1.0; }   // false for NaN
 uint32_t dropout_threshold(double p) { return (uint32_t)floor(p * 4294967296.0); }
 float dropout_scale(double p) { return (float)(1.0 / (1.0 - p)); }
 
+// Checks of the batched adapters' calls (M tokens, S slots of rank r).
+int check_batch_sizes(int64_t M, int64_t K, int64_t N, int r, int S) {
+  if (M <= 0 || M > kMaxDim || K <= 0 || N <= 0 || K % 8 != 0 || N % 8 != 0) return QLORA_ERR_SHAPE;
+  if (K > kMaxBatchDim || N > kMaxBatchDim) return QLORA_ERR_SHAPE;
+  if (S < 1 || S > qlk::kMaxSlots || r < 8 || r > kMaxRank || r % 8 != 0) return QLORA_ERR_SHAPE;
+  // 32-bit offsets into X, dY and the bf16 terms of T and U
+  if (M * K * 2 >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes || M * r * 6 >= kMaxBufferBytes)
+    return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+qlk::BatchDropout batch_dropout(double p, uint64_t seed) {
+  qlk::BatchDropout d{};
+  d.on = p > 0.0;
+  d.threshold = dropout_threshold(p);
+  d.k0 = (uint32_t)seed;
+  d.k1 = (uint32_t)(seed >> 32);
+  d.scale = dropout_scale(p);
+  return d;
+}
+int check_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
 int quantize_common(const float* W0, int64_t N, int64_t K, int blocksize, const qlk::Codebook4& cb,
                     uint8_t* packed, float* absmax, void* stream) {
   if (!W0 || !packed || !absmax) return QLORA_ERR_NULL;
@@ -422,6 +449,68 @@ int lora_dropout(const uint16_t* X, int64_t M, int64_t K, double p, uint64_t see
   if (!aligned16(X) || !aligned16(Xd) || !aligned16(mask)) return QLORA_ERR_ALIGN;
   return launch_status(qlk::launch_lora_dropout(X, M * K, dropout_threshold(p), dropout_scale(p),
                                                 seed, Xd, mask, as_stream(stream)));
+}
+
+int64_t lora_adapter_tiles(int64_t M, int S) {
+  if (M <= 0 || M > kMaxDim || S < 1 || S > qlk::kMaxSlots) return 0;
+  return qlk::adapter_plan_tiles(M, S);
+}
+
+int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, int64_t M, int S,
+                      int32_t* token_slot, int32_t* order, int32_t* start, int32_t* tiles,
+                      void* stream) {
+  if ((Q > 0 && !slots) || !token_slot || !order || !start || !tiles) return QLORA_ERR_NULL;
+  if (M <= 0 || M > kMaxDim || Q < 0 || Q > kMaxDim || S < 1 || S > qlk::kMaxSlots)
+    return QLORA_ERR_SHAPE;
+  if (!lengths && Q > M) return QLORA_ERR_SHAPE;
+  const int bad = check_aligned({lengths, slots, token_slot, order, start, tiles});
+  if (bad) return bad;
+  return launch_status(qlk::launch_adapter_plan(lengths, slots, Q, M, S, token_slot, order, start,
+                                                tiles, as_stream(stream)));
+}
+
+size_t lora_adapters_workspace_bytes(int64_t M, int r, int is_bwd) {
+  if (check_batch_sizes(M, 8, 8, r, 1) != QLORA_OK) return 0;
+  return qlk::batch_workspace(M, r, is_bwd != 0).bytes;
+}
+
+int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint16_t* A,
+                      const uint16_t* B, const float* scale, int r, int S, const int32_t* order,
+                      const int32_t* start, const int32_t* tiles, const uint16_t* Y, double p,
+                      uint64_t seed, uint16_t* out, float* T_out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (!X || !A || !B || !scale || !order || !start || !tiles || !out) return QLORA_ERR_NULL;
+  int st = check_batch_sizes(M, K, N, r, S);
+  if (st) return st;
+  if (!valid_p(p)) return QLORA_ERR_ARG;
+  st = check_aligned({X, A, B, scale, order, start, tiles, Y, out, T_out, workspace});
+  if (st) return st;
+  if (!workspace || workspace_bytes < qlk::batch_workspace(M, r, false).bytes)
+    return QLORA_ERR_WORKSPACE;
+  const qlk::BatchAdapters a{A, B, scale, r, S, order, start, tiles};
+  return launch_status(qlk::launch_batch_fwd(X, M, K, N, a, Y, batch_dropout(p, seed), out, T_out,
+                                             workspace, as_stream(stream)));
+}
+
+int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                      const uint16_t* A, const uint16_t* B, const float* scale, int r, int S,
+                      const int32_t* order, const int32_t* start, const int32_t* tiles,
+                      const float* T, const uint16_t* dX0, double p, uint64_t seed, uint16_t* dX,
+                      float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (!dY || !X || !A || !B || !scale || !order || !start || !tiles || !dA || !dB)
+    return QLORA_ERR_NULL;
+  if (dX0 && !dX) return QLORA_ERR_NULL;
+  int st = check_batch_sizes(M, K, N, r, S);
+  if (st) return st;
+  if (!valid_p(p)) return QLORA_ERR_ARG;
+  st = check_aligned({dY, X, A, B, scale, order, start, tiles, T, dX0, dX, dA, dB, workspace});
+  if (st) return st;
+  if (!workspace || workspace_bytes < qlk::batch_workspace(M, r, true).bytes)
+    return QLORA_ERR_WORKSPACE;
+  const qlk::BatchAdapters a{A, B, scale, r, S, order, start, tiles};
+  return launch_status(qlk::launch_batch_bwd(dY, X, M, K, N, a, T, dX0, batch_dropout(p, seed), dX,
+                                             dA, dB, workspace, as_stream(stream)));
 }
 
 int qlora_merge(const uint8_t* packed, const uint8_t* codes, const float* scales,

@@ -302,6 +302,83 @@ int qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* Xd, const uint3
  * needs for these sizes; 0 means none.  Returns 0 for invalid sizes too. */
 size_t qlora_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int is_bwd);
 
+/* ---- adapters of many requests beside one shared projection ------------- */
+
+/* The base weight is frozen, so one projection can serve or train many
+ * adapters at once.  S slots hold adapters of one rank r for a projection of K
+ * inputs and N outputs: A bf16 [S, r, K], B bf16 [S, N, r], scale fp32 [S]
+ * (alpha / r of each; an adapter of a smaller rank is padded with zero rows of
+ * A and zero columns of B).  A batch holds M token rows; every token has a
+ * slot or none.  These calls add the adapters' term (llm-compass "QLoRA",
+ * 方法与公式, the equation's second term, each token with its own A and B) to
+ * what the shared projection gave. */
+
+/* Rows of `tiles` for M tokens and S slots: M / 64 + min(M, S + 1); 0 for
+ * invalid sizes. */
+int64_t lora_adapter_tiles(int64_t M, int S);
+
+/* The batch's plan, built on the device from its requests: request q covers
+ * the lengths[q] rows after those of the requests before it and uses the
+ * adapter in slot slots[q].  A slot outside [0, S) means no adapter, a negative
+ * length zero; rows past M are cut, rows behind the last request have no
+ * adapter.  lengths NULL: every request has one row (Q <= M).  Built once per
+ * batch and used for all its projections.
+ * In:  lengths int32 [Q] or NULL, slots int32 [Q] (device).
+ * Out (int32): token_slot [M], the token's slot or -1;
+ *      order [M], the tokens by slot, within a slot in their own order, those
+ *      without an adapter last;
+ *      start [S + 2], where each slot's tokens start in order, then where those
+ *      without an adapter start, then M;
+ *      tiles [lora_adapter_tiles(M, S)][3], (slot, first, count): runs of up to
+ *      64 positions of order, slot after slot, those without an adapter as
+ *      slot -1; unused rows (-1, 0, 0).
+ * Requires 1 <= S <= 1024, M >= 1, Q >= 0.  Bit-exact. */
+int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, int64_t M, int S,
+                      int32_t* token_slot, int32_t* order, int32_t* start, int32_t* tiles,
+                      void* stream);
+
+/* Forward: for a token m of slot a
+ *   T[m] = drop(X[m]) A_a^T,   out[m] = RNE_bf16(Y[m] + scale[a] T[m] B_a^T)
+ * and T[m] = 0, out[m] = Y[m] without an adapter.  T is fp32 [M, r] (T_out, or
+ * NULL if not wanted); the sum is held in fp32 and rounded once (T enters the
+ * product as two bf16 terms, within 2^-17).
+ * drop() is lora_dropout's mask for (p, seed) -- the same elements are kept --
+ * times 1 / (1 - p), regenerated where elements are used: neither the mask nor
+ * a dropped copy of X is stored, and X's kept values are not rounded.  p = 0
+ * drops nothing.  A captured graph repeats the seed it was captured with.
+ *   Y bf16 [M, N] (NULL: zeros), out bf16 [M, N]; out may be Y, and otherwise
+ *   no output may overlap an input.
+ *   order, start, tiles: from lora_adapter_plan with the same M and S.
+ * Requires r % 8 == 0, 8 <= r <= 256; K % 8 == 0, N % 8 == 0, both at most
+ * 2^23; X, Y under 2 GiB; 6 M r < 2^31; workspace of
+ * lora_adapters_workspace_bytes(M, r, 0). */
+int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint16_t* A,
+                      const uint16_t* B, const float* scale, int r, int S, const int32_t* order,
+                      const int32_t* start, const int32_t* tiles, const uint16_t* Y, double p,
+                      uint64_t seed, uint16_t* out, float* T_out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Backward, with U[m] = dY[m] B_a for a token m of slot a:
+ *   dX[m] = RNE_bf16(dX0[m] + drop(scale[a] U[m] A_a))       bf16 [M, K]
+ *   dA_a  = scale[a] sum_m U[m]^T drop(X[m])                  fp32 [S, r, K]
+ *   dB_a  = scale[a] sum_m dY[m]^T T[m]                       fp32 [S, N, r]
+ * over the slot's tokens, drop() as in the forward with the same p and seed.
+ * dX[m] = dX0[m] without an adapter; a slot without tokens gets zeros.
+ *   T fp32 [M, r] from the forward (NULL: computed again); dX0 bf16 [M, K]
+ *   (NULL: zeros); dX may be dX0, or NULL to skip it.
+ * U and T enter dA and dB as three bf16 terms (within 2^-25); the order of
+ * every sum is fixed.  Sizes as in the forward; workspace of
+ * lora_adapters_workspace_bytes(M, r, 1). */
+int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                      const uint16_t* A, const uint16_t* B, const float* scale, int r, int S,
+                      const int32_t* order, const int32_t* start, const int32_t* tiles,
+                      const float* T, const uint16_t* dX0, double p, uint64_t seed, uint16_t* dX,
+                      float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Bytes of workspace of the two calls above; 0 for invalid sizes. */
+size_t lora_adapters_workspace_bytes(int64_t M, int r, int is_bwd);
+
 /* ---- fused gate/up projections of a SiLU-gated MLP ---------------------- */
 
 /* One QLoRA linear of the MLP: NF4 base [I, K] as nf4_quantize + double_quant

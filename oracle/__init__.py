@@ -46,6 +46,9 @@ Functions and what pins them (tests/test_oracle_*.py):
                     round trip of the levels; nearest-level bound; fewer
                     absmax reconstruction errors than the linear code on a
                     heavy-tailed group
+  adapters          one slot reduces to the single-adapter layer without its
+                    base; differences of a scalar of the output against every
+                    gradient; the plan's invariants
 No function is "parity unpinned".
 """
 from .nf4 import (  # noqa: F401
@@ -62,3 +65,4 @@ from .dropout import (  # noqa: F401
     philox, philox4x32_words, dropout_threshold, dropout_scale, dropout_mask, dropout_apply,
     pack_mask, forward_dropout, backward_dropout,
 )
+from .adapters import adapter_plan, adapters_forward, adapters_backward  # noqa: F401

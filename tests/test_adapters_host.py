@@ -1,0 +1,160 @@
+"""Refusals of the adapters of many requests, without a GPU: the C ABI's status
+codes (validation runs before any launch, so fake, never dereferenced device
+addresses suffice) and the binding's ValueErrors on CPU tensors."""
+import os
+
+import pytest
+
+import bit_nf4_quantized_07_amd as q
+
+torch = pytest.importorskip("torch")
+if not os.path.exists(q.LIB_PATH):
+    pytest.skip("libqlora.so not built", allow_module_level=True)
+
+lib = q.load_library()
+D = 0x7f0000000000           # fake 16-byte aligned "device" address (never touched)
+MIS = D + 4
+BIG = 1 << 40
+
+
+def test_plan_sizes():
+    assert lib.lora_adapter_tiles(1, 1) == 1
+    assert lib.lora_adapter_tiles(64, 4) == 1 + 5
+    assert lib.lora_adapter_tiles(3, 1024) == 3
+    assert lib.lora_adapter_tiles(130, 1) == 2 + 2
+    for M, S in ((0, 1), (-5, 1), (1 << 31, 1), (4, 0), (4, 1025), (4, -1)):
+        assert lib.lora_adapter_tiles(M, S) == 0
+
+
+def test_plan_refusals():
+    ok = dict(lengths=D, slots=D, Q=3, M=10, S=4, token_slot=D, order=D, start=D, tiles=D)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return lib.lora_adapter_plan(a["lengths"], a["slots"], a["Q"], a["M"], a["S"],
+                                     a["token_slot"], a["order"], a["start"], a["tiles"], None)
+
+    for name in ("slots", "token_slot", "order", "start", "tiles"):
+        assert call(**{name: None}) == q.ERR_NULL, name
+    for name in ("lengths", "slots", "token_slot", "order", "start", "tiles"):
+        assert call(**{name: MIS}) == q.ERR_ALIGN, name
+    for kw in (dict(M=0), dict(M=1 << 31), dict(S=0), dict(S=1025), dict(Q=-1), dict(Q=1 << 31),
+               dict(lengths=None, Q=11)):
+        assert call(**kw) == q.ERR_SHAPE, kw
+
+
+FWD = ("X", "M", "K", "N", "A", "B", "scale", "r", "S", "order", "start", "tiles", "Y", "p",
+       "seed", "out", "T", "ws", "wsb", "stream")
+BWD = ("dY", "X", "M", "K", "N", "A", "B", "scale", "r", "S", "order", "start", "tiles", "T",
+       "dX0", "p", "seed", "dX", "dA", "dB", "ws", "wsb", "stream")
+BASE = dict(M=32, K=64, N=40, r=16, S=4, p=0.1, seed=1, wsb=1 << 30, stream=None)
+
+
+def _call(fn, names, **kw):
+    a = {n: D for n in names}
+    a.update({k: v for k, v in BASE.items() if k in names})
+    a.update(kw)
+    return fn(*(a[n] for n in names))
+
+
+@pytest.mark.parametrize("fn,names,required,optional", [
+    (lib.lora_adapters_fwd, FWD, ("X", "A", "B", "scale", "order", "start", "tiles", "out"),
+     ("Y", "T")),
+    (lib.lora_adapters_bwd, BWD,
+     ("dY", "X", "A", "B", "scale", "order", "start", "tiles", "dA", "dB"), ("T", "dX0", "dX")),
+])
+def test_layer_refusals(fn, names, required, optional):
+    for n in required:
+        assert _call(fn, names, **{n: None}) == q.ERR_NULL, n
+    for n in required + optional + ("ws",):
+        assert _call(fn, names, **{n: MIS}) == q.ERR_ALIGN, n
+    for kw in (dict(M=0), dict(M=1 << 31), dict(K=0), dict(K=60), dict(N=0), dict(N=42),
+               dict(r=0), dict(r=12), dict(r=264), dict(S=0), dict(S=1025),
+               dict(K=(1 << 23) + 8), dict(N=(1 << 23) + 8),
+               dict(M=1 << 20, K=1 << 10), dict(M=1 << 20, N=1 << 10), dict(M=1 << 21, K=8, N=8, r=256)):
+        assert _call(fn, names, **kw) == q.ERR_SHAPE, kw
+    for p in (-0.1, 1.0, 1.5, float("nan"), float("inf")):
+        assert _call(fn, names, p=p) == q.ERR_ARG, p
+    assert _call(fn, names, ws=None) == q.ERR_WORKSPACE
+    need = lib.lora_adapters_workspace_bytes(32, 16, 1 if "dY" in names else 0)
+    assert need > 0
+    assert _call(fn, names, wsb=need - 1) == q.ERR_WORKSPACE
+
+
+def test_dX0_without_dX_is_refused():
+    assert _call(lib.lora_adapters_bwd, BWD, dX=None) == q.ERR_NULL
+
+
+def test_workspace_bytes_of_invalid_sizes():
+    for M, r in ((0, 16), (8, 12), (8, 0), (8, 264), (1 << 31, 8)):
+        assert lib.lora_adapters_workspace_bytes(M, r, 0) == 0
+        assert lib.lora_adapters_workspace_bytes(M, r, 1) == 0
+
+
+# ---- the binding ------------------------------------------------------------
+
+M, K, N, R, S = 6, 64, 32, 8, 3
+bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _plan(M=M, S=S):
+    nt = lib.lora_adapter_tiles(M, S)
+    z = lambda *s: torch.zeros(*s, dtype=i32)
+    return q.AdapterPlan(z(M), z(M), z(S + 2), z(nt, 3), S)
+
+
+def _args():
+    return dict(X=torch.zeros(M, K, dtype=bf), Y=torch.zeros(M, N, dtype=bf),
+                A=torch.zeros(S, R, K, dtype=bf), B=torch.zeros(S, N, R, dtype=bf),
+                scale=torch.zeros(S), plan=_plan())
+
+
+def _raises(match, fn, **kw):
+    with pytest.raises(ValueError, match=match):
+        fn(**kw)
+
+
+@pytest.mark.parametrize("name,bad,match", [
+    ("X", torch.zeros(M, K), "X: dtype"),
+    ("X", torch.zeros(M, 2 * K, dtype=bf)[:, ::2], "X: not contiguous"),
+    ("Y", torch.zeros(M, N + 8, dtype=bf), "Y: shape"),
+    ("A", torch.zeros(R, K, dtype=bf), "A: a bf16"),
+    ("A", torch.zeros(S + 1, R, K, dtype=bf), "plan: built for"),
+    ("B", torch.zeros(N, R, dtype=bf), "B: a bf16"),
+    ("B", torch.zeros(S, N, R + 8, dtype=bf), "B: shape"),
+    ("scale", torch.zeros(S, dtype=bf), "scale: dtype"),
+    ("scale", torch.zeros(S + 1), "scale: shape"),
+    ("plan", None, "plan: an AdapterPlan"),
+    ("plan", _plan(M=M + 1), "order: shape"),
+])
+def test_forward_and_backward_refuse_bad_tensors(name, bad, match):
+    a = _args()
+    a[name] = bad
+    _raises(match, q.adapters_fwd, **a)
+    b = dict(a, dY=a["Y"])
+    b.pop("Y")
+    if name == "Y":
+        match = "dY: shape"
+    _raises(match, q.adapters_bwd, **b)
+
+
+def test_outputs_and_devices_are_checked():
+    a = _args()
+    _raises("not on a CUDA", q.adapters_fwd, **a)
+    _raises("out: shape", q.adapters_fwd, **a, out=torch.zeros(M, N + 8, dtype=bf))
+    _raises("T_out: dtype", q.adapters_fwd, **a, T_out=torch.zeros(M, R, dtype=bf))
+    b = {k: v for k, v in a.items() if k != "Y"}
+    b["dY"] = a["Y"]
+    _raises("T: dtype", q.adapters_bwd, **b, T=torch.zeros(M, R, dtype=bf))
+    _raises("dA: shape", q.adapters_bwd, **b, dA_out=torch.zeros(S, R, K + 64))
+    _raises("dB: shape", q.adapters_bwd, **b, dB_out=torch.zeros(S, R, N))
+    _raises("dX: shape", q.adapters_bwd, **b, dX=torch.zeros(M, N, dtype=bf))
+
+
+def test_plan_binding_refusals():
+    s = torch.zeros(4, dtype=i32)
+    _raises("slots: a 1-D", q.adapter_plan, slots=[0, 1], S=2)
+    _raises("slots: dtype", q.adapter_plan, slots=s.long(), S=2)
+    _raises("lengths: shape", q.adapter_plan, slots=s, S=2, lengths=s[:3], tokens=8)
+    _raises("tokens:", q.adapter_plan, slots=s, S=2, lengths=s)
+    _raises("not on a CUDA", q.adapter_plan, slots=s, S=2)
