@@ -11,7 +11,6 @@ or no GPU is visible, the compute calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -26,6 +25,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 BWD_ACCUMULATE_DX = 1
 BLOCKSIZE = 64
 DQ_BLOCKSIZE = 256
+PLAN_TILE = 64
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -99,7 +99,7 @@ SIGNATURES = {
                                     ctypes.POINTER(TimingC)]),
     "lora_adapter_tiles": (_I64, [_I64, _I]),
     "lora_adapter_plan": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _P, _P, _P]),
-    "lora_adapters_workspace_bytes": (ctypes.c_size_t, [_I64, _I, _I]),
+    "lora_adapters_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I, _I, _I]),
     "lora_adapters_fwd": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _P, _P, _P, _P,
                                ctypes.c_double, ctypes.c_uint64, _P, _P, _P, ctypes.c_size_t, _P]),
     "lora_adapters_bwd": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P,
@@ -552,14 +552,33 @@ class AdapterPlan(NamedTuple):
     S: int
 
 
-@contextlib.contextmanager
-def _on_device(dev):
+def _checked(items):
+    """_Checker's checks of (name, tensor, dtype, shape) items, all required,
+    and their device.  These calls are short, so what passes takes one quick
+    pass; anything else goes to _Checker, which names the first fault."""
+    tensor = _torch().Tensor
+    first = items[0][1]
+    index = first.get_device() if type(first) is tensor else -1
+    for _, t, dtype, shape in items:
+        if (type(t) is not tensor or t.dtype is not dtype or t.shape != shape
+                or not t.is_contiguous() or t.get_device() != index):
+            break
+    else:
+        if index >= 0:
+            return first.device
+    chk = _Checker()
+    for name, t, dtype, shape in items:
+        chk(name, t, dtype, shape)
+    return chk.device()
+
+
+def _on_device(dev, call):
+    """call(stream) with `dev` current and its current stream."""
     torch = _torch()
     if torch.cuda.current_device() == dev.index:
-        yield
-    else:
-        with torch.cuda.device(dev):
-            yield
+        return call(torch.cuda.current_stream(dev))
+    with torch.cuda.device(dev):
+        return call(torch.cuda.current_stream(dev))
 
 
 def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> AdapterPlan:
@@ -568,17 +587,17 @@ def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> A
     each).  `tokens` is the batch's number of rows M (default, without lengths:
     Q); rows behind the last request have no adapter."""
     torch = _torch()
-    chk = _Checker()
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots: a 1-D int32 tensor")
     Q = slots.shape[0]
-    chk("slots", slots, torch.int32, (Q,))
-    chk.opt("lengths", lengths, torch.int32, (Q,))
+    items = [("slots", slots, torch.int32, (Q,))]
+    if lengths is not None:
+        items.append(("lengths", lengths, torch.int32, (Q,)))
     if tokens is None:
         if lengths is not None:
             raise ValueError("tokens: the batch's number of rows, where lengths are given")
         tokens = Q
-    dev = chk.device()
+    dev = _checked(items)
     M, S = int(tokens), int(S)
     lib = load_library()
     nt = lib.lora_adapter_tiles(M, S) if abs(M) < 2**62 and abs(S) < 2**31 else 0
@@ -587,33 +606,36 @@ def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> A
     # one allocation, each array at a multiple of 16 bytes
     mp, sp = (M + 3) & ~3, (S + 5) & ~3
     buf = torch.empty(2 * mp + sp + 3 * nt, dtype=torch.int32, device=dev)
-    plan = AdapterPlan(buf[:M], buf[mp:mp + M], buf[2 * mp:2 * mp + S + 2],
+    at = buf.data_ptr()
+    _check("lora_adapter_plan", _on_device(dev, lambda st: lib.lora_adapter_plan(
+        None if lengths is None else lengths.data_ptr(), slots.data_ptr() if Q else None, Q, M, S,
+        at, at + 4 * mp, at + 8 * mp, at + 8 * mp + 4 * sp, st.cuda_stream)))
+    return AdapterPlan(buf[:M], buf[mp:mp + M], buf[2 * mp:2 * mp + S + 2],
                        buf[2 * mp + sp:].view(nt, 3), S)
-    with _on_device(dev):
-        _check("lora_adapter_plan", lib.lora_adapter_plan(
-            _ptr(lengths), _ptr(slots) if Q else None, Q, M, S, _ptr(plan.token_slot),
-            _ptr(plan.order), _ptr(plan.start), _ptr(plan.tiles), _stream(dev)))
-    return plan
 
 
-def _batch_adapters(chk, A, B, scale, plan, M, K, N):
-    """Checks the bank and the plan; returns (r, S)."""
+def _batch_items(X, A, B, scale, plan):
+    """(M, K, N, r, S) and the check items of X, the adapters and the plan."""
     torch = _torch()
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X: a 2-D tensor")
     if not isinstance(A, torch.Tensor) or A.dim() != 3:
         raise ValueError("A: a bf16 [S, r, K] tensor")
+    if not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("B: a bf16 [S, N, r] tensor")
     if not isinstance(plan, AdapterPlan):
         raise ValueError("plan: an AdapterPlan")
-    S, r = A.shape[0], A.shape[1]
+    M, K = X.shape
+    S, r, _ = A.shape
+    N = B.shape[1]
     if plan.S != S:
         raise ValueError(f"plan: built for {plan.S} slots, the adapters have {S}")
-    chk("A", A, torch.bfloat16, (S, r, K))
-    chk("B", B, torch.bfloat16, (S, N, r))
-    chk("scale", scale, torch.float32, (S,))
-    chk("order", plan.order, torch.int32, (M,))
-    chk("start", plan.start, torch.int32, (S + 2,))
-    chk("tiles", plan.tiles, torch.int32,
-        (load_library().lora_adapter_tiles(M, S), 3))
-    return r, S
+    bf, i32 = torch.bfloat16, torch.int32
+    nt = M // PLAN_TILE + min(M, S + 1)
+    return (M, K, N, r, S), [
+        ("X", X, bf, (M, K)), ("A", A, bf, (S, r, K)), ("B", B, bf, (S, N, r)),
+        ("scale", scale, torch.float32, (S,)), ("order", plan.order, i32, (M,)),
+        ("start", plan.start, i32, (S + 2,)), ("tiles", plan.tiles, i32, (nt, 3))]
 
 
 def _dropout_args(dropout):
@@ -621,6 +643,12 @@ def _dropout_args(dropout):
         return 0.0, 0
     p, seed = dropout
     return float(p), int(seed) & (2**64 - 1)
+
+
+def _batch_workspace(dev, stream, nbytes, workspace):
+    ws = workspace if workspace is not None else default_workspace(dev, stream)
+    buf, size = ws.get(nbytes, stream)
+    return (buf.data_ptr() if buf is not None else None), size
 
 
 def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: bool = True,
@@ -631,28 +659,31 @@ def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: boo
     (p, seed), lora_dropout's mask, regenerated where it is needed.  Returns
     (out bf16 [M, N], T fp32 [M, r] or None)."""
     torch = _torch()
-    chk = _Checker()
-    M, K = chk.mat("X", X, torch.bfloat16)
-    if not isinstance(B, torch.Tensor) or B.dim() != 3:
-        raise ValueError("B: a bf16 [S, N, r] tensor")
-    N = B.shape[1]
-    r, S = _batch_adapters(chk, A, B, scale, plan, M, K, N)
-    chk.opt("Y", Y, torch.bfloat16, (M, N))
-    chk.opt("out", out, torch.bfloat16, (M, N))
-    chk.opt("T_out", T_out, torch.float32, (M, r))
+    (M, K, N, r, S), items = _batch_items(X, A, B, scale, plan)
+    if Y is not None:
+        items.append(("Y", Y, torch.bfloat16, (M, N)))
+    if out is not None:
+        items.append(("out", out, torch.bfloat16, (M, N)))
+    if T_out is not None:
+        items.append(("T_out", T_out, torch.float32, (M, r)))
     p, seed = _dropout_args(dropout)
-    dev = chk.device()
+    dev = _checked(items)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    T = T_out if T_out is not None else (
-        torch.empty(M, r, dtype=torch.float32, device=dev) if save_T else None)
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    T = T_out
+    if T is None and save_T:
+        T = torch.empty((M, r), dtype=torch.float32, device=dev)
     lib = load_library()
-    with _on_device(dev):
-        ws, wsb = _ws(dev, lib.lora_adapters_workspace_bytes(M, r, 0), workspace)
-        _check("lora_adapters_fwd", lib.lora_adapters_fwd(
-            _ptr(X), M, K, N, _ptr(A), _ptr(B), _ptr(scale), r, S, _ptr(plan.order),
-            _ptr(plan.start), _ptr(plan.tiles), _ptr(Y), p, seed, _ptr(out), _ptr(T), _ptr(ws),
-            wsb, _stream(dev)))
+
+    def call(st):
+        ws, wsb = _batch_workspace(dev, st, lib.lora_adapters_workspace_bytes(M, K, N, r, S, 0), workspace)
+        return lib.lora_adapters_fwd(
+            X.data_ptr(), M, K, N, A.data_ptr(), B.data_ptr(), scale.data_ptr(), r, S,
+            plan.order.data_ptr(), plan.start.data_ptr(), plan.tiles.data_ptr(),
+            None if Y is None else Y.data_ptr(), p, seed, out.data_ptr(),
+            None if T is None else T.data_ptr(), ws, wsb, st.cuda_stream)
+
+    _check("lora_adapters_fwd", _on_device(dev, call))
     return out, T
 
 
@@ -663,34 +694,35 @@ def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout
     gave: the adapters' term is added to it (dX_out may be the same tensor).
     T from the forward (None: computed again); dropout as in the forward."""
     torch = _torch()
-    chk = _Checker()
-    M, K = chk.mat("X", X, torch.bfloat16)
-    if not isinstance(B, torch.Tensor) or B.dim() != 3:
-        raise ValueError("B: a bf16 [S, N, r] tensor")
-    N = B.shape[1]
-    r, S = _batch_adapters(chk, A, B, scale, plan, M, K, N)
-    chk("dY", dY, torch.bfloat16, (M, N))
-    chk.opt("T", T, torch.float32, (M, r))
-    chk.opt("dX", dX, torch.bfloat16, (M, K))
-    chk.opt("dX_out", dX_out, torch.bfloat16, (M, K))
-    chk.opt("dA", dA_out, torch.float32, (S, r, K))
-    chk.opt("dB", dB_out, torch.float32, (S, N, r))
+    f32 = torch.float32
+    (M, K, N, r, S), items = _batch_items(X, A, B, scale, plan)
+    items.append(("dY", dY, torch.bfloat16, (M, N)))
+    for name, t, dtype, shape in (("T", T, f32, (M, r)), ("dX", dX, torch.bfloat16, (M, K)),
+                                  ("dX_out", dX_out, torch.bfloat16, (M, K)),
+                                  ("dA", dA_out, f32, (S, r, K)), ("dB", dB_out, f32, (S, N, r))):
+        if t is not None:
+            items.append((name, t, dtype, shape))
     p, seed = _dropout_args(dropout)
-    dev = chk.device()
+    dev = _checked(items)
     if not need_dX:
         if dX is not None or dX_out is not None:
             raise ValueError("dX: given, but need_dX is False")
     elif dX_out is None:
-        dX_out = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-    dA = dA_out if dA_out is not None else torch.empty(S, r, K, dtype=torch.float32, device=dev)
-    dB = dB_out if dB_out is not None else torch.empty(S, N, r, dtype=torch.float32, device=dev)
+        dX_out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    dA = dA_out if dA_out is not None else torch.empty((S, r, K), dtype=f32, device=dev)
+    dB = dB_out if dB_out is not None else torch.empty((S, N, r), dtype=f32, device=dev)
     lib = load_library()
-    with _on_device(dev):
-        ws, wsb = _ws(dev, lib.lora_adapters_workspace_bytes(M, r, 1), workspace)
-        _check("lora_adapters_bwd", lib.lora_adapters_bwd(
-            _ptr(dY), _ptr(X), M, K, N, _ptr(A), _ptr(B), _ptr(scale), r, S, _ptr(plan.order),
-            _ptr(plan.start), _ptr(plan.tiles), _ptr(T), _ptr(dX), p, seed, _ptr(dX_out),
-            _ptr(dA), _ptr(dB), _ptr(ws), wsb, _stream(dev)))
+
+    def call(st):
+        ws, wsb = _batch_workspace(dev, st, lib.lora_adapters_workspace_bytes(M, K, N, r, S, 1), workspace)
+        return lib.lora_adapters_bwd(
+            dY.data_ptr(), X.data_ptr(), M, K, N, A.data_ptr(), B.data_ptr(), scale.data_ptr(), r,
+            S, plan.order.data_ptr(), plan.start.data_ptr(), plan.tiles.data_ptr(),
+            None if T is None else T.data_ptr(), None if dX is None else dX.data_ptr(), p, seed,
+            None if dX_out is None else dX_out.data_ptr(), dA.data_ptr(), dB.data_ptr(), ws, wsb,
+            st.cuda_stream)
+
+    _check("lora_adapters_bwd", _on_device(dev, call))
     return dX_out, dA, dB
 
 

@@ -52,12 +52,19 @@ __device__ __forceinline__ TileRow tile_row(const int* tiles, int i, int M, int 
 }
 
 // ---------------------------------------------------------------------------
-// T = X A_a^T and U = dY B_a, fp32 [M, r].  One workgroup takes `rows` (8 or
-// 16) tokens of one slot, gathered through the plan's order; its NW waves take
-// every NW-th 64-wide piece of the contraction and add their sums through LDS
-// in a fixed order.  Bound: HBM, one pass over X (dY); each workgroup reads
-// its slot's A (B) once, from L2 where workgroups share the slot.
-constexpr int kDownRows = 16;
+// T = X A_a^T and U = dY B_a as fp32 sums over slices of the contraction,
+// part[z] [M, r].  One workgroup takes a tile of the plan (up to 64 tokens of
+// one slot, gathered through the order), one slice and up to 64 ranks; its
+// four waves take every fourth 64-wide step, each for all 64 tokens, with the
+// loads of the next step in flight, and add their sums through LDS in a fixed
+// order.  The readers of T and U add the slices in their order.
+//
+// Bound: HBM, one pass over X (dY), where there are many tokens; the slot's A
+// (B) where there are few.  64 tokens per workgroup make the tile's own bytes
+// at least the adapter's (which come from L2) up to rank 64, and slices fill
+// the device where there are few tiles.  A slice is the fast grid index, so
+// that an XCD keeps to its part of the adapters.
+constexpr int kDownWaves = 4;
 
 struct DownArgs {
   const uint16_t* S;     // [M, C] bf16
@@ -67,160 +74,205 @@ struct DownArgs {
   int r, slots;
   const int* order;
   const int* tiles;
-  int rows;              // tokens per workgroup
-  float* out;            // fp32 [M, r]
-  uint16_t* planes;      // bf16 terms of out, [3][M, r], or null
+  int zlen;              // steps per slice
+  float* part;           // fp32 [slices][M, r]
   DropKey drop;
   float keep_scale;
 };
 
-template <bool WT, bool DROP, int RT, int NW, int kB>
-__global__ void __launch_bounds__(NW * 64) k_batch_down(DownArgs g) {
-  __shared__ float red[NW - 1][kDownRows][RT * 16];
-  // WT: one 64 (c) x 16 (j) slice of B per wave, row-major.
-  __shared__ __attribute__((aligned(16))) uint16_t slab[WT ? NW : 1][64 * 16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+template <bool WT, bool DROP, int RT>
+__global__ void __launch_bounds__(64 * kDownWaves) k_batch_down(DownArgs g) {
+  constexpr int SW = 16 * RT + 8;   // WT: row of a wave's 64 (c) x 16 RT (j) slab, padded
+  constexpr int SLAB = WT ? kDownWaves * 64 * SW * 2 : 16, RED = 4 * 3 * RT * 64 * 16;
+  __shared__ __attribute__((aligned(16))) char smem[SLAB > RED ? SLAB : RED];
+  __shared__ int rows[kPlanTile];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15, grp = lane >> 4;
-  const int subs = kPlanTile / g.rows;
-  const TileRow t = tile_row(g.tiles, (int)blockIdx.x / subs, g.M, g.slots);
-  const int off = ((int)blockIdx.x % subs) * g.rows;
-  const int n = min(g.rows, t.count - off);
-  if (n <= 0) return;
-  const int r = g.r;
-  const int* const ord = g.order + t.first + off;
-  if (t.slot < 0) {   // no adapter: zeros
-    for (int e = tid; e < n * r; e += NW * 64) {
-      const int m = ord[e / r];
-      if ((unsigned)m >= (unsigned)g.M) continue;
-      g.out[(int64_t)m * r + e % r] = 0.0f;
-    }
-    return;
+  const TileRow t = tile_row(g.tiles, blockIdx.y, g.M, g.slots);
+  if (t.count <= 0 || t.slot < 0) return;
+  if (tid < kPlanTile) {
+    const int m = tid < t.count ? g.order[t.first + tid] : -1;
+    rows[tid] = (unsigned)m < (unsigned)g.M ? m : -1;
   }
-  // Rows past the tile read the tile's last row (its lines are loaded anyway).
-  int m = ord[min(row, n - 1)];
-  const bool mvalid = row < n && (unsigned)m < (unsigned)g.M;
-  if ((unsigned)m >= (unsigned)g.M) m = 0;
-  const int64_t C = g.C;
-  const int64_t nsteps = (C + 63) / 64;
-  const uint16_t* const srow = g.S + (int64_t)m * C;
-  const uint16_t* const W = g.W + (int64_t)t.slot * C * r;
-  const int wrow = lane >> 1, wcol = 8 * (lane & 1);
-  uint16_t* const my = slab[WT ? wave : 0];
-  const int rd = (16 * grp + (row >> 2)) * 16 + 4 * (row & 3);
+  const int z = blockIdx.x, j0 = (int)blockIdx.z * 64;
+  const int r = g.r, ntg = (t.count + 15) / 16;
+  const int C = (int)g.C;
+  const int nsteps = (C + 63) / 64;
+  const int s0 = z * g.zlen, s1 = min(nsteps, s0 + g.zlen);
+  __syncthreads();
 
-  f32x4_t acc[RT];
+  // Byte offsets of a lane's pieces at step 0; a step adds 128 bytes (WT: 64
+  // rows of B) through the scalar offset.  Lane (row, grp) holds the 16
+  // contiguous indices 16 grp .. +15 of the step, MFMA h takes 16 grp + 8 h ..
+  // +7, the same permutation for both operands.
+  const __amdgpu_buffer_rsrc_t rs = rsrc_whole(g.S, (uint32_t)((int64_t)g.M * C * 2));
+  const __amdgpu_buffer_rsrc_t rw =
+      rsrc_whole(g.W + (int64_t)t.slot * C * r, (uint32_t)((int64_t)C * r * 2));
+  uint32_t xoff[4], woff[2 * RT];
 #pragma unroll
-  for (int q = 0; q < RT; ++q) acc[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int tg = 0; tg < 4; ++tg) {
+    const int m = rows[16 * tg + row];
+    xoff[tg] = m >= 0 ? (uint32_t)(((int64_t)m * C + 16 * grp) * 2) : kOOB;
+  }
+#pragma unroll
+  for (int q = 0; q < 2 * RT; ++q) {
+    if (!WT) {
+      const int j = j0 + 16 * (q >> 1) + row;
+      woff[q] = j < r ? (uint32_t)(((int64_t)j * C + 16 * grp + 8 * (q & 1)) * 2) : kOOB;
+    } else {
+      const int p = 64 * q + lane;          // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
+      const int j = j0 + 8 * (p % (2 * RT));
+      woff[q] = j < r ? (uint32_t)(((p / (2 * RT)) * r + j) * 2) : kOOB;
+    }
+  }
+  f32x4_t acc[4][RT];
+#pragma unroll
+  for (int tg = 0; tg < 4; ++tg)
+#pragma unroll
+    for (int q = 0; q < RT; ++q) acc[tg][q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int64_t b0 = wave; b0 < nsteps; b0 += (int64_t)NW * kB) {
-    uint4 xv[kB][2], wv[kB][RT][2];
+  auto load = [&](int st, uint4 (&xv)[4][2], uint4 (&wv)[2 * RT]) {
+    const uint32_t ss = (uint32_t)__builtin_amdgcn_readfirstlane(st);
+    const int left = C - 64 * st;           // indices of this step inside the operand
 #pragma unroll
-    for (int b = 0; b < kB; ++b) {
-      const int64_t ks = b0 + (int64_t)NW * b;
-      const bool sv = ks < nsteps;
+    for (int q = 0; q < 2 * RT; ++q) {
+      const int at = WT ? (64 * q + lane) / (2 * RT) : 16 * grp + 8 * (q & 1);
+      wv[q] = bload128s(rw, at < left ? woff[q] : kOOB, WT ? ss * 128u * (uint32_t)r : ss * 128u);
+    }
+#pragma unroll
+    for (int tg = 0; tg < 4; ++tg) {
+      if (tg >= ntg) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        xv[tg][h] = bload128s(
+            rs, xoff[tg] != kOOB && 16 * grp + 8 * h < left ? xoff[tg] + 16 * h : kOOB, ss * 128u);
+    }
+  };
+  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + (WT ? wave * 64 * SW : 0);
+  auto mul = [&](int st, uint4 (&xv)[4][2], const uint4 (&wv)[2 * RT]) {
+    bf16x8_t wop[RT][2];
+    if constexpr (!WT) {
+#pragma unroll
+      for (int q = 0; q < 2 * RT; ++q) wop[q >> 1][q & 1] = __builtin_bit_cast(bf16x8_t, wv[q]);
+    } else {
+      // A wave's LDS operations run in issue order: the stores are complete
+      // before the reads, which complete before the next stores.
+#pragma unroll
+      for (int q = 0; q < 2 * RT; ++q) {
+        const int p = 64 * q + lane;
+        *reinterpret_cast<uint4*>(my + (p / (2 * RT)) * SW + 8 * (p % (2 * RT))) = wv[q];
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+#pragma unroll
+      for (int q = 0; q < RT; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint16_t* p = my + (16 * grp + 8 * h + (row >> 2)) * SW + 16 * q + 4 * (row & 3);
+          const v4s_t lo = lds_read_tr16(p);
+          const v4s_t hi = lds_read_tr16(p + 4 * SW);
+          const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          wop[q][h] = __builtin_bit_cast(bf16x8_t, v);
+        }
+    }
+#pragma unroll
+    for (int tg = 0; tg < 4; ++tg) {
+      if (tg >= ntg) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t k = ks * 64 + 16 * grp + 8 * h;   // 8 contraction indices
-        const bool kvalid = sv && k < C;
-        xv[b][h] = keep_or_zero(mvalid && kvalid,
-                                *reinterpret_cast<const uint4*>(srow + (kvalid ? k : 0)));
-#pragma unroll
-        for (int q = 0; q < RT; ++q) {
-          if (!WT) {
-            const int j = 16 * q + row;
-            const bool ok = kvalid && j < r;
-            wv[b][q][h] = keep_or_zero(
-                ok, *reinterpret_cast<const uint4*>(W + (ok ? (int64_t)j * C + k : 0)));
-          } else {
-            const int64_t c = ks * 64 + 32 * h + wrow;
-            const int j = 16 * q + wcol;
-            const bool ok = sv && c < C && j < r;
-            wv[b][q][h] =
-                keep_or_zero(ok, *reinterpret_cast<const uint4*>(W + (ok ? c * r + j : 0)));
-          }
+        uint4 x = xv[tg][h];
+        if constexpr (DROP) {
+          const uint32_t m = (uint32_t)max(rows[16 * tg + row], 0);
+          x = philox_drop8(x, (uint64_t)m * (uint32_t)C + (uint32_t)(64 * st + 16 * grp + 8 * h),
+                           g.drop);
         }
+#pragma unroll
+        for (int q = 0; q < RT; ++q)
+          acc[tg][q] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, x), wop[q][h], acc[tg][q]);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);   // every load of the batch before the first MFMA
-#pragma unroll
-    for (int b = 0; b < kB; ++b) {
-      if constexpr (DROP) {
-        const int64_t ks = b0 + (int64_t)NW * b;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          xv[b][h] = philox_drop8(
-              xv[b][h], (uint64_t)((int64_t)m * C + ks * 64 + 16 * grp + 8 * h), g.drop);
-      }
-#pragma unroll
-      for (int q = 0; q < RT; ++q) {
-        bf16x8_t bop[2];
-        if (!WT) {
-          bop[0] = __builtin_bit_cast(bf16x8_t, wv[b][q][0]);
-          bop[1] = __builtin_bit_cast(bf16x8_t, wv[b][q][1]);
-        } else {
-          // A wave's LDS operations run in issue order: the stores are
-          // complete before the reads, which complete before the next stores.
-          *reinterpret_cast<uint4*>(my + wrow * 16 + wcol) = wv[b][q][0];
-          *reinterpret_cast<uint4*>(my + (32 + wrow) * 16 + wcol) = wv[b][q][1];
-          __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v4s_t lo = lds_read_tr16(my + rd + 8 * h * 16);
-            const v4s_t hi = lds_read_tr16(my + rd + (8 * h + 4) * 16);
-            const v8s_t bv = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            bop[h] = __builtin_bit_cast(bf16x8_t, bv);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[q] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xv[b][h]), bop[h], acc[q]);
-      }
+  };
+  {
+    uint4 xa[4][2], xb[4][2], wa[2 * RT], wb[2 * RT];
+    int st = s0 + wave;
+    if (st < s1) load(st, xa, wa);
+    for (; st < s1; st += 2 * kDownWaves) {
+      const bool two = st + kDownWaves < s1;
+      if (two) load(st + kDownWaves, xb, wb);
+      mul(st, xa, wa);
+      if (st + 2 * kDownWaves < s1) load(st + 2 * kDownWaves, xa, wa);
+      if (two) mul(st + kDownWaves, xb, wb);
     }
   }
 
-  // acc[q][v]: row 4 grp + v, column 16 q + row of the tile.
-  if (wave > 0) {
+  // acc[tg][q][v]: token 16 tg + 4 grp + v, rank j0 + 16 q + row.  Wave w adds
+  // the four waves' sums of token group w in the order 0, 1, 2, 3.
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem);
+  if (WT) __syncthreads();   // the slabs are free
+#pragma unroll
+  for (int tg = 0; tg < 4; ++tg) {
+    if (tg >= ntg || tg == wave) continue;
 #pragma unroll
     for (int q = 0; q < RT; ++q)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave - 1][4 * grp + v][16 * q + row] = acc[q][v];
+      red[((tg * 3 + (wave < tg ? wave : wave - 1)) * RT + q) * 64 + lane] = acc[tg][q];
   }
   __syncthreads();
-  if (wave != 0) return;
-  int mo[4];
+  float* const out = g.part + (int64_t)z * g.M * r;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) mo[v] = 4 * grp + v < n ? ord[4 * grp + v] : -1;
+  for (int tg = 0; tg < 4; ++tg) {
+    if (tg >= ntg || tg != wave) continue;
+    int mo[4];
 #pragma unroll
-  for (int q = 0; q < RT; ++q) {
-    const int j = 16 * q + row;
+    for (int v = 0; v < 4; ++v) mo[v] = rows[16 * tg + 4 * grp + v];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float sum = acc[q][v];
+    for (int q = 0; q < RT; ++q) {
+      f32x4_t sum = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < NW - 1; ++w) sum += red[w][4 * grp + v][j];
-      if (DROP) sum *= g.keep_scale;
-      if ((unsigned)mo[v] >= (unsigned)g.M || j >= r) continue;
-      const int64_t o = (int64_t)mo[v] * r + j;
-      g.out[o] = sum;
-      if (g.planes) {
-        const int64_t plane = (int64_t)g.M * r;
-        split3(sum, g.planes[o], g.planes[plane + o], g.planes[2 * plane + o]);
+      for (int w = 0; w < kDownWaves; ++w) {
+        const f32x4_t a =
+            w == tg ? acc[tg][q] : red[((tg * 3 + (w < tg ? w : w - 1)) * RT + q) * 64 + lane];
+        sum[0] += a[0]; sum[1] += a[1]; sum[2] += a[2]; sum[3] += a[3];
       }
+      const int j = j0 + 16 * q + row;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (mo[v] >= 0 && j < r) out[(int64_t)mo[v] * r + j] = DROP ? sum[v] * g.keep_scale : sum[v];
     }
   }
 }
 
-// The bf16 terms of an fp32 [M, r], for the gradients' kernel.
-__global__ void __launch_bounds__(256)
-k_batch_split(const float* __restrict__ x, int64_t n, uint16_t* __restrict__ planes) {
+// The sum of the slices of part ([slices][M, r]) and its bf16 terms, for the
+// gradients: four elements per thread, U and T in one launch (two halves of
+// the grid).  Rows without an adapter hold nothing and are not read.
+struct SplitJob {
+  const float* part;
+  int slices;
+  uint16_t* planes;   // [3][M, r]
+};
+__global__ void __launch_bounds__(256) k_batch_split(SplitJob ju, SplitJob jt, int64_t n4) {
+  const SplitJob& j = blockIdx.y ? jt : ju;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) split3(x[i], planes[i], planes[n + i], planes[2 * n + i]);
+  if (i >= n4) return;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int z = 0; z < j.slices; ++z) {
+    const float4 p = reinterpret_cast<const float4*>(j.part)[z * n4 + i];
+    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+  }
+  const float e[4] = {v.x, v.y, v.z, v.w};
+  uint16_t t[3][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split3(e[k], t[0][k], t[1][k], t[2][k]);
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+    reinterpret_cast<uint2*>(j.planes)[p * n4 + i] =
+        make_uint2(t[p][0] | (uint32_t)t[p][1] << 16, t[p][2] | (uint32_t)t[p][3] << 16);
 }
 
 // ---------------------------------------------------------------------------
 // out = base + c_a t W_a^T with t = T, W = B ([cols, r] per slot), or, WT,
-// t = U, W = A ([r, cols] per slot) and the dropout of the product.  One
-// workgroup takes a tile of the plan (up to 64 tokens of one slot) and 256
+// t = U, W = A ([r, cols] per slot) and the dropout of the product (the
+// backward's dX beyond the ranks that its fused kernel takes).  One workgroup
+// takes a tile of the plan (up to 64 tokens of one slot) and blocks of 256
 // columns, a wave 64 columns of all its tokens.
 //
 //  * v_mfma_f32_16x16x32_bf16 with W rows as the row operand and tokens as
@@ -232,21 +284,21 @@ k_batch_split(const float* __restrict__ x, int64_t n, uint16_t* __restrict__ pla
 //    pieces (64 bytes) of 16 tokens per instruction.
 //  * A lane reads and writes the same places of base and out, which may
 //    therefore be one tensor.
+//  * base and (up to rank 64) W of a block are asked for together, the first
+//    block's before T is gathered.
 // Bound: HBM, base read and out written once; W comes from L2 once per tile.
-constexpr int kUpCols = 256;    // columns per workgroup
+// The column block is the fast grid index: an XCD keeps to its part of W.
+constexpr int kUpCols = 256;    // columns per block
 constexpr int kUpWaveCols = 64;
-constexpr int kUpRanks = 128;   // ranks whose terms are in LDS at a time
-// LDS row of a token (elements): 16 hi and 16 mid terms per 16 ranks, padded.
-__host__ __device__ constexpr int up_lds_row(int r) {
-  return ((r < kUpRanks ? r : kUpRanks) + 15) / 16 * 32 + 8;
-}
 
 struct UpArgs {
   const uint16_t* base;  // [M, cols] bf16 or null (zeros)
   uint16_t* out;         // [M, cols] bf16
   int M;
   int64_t cols;
-  const float* t;        // fp32 [M, r]
+  const float* part;     // t: fp32 [slices][M, r], to be added
+  int slices;
+  float* t_out;          // t itself, fp32 [M, r], or null
   const uint16_t* W;
   const float* scale;    // [slots]
   int r, slots;
@@ -256,160 +308,220 @@ struct UpArgs {
   float keep_scale;
 };
 
-template <bool WT, bool DROP>
+// RTL: 16-rank chunks held in LDS (at least ceil(r / 16)).
+template <bool WT, bool DROP, int RTL>
 __global__ void __launch_bounds__(256) k_batch_up(UpArgs g) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  constexpr int LD = RTL * 32 + 8;   // LDS row of a token: 16 hi and 16 mid terms per chunk
+  constexpr bool AHEAD = RTL <= 4;   // W of a block in registers ahead of its use
+  constexpr int WR = AHEAD ? RTL : 1;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[kPlanTile * LD];
   __shared__ __attribute__((aligned(16))) uint16_t slab[WT ? 4 : 1][WT ? 16 * 80 : 8];
   __shared__ int rows[kPlanTile];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, q4 = lane >> 4;
-  const TileRow t = tile_row(g.tiles, blockIdx.x, g.M, g.slots);
+  const TileRow t = tile_row(g.tiles, blockIdx.y, g.M, g.slots);
   if (t.count <= 0) return;
   const int64_t cols = g.cols;
-  const int64_t n0 = (int64_t)blockIdx.y * kUpCols;
+  const int blocks = (int)((cols + kUpCols - 1) / kUpCols);
+  const int r = g.r;
   if (tid < kPlanTile) {
     const int m = tid < t.count ? g.order[t.first + tid] : -1;
     rows[tid] = (unsigned)m < (unsigned)g.M ? m : -1;
   }
   __syncthreads();
-  if (t.slot < 0) {   // no adapter: the base alone
+  if (t.slot < 0) {   // no adapter: t = 0, the base alone
+    if (g.t_out && blockIdx.x == 0)
+      for (int e = tid; e < t.count * r; e += 256)
+        if (rows[e / r] >= 0) g.t_out[(int64_t)rows[e / r] * r + e % r] = 0.0f;
     if (g.out == g.base) return;
-    for (int e = tid; e < t.count * (kUpCols / 8); e += 256) {
-      const int m = rows[e / (kUpCols / 8)];
-      const int64_t c = n0 + 8 * (e % (kUpCols / 8));
-      if (m < 0 || c >= cols) continue;
-      const int64_t o = (int64_t)m * cols + c;
-      *reinterpret_cast<uint4*>(g.out + o) =
-          g.base ? *reinterpret_cast<const uint4*>(g.base + o) : make_uint4(0, 0, 0, 0);
-    }
+    for (int cb = blockIdx.x; cb < blocks; cb += gridDim.x)
+      for (int e = tid; e < t.count * (kUpCols / 8); e += 256) {
+        const int m = rows[e / (kUpCols / 8)];
+        const int64_t c = (int64_t)cb * kUpCols + 8 * (e % (kUpCols / 8));
+        if (m < 0 || c >= cols) continue;
+        const int64_t o = (int64_t)m * cols + c;
+        *reinterpret_cast<uint4*>(g.out + o) =
+            g.base ? *reinterpret_cast<const uint4*>(g.base + o) : make_uint4(0, 0, 0, 0);
+      }
     return;
   }
-  const int r = g.r;
-  const int ld = up_lds_row(r);
+  const int ntg = (t.count + 15) / 16;
+  const int chunks = (r + 15) / 16;
   const float c_a = g.scale[t.slot];
   const uint16_t* const W = g.W + (int64_t)t.slot * cols * r;
-  const int64_t nw = n0 + kUpWaveCols * wave;
-  f32x4_t acc[4][2][2];   // [token group][unit][pair half]
+  uint16_t* const my = slab[WT ? wave : 0];
+
+  // Four 16-byte pieces of chunk ch of W (two for WT): rows n of the MFMA's
+  // row operand, or rows of A that pass through the slab.
+  auto load_w = [&](int64_t nw, int ch, uint4 (&wv)[4]) {
+    if constexpr (!WT) {
+      const int j = 16 * ch + 8 * (q4 & 1);
 #pragma unroll
-  for (int tg = 0; tg < 4; ++tg)
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int jj = 0; jj < 2; ++jj) acc[tg][u][jj] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int r0 = 0; r0 < r; r0 += kUpRanks) {
-    const int rn = min(kUpRanks, r - r0), chunks = (rn + 15) / 16;
-    if (r0) __syncthreads();   // the last block's reads
-    for (int e = tid; e < kPlanTile * chunks * 16; e += 256) {
-      const int tok = e / (chunks * 16), j = e % (chunks * 16);
-      const int m = rows[tok];
-      uint16_t hi, mid, lo;
-      split3(m >= 0 && j < rn ? c_a * g.t[(int64_t)m * r + r0 + j] : 0.0f, hi, mid, lo);
-      uint16_t* const d = lds + tok * ld + (j >> 4) * 32 + (j & 15);
-      d[0] = hi;
-      d[16] = mid;
-    }
-    __syncthreads();
-    for (int ch = 0; ch < chunks; ++ch) {
-      bf16x8_t wop[2][2];
-      if constexpr (!WT) {
-        const int j = r0 + 16 * ch + 8 * (q4 & 1);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int64_t c = nw + 32 * u + 8 * (i >> 2) + 4 * jj + (i & 3);
-            const bool ok = c < cols && j < r;
-            wop[u][jj] = __builtin_bit_cast(
-                bf16x8_t,
-                keep_or_zero(ok, *reinterpret_cast<const uint4*>(W + (ok ? c * r + j : 0))));
-          }
-      } else {
-        // 16 ranks x 64 columns of A through LDS (rows of 80), read back
-        // transposed: lane i of a 16-lane group gets column 8 (i / 4) + 4 jj +
-        // i % 4 of ranks 8 (q4 & 1) .. +7.
-        uint16_t* const my = slab[wave];
-        const int jr = r0 + 16 * ch + (lane >> 2);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t c = nw + 16 * (lane & 3) + 8 * h;
-          const bool ok = c < cols && jr < r;
-          *reinterpret_cast<uint4*>(my + (lane >> 2) * 80 + 16 * (lane & 3) + 8 * h) = keep_or_zero(
-              ok, *reinterpret_cast<const uint4*>(W + (ok ? (int64_t)jr * cols + c : 0)));
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): one wave's LDS operations are in order
-        const int rr = 8 * (q4 & 1) + (i >> 2);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int cc = 32 * u + 8 * (i & 3) + 4 * jj;
-            const v4s_t lo = lds_read_tr16(my + rr * 80 + cc);
-            const v4s_t hi = lds_read_tr16(my + (rr + 4) * 80 + cc);
-            const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            wop[u][jj] = __builtin_bit_cast(bf16x8_t, v);
-          }
+      for (int k = 0; k < 4; ++k) {
+        const int64_t c = nw + 32 * (k >> 1) + 8 * (i >> 2) + 4 * (k & 1) + (i & 3);
+        const bool ok = c < cols && j < r;
+        wv[k] = keep_or_zero(ok, *reinterpret_cast<const uint4*>(W + (ok ? c * r + j : 0)));
       }
+    } else {
+      const int j = 16 * ch + (lane >> 2);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t c = nw + 16 * (lane & 3) + 8 * k;
+        const bool ok = c < cols && j < r;
+        wv[k] = keep_or_zero(ok, *reinterpret_cast<const uint4*>(W + (ok ? j * cols + c : 0)));
+      }
+    }
+  };
+  auto w_operand = [&](const uint4 (&wv)[4], bf16x8_t (&wop)[4]) {
+    if constexpr (!WT) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) wop[k] = __builtin_bit_cast(bf16x8_t, wv[k]);
+    } else {
+      // 16 ranks x 64 columns of A through LDS (rows of 80), read back
+      // transposed: lane i of a 16-lane group gets column 8 (i / 4) + 4 jj +
+      // i % 4 of ranks 8 (q4 & 1) .. +7.
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint4*>(my + (lane >> 2) * 80 + 16 * (lane & 3) + 8 * k) = wv[k];
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): one wave's LDS operations are in order
+      const int rr = 8 * (q4 & 1) + (i >> 2);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int cc = 32 * (k >> 1) + 8 * (i & 3) + 4 * (k & 1);
+        const v4s_t lo = lds_read_tr16(my + rr * 80 + cc);
+        const v4s_t hi = lds_read_tr16(my + (rr + 4) * 80 + cc);
+        const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        wop[k] = __builtin_bit_cast(bf16x8_t, v);
+      }
+    }
+  };
+
+  for (int cb = blockIdx.x; cb < blocks; cb += gridDim.x) {
+    const int64_t nw = (int64_t)cb * kUpCols + kUpWaveCols * wave;
+    uint4 bv[4][2], wv[WR][4];
+#pragma unroll
+    for (int tg = 0; tg < 4; ++tg) {
+      if (tg >= ntg) break;
+      const int m = rows[16 * tg + i];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t c = nw + 32 * u + 8 * q4;
+        const bool ok = m >= 0 && c < cols;
+        bv[tg][u] = make_uint4(0, 0, 0, 0);
+        if (g.base && ok) bv[tg][u] = *reinterpret_cast<const uint4*>(g.base + (int64_t)m * cols + c);
+      }
+    }
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int ch = 0; ch < RTL; ++ch) load_w(nw, ch, wv[ch]);
+    }
+    if (cb == (int)blockIdx.x) {   // t of the tile, once
+      for (int e = tid; e < kPlanTile * RTL * 4; e += 256) {
+        const int tok = e / (RTL * 4), j = 4 * (e % (RTL * 4));
+        const int m = rows[tok];
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (m >= 0 && j < r) {
+          const int64_t at = (int64_t)m * r + j, plane = (int64_t)g.M * r;
+          for (int z = 0; z < g.slices; ++z) {
+            const float4 p = *reinterpret_cast<const float4*>(g.part + z * plane + at);
+            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+          }
+          if (g.t_out && blockIdx.x == 0) *reinterpret_cast<float4*>(g.t_out + at) = v;
+        }
+        const float f[4] = {c_a * v.x, c_a * v.y, c_a * v.z, c_a * v.w};
+        uint16_t hi[4], mid[4], lo;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split3(m >= 0 && j < r ? f[k] : 0.0f, hi[k], mid[k], lo);
+        uint16_t* const d = lds + tok * LD + (j >> 4) * 32 + (j & 15);
+        *reinterpret_cast<uint2*>(d) =
+            make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+        *reinterpret_cast<uint2*>(d + 16) =
+            make_uint2(mid[0] | (uint32_t)mid[1] << 16, mid[2] | (uint32_t)mid[3] << 16);
+      }
+      __syncthreads();
+    }
+
+    f32x4_t acc[4][4];   // [token group][unit, pair half]
+#pragma unroll
+    for (int tg = 0; tg < 4; ++tg)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[tg][k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    auto chunk = [&](int ch, const uint4 (&w)[4]) {
+      bf16x8_t wop[4];
+      w_operand(w, wop);
 #pragma unroll
       for (int tg = 0; tg < 4; ++tg) {
-        if (16 * tg >= t.count) continue;
+        if (tg >= ntg) break;
         const bf16x8_t top =
-            *reinterpret_cast<const bf16x8_t*>(lds + (16 * tg + i) * ld + 32 * ch + 8 * q4);
+            *reinterpret_cast<const bf16x8_t*>(lds + (16 * tg + i) * LD + 32 * ch + 8 * q4);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < 4; ++k) acc[tg][k] = mfma_16x16x32(wop[k], top, acc[tg][k]);
+      }
+    };
+    if constexpr (AHEAD) {
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj)
-            acc[tg][u][jj] = mfma_16x16x32(wop[u][jj], top, acc[tg][u][jj]);
+      for (int ch = 0; ch < RTL; ++ch) chunk(ch, wv[ch]);
+    } else {
+      for (int ch = 0; ch < chunks; ++ch) {
+        load_w(nw, ch, wv[0]);
+        chunk(ch, wv[0]);
       }
     }
-  }
-  // acc[tg][u][jj][v]: token 16 tg + i, column nw + 32 u + 8 q4 + 4 jj + v.
+    // acc[tg][2 u + jj][v]: token 16 tg + i, column nw + 32 u + 8 q4 + 4 jj + v.
 #pragma unroll
-  for (int tg = 0; tg < 4; ++tg) {
-    if (16 * tg >= t.count) continue;
-    const int m = rows[16 * tg + i];
+    for (int tg = 0; tg < 4; ++tg) {
+      if (tg >= ntg) break;
+      const int m = rows[16 * tg + i];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t c = nw + 32 * u + 8 * q4;
-      if (m < 0 || c >= cols) continue;
-      const int64_t o = (int64_t)m * cols + c;
-      uint4 b = make_uint4(0, 0, 0, 0);
-      if (g.base) b = *reinterpret_cast<const uint4*>(g.base + o);
-      const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-      float v[8];
+      for (int u = 0; u < 2; ++u) {
+        const int64_t c = nw + 32 * u + 8 * q4;
+        if (m < 0 || c >= cols) continue;
+        const int64_t o = (int64_t)m * cols + c;
+        const uint32_t bw[4] = {bv[tg][u].x, bv[tg][u].y, bv[tg][u].z, bv[tg][u].w};
+        float v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = acc[tg][u][0][e];
-        v[4 + e] = acc[tg][u][1][e];
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[tg][2 * u][e];
+          v[4 + e] = acc[tg][2 * u + 1][e];
+        }
+        if constexpr (DROP) {
+          const uint32_t keep = philox_keep8((uint64_t)o, g.drop);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = (keep >> e) & 1u ? v[e] * g.keep_scale : 0.0f;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_bf16x2(bf16_to_f32(bw[e] & 0xffffu) + v[2 * e],
+                             bf16_to_f32(bw[e] >> 16) + v[2 * e + 1]);
+        *reinterpret_cast<uint4*>(g.out + o) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if constexpr (DROP) {
-        const uint32_t keep = philox_keep8((uint64_t)o, g.drop);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (keep >> e) & 1u ? v[e] * g.keep_scale : 0.0f;
-      }
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = pack_bf16x2(bf16_to_f32(bw[e] & 0xffffu) + v[2 * e],
-                           bf16_to_f32(bw[e] >> 16) + v[2 * e + 1]);
-      *reinterpret_cast<uint4*>(g.out + o) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// dA_a = c_a U^T drop(X) and dB_a = c_a dY^T T over the tokens of each slot,
-// fp32, every slot written (zeros without tokens).  Both contract over tokens:
-// O[c][j] = sum P[m][c] Q[m][j], (P, Q) = (X, U) with O = dA^T or (dY, T) with
-// O = dB.  A workgroup owns a slot, a slice of 16 H columns of P and up to 64
-// ranks, and contracts over all of the slot's tokens, gathered through the
-// plan's order: no partial sums in memory, no atomics.  Its four waves take
-// every fourth 32-token chunk; the chunk's pieces of P and of the three bf16
-// planes of Q pass through a slab of LDS per wave and come back as MFMA
-// operands with the transposing read, tokens along the contraction.  The
-// waves' sums are added in the order 0, 1, 2, 3.
-// Bound: HBM, X and dY read once and all slots' dA and dB written.
+// The backward's sums over tokens, dA_a = c_a U^T drop(X) and dB_a = c_a dY^T T
+// in fp32 (every slot written, zeros without tokens), and, on the way over X's
+// columns, dX = dX0 + drop(c_a U A_a).  Both gradients are O[c][j] = sum P[m][c]
+// Q[m][j], (P, Q) = (X, U) with O = dA^T or (dY, T) with O = dB.
+//
+// A workgroup owns a slot, 64 columns of P and up to 64 ranks, and contracts
+// over all of the slot's tokens, gathered through the plan's order: no partial
+// sums in memory, no atomics.  Its eight waves take every eighth 32-token
+// chunk.  Lane (i, q4) loads the 8 columns 32 u + 8 q4 of tokens 16 tg + i, the
+// places of dX that it will write, so that the dropout's words are drawn once
+// for both.  P and the three bf16 planes of Q pass through a slab of LDS per
+// wave and come back as MFMA operands with the transposing read, tokens along
+// the contraction; U's rows of the same slab are the column operand of dX,
+// whose row operand, the slot's A over these columns, stays in LDS.  The
+// waves' sums are added in the order 0, 1, ..., 7.
+// Bound: HBM, X, dY and dX0 read once, dX and all slots' dA and dB written;
+// Q is read by every column slice, from L2.
 constexpr int kGradRanks = 64;
+constexpr int kGradSlice = 64;
+constexpr int kGradWaves = 8;
 
 struct BatchGradJob {
   const uint16_t* P;   // [M, cols] bf16
@@ -417,182 +529,282 @@ struct BatchGradJob {
   const uint16_t* Q;   // [3][M, r] bf16 planes
   float* out;          // trans: [slots, r, cols] (dA); else [slots, cols, r] (dB)
   int trans, slices;
-  int drop;
+};
+struct BatchGradArgs {
+  BatchGradJob a, b;   // dA (with dX), dB
+  int M, r, slots;
+  const float* scale;
+  const int* order;
+  const int* start;
+  const uint16_t* A;   // [slots, r, K], for dX
+  const uint16_t* dX0;
+  uint16_t* dX;
+  DropKey drop;
+  float keep_scale;
 };
 
-template <int RT, int H, int KB, bool DROP>
-__global__ void __launch_bounds__(256)
-k_batch_grads(BatchGradJob ja, BatchGradJob jb, int M, int r, int slots, const float* scale,
-              const int* order, const int* start, DropKey drop, float keep_scale) {
-  constexpr int C = 16 * H;                        // columns of P per workgroup
-  constexpr int PPR = C / 8;                       // 16-byte pieces per row of P
+template <int RT, bool DROP, bool DX>
+__global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g) {
   constexpr int QW = 16 * RT;
-  constexpr int CE = 32 * C + 3 * 32 * QW;         // elements of a chunk in the slab
-  constexpr int SLAB = 4 * KB * CE * 2, RED = 3 * H * RT * 64 * 16;
+  constexpr int PE = 32 * kGradSlice, CE = PE + 3 * 32 * QW;   // elements of a chunk
+  constexpr int AW = 16 * RT + 8;                              // LDS row of a column of A
+  constexpr int SLAB = kGradWaves * CE * 2, RED = kGradWaves * 4 * RT * 64 * 16;
   __shared__ __attribute__((aligned(16))) char smem[SLAB > RED ? SLAB : RED];
+  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? kGradSlice * AW : 8];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i = lane & 15, g = lane >> 4;
-  const bool first = (int)blockIdx.x < ja.slices;
-  const BatchGradJob& jb_ = first ? ja : jb;
-  const uint16_t* const P = jb_.P;
-  const uint16_t* const Q = jb_.Q;
-  const int64_t cols = jb_.cols;
-  const int trans = jb_.trans;
-  const bool dropped = DROP && jb_.drop;
-  const int sl = first ? (int)blockIdx.x : (int)blockIdx.x - ja.slices;
-  const int64_t c0 = (int64_t)sl * C;
-  const int slot = blockIdx.y;
+  const int i = lane & 15, q4 = lane >> 4;
+  const bool first = (int)blockIdx.x < g.a.slices;
+  const BatchGradJob& job = first ? g.a : g.b;
+  const int64_t cols = job.cols;
+  const int64_t c0 = (int64_t)(first ? (int)blockIdx.x : (int)blockIdx.x - g.a.slices) * kGradSlice;
+  const int M = g.M, r = g.r, slot = blockIdx.y;
   const int j0 = (int)blockIdx.z * kGradRanks;
   // The slot's range of the order, cut to M tokens whatever the plan holds.
-  const int s0 = min(max(start[slot], 0), M), s1 = min(max(start[slot + 1], s0), M);
+  const int s0 = min(max(g.start[slot], 0), M), s1 = min(max(g.start[slot + 1], s0), M);
   const int nt = s1 - s0;
-
-  const __amdgpu_buffer_rsrc_t rp = rsrc_whole(P, (uint32_t)((int64_t)M * cols * 2));
-  const __amdgpu_buffer_rsrc_t rq = rsrc_whole(Q, (uint32_t)((int64_t)M * r * 6));
-  const int prow = lane / PPR, pcol = 8 * (lane % PPR);
-  const bool pcol_ok = c0 + pcol < cols;
-  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * KB * CE;
-  const int nchunks = (nt + 31) / 32;
-  const int per_wave = (nchunks + 3) / 4;
-  const int nb = (per_wave + KB - 1) / KB;   // batches, the same for every wave
-
-  f32x4_t acc[H][RT];
+  if (DX && slot == g.slots) {   // tokens without an adapter: dX = dX0
+    if (!first || g.dX == g.dX0) return;
+    for (int e = tid; e < nt * (kGradSlice / 8); e += 64 * kGradWaves) {
+      const int m = g.order[s0 + e / (kGradSlice / 8)];
+      const int64_t c = c0 + 8 * (e % (kGradSlice / 8));
+      if ((unsigned)m >= (unsigned)M || c >= cols) continue;
+      const int64_t o = (int64_t)m * cols + c;
+      *reinterpret_cast<uint4*>(g.dX + o) =
+          g.dX0 ? *reinterpret_cast<const uint4*>(g.dX0 + o) : make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const bool dx = DX && first, dropped = DROP && first;
+  const __amdgpu_buffer_rsrc_t rp = rsrc_whole(job.P, (uint32_t)((int64_t)M * cols * 2));
+  const __amdgpu_buffer_rsrc_t rq = rsrc_whole(job.Q, (uint32_t)((int64_t)M * r * 6));
+  const float c_a = g.scale[slot];
+  if (dx && nt > 0) {   // as[column][rank] = A, transposed
+    const uint16_t* const A = g.A + (int64_t)slot * r * cols;
+    for (int e = tid; e < QW * (kGradSlice / 8); e += 64 * kGradWaves) {
+      const int j = e / (kGradSlice / 8), c = 8 * (e % (kGradSlice / 8));
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (j < r && c0 + c < cols) v = *reinterpret_cast<const uint4*>(A + j * cols + c0 + c);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int h = 0; h < H; ++h)
+      for (int k = 0; k < 8; ++k) as[(c + k) * AW + j] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+  __syncthreads();
+
+  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * CE;
+  f32x4_t acc[4][RT];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto consume = [&](const uint4 (&pv)[KB][H], const uint4 (&qv)[KB][3][RT]) {
+  const int nchunks = (nt + 31) / 32;
+  for (int ci = wave; ci < nchunks; ci += kGradWaves) {
+    const int pos = ci * 32 + (lane & 31);
+    int tok = pos < nt ? g.order[s0 + pos] : -1;
+    if ((unsigned)tok >= (unsigned)M) tok = -1;
+    int mt[2];
+    uint4 pv[2][2], qv[3][RT], xv[2][2];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      uint16_t* const c = my + b * CE;
+    for (int tg = 0; tg < 2; ++tg) {
+      mt[tg] = __shfl(tok, 16 * tg + i);
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-        *reinterpret_cast<uint4*>(c + (h * (64 / PPR) + prow) * C + pcol) = pv[b][h];
-#pragma unroll
-      for (int z = 0; z < 3; ++z)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const int p = 64 * t + lane;
-          *reinterpret_cast<uint4*>(c + 32 * C + z * 32 * QW + (p / (2 * RT)) * QW +
-                                    8 * (p % (2 * RT))) = qv[b][z][t];
-        }
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): one wave's LDS operations are in order
-    const int rr = 8 * g + (i >> 2), cc = 4 * (i & 3);
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const uint16_t* const c = my + b * CE;
-      bf16x8_t aop[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const v4s_t lo = lds_read_tr16(c + rr * C + 16 * h + cc);
-        const v4s_t hi = lds_read_tr16(c + (rr + 4) * C + 16 * h + cc);
-        const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        aop[h] = __builtin_bit_cast(bf16x8_t, v);
-      }
-#pragma unroll
-      for (int z = 2; z >= 0; --z)          // the small terms first
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const uint16_t* const qs = c + 32 * C + z * 32 * QW + 16 * t + cc;
-          const v4s_t lo = lds_read_tr16(qs + rr * QW);
-          const v4s_t hi = lds_read_tr16(qs + (rr + 4) * QW);
-          const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          const bf16x8_t bop = __builtin_bit_cast(bf16x8_t, v);
-#pragma unroll
-          for (int h = 0; h < H; ++h) acc[h][t] = mfma_16x16x32(aop[h], bop, acc[h][t]);
-        }
-    }
-  };
-
-  for (int b = 0; b < nb; ++b) {
-    uint4 pv[KB][H], qv[KB][3][RT];
-#pragma unroll
-    for (int q = 0; q < KB; ++q) {
-      const int t0 = ((b * KB + q) * 4 + wave) * 32;   // first position of the chunk
-      const int pos = t0 + (lane & 31);
-      int tok = pos < nt ? order[s0 + pos] : -1;
-      if ((unsigned)tok >= (unsigned)M) tok = -1;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const int m = __shfl(tok, h * (64 / PPR) + prow);
-        const bool ok = m >= 0 && pcol_ok;
-        pv[q][h] = bload128s(rp, ok ? (uint32_t)(((int64_t)m * cols + c0 + pcol) * 2) : kOOB, 0);
-      }
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int p = 64 * t + lane;            // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
-        const int m = __shfl(tok, p / (2 * RT));
-        const int j = j0 + 8 * (p % (2 * RT));
-        const bool ok = m >= 0 && j < r;
-#pragma unroll
-        for (int z = 0; z < 3; ++z)
-          qv[q][z][t] = bload128s(
-              rq, ok ? (uint32_t)((((int64_t)z * M + m) * r + j) * 2) : kOOB, 0);
-      }
-      if (DROP && dropped) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const int m = __shfl(tok, h * (64 / PPR) + prow);
-          pv[q][h] = philox_drop8(
-              pv[q][h], (uint64_t)((int64_t)max(m, 0) * cols + c0 + pcol), drop);
-        }
+      for (int u = 0; u < 2; ++u) {
+        const int64_t c = c0 + 32 * u + 8 * q4;
+        const bool ok = mt[tg] >= 0 && c < cols;
+        pv[tg][u] = bload128s(rp, ok ? (uint32_t)(((int64_t)mt[tg] * cols + c) * 2) : kOOB, 0);
       }
     }
-    consume(pv, qv);
-  }
-
-  // acc[h][t][v] = O[c0 + 16 h + 4 g + v][j0 + 16 t + i]
-  __syncthreads();   // the slabs are free
-  f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem);
-  if (wave > 0) {
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int t = 0; t < RT; ++t) red[((wave - 1) * H * RT + h * RT + t) * 64 + lane] = acc[h][t];
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  const float s = dropped ? scale[slot] * keep_scale : scale[slot];
-  float* const out = jb_.out + (int64_t)slot * cols * r;
-#pragma unroll
-  for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      f32x4_t v = acc[h][t];
+      const int p = 64 * t + lane;              // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
+      const int m = __shfl(tok, p / (2 * RT));
+      const int j = j0 + 8 * (p % (2 * RT));
+      const bool ok = m >= 0 && j < r;
 #pragma unroll
-      for (int w = 0; w < 3; ++w) {
-        const f32x4_t o = red[(w * H * RT + h * RT + t) * 64 + lane];
-        v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
-      }
-      const int64_t c = c0 + 16 * h + 4 * g;     // c .. c + 3 (cols is a multiple of 8)
-      const int j = j0 + 16 * t + i;
-      if (c >= cols || j >= r) continue;
-      // A slot without tokens has no products: plain zeros, whatever its scale.
-      const f32x4_t res = nt > 0 ? f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]}
-                                 : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if (trans) {
-        *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + c) = res;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[(c + e) * r + j] = res[e];
-      }
+      for (int z = 0; z < 3; ++z)
+        qv[z][t] = bload128s(rq, ok ? (uint32_t)((((int64_t)z * M + m) * r + j) * 2) : kOOB, 0);
     }
+    if (dx) {
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int64_t c = c0 + 32 * u + 8 * q4;
+          xv[tg][u] = make_uint4(0, 0, 0, 0);
+          if (g.dX0 && mt[tg] >= 0 && c < cols)
+            xv[tg][u] = *reinterpret_cast<const uint4*>(g.dX0 + (int64_t)mt[tg] * cols + c);
+        }
+    }
+    uint32_t keep = 0;   // 8 bits per (tg, u)
+    if (dropped) {
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          keep |= philox_keep8((uint64_t)((int64_t)max(mt[tg], 0) * cols + c0 + 32 * u + 8 * q4),
+                               g.drop) << (8 * (2 * tg + u));
+    }
+#pragma unroll
+    for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 v = pv[tg][u];
+        if (dropped) {
+          const uint32_t k8 = keep >> (8 * (2 * tg + u));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] &= ((k8 >> (2 * e)) & 1u ? 0xffffu : 0u) | ((k8 >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(my + (16 * tg + i) * kGradSlice + 32 * u + 8 * q4) = v;
+      }
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        *reinterpret_cast<uint4*>(my + PE + z * 32 * QW + 8 * (64 * t + lane)) = qv[z][t];
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): one wave's LDS operations are in order
+    const int rr = 8 * q4 + (i >> 2), cc = 4 * (i & 3);
+    bf16x8_t aop[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const v4s_t lo = lds_read_tr16(my + rr * kGradSlice + 16 * h + cc);
+      const v4s_t hi = lds_read_tr16(my + (rr + 4) * kGradSlice + 16 * h + cc);
+      const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      aop[h] = __builtin_bit_cast(bf16x8_t, v);
+    }
+#pragma unroll
+    for (int z = 2; z >= 0; --z)          // the small terms first
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const uint16_t* const qs = my + PE + z * 32 * QW + 16 * t + cc;
+        const v4s_t lo = lds_read_tr16(qs + rr * QW);
+        const v4s_t hi = lds_read_tr16(qs + (rr + 4) * QW);
+        const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        const bf16x8_t bop = __builtin_bit_cast(bf16x8_t, v);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) acc[h][t] = mfma_16x16x32(aop[h], bop, acc[h][t]);
+      }
+    if (dx) {
+      // dX[m][c]: row operand A's column 32 u + 8 (i / 4) + 4 jj + i % 4, ranks
+      // 16 ch + 8 (q4 & 1) ..; column operand U's token 16 tg + i, the hi terms
+      // (q4 < 2) and the mid terms of the same ranks.
+      f32x4_t d[2][4];
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[tg][k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ch = 0; ch < RT; ++ch) {
+        bf16x8_t uop[2];
+#pragma unroll
+        for (int tg = 0; tg < 2; ++tg)
+          uop[tg] = *reinterpret_cast<const bf16x8_t*>(
+              my + PE + (q4 >> 1) * 32 * QW + (16 * tg + i) * QW + 16 * ch + 8 * (q4 & 1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 32 * (k >> 1) + 8 * (i >> 2) + 4 * (k & 1) + (i & 3);
+          const bf16x8_t wop =
+              *reinterpret_cast<const bf16x8_t*>(as + c * AW + 16 * ch + 8 * (q4 & 1));
+#pragma unroll
+          for (int tg = 0; tg < 2; ++tg) d[tg][k] = mfma_16x16x32(wop, uop[tg], d[tg][k]);
+        }
+      }
+      const float s = DROP ? c_a * g.keep_scale : c_a;
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int64_t c = c0 + 32 * u + 8 * q4;
+          if (mt[tg] < 0 || c >= cols) continue;
+          const uint32_t bw[4] = {xv[tg][u].x, xv[tg][u].y, xv[tg][u].z, xv[tg][u].w};
+          const uint32_t k8 = keep >> (8 * (2 * tg + u));
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = s * d[tg][2 * u + (e >> 2)][e & 3];
+            if (DROP) v[e] = (k8 >> e) & 1u ? v[e] : 0.0f;
+          }
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(bf16_to_f32(bw[e] & 0xffffu) + v[2 * e],
+                               bf16_to_f32(bw[e] >> 16) + v[2 * e + 1]);
+          *reinterpret_cast<uint4*>(g.dX + (int64_t)mt[tg] * cols + c) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+  }
+
+  // acc[h][t][v] = O[c0 + 16 h + 4 q4 + v][j0 + 16 t + i]; the unit (h, t) is
+  // added by wave (h RT + t) mod 8.
+  __syncthreads();   // the slabs are free
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem);
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) red[(wave * 4 * RT + h * RT + t) * 64 + lane] = acc[h][t];
+  __syncthreads();
+  const float s = dropped ? c_a * g.keep_scale : c_a;
+  float* const out = job.out + (int64_t)slot * cols * r;
+  for (int unit = wave; unit < 4 * RT; unit += kGradWaves) {
+    f32x4_t v = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kGradWaves; ++w) {
+      const f32x4_t o = red[(w * 4 * RT + unit) * 64 + lane];
+      v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
+    }
+    const int64_t c = c0 + 16 * (unit / RT) + 4 * q4;   // c .. c + 3 (cols is a multiple of 8)
+    const int j = j0 + 16 * (unit % RT) + i;
+    if (c >= cols || j >= r) continue;
+    // A slot without tokens has no products: plain zeros, whatever its scale.
+    const f32x4_t res = nt > 0 ? f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]}
+                               : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (job.trans) {
+      *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + c) = res;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[(c + e) * r + j] = res[e];
+    }
+  }
 }
 
 // ------------------------------- launchers ---------------------------------
 
 static inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-BatchWorkspace batch_workspace(int64_t M, int r, bool backward) {
+// Tiles that a batch may be expected to have: its tokens' own, and more where
+// slots are many beside them (the host does not know the slots in use).
+static int64_t expected_tiles(int64_t M, int S) {
+  const int64_t more = M / 8 < S ? M / 8 : S;
+  return (M + kPlanTile - 1) / kPlanTile + more;
+}
+
+// Steps per slice of the down projections' contraction: slices that give about
+// two workgroups per CU.
+static int down_zlen(int64_t M, int S, int64_t C) {
+  const int64_t steps = (C + 63) / 64;
+  int64_t want = 2 * kCUs / expected_tiles(M, S);
+  if (want < 1) want = 1;
+  const int64_t per = (steps + want * kDownWaves - 1) / (want * kDownWaves);   // steps per wave
+  return (int)(per * kDownWaves);
+}
+static int down_slices(int64_t M, int S, int64_t C) {
+  const int64_t steps = (C + 63) / 64;
+  const int zl = down_zlen(M, S, C);
+  return (int)((steps + zl - 1) / zl);
+}
+
+BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bool backward) {
   BatchWorkspace w{};
-  const size_t f32 = align256((size_t)M * r * 4), planes = align256((size_t)M * r * 6);
   size_t off = 0;
-  w.off_T = off; off += f32;
+  w.off_T = off; off += align256((size_t)down_slices(M, S, K) * M * r * 4);
   if (backward) {
-    w.off_U = off; off += f32;
+    const size_t planes = align256((size_t)M * r * 6);
+    w.off_U = off; off += align256((size_t)down_slices(M, S, N) * M * r * 4);
     w.off_Up = off; off += planes;
     w.off_Tp = off; off += planes;
   }
@@ -601,101 +813,132 @@ BatchWorkspace batch_workspace(int64_t M, int r, bool backward) {
 }
 
 template <bool WT, bool DROP>
-static hipError_t down(DownArgs g, int ntiles, hipStream_t st) {
-  // 8 tokens per workgroup while 16 would leave CUs without one.
-  g.rows = (g.M + kDownRows - 1) / kDownRows < kCUs ? 8 : kDownRows;
-  const dim3 grid((unsigned)(ntiles * (kPlanTile / g.rows)));
-  const int rt = (g.r + 15) / 16;
-  if (rt <= 1) hipLaunchKernelGGL((k_batch_down<WT, DROP, 1, 16, 4>), grid, dim3(1024), 0, st, g);
-  else if (rt <= 2) hipLaunchKernelGGL((k_batch_down<WT, DROP, 2, 16, 2>), grid, dim3(1024), 0, st, g);
-  else if (rt <= 4) hipLaunchKernelGGL((k_batch_down<WT, DROP, 4, 8, 1>), grid, dim3(512), 0, st, g);
-  else if (rt <= 8) hipLaunchKernelGGL((k_batch_down<WT, DROP, 8, 4, 1>), grid, dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((k_batch_down<WT, DROP, 16, 4, 1>), grid, dim3(256), 0, st, g);
+static hipError_t down(DownArgs g, hipStream_t st) {
+  g.zlen = down_zlen(g.M, g.slots, g.C);
+  const dim3 grid((unsigned)down_slices(g.M, g.slots, g.C),
+                  (unsigned)adapter_plan_tiles(g.M, g.slots), (unsigned)((g.r + 63) / 64));
+  const dim3 block(64 * kDownWaves);
+  if (g.r <= 16) hipLaunchKernelGGL((k_batch_down<WT, DROP, 1>), grid, block, 0, st, g);
+  else if (g.r <= 32) hipLaunchKernelGGL((k_batch_down<WT, DROP, 2>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((k_batch_down<WT, DROP, 4>), grid, block, 0, st, g);
   return hipGetLastError();
 }
 
 template <bool WT, bool DROP>
-static hipError_t up(const UpArgs& g, int ntiles, hipStream_t st) {
-  const dim3 grid((unsigned)ntiles, (unsigned)((g.cols + kUpCols - 1) / kUpCols));
-  const size_t lds = (size_t)kPlanTile * up_lds_row(g.r) * 2;
-  hipLaunchKernelGGL((k_batch_up<WT, DROP>), grid, dim3(256), lds, st, g);
+static hipError_t up(const UpArgs& g, hipStream_t st) {
+  // Column blocks per workgroup: about four workgroups per CU, whole multiples
+  // of the XCDs where there are that many.
+  const int64_t blocks = (g.cols + kUpCols - 1) / kUpCols;
+  int64_t gx = 4 * kCUs / expected_tiles(g.M, g.slots);
+  if (gx >= kXCDs) gx -= gx % kXCDs;
+  if (gx < 1) gx = 1;
+  if (gx > blocks) gx = blocks;
+  const dim3 grid((unsigned)gx, (unsigned)adapter_plan_tiles(g.M, g.slots));
+  if constexpr (!WT) {
+    if (g.r <= 16) {
+      hipLaunchKernelGGL((k_batch_up<WT, DROP, 1>), grid, dim3(256), 0, st, g);
+      return hipGetLastError();
+    }
+    if (g.r <= 32) {
+      hipLaunchKernelGGL((k_batch_up<WT, DROP, 2>), grid, dim3(256), 0, st, g);
+      return hipGetLastError();
+    }
+    if (g.r <= 64) {
+      hipLaunchKernelGGL((k_batch_up<WT, DROP, 4>), grid, dim3(256), 0, st, g);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_batch_up<WT, DROP, 16>), grid, dim3(256), 0, st, g);
   return hipGetLastError();
 }
 
 #define QLK_TRY(x) do { hipError_t e_ = (x); if (e_ != hipSuccess) return e_; } while (0)
 
+// The slices of T = drop(X) A^T.
 static hipError_t batch_T(const uint16_t* X, const BatchAdapters& a, int64_t M, int64_t K,
-                          const BatchDropout& d, float* T, hipStream_t st) {
+                          const BatchDropout& d, float* part, hipStream_t st) {
   DownArgs g{};
   g.S = X; g.M = (int)M; g.C = K; g.W = a.A; g.r = a.r; g.slots = a.slots;
-  g.order = a.order; g.tiles = a.tiles; g.out = T; g.planes = nullptr;
+  g.order = a.order; g.tiles = a.tiles; g.part = part;
   g.drop = DropKey{d.threshold, d.k0, d.k1}; g.keep_scale = d.scale;
-  const int nt = (int)adapter_plan_tiles(M, a.slots);
-  return d.on ? down<false, true>(g, nt, st) : down<false, false>(g, nt, st);
+  return d.on ? down<false, true>(g, st) : down<false, false>(g, st);
 }
 
 hipError_t launch_batch_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N,
                             const BatchAdapters& a, const uint16_t* Y, const BatchDropout& d,
                             uint16_t* out, float* T_out, void* ws, hipStream_t st) {
-  const BatchWorkspace w = batch_workspace(M, a.r, false);
-  float* const T = T_out ? T_out : reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + w.off_T);
-  QLK_TRY(batch_T(X, a, M, K, d, T, st));
+  const BatchWorkspace w = batch_workspace(M, K, N, a.r, a.slots, false);
+  float* const part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + w.off_T);
+  QLK_TRY(batch_T(X, a, M, K, d, part, st));
   UpArgs u{};
-  u.base = Y; u.out = out; u.M = (int)M; u.cols = N; u.t = T; u.W = a.B; u.scale = a.scale;
+  u.base = Y; u.out = out; u.M = (int)M; u.cols = N; u.part = part;
+  u.slices = down_slices(M, a.slots, K); u.t_out = T_out; u.W = a.B; u.scale = a.scale;
   u.r = a.r; u.slots = a.slots; u.order = a.order; u.tiles = a.tiles;
-  return up<false, false>(u, (int)adapter_plan_tiles(M, a.slots), st);
+  return up<false, false>(u, st);
+}
+
+template <int RT, bool DROP, bool DX>
+static void grads(const BatchGradArgs& g, hipStream_t st) {
+  const dim3 grid((unsigned)(g.a.slices + g.b.slices), (unsigned)(g.slots + (DX ? 1 : 0)),
+                  (unsigned)((g.r + kGradRanks - 1) / kGradRanks));
+  hipLaunchKernelGGL((k_batch_grads<RT, DROP, DX>), grid, dim3(64 * kGradWaves), 0, st, g);
+}
+template <bool DROP, bool DX>
+static void grads_rt(const BatchGradArgs& g, hipStream_t st) {
+  if (g.r <= 16) grads<1, DROP, DX>(g, st);
+  else if (g.r <= 32) grads<2, DROP, DX>(g, st);
+  else grads<4, DROP, DX>(g, st);
 }
 
 hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t K, int64_t N,
                             const BatchAdapters& a, const float* T, const uint16_t* dX0,
                             const BatchDropout& d, uint16_t* dX, float* dA, float* dB, void* ws,
                             hipStream_t st) {
-  const BatchWorkspace w = batch_workspace(M, a.r, true);
+  const BatchWorkspace w = batch_workspace(M, K, N, a.r, a.slots, true);
   char* const base = reinterpret_cast<char*>(ws);
   float* const U = reinterpret_cast<float*>(base + w.off_U);
   uint16_t* const Up = reinterpret_cast<uint16_t*>(base + w.off_Up);
   uint16_t* const Tp = reinterpret_cast<uint16_t*>(base + w.off_Tp);
-  const int nt = (int)adapter_plan_tiles(M, a.slots);
+  SplitJob ju{U, down_slices(M, a.slots, N), Up}, jt{T, 1, Tp};
   if (!T) {
-    float* const Tw = reinterpret_cast<float*>(base + w.off_T);
-    QLK_TRY(batch_T(X, a, M, K, d, Tw, st));
-    T = Tw;
+    float* const part = reinterpret_cast<float*>(base + w.off_T);
+    QLK_TRY(batch_T(X, a, M, K, d, part, st));
+    jt.part = part;
+    jt.slices = down_slices(M, a.slots, K);
   }
   DownArgs g{};
   g.S = dY; g.M = (int)M; g.C = N; g.W = a.B; g.r = a.r; g.slots = a.slots;
-  g.order = a.order; g.tiles = a.tiles; g.out = U; g.planes = Up;
-  QLK_TRY((down<true, false>(g, nt, st)));
+  g.order = a.order; g.tiles = a.tiles; g.part = U;
+  QLK_TRY((down<true, false>(g, st)));
+  const int64_t n4 = M * a.r / 4;
+  hipLaunchKernelGGL(k_batch_split, dim3((unsigned)((n4 + 255) / 256), 2), dim3(256), 0, st, ju, jt,
+                     n4);
+  QLK_TRY(hipGetLastError());
   const DropKey key{d.threshold, d.k0, d.k1};
-  if (dX) {
+  // Beyond 64 ranks a workgroup of the gradients' kernel sees only a part of
+  // them: dX has its own launch there.
+  const bool fused = dX != nullptr && a.r <= kGradRanks;
+  if (dX && !fused) {
     UpArgs u{};
-    u.base = dX0; u.out = dX; u.M = (int)M; u.cols = K; u.t = U; u.W = a.A; u.scale = a.scale;
+    u.base = dX0; u.out = dX; u.M = (int)M; u.cols = K; u.part = U; u.slices = ju.slices;
+    u.t_out = nullptr; u.W = a.A; u.scale = a.scale;
     u.r = a.r; u.slots = a.slots; u.order = a.order; u.tiles = a.tiles;
     u.drop = key; u.keep_scale = d.scale;
-    QLK_TRY((d.on ? up<true, true>(u, nt, st) : up<true, false>(u, nt, st)));
+    QLK_TRY((d.on ? up<true, true>(u, st) : up<true, false>(u, st)));
   }
-  const int64_t n = M * a.r;
-  hipLaunchKernelGGL(k_batch_split, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, T, n, Tp);
-  QLK_TRY(hipGetLastError());
-  auto go = [&](auto rt, auto h, auto kb) {
-    constexpr int RT = decltype(rt)::value, H = decltype(h)::value, KB = decltype(kb)::value;
-    const int C = 16 * H;
-    BatchGradJob ja{X, K, Up, dA, 1, (int)((K + C - 1) / C), 1};
-    BatchGradJob jb{dY, N, Tp, dB, 0, (int)((N + C - 1) / C), 0};
-    const dim3 grid((unsigned)(ja.slices + jb.slices), (unsigned)a.slots,
-                    (unsigned)((a.r + kGradRanks - 1) / kGradRanks));
-    if (d.on)
-      hipLaunchKernelGGL((k_batch_grads<RT, H, KB, true>), grid, dim3(256), 0, st, ja, jb, (int)M,
-                         a.r, a.slots, a.scale, a.order, a.start, key, d.scale);
-    else
-      hipLaunchKernelGGL((k_batch_grads<RT, H, KB, false>), grid, dim3(256), 0, st, ja, jb, (int)M,
-                         a.r, a.slots, a.scale, a.order, a.start, key, d.scale);
-  };
-  using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I4 = std::integral_constant<int, 4>;
-  if (a.r <= 16) go(I1(), I2(), I2());
-  else if (a.r <= 32) go(I2(), I2(), I1());
-  else go(I4(), I2(), I1());
+  auto slices = [](int64_t cols) { return (int)((cols + kGradSlice - 1) / kGradSlice); };
+  BatchGradArgs ga{};
+  ga.a = BatchGradJob{X, K, Up, dA, 1, slices(K)};
+  ga.b = BatchGradJob{dY, N, Tp, dB, 0, slices(N)};
+  ga.M = (int)M; ga.r = a.r; ga.slots = a.slots; ga.scale = a.scale; ga.order = a.order;
+  ga.start = a.start; ga.A = a.A; ga.dX0 = dX0; ga.dX = dX; ga.drop = key; ga.keep_scale = d.scale;
+  if (d.on) {
+    if (fused) grads_rt<true, true>(ga, st);
+    else grads_rt<true, false>(ga, st);
+  } else {
+    if (fused) grads_rt<false, true>(ga, st);
+    else grads_rt<false, false>(ga, st);
+  }
   return hipGetLastError();
 }
 

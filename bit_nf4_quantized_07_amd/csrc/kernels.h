@@ -281,7 +281,7 @@ struct BatchDropout {
 struct BatchWorkspace {
   size_t off_T, off_U, off_Up, off_Tp, bytes;
 };
-BatchWorkspace batch_workspace(int64_t M, int r, bool backward);
+BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bool backward);
 // out = Y + c T B^T (Y null: zeros; out may be Y), T = drop(X) A^T to T_out
 // (null: kept in ws).
 hipError_t launch_batch_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N,

@@ -18,7 +18,8 @@ constexpr int64_t kMaxDim = (int64_t)1 << 30;   // keeps every tile index in int
 constexpr int64_t kMaxBufferBytes = (int64_t)1 << 31;
 
 constexpr int kMaxRank = 256;
-constexpr int64_t kMaxBatchDim = (int64_t)1 << 23;   // batched adapters: column blocks fit the grid
+constexpr int64_t kMaxBatchDim = (int64_t)1 << 23;   // batched adapters' K and N
+constexpr int64_t kMaxGridRows = 65535;
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -258,8 +259,11 @@ int check_batch_sizes(int64_t M, int64_t K, int64_t N, int r, int S) {
   if (M <= 0 || M > kMaxDim || K <= 0 || N <= 0 || K % 8 != 0 || N % 8 != 0) return QLORA_ERR_SHAPE;
   if (K > kMaxBatchDim || N > kMaxBatchDim) return QLORA_ERR_SHAPE;
   if (S < 1 || S > qlk::kMaxSlots || r < 8 || r > kMaxRank || r % 8 != 0) return QLORA_ERR_SHAPE;
-  // 32-bit offsets into X, dY and the bf16 terms of T and U
-  if (M * K * 2 >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes || M * r * 6 >= kMaxBufferBytes)
+  // 32-bit offsets into X, dY, one slot's A and B, and the bf16 terms of T and U;
+  // tiles of the plan and slots are grid rows
+  if (M * K * 2 >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes ||
+      (int64_t)r * K * 2 >= kMaxBufferBytes || (int64_t)r * N * 2 >= kMaxBufferBytes ||
+      M * r * 6 >= kMaxBufferBytes || qlk::adapter_plan_tiles(M, S) > kMaxGridRows)
     return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
@@ -469,9 +473,9 @@ int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, i
                                                 tiles, as_stream(stream)));
 }
 
-size_t lora_adapters_workspace_bytes(int64_t M, int r, int is_bwd) {
-  if (check_batch_sizes(M, 8, 8, r, 1) != QLORA_OK) return 0;
-  return qlk::batch_workspace(M, r, is_bwd != 0).bytes;
+size_t lora_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int S, int is_bwd) {
+  if (check_batch_sizes(M, K, N, r, S) != QLORA_OK) return 0;
+  return qlk::batch_workspace(M, K, N, r, S, is_bwd != 0).bytes;
 }
 
 int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint16_t* A,
@@ -485,7 +489,7 @@ int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const 
   if (!valid_p(p)) return QLORA_ERR_ARG;
   st = check_aligned({X, A, B, scale, order, start, tiles, Y, out, T_out, workspace});
   if (st) return st;
-  if (!workspace || workspace_bytes < qlk::batch_workspace(M, r, false).bytes)
+  if (!workspace || workspace_bytes < qlk::batch_workspace(M, K, N, r, S, false).bytes)
     return QLORA_ERR_WORKSPACE;
   const qlk::BatchAdapters a{A, B, scale, r, S, order, start, tiles};
   return launch_status(qlk::launch_batch_fwd(X, M, K, N, a, Y, batch_dropout(p, seed), out, T_out,
@@ -506,7 +510,7 @@ int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t 
   if (!valid_p(p)) return QLORA_ERR_ARG;
   st = check_aligned({dY, X, A, B, scale, order, start, tiles, T, dX0, dX, dA, dB, workspace});
   if (st) return st;
-  if (!workspace || workspace_bytes < qlk::batch_workspace(M, r, true).bytes)
+  if (!workspace || workspace_bytes < qlk::batch_workspace(M, K, N, r, S, true).bytes)
     return QLORA_ERR_WORKSPACE;
   const qlk::BatchAdapters a{A, B, scale, r, S, order, start, tiles};
   return launch_status(qlk::launch_batch_bwd(dY, X, M, K, N, a, T, dX0, batch_dropout(p, seed), dX,

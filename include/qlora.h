@@ -350,8 +350,8 @@ int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, i
  *   no output may overlap an input.
  *   order, start, tiles: from lora_adapter_plan with the same M and S.
  * Requires r % 8 == 0, 8 <= r <= 256; K % 8 == 0, N % 8 == 0, both at most
- * 2^23; X, Y under 2 GiB; 6 M r < 2^31; workspace of
- * lora_adapters_workspace_bytes(M, r, 0). */
+ * 2^23; X, Y and one slot's A and B under 2 GiB each; 6 M r < 2^31; at most
+ * 65535 tiles; workspace of lora_adapters_workspace_bytes(M, K, N, r, S, 0). */
 int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint16_t* A,
                       const uint16_t* B, const float* scale, int r, int S, const int32_t* order,
                       const int32_t* start, const int32_t* tiles, const uint16_t* Y, double p,
@@ -368,7 +368,7 @@ int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const 
  *   (NULL: zeros); dX may be dX0, or NULL to skip it.
  * U and T enter dA and dB as three bf16 terms (within 2^-25); the order of
  * every sum is fixed.  Sizes as in the forward; workspace of
- * lora_adapters_workspace_bytes(M, r, 1). */
+ * lora_adapters_workspace_bytes(M, K, N, r, S, 1). */
 int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t K, int64_t N,
                       const uint16_t* A, const uint16_t* B, const float* scale, int r, int S,
                       const int32_t* order, const int32_t* start, const int32_t* tiles,
@@ -377,7 +377,7 @@ int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t 
                       void* stream);
 
 /* Bytes of workspace of the two calls above; 0 for invalid sizes. */
-size_t lora_adapters_workspace_bytes(int64_t M, int r, int is_bwd);
+size_t lora_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int S, int is_bwd);
 
 /* ---- fused gate/up projections of a SiLU-gated MLP ---------------------- */
 

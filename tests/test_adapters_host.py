@@ -71,12 +71,13 @@ def test_layer_refusals(fn, names, required, optional):
     for kw in (dict(M=0), dict(M=1 << 31), dict(K=0), dict(K=60), dict(N=0), dict(N=42),
                dict(r=0), dict(r=12), dict(r=264), dict(S=0), dict(S=1025),
                dict(K=(1 << 23) + 8), dict(N=(1 << 23) + 8),
-               dict(M=1 << 20, K=1 << 10), dict(M=1 << 20, N=1 << 10), dict(M=1 << 21, K=8, N=8, r=256)):
+               dict(M=1 << 20, K=1 << 10), dict(M=1 << 20, N=1 << 10), dict(M=1 << 21, K=8, N=8, r=256),
+               dict(M=1 << 23, K=8, N=8, r=8), dict(K=1 << 22, r=256)):
         assert _call(fn, names, **kw) == q.ERR_SHAPE, kw
     for p in (-0.1, 1.0, 1.5, float("nan"), float("inf")):
         assert _call(fn, names, p=p) == q.ERR_ARG, p
     assert _call(fn, names, ws=None) == q.ERR_WORKSPACE
-    need = lib.lora_adapters_workspace_bytes(32, 16, 1 if "dY" in names else 0)
+    need = lib.lora_adapters_workspace_bytes(32, 64, 40, 16, 4, 1 if "dY" in names else 0)
     assert need > 0
     assert _call(fn, names, wsb=need - 1) == q.ERR_WORKSPACE
 
@@ -87,8 +88,8 @@ def test_dX0_without_dX_is_refused():
 
 def test_workspace_bytes_of_invalid_sizes():
     for M, r in ((0, 16), (8, 12), (8, 0), (8, 264), (1 << 31, 8)):
-        assert lib.lora_adapters_workspace_bytes(M, r, 0) == 0
-        assert lib.lora_adapters_workspace_bytes(M, r, 1) == 0
+        assert lib.lora_adapters_workspace_bytes(M, 64, 64, r, 4, 0) == 0
+        assert lib.lora_adapters_workspace_bytes(M, 64, 64, r, 4, 1) == 0
 
 
 # ---- the binding ------------------------------------------------------------

@@ -405,7 +405,7 @@ def test_captured_step_replays_the_eager_bits():
     d = c.d
     lengths, slots = dev_i32([60, 40, 20]), dev_i32([0, 2, -1])
     ws = q.Workspace("cuda")
-    ws.get(q.load_library().lora_adapters_workspace_bytes(M, r, 1))
+    ws.get(q.load_library().lora_adapters_workspace_bytes(M, K, N, r, S, 1))
     keep = {}
 
     def step():
