@@ -26,6 +26,13 @@
 namespace qlk {
 
 typedef short v8s_t __attribute__((ext_vector_type(8)));
+typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
+
+// Store through a buffer resource; a lane at kOOB stores nothing.
+__device__ __forceinline__ void bstore128s(__amdgpu_buffer_rsrc_t r, uint4 v, uint32_t voff,
+                                           uint32_t soff) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u_t, v), r, (int)voff, (int)soff, 0);
+}
 
 __device__ __forceinline__ uint4 keep_or_zero(bool ok, uint4 v) {
   return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
@@ -272,24 +279,28 @@ __global__ void __launch_bounds__(256) k_batch_split(SplitJob ju, SplitJob jt, i
 // out = base + c_a t W_a^T with t = T, W = B ([cols, r] per slot), or, WT,
 // t = U, W = A ([r, cols] per slot) and the dropout of the product (the
 // backward's dX beyond the ranks that its fused kernel takes).  One workgroup
-// takes a tile of the plan (up to 64 tokens of one slot) and blocks of 256
-// columns, a wave 64 columns of all its tokens.
+// takes a tile of the plan (up to 64 tokens of one slot) and blocks of 128
+// columns; each of its four waves takes 32 of the tokens and 64 of the columns.
 //
 //  * v_mfma_f32_16x16x32_bf16 with W rows as the row operand and tokens as
-//    columns.  Its 32 contraction indices hold 16 ranks twice: the hi terms of
-//    c_a t against W, then the mid terms against the same W.
-//  * MFMA row rho of pair jj stands for column 8 (rho / 4) + 4 jj + rho % 4 of
-//    a 32-column unit, so that a lane's two accumulators of a token are 8
-//    consecutive columns: base and out move as 16-byte pieces, a wave four
-//    pieces (64 bytes) of 16 tokens per instruction.
+//    columns.  Up to 16 ranks (RK = 16) its 32 contraction indices hold the hi
+//    terms of c_a t against W and then the mid terms against the same W; above,
+//    32 ranks, and the hi and mid terms take one MFMA each on one W operand.
+//  * Every global access is by whole 128-byte lines of consecutive lanes: a
+//    wave instruction whose neighbouring lanes lie in different lines takes
+//    the address unit four times as long, which bounded the form of this
+//    kernel that loaded operands and base in the MFMA's own layout (4096 x
+//    11008 at rank 64: 67 us).  W passes through LDS, and the fp32 products
+//    through a per-wave slab from which the lanes take 16-byte pieces of rows.
 //  * A lane reads and writes the same places of base and out, which may
 //    therefore be one tensor.
-//  * base and (up to rank 64) W of a block are asked for together, the first
-//    block's before T is gathered.
+//  * base and W of the next block are on their way while a block is computed,
+//    the first block's while t is gathered from its slices.
 // Bound: HBM, base read and out written once; W comes from L2 once per tile.
 // The column block is the fast grid index: an XCD keeps to its part of W.
-constexpr int kUpCols = 256;    // columns per block
-constexpr int kUpWaveCols = 64;
+constexpr int kUpCols = 128;    // columns per block
+constexpr int kUpWaves = kPlanTile / 16;
+constexpr int kUpSlab = 64 + 4; // row of a wave's 16 x 64 fp32 slab
 
 struct UpArgs {
   const uint16_t* base;  // [M, cols] bf16 or null (zeros)
@@ -308,197 +319,343 @@ struct UpArgs {
   float keep_scale;
 };
 
-// RTL: 16-rank chunks held in LDS (at least ceil(r / 16)).
-template <bool WT, bool DROP, int RTL>
-__global__ void __launch_bounds__(256) k_batch_up(UpArgs g) {
-  constexpr int LD = RTL * 32 + 8;   // LDS row of a token: 16 hi and 16 mid terms per chunk
-  constexpr bool AHEAD = RTL <= 4;   // W of a block in registers ahead of its use
-  constexpr int WR = AHEAD ? RTL : 1;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[kPlanTile * LD];
-  __shared__ __attribute__((aligned(16))) uint16_t slab[WT ? 4 : 1][WT ? 16 * 80 : 8];
+// LDS operations done, then the workgroup's barrier; loads from memory into
+// registers stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// RK ranks of W in LDS at a time, in NS stages (NS = 1: all of them).
+template <bool WT, bool DROP, int RK, int NS>
+__global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
+  constexpr int LD = NS * RK * 2 + 8;            // LDS row of a token: RK hi, RK mid terms per stage
+  constexpr int LW = WT ? kUpCols + 8 : RK + 8;  // LDS row of W: a rank's columns or a column's ranks
+  constexpr int WP = RK / 16;                    // 16-byte pieces of W per lane and stage
+  __shared__ __attribute__((aligned(16))) uint16_t tl[kPlanTile * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t wl[WT ? RK * LW : kUpCols * LW];
+  __shared__ __attribute__((aligned(16))) float slab[kUpWaves][16 * kUpSlab];
   __shared__ int rows[kPlanTile];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, q4 = lane >> 4;
   const TileRow t = tile_row(g.tiles, blockIdx.y, g.M, g.slots);
   if (t.count <= 0) return;
-  const int64_t cols = g.cols;
-  const int blocks = (int)((cols + kUpCols - 1) / kUpCols);
+  const int cols = (int)g.cols;
+  const int blocks = (cols + kUpCols - 1) / kUpCols;
   const int r = g.r;
   if (tid < kPlanTile) {
     const int m = tid < t.count ? g.order[t.first + tid] : -1;
     rows[tid] = (unsigned)m < (unsigned)g.M ? m : -1;
   }
   __syncthreads();
+  const int th = wave & 1, wc = 64 * (wave >> 1);   // token half, first column of the wave
+  float* const my = slab[wave];
+  // Byte offsets of this lane's pieces in block 0; a block adds its columns
+  // through the scalar offset, and columns past the last are left out.
+  const uint32_t brow = (uint32_t)cols * 2;
+  const __amdgpu_buffer_rsrc_t rb = rsrc_whole(g.base, g.base ? (uint32_t)g.M * brow : 0u);
+  const __amdgpu_buffer_rsrc_t ro = rsrc_whole(g.out, (uint32_t)g.M * brow);
+  // Piece (tg, h): token 32 th + 16 tg + 8 h + lane / 8, columns pc .. of a block.
+  const int pc = wc + 8 * (lane & 7);
+  const int pt = 32 * th + (lane >> 3);
+  uint32_t boff[2][2];
+#pragma unroll
+  for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = rows[pt + 16 * tg + 8 * h];
+      boff[tg][h] = m >= 0 ? (uint32_t)m * brow + (uint32_t)pc * 2 : kOOB;
+    }
+  auto load_b = [&](int cb, uint4 (&bv)[2][2]) {
+    const bool ok = pc < cols - cb * kUpCols;
+#pragma unroll
+    for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        bv[tg][h] = bload128s(rb, ok ? boff[tg][h] : kOOB, (uint32_t)cb * (kUpCols * 2));
+  };
+  const int step = gridDim.x;
+  uint4 ba[2][2], bb[2][2];
+  int cb = blockIdx.x;
   if (t.slot < 0) {   // no adapter: t = 0, the base alone
+    if (cb < blocks) load_b(cb, ba);
     if (g.t_out && blockIdx.x == 0)
-      for (int e = tid; e < t.count * r; e += 256)
+      for (int e = tid; e < t.count * r; e += 64 * kUpWaves)
         if (rows[e / r] >= 0) g.t_out[(int64_t)rows[e / r] * r + e % r] = 0.0f;
     if (g.out == g.base) return;
-    for (int cb = blockIdx.x; cb < blocks; cb += gridDim.x)
-      for (int e = tid; e < t.count * (kUpCols / 8); e += 256) {
-        const int m = rows[e / (kUpCols / 8)];
-        const int64_t c = (int64_t)cb * kUpCols + 8 * (e % (kUpCols / 8));
-        if (m < 0 || c >= cols) continue;
-        const int64_t o = (int64_t)m * cols + c;
-        *reinterpret_cast<uint4*>(g.out + o) =
-            g.base ? *reinterpret_cast<const uint4*>(g.base + o) : make_uint4(0, 0, 0, 0);
-      }
+    auto copy = [&](int cb, const uint4 (&cur)[2][2], uint4 (&next)[2][2]) {
+      const bool ok = pc < cols - cb * kUpCols;
+      load_b(cb + step, next);
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          bstore128s(ro, cur[tg][h], ok ? boff[tg][h] : kOOB, (uint32_t)cb * (kUpCols * 2));
+    };
+    while (cb < blocks) {
+      copy(cb, ba, bb);
+      cb += step;
+      if (cb >= blocks) break;
+      copy(cb, bb, ba);
+      cb += step;
+    }
     return;
   }
-  const int ntg = (t.count + 15) / 16;
-  const int chunks = (r + 15) / 16;
+  const int stages = NS == 1 ? 1 : (r + RK - 1) / RK;
   const float c_a = g.scale[t.slot];
   const uint16_t* const W = g.W + (int64_t)t.slot * cols * r;
-  uint16_t* const my = slab[WT ? wave : 0];
-
-  // Four 16-byte pieces of chunk ch of W (two for WT): rows n of the MFMA's
-  // row operand, or rows of A that pass through the slab.
-  auto load_w = [&](int64_t nw, int ch, uint4 (&wv)[4]) {
-    if constexpr (!WT) {
-      const int j = 16 * ch + 8 * (q4 & 1);
+  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(W, brow * (uint32_t)r);
+  auto load_w = [&](int cb, int j0, uint4 (&wv)[WP]) {
+    const int left = cols - cb * kUpCols;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t c = nw + 32 * (k >> 1) + 8 * (i >> 2) + 4 * (k & 1) + (i & 3);
-        const bool ok = c < cols && j < r;
-        wv[k] = keep_or_zero(ok, *reinterpret_cast<const uint4*>(W + (ok ? c * r + j : 0)));
-      }
-    } else {
-      const int j = 16 * ch + (lane >> 2);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int64_t c = nw + 16 * (lane & 3) + 8 * k;
-        const bool ok = c < cols && j < r;
-        wv[k] = keep_or_zero(ok, *reinterpret_cast<const uint4*>(W + (ok ? j * cols + c : 0)));
+    for (int q = 0; q < WP; ++q) {
+      const int p = 256 * q + tid;
+      if constexpr (!WT) {
+        const int c = p / (RK / 8), j = j0 + 8 * (p % (RK / 8));
+        wv[q] = bload128s(rw, c < left && j < r ? (uint32_t)(c * r + j) * 2 : kOOB,
+                          (uint32_t)cb * (kUpCols * 2) * (uint32_t)r);
+      } else {
+        const int j = j0 + p / (kUpCols / 8), c = 8 * (p % (kUpCols / 8));
+        wv[q] = bload128s(rw, c < left && j < r ? (uint32_t)j * brow + 2 * c : kOOB,
+                          (uint32_t)cb * (kUpCols * 2));
       }
     }
   };
-  auto w_operand = [&](const uint4 (&wv)[4], bf16x8_t (&wop)[4]) {
-    if constexpr (!WT) {
+  auto store_w = [&](const uint4 (&wv)[WP]) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) wop[k] = __builtin_bit_cast(bf16x8_t, wv[k]);
-    } else {
-      // 16 ranks x 64 columns of A through LDS (rows of 80), read back
-      // transposed: lane i of a 16-lane group gets column 8 (i / 4) + 4 jj +
-      // i % 4 of ranks 8 (q4 & 1) .. +7.
+    for (int q = 0; q < WP; ++q) {
+      const int p = 256 * q + tid;
+      constexpr int PPR = WT ? kUpCols / 8 : RK / 8;
+      *reinterpret_cast<uint4*>(wl + (p / PPR) * LW + 8 * (p % PPR)) = wv[q];
+    }
+  };
+  // Operands of t: RK ranks of token 32 th + 16 tg + i, as hi and mid terms.
+  constexpr int NT = RK == 16 ? 1 : RK / 16;
+  bf16x8_t top[2][NT];
+  auto load_t = [&](int stage) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<uint4*>(my + (lane >> 2) * 80 + 16 * (lane & 3) + 8 * k) = wv[k];
-      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): one wave's LDS operations are in order
-      const int rr = 8 * (q4 & 1) + (i >> 2);
+    for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+        top[tg][k] = *reinterpret_cast<const bf16x8_t*>(
+            tl + (32 * th + 16 * tg + i) * LD + stage * 2 * RK + 32 * k + 8 * q4);
+  };
+  f32x4_t acc[2][4];   // [token group][columns wc + 16 k + 4 q4 + v]
+  auto multiply = [&](int tgs) {
+#pragma unroll
+    for (int ch = 0; ch < (RK + 31) / 32; ++ch) {
+      const int jw = RK == 16 ? 8 * (q4 & 1) : 32 * ch + 8 * q4;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int cc = 32 * (k >> 1) + 8 * (i & 3) + 4 * (k & 1);
-        const v4s_t lo = lds_read_tr16(my + rr * 80 + cc);
-        const v4s_t hi = lds_read_tr16(my + (rr + 4) * 80 + cc);
-        const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        wop[k] = __builtin_bit_cast(bf16x8_t, v);
+        bf16x8_t wop;
+        if constexpr (!WT) {
+          wop = *reinterpret_cast<const bf16x8_t*>(wl + (wc + 16 * k + i) * LW + jw);
+        } else {
+          const uint16_t* const p = wl + (jw + (i >> 2)) * LW + wc + 16 * k + 4 * (i & 3);
+          const v4s_t lo = lds_read_tr16(p);
+          const v4s_t hi = lds_read_tr16(p + 4 * LW);
+          const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          wop = __builtin_bit_cast(bf16x8_t, v);
+        }
+#pragma unroll
+        for (int tg = 0; tg < 2; ++tg) {
+          if (tg >= tgs) break;
+          if (RK > 16) acc[tg][k] = mfma_16x16x32(wop, top[tg][RK / 32 + ch], acc[tg][k]);   // mid first
+          acc[tg][k] = mfma_16x16x32(wop, top[tg][ch], acc[tg][k]);
+        }
       }
     }
   };
-
-  for (int cb = blockIdx.x; cb < blocks; cb += gridDim.x) {
-    const int64_t nw = (int64_t)cb * kUpCols + kUpWaveCols * wave;
-    uint4 bv[4][2], wv[WR][4];
+  auto finish = [&](int cb, int tgs, const uint4 (&bv)[2][2]) {
+    const bool ok = pc < cols - cb * kUpCols;
 #pragma unroll
-    for (int tg = 0; tg < 4; ++tg) {
-      if (tg >= ntg) break;
-      const int m = rows[16 * tg + i];
+    for (int tg = 0; tg < 2; ++tg) {
+      if (tg >= tgs) break;
+      // A wave's LDS operations run in issue order: these stores land after
+      // the last group's reads.
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t c = nw + 32 * u + 8 * q4;
-        const bool ok = m >= 0 && c < cols;
-        bv[tg][u] = make_uint4(0, 0, 0, 0);
-        if (g.base && ok) bv[tg][u] = *reinterpret_cast<const uint4*>(g.base + (int64_t)m * cols + c);
-      }
-    }
-    if constexpr (AHEAD) {
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<f32x4_t*>(my + i * kUpSlab + 16 * k + 4 * q4) = acc[tg][k];
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
 #pragma unroll
-      for (int ch = 0; ch < RTL; ++ch) load_w(nw, ch, wv[ch]);
-    }
-    if (cb == (int)blockIdx.x) {   // t of the tile, once
-      for (int e = tid; e < kPlanTile * RTL * 4; e += 256) {
-        const int tok = e / (RTL * 4), j = 4 * (e % (RTL * 4));
-        const int m = rows[tok];
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (m >= 0 && j < r) {
-          const int64_t at = (int64_t)m * r + j, plane = (int64_t)g.M * r;
-          for (int z = 0; z < g.slices; ++z) {
-            const float4 p = *reinterpret_cast<const float4*>(g.part + z * plane + at);
-            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-          }
-          if (g.t_out && blockIdx.x == 0) *reinterpret_cast<float4*>(g.t_out + at) = v;
-        }
-        const float f[4] = {c_a * v.x, c_a * v.y, c_a * v.z, c_a * v.w};
-        uint16_t hi[4], mid[4], lo;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) split3(m >= 0 && j < r ? f[k] : 0.0f, hi[k], mid[k], lo);
-        uint16_t* const d = lds + tok * LD + (j >> 4) * 32 + (j & 15);
-        *reinterpret_cast<uint2*>(d) =
-            make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
-        *reinterpret_cast<uint2*>(d + 16) =
-            make_uint2(mid[0] | (uint32_t)mid[1] << 16, mid[2] | (uint32_t)mid[3] << 16);
-      }
-      __syncthreads();
-    }
-
-    f32x4_t acc[4][4];   // [token group][unit, pair half]
-#pragma unroll
-    for (int tg = 0; tg < 4; ++tg)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[tg][k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    auto chunk = [&](int ch, const uint4 (&w)[4]) {
-      bf16x8_t wop[4];
-      w_operand(w, wop);
-#pragma unroll
-      for (int tg = 0; tg < 4; ++tg) {
-        if (tg >= ntg) break;
-        const bf16x8_t top =
-            *reinterpret_cast<const bf16x8_t*>(lds + (16 * tg + i) * LD + 32 * ch + 8 * q4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[tg][k] = mfma_16x16x32(wop[k], top, acc[tg][k]);
-      }
-    };
-    if constexpr (AHEAD) {
-#pragma unroll
-      for (int ch = 0; ch < RTL; ++ch) chunk(ch, wv[ch]);
-    } else {
-      for (int ch = 0; ch < chunks; ++ch) {
-        load_w(nw, ch, wv[0]);
-        chunk(ch, wv[0]);
-      }
-    }
-    // acc[tg][2 u + jj][v]: token 16 tg + i, column nw + 32 u + 8 q4 + 4 jj + v.
-#pragma unroll
-    for (int tg = 0; tg < 4; ++tg) {
-      if (tg >= ntg) break;
-      const int m = rows[16 * tg + i];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t c = nw + 32 * u + 8 * q4;
-        if (m < 0 || c >= cols) continue;
-        const int64_t o = (int64_t)m * cols + c;
-        const uint32_t bw[4] = {bv[tg][u].x, bv[tg][u].y, bv[tg][u].z, bv[tg][u].w};
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[tg][2 * u][e];
-          v[4 + e] = acc[tg][2 * u + 1][e];
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float* const e = my + (8 * h + (lane >> 3)) * kUpSlab + 8 * (lane & 7);
+        const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(e);
+        const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(e + 4);
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         if constexpr (DROP) {
-          const uint32_t keep = philox_keep8((uint64_t)o, g.drop);
+          const uint64_t o = (uint64_t)max(rows[pt + 16 * tg + 8 * h], 0) * (uint64_t)cols +
+                             (uint64_t)(cb * kUpCols + pc);
+          const uint32_t keep = philox_keep8(o, g.drop);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = (keep >> e) & 1u ? v[e] * g.keep_scale : 0.0f;
+          for (int k = 0; k < 8; ++k) v[k] = (keep >> k) & 1u ? v[k] * g.keep_scale : 0.0f;
         }
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = pack_bf16x2(bf16_to_f32(bw[e] & 0xffffu) + v[2 * e],
-                             bf16_to_f32(bw[e] >> 16) + v[2 * e + 1]);
-        *reinterpret_cast<uint4*>(g.out + o) = make_uint4(w[0], w[1], w[2], w[3]);
+        const uint4 b = bv[tg][h];
+        uint4 w;
+        w.x = pack_bf16x2(bf16_to_f32(b.x & 0xffffu) + v[0], bf16_to_f32(b.x >> 16) + v[1]);
+        w.y = pack_bf16x2(bf16_to_f32(b.y & 0xffffu) + v[2], bf16_to_f32(b.y >> 16) + v[3]);
+        w.z = pack_bf16x2(bf16_to_f32(b.z & 0xffffu) + v[4], bf16_to_f32(b.z >> 16) + v[5]);
+        w.w = pack_bf16x2(bf16_to_f32(b.w & 0xffffu) + v[6], bf16_to_f32(b.w >> 16) + v[7]);
+        bstore128s(ro, w, ok ? boff[tg][h] : kOOB, (uint32_t)cb * (kUpCols * 2));
       }
+    }
+  };
+
+  uint4 wv[WP];
+  // A narrow tile's pieces: base of token i, W rows of the wave's 64 columns.
+  constexpr bool NARROW = !WT && NS == 1;
+  constexpr int NQ = (RK + 31) / 32;
+  const bool narrow = NARROW && t.count <= 16;
+  uint4 na[2], nb[2], wa[2][NQ][2], wb[2][NQ][2];
+  const int mi = rows[i];
+  const uint32_t noff = mi >= 0 ? (uint32_t)mi * brow + (uint32_t)(64 * wave + 8 * q4) * 2 : kOOB;
+  auto load_n = [&](int cb, uint4 (&bv)[2], uint4 (&w)[2][NQ][2]) {
+    const int left = cols - cb * kUpCols;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = 64 * wave + 32 * u;
+#pragma unroll
+      for (int ch = 0; ch < NQ; ++ch)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int n = c + 8 * (i >> 2) + 4 * k + (i & 3);
+          const int j = RK == 16 ? 8 * (q4 & 1) : 32 * ch + 8 * q4;
+          w[u][ch][k] = bload128s(rw, n < left && j < r ? (uint32_t)(n * r + j) * 2 : kOOB,
+                                  (uint32_t)cb * (kUpCols * 2) * (uint32_t)r);
+        }
+      bv[u] = bload128s(rb, noff != kOOB && c + 8 * q4 < left ? noff + 64 * u : kOOB,
+                        (uint32_t)cb * (kUpCols * 2));
+    }
+  };
+  if (NARROW && narrow) {
+    cb = 2 * blockIdx.x;
+    load_n(cb, na, wa);
+  } else if (cb < blocks) {
+    load_b(cb, ba);
+    load_w(cb, 0, wv);
+  }
+  // t of the tile: its slices added in order, four loads at a time.
+  for (int e = tid; e < kPlanTile * NS * RK / 4; e += 64 * kUpWaves) {
+    const int tok = e / (NS * RK / 4), j = 4 * (e % (NS * RK / 4));
+    const int m = rows[tok];
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (m >= 0 && j < r) {
+      const int64_t at = (int64_t)m * r + j, plane = (int64_t)g.M * r;
+      for (int z = 0; z < g.slices; z += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          p[k] = *reinterpret_cast<const float4*>(g.part + min(z + k, g.slices - 1) * plane + at);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (z + k < g.slices) { v.x += p[k].x; v.y += p[k].y; v.z += p[k].z; v.w += p[k].w; }
+      }
+      if (g.t_out && blockIdx.x == 0) *reinterpret_cast<float4*>(g.t_out + at) = v;
+      v.x *= c_a; v.y *= c_a; v.z *= c_a; v.w *= c_a;
+    }
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint16_t hi[4], mid[4], lo;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split3(f[k], hi[k], mid[k], lo);
+    uint16_t* const d = tl + tok * LD + (j / RK) * 2 * RK + j % RK;
+    *reinterpret_cast<uint2*>(d) =
+        make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+    *reinterpret_cast<uint2*>(d + RK) =
+        make_uint2(mid[0] | (uint32_t)mid[1] << 16, mid[2] | (uint32_t)mid[3] << 16);
+  }
+  __syncthreads();
+  if constexpr (NARROW) {
+    if (narrow) {
+      // Up to 16 tokens (a step of single tokens): W is what is read, once per
+      // tile, and goes straight into the MFMA's operand registers, two blocks
+      // at a time, a wave 64 columns; no barrier.  Row rho of half k stands for
+      // column 8 (rho / 4) + 4 k + rho % 4 of 32, so that a lane's two products
+      // of a token are 8 consecutive columns.
+      bf16x8_t tn[NT];
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+        tn[k] = *reinterpret_cast<const bf16x8_t*>(tl + i * LD + 32 * k + 8 * q4);
+      auto done = [&](int cb, const uint4 (&bv)[2], const uint4 (&w)[2][NQ][2]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = cb * kUpCols + 64 * wave + 32 * u + 8 * q4;
+          f32x4_t d[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            d[k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int ch = 0; ch < NQ; ++ch) {
+              const bf16x8_t wop = __builtin_bit_cast(bf16x8_t, w[u][ch][k]);
+              if (RK > 16) d[k] = mfma_16x16x32(wop, tn[RK / 32 + ch], d[k]);   // mid first
+              d[k] = mfma_16x16x32(wop, tn[ch], d[k]);
+            }
+          }
+          uint4 o;
+          o.x = pack_bf16x2(bf16_to_f32(bv[u].x & 0xffffu) + d[0][0], bf16_to_f32(bv[u].x >> 16) + d[0][1]);
+          o.y = pack_bf16x2(bf16_to_f32(bv[u].y & 0xffffu) + d[0][2], bf16_to_f32(bv[u].y >> 16) + d[0][3]);
+          o.z = pack_bf16x2(bf16_to_f32(bv[u].z & 0xffffu) + d[1][0], bf16_to_f32(bv[u].z >> 16) + d[1][1]);
+          o.w = pack_bf16x2(bf16_to_f32(bv[u].w & 0xffffu) + d[1][2], bf16_to_f32(bv[u].w >> 16) + d[1][3]);
+          bstore128s(ro, o, noff != kOOB && c < cols ? noff + 64 * u : kOOB, (uint32_t)cb * (kUpCols * 2));
+        }
+      };
+      const int nstep = 2 * step;
+      while (cb < blocks) {
+        load_n(cb + nstep, nb, wb);
+        done(cb, na, wa);
+        cb += nstep;
+        if (cb >= blocks) break;
+        load_n(cb + nstep, na, wa);
+        done(cb, nb, wb);
+        cb += nstep;
+      }
+      return;
     }
   }
+  if (NS == 1) load_t(0);
+  // One block: W from registers to LDS (every wave is done with the last
+  // block's), the next block's loads, the products, the epilogue.  FULL: all
+  // token groups hold tokens.  Loads are issued whether or not there is a next
+  // block (at kOOB past the last), so that the count of those in flight is the
+  // same on every path and a wait for W leaves the younger ones alone.
+  auto run = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const int tgs = FULL ? 2 : max(0, min(2, (t.count - 32 * th + 15) / 16));
+    auto block = [&](int cb, uint4 (&cur)[2][2], uint4 (&next)[2][2]) {
+#pragma unroll
+      for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[tg][k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (NS == 1) {
+        lds_barrier();
+        store_w(wv);
+        load_w(cb + step, 0, wv);
+        if (FULL || tgs > 0) load_b(cb + step, next);
+        lds_barrier();
+        if (FULL || tgs > 0) multiply(tgs);
+      } else {
+        for (int stage = 0; stage < stages; ++stage) {
+          lds_barrier();
+          store_w(wv);
+          const bool last = stage + 1 == stages;
+          load_w(last ? cb + step : cb, last ? 0 : (stage + 1) * RK, wv);
+          lds_barrier();
+          load_t(stage);
+          multiply(tgs);
+        }
+        load_b(cb + step, next);
+      }
+      if (FULL || tgs > 0) finish(cb, tgs, cur);
+    };
+    while (cb < blocks) {
+      block(cb, ba, bb);
+      cb += step;
+      if (cb >= blocks) break;
+      block(cb, bb, ba);
+      cb += step;
+    }
+  };
+  if (t.count > kPlanTile - 16) run(std::true_type());
+  else run(std::false_type());
 }
 
 // ---------------------------------------------------------------------------
@@ -565,13 +722,26 @@ __global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g
   const int nt = s1 - s0;
   if (DX && slot == g.slots) {   // tokens without an adapter: dX = dX0
     if (!first || g.dX == g.dX0) return;
-    for (int e = tid; e < nt * (kGradSlice / 8); e += 64 * kGradWaves) {
-      const int m = g.order[s0 + e / (kGradSlice / 8)];
-      const int64_t c = c0 + 8 * (e % (kGradSlice / 8));
-      if ((unsigned)m >= (unsigned)M || c >= cols) continue;
-      const int64_t o = (int64_t)m * cols + c;
-      *reinterpret_cast<uint4*>(g.dX + o) =
-          g.dX0 ? *reinterpret_cast<const uint4*>(g.dX0 + o) : make_uint4(0, 0, 0, 0);
+    // Four pieces of a thread are on their way together.
+    const int n = nt * (kGradSlice / 8);
+    for (int e0 = tid; e0 < n; e0 += 4 * 64 * kGradWaves) {
+      int64_t o[4];
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = e0 + k * 64 * kGradWaves;
+        const int m = e < n ? g.order[s0 + e / (kGradSlice / 8)] : -1;
+        const int64_t c = c0 + 8 * (e % (kGradSlice / 8));
+        o[k] = (unsigned)m < (unsigned)M && c < cols ? (int64_t)m * cols + c : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (g.dX0 && o[k] >= 0) v[k] = *reinterpret_cast<const uint4*>(g.dX0 + o[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (o[k] >= 0) *reinterpret_cast<uint4*>(g.dX + o[k]) = v[k];
     }
     return;
   }
@@ -776,19 +946,25 @@ __global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g
 
 static inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Tiles that a batch may be expected to have: its tokens' own, and more where
-// slots are many beside them (the host does not know the slots in use).
+// Tiles that a batch may be expected to have (the host does not know the slots
+// in use): its tokens' own, and one more per slot it may hold.  A batch of few
+// tokens may be one of single tokens and hold as many adapters; one of many
+// holds prompts, and fewer of them.
 static int64_t expected_tiles(int64_t M, int S) {
-  const int64_t more = M / 8 < S ? M / 8 : S;
-  return (M + kPlanTile - 1) / kPlanTile + more;
+  int64_t more = 32 + M / 32;
+  if (more > M) more = M;
+  if (more > S) more = S;
+  return M / kPlanTile + more;
 }
 
 // Steps per slice of the down projections' contraction: slices that give about
-// two workgroups per CU.
+// two workgroups per CU, at most kMaxSlices (their sums are read back).
+constexpr int kMaxSlices = 16;
 static int down_zlen(int64_t M, int S, int64_t C) {
   const int64_t steps = (C + 63) / 64;
   int64_t want = 2 * kCUs / expected_tiles(M, S);
   if (want < 1) want = 1;
+  if (want > kMaxSlices) want = kMaxSlices;
   const int64_t per = (steps + want * kDownWaves - 1) / (want * kDownWaves);   // steps per wave
   return (int)(per * kDownWaves);
 }
@@ -826,29 +1002,26 @@ static hipError_t down(DownArgs g, hipStream_t st) {
 
 template <bool WT, bool DROP>
 static hipError_t up(const UpArgs& g, hipStream_t st) {
-  // Column blocks per workgroup: about four workgroups per CU, whole multiples
-  // of the XCDs where there are that many.
+  // Workgroups per tile: about four per CU in all, two where most tiles are
+  // narrow (a narrow tile takes two blocks at a time; 16 single tokens, 28672
+  // columns: 7.8 against 11.0 us; 2048 tokens, 4096 columns: 11.0 against 10.2),
+  // whole multiples of the XCDs where there are that many.
   const int64_t blocks = (g.cols + kUpCols - 1) / kUpCols;
-  int64_t gx = 4 * kCUs / expected_tiles(g.M, g.slots);
+  const int64_t tiles = expected_tiles(g.M, g.slots);
+  int64_t gx = (g.M <= 16 * tiles ? 2 : 4) * kCUs / tiles;
   if (gx >= kXCDs) gx -= gx % kXCDs;
   if (gx < 1) gx = 1;
   if (gx > blocks) gx = blocks;
   const dim3 grid((unsigned)gx, (unsigned)adapter_plan_tiles(g.M, g.slots));
-  if constexpr (!WT) {
-    if (g.r <= 16) {
-      hipLaunchKernelGGL((k_batch_up<WT, DROP, 1>), grid, dim3(256), 0, st, g);
-      return hipGetLastError();
-    }
-    if (g.r <= 32) {
-      hipLaunchKernelGGL((k_batch_up<WT, DROP, 2>), grid, dim3(256), 0, st, g);
-      return hipGetLastError();
-    }
-    if (g.r <= 64) {
-      hipLaunchKernelGGL((k_batch_up<WT, DROP, 4>), grid, dim3(256), 0, st, g);
-      return hipGetLastError();
-    }
+  const dim3 block(64 * kUpWaves);
+  if constexpr (WT) {
+    hipLaunchKernelGGL((k_batch_up<WT, DROP, 64, 4>), grid, block, 0, st, g);
+  } else {
+    if (g.r <= 16) hipLaunchKernelGGL((k_batch_up<WT, DROP, 16, 1>), grid, block, 0, st, g);
+    else if (g.r <= 32) hipLaunchKernelGGL((k_batch_up<WT, DROP, 32, 1>), grid, block, 0, st, g);
+    else if (g.r <= 64) hipLaunchKernelGGL((k_batch_up<WT, DROP, 64, 1>), grid, block, 0, st, g);
+    else hipLaunchKernelGGL((k_batch_up<WT, DROP, 64, 4>), grid, block, 0, st, g);
   }
-  hipLaunchKernelGGL((k_batch_up<WT, DROP, 16>), grid, dim3(256), 0, st, g);
   return hipGetLastError();
 }
 
