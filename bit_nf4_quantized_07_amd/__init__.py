@@ -552,33 +552,35 @@ class AdapterPlan(NamedTuple):
     S: int
 
 
-def _checked(items):
-    """_Checker's checks of (name, tensor, dtype, shape) items, all required,
-    and their device.  These calls are short, so what passes takes one quick
-    pass; anything else goes to _Checker, which names the first fault."""
-    tensor = _torch().Tensor
-    first = items[0][1]
-    index = first.get_device() if type(first) is tensor else -1
-    for _, t, dtype, shape in items:
-        if (type(t) is not tensor or t.dtype is not dtype or t.shape != shape
-                or not t.is_contiguous() or t.get_device() != index):
-            break
-    else:
-        if index >= 0:
-            return first.device
+_bound_calls = None
+
+
+def _load_calls():
+    """The calls' C++ marshalling (csrc/calls.cpp), bound to libqlora.so; raises
+    if it has not been built."""
+    global _bound_calls
+    if _bound_calls is None:
+        lib = load_library()
+        try:
+            from . import _calls as mod
+        except ImportError as e:
+            raise RuntimeError("the batched adapters' binding is missing: build it with "
+                               "`python -m bit_nf4_quantized_07_amd.build`") from e
+        mod.bind(*(ctypes.cast(getattr(lib, n), _P).value for n in (
+            "lora_adapter_tiles", "lora_adapter_plan", "lora_adapters_workspace_bytes",
+            "lora_adapters_fwd", "lora_adapters_bwd")))
+        _bound_calls = mod
+    return _bound_calls
+
+
+def _refused(items):
+    """Raises for the first item (name, tensor, dtype, shape) that _Checker
+    refuses; the calls' own quick checks refused one of them."""
     chk = _Checker()
     for name, t, dtype, shape in items:
         chk(name, t, dtype, shape)
-    return chk.device()
-
-
-def _on_device(dev, call):
-    """call(stream) with `dev` current and its current stream."""
-    torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        return call(torch.cuda.current_stream(dev))
-    with torch.cuda.device(dev):
-        return call(torch.cuda.current_stream(dev))
+    chk.device()
+    raise ValueError("a tensor was refused")
 
 
 def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> AdapterPlan:
@@ -586,36 +588,27 @@ def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> A
     slot (outside [0, S): none), lengths int32 [Q], its token rows (None: one
     each).  `tokens` is the batch's number of rows M (default, without lengths:
     Q); rows behind the last request have no adapter."""
-    torch = _torch()
-    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
-        raise ValueError("slots: a 1-D int32 tensor")
-    Q = slots.shape[0]
-    items = [("slots", slots, torch.int32, (Q,))]
-    if lengths is not None:
-        items.append(("lengths", lengths, torch.int32, (Q,)))
     if tokens is None:
         if lengths is not None:
             raise ValueError("tokens: the batch's number of rows, where lengths are given")
-        tokens = Q
-    dev = _checked(items)
-    M, S = int(tokens), int(S)
-    lib = load_library()
-    nt = lib.lora_adapter_tiles(M, S) if abs(M) < 2**62 and abs(S) < 2**31 else 0
-    if nt <= 0:
-        raise QLoRAError("lora_adapter_plan", ERR_SHAPE)
-    # one allocation, each array at a multiple of 16 bytes
-    mp, sp = (M + 3) & ~3, (S + 5) & ~3
-    buf = torch.empty(2 * mp + sp + 3 * nt, dtype=torch.int32, device=dev)
-    at = buf.data_ptr()
-    _check("lora_adapter_plan", _on_device(dev, lambda st: lib.lora_adapter_plan(
-        None if lengths is None else lengths.data_ptr(), slots.data_ptr() if Q else None, Q, M, S,
-        at, at + 4 * mp, at + 8 * mp, at + 8 * mp + 4 * sp, st.cuda_stream)))
-    return AdapterPlan(buf[:M], buf[mp:mp + M], buf[2 * mp:2 * mp + S + 2],
-                       buf[2 * mp + sp:].view(nt, 3), S)
+        tokens = len(slots)
+    res = (_bound_calls or _load_calls()).plan(slots, lengths, tokens, S)
+    if res is None:
+        torch = _torch()
+        if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+            raise ValueError("slots: a 1-D int32 tensor")
+        shape = tuple(slots.shape)
+        _refused([("slots", slots, torch.int32, shape)]
+                 + ([("lengths", lengths, torch.int32, shape)] if lengths is not None else []))
+    if res[0] != OK:
+        raise QLoRAError("lora_adapter_plan", res[0])
+    return AdapterPlan(res[1], res[2], res[3], res[4], S)
 
 
-def _batch_items(X, A, B, scale, plan):
-    """(M, K, N, r, S) and the check items of X, the adapters and the plan."""
+def _refused_batch(X, A, B, scale, plan, others):
+    """_refused for the tensors that the forward and the backward share;
+    others(M, K, N, r, S) gives the call's own (name, tensor or None, dtype,
+    shape) items."""
     torch = _torch()
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X: a 2-D tensor")
@@ -632,23 +625,27 @@ def _batch_items(X, A, B, scale, plan):
         raise ValueError(f"plan: built for {plan.S} slots, the adapters have {S}")
     bf, i32 = torch.bfloat16, torch.int32
     nt = M // PLAN_TILE + min(M, S + 1)
-    return (M, K, N, r, S), [
-        ("X", X, bf, (M, K)), ("A", A, bf, (S, r, K)), ("B", B, bf, (S, N, r)),
-        ("scale", scale, torch.float32, (S,)), ("order", plan.order, i32, (M,)),
-        ("start", plan.start, i32, (S + 2,)), ("tiles", plan.tiles, i32, (nt, 3))]
+    items = [("X", X, bf, (M, K)), ("A", A, bf, (S, r, K)), ("B", B, bf, (S, N, r)),
+             ("scale", scale, torch.float32, (S,)), ("order", plan.order, i32, (M,)),
+             ("start", plan.start, i32, (S + 2,)), ("tiles", plan.tiles, i32, (nt, 3))]
+    _refused(items + [it for it in others(M, K, N, r, S) if it[1] is not None])
 
 
 def _dropout_args(dropout):
-    if dropout is None:
-        return 0.0, 0
     p, seed = dropout
     return float(p), int(seed) & (2**64 - 1)
 
 
-def _batch_workspace(dev, stream, nbytes, workspace):
-    ws = workspace if workspace is not None else default_workspace(dev, stream)
-    buf, size = ws.get(nbytes, stream)
-    return (buf.data_ptr() if buf is not None else None), size
+def _batch_workspace(workspace, X, A, B, backward):
+    """The memory of a caller's Workspace for this call (None: none given; the
+    call then takes scratch memory from torch's allocator)."""
+    torch = _torch()
+    if not all(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == d
+               for t, d in ((X, 2), (A, 3), (B, 3))):
+        return None                     # refused by the call
+    need = load_library().lora_adapters_workspace_bytes(
+        X.shape[0], X.shape[1], B.shape[1], A.shape[1], A.shape[0], 1 if backward else 0)
+    return workspace.get(need, torch.cuda.current_stream(X.device))[0]
 
 
 def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: bool = True,
@@ -656,35 +653,20 @@ def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: boo
     """out = Y + scale (drop(X) A^T) B^T, every token with its slot's A [S, r,
     K], B [S, N, r] and scale [S].  Y bf16 [M, N] is the shared projection's
     output (None: the adapters' term alone; out may be Y).  dropout: None or
-    (p, seed), lora_dropout's mask, regenerated where it is needed.  Returns
-    (out bf16 [M, N], T fp32 [M, r] or None)."""
-    torch = _torch()
-    (M, K, N, r, S), items = _batch_items(X, A, B, scale, plan)
-    if Y is not None:
-        items.append(("Y", Y, torch.bfloat16, (M, N)))
-    if out is not None:
-        items.append(("out", out, torch.bfloat16, (M, N)))
-    if T_out is not None:
-        items.append(("T_out", T_out, torch.float32, (M, r)))
-    p, seed = _dropout_args(dropout)
-    dev = _checked(items)
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    T = T_out
-    if T is None and save_T:
-        T = torch.empty((M, r), dtype=torch.float32, device=dev)
-    lib = load_library()
-
-    def call(st):
-        ws, wsb = _batch_workspace(dev, st, lib.lora_adapters_workspace_bytes(M, K, N, r, S, 0), workspace)
-        return lib.lora_adapters_fwd(
-            X.data_ptr(), M, K, N, A.data_ptr(), B.data_ptr(), scale.data_ptr(), r, S,
-            plan.order.data_ptr(), plan.start.data_ptr(), plan.tiles.data_ptr(),
-            None if Y is None else Y.data_ptr(), p, seed, out.data_ptr(),
-            None if T is None else T.data_ptr(), ws, wsb, st.cuda_stream)
-
-    _check("lora_adapters_fwd", _on_device(dev, call))
-    return out, T
+    (p, seed), lora_dropout's mask, regenerated where it is needed.  Scratch
+    memory is torch's unless a Workspace is given.  Returns (out bf16 [M, N], T
+    fp32 [M, r] or None)."""
+    p, seed = (0.0, 0) if dropout is None else _dropout_args(dropout)
+    ws = None if workspace is None else _batch_workspace(workspace, X, A, B, False)
+    res = (_bound_calls or _load_calls()).fwd(X, Y, A, B, scale, plan, p, seed, save_T, out, T_out, ws)
+    if res is None:
+        torch = _torch()
+        bf = torch.bfloat16
+        _refused_batch(X, A, B, scale, plan, lambda M, K, N, r, S: [
+            ("Y", Y, bf, (M, N)), ("out", out, bf, (M, N)), ("T_out", T_out, torch.float32, (M, r))])
+    if res[0] != OK:
+        raise QLoRAError("lora_adapters_fwd", res[0])
+    return res[1], res[2]
 
 
 def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout=None,
@@ -692,38 +674,26 @@ def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout
     """Backward of adapters_fwd: (dX bf16 [M, K] or None, dA fp32 [S, r, K],
     dB fp32 [S, N, r]).  dX, if given, is what the shared projection's backward
     gave: the adapters' term is added to it (dX_out may be the same tensor).
-    T from the forward (None: computed again); dropout as in the forward."""
-    torch = _torch()
-    f32 = torch.float32
-    (M, K, N, r, S), items = _batch_items(X, A, B, scale, plan)
-    items.append(("dY", dY, torch.bfloat16, (M, N)))
-    for name, t, dtype, shape in (("T", T, f32, (M, r)), ("dX", dX, torch.bfloat16, (M, K)),
-                                  ("dX_out", dX_out, torch.bfloat16, (M, K)),
-                                  ("dA", dA_out, f32, (S, r, K)), ("dB", dB_out, f32, (S, N, r))):
-        if t is not None:
-            items.append((name, t, dtype, shape))
-    p, seed = _dropout_args(dropout)
-    dev = _checked(items)
-    if not need_dX:
-        if dX is not None or dX_out is not None:
-            raise ValueError("dX: given, but need_dX is False")
-    elif dX_out is None:
-        dX_out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    dA = dA_out if dA_out is not None else torch.empty((S, r, K), dtype=f32, device=dev)
-    dB = dB_out if dB_out is not None else torch.empty((S, N, r), dtype=f32, device=dev)
-    lib = load_library()
-
-    def call(st):
-        ws, wsb = _batch_workspace(dev, st, lib.lora_adapters_workspace_bytes(M, K, N, r, S, 1), workspace)
-        return lib.lora_adapters_bwd(
-            dY.data_ptr(), X.data_ptr(), M, K, N, A.data_ptr(), B.data_ptr(), scale.data_ptr(), r,
-            S, plan.order.data_ptr(), plan.start.data_ptr(), plan.tiles.data_ptr(),
-            None if T is None else T.data_ptr(), None if dX is None else dX.data_ptr(), p, seed,
-            None if dX_out is None else dX_out.data_ptr(), dA.data_ptr(), dB.data_ptr(), ws, wsb,
-            st.cuda_stream)
-
-    _check("lora_adapters_bwd", _on_device(dev, call))
-    return dX_out, dA, dB
+    T from the forward (None: computed again); dropout as in the forward.
+    Scratch memory is torch's unless a Workspace is given."""
+    if not need_dX and (dX is not None or dX_out is not None):
+        raise ValueError("dX: given, but need_dX is False")
+    p, seed = (0.0, 0) if dropout is None else _dropout_args(dropout)
+    ws = None if workspace is None else _batch_workspace(workspace, X, A, B, True)
+    res = (_bound_calls or _load_calls()).bwd(dY, X, A, B, scale, plan, T, dX, p, seed, need_dX, dX_out,
+                                        dA_out, dB_out, ws)
+    if res is None:
+        torch = _torch()
+        bf, f32 = torch.bfloat16, torch.float32
+        if dY is None:
+            raise ValueError("dY: missing")
+        _refused_batch(X, A, B, scale, plan, lambda M, K, N, r, S: [
+            ("dY", dY, bf, (M, N)), ("T", T, f32, (M, r)), ("dX", dX, bf, (M, K)),
+            ("dX_out", dX_out, bf, (M, K)), ("dA", dA_out, f32, (S, r, K)),
+            ("dB", dB_out, f32, (S, N, r))])
+    if res[0] != OK:
+        raise QLoRAError("lora_adapters_bwd", res[0])
+    return res[1], res[2], res[3]
 
 
 def linear_fwd_dropout(X, Xd, qw: QuantizedWeight, A, B, alpha: float, save_T: bool = True,

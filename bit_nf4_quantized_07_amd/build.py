@@ -1,4 +1,5 @@
-"""Build libqlora.so (gfx950) from the HIP sources in csrc/ with hipcc.
+"""Build libqlora.so (gfx950) from the HIP sources in csrc/ with hipcc, and
+_calls.so, the C++ marshalling of the batched adapters' calls, with g++.
 
     python -m bit_nf4_quantized_07_amd.build [--verbose]
 
@@ -12,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqlora.so")
+CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["quant_kernels.hip", "gemm_kernels.hip", "fwd_kernels.hip", "dx_kernels.hip", "adapter_kernels.hip", "gemv_kernels.hip", "elementwise.hip",
            "merge_kernels.hip", "dropout_kernels.hip", "batch_plan_kernels.hip", "batch_kernels.hip",
            "qlora_api.hip"]
@@ -55,11 +58,33 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_calls(verbose: bool) -> None:
+    """csrc/calls.cpp against torch's and Python's headers (host code only; it
+    gets the addresses of libqlora.so's functions when it is loaded)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-I{root}/include", "-I/opt/rocm/include", f"-I{sysconfig.get_paths()['include']}",
+           os.path.join(CSRC, "calls.cpp"), "-o", tmp, f"-L{root}/lib", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link the shared library; returns its path."""
+    """Compile every source and link the shared libraries; returns libqlora.so's path."""
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     if verbose:
