@@ -28,10 +28,13 @@ namespace qlk {
 typedef short v8s_t __attribute__((ext_vector_type(8)));
 typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
 
-// Store through a buffer resource; a lane at kOOB stores nothing.
-__device__ __forceinline__ void bstore128s(__amdgpu_buffer_rsrc_t r, uint4 v, uint32_t voff,
-                                           uint32_t soff) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u_t, v), r, (int)voff, (int)soff, 0);
+// Store through a buffer resource; a lane at kOOB stores nothing.  The whole
+// offset goes in the lane's: with a scalar offset register the compiler takes
+// a 16-byte store's data registers as free in the next cycle, and a vector
+// instruction that wrote them there has replaced the first word of the last
+// lanes' data (seen as column indices in out).
+__device__ __forceinline__ void bstore128(__amdgpu_buffer_rsrc_t r, uint4 v, uint32_t off) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u_t, v), r, (int)off, 0, 0);
 }
 
 __device__ __forceinline__ uint4 keep_or_zero(bool ok, uint4 v) {
@@ -366,13 +369,16 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
       const int m = rows[pt + 16 * tg + 8 * h];
       boff[tg][h] = m >= 0 ? (uint32_t)m * brow + (uint32_t)pc * 2 : kOOB;
     }
+  // A block past the last has no columns: every lane is at kOOB, and the scalar
+  // offset stays inside the operand.
+  auto block_at = [&](int cb, uint32_t bytes) { return cb < blocks ? (uint32_t)cb * bytes : 0u; };
   auto load_b = [&](int cb, uint4 (&bv)[2][2]) {
     const bool ok = pc < cols - cb * kUpCols;
+    const uint32_t at = block_at(cb, kUpCols * 2);
 #pragma unroll
     for (int tg = 0; tg < 2; ++tg)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        bv[tg][h] = bload128s(rb, ok ? boff[tg][h] : kOOB, (uint32_t)cb * (kUpCols * 2));
+      for (int h = 0; h < 2; ++h) bv[tg][h] = bload128s(rb, ok ? boff[tg][h] : kOOB, at);
   };
   const int step = gridDim.x;
   uint4 ba[2][2], bb[2][2];
@@ -385,12 +391,13 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
     if (g.out == g.base) return;
     auto copy = [&](int cb, const uint4 (&cur)[2][2], uint4 (&next)[2][2]) {
       const bool ok = pc < cols - cb * kUpCols;
+      const uint32_t at = (uint32_t)cb * (kUpCols * 2);
       load_b(cb + step, next);
 #pragma unroll
       for (int tg = 0; tg < 2; ++tg)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          bstore128s(ro, cur[tg][h], ok ? boff[tg][h] : kOOB, (uint32_t)cb * (kUpCols * 2));
+          bstore128(ro, cur[tg][h], ok && boff[tg][h] != kOOB ? boff[tg][h] + at : kOOB);
     };
     while (cb < blocks) {
       copy(cb, ba, bb);
@@ -407,17 +414,16 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
   const __amdgpu_buffer_rsrc_t rw = rsrc_whole(W, brow * (uint32_t)r);
   auto load_w = [&](int cb, int j0, uint4 (&wv)[WP]) {
     const int left = cols - cb * kUpCols;
+    const uint32_t at = block_at(cb, WT ? kUpCols * 2 : kUpCols * 2 * (uint32_t)r);
 #pragma unroll
     for (int q = 0; q < WP; ++q) {
       const int p = 256 * q + tid;
       if constexpr (!WT) {
         const int c = p / (RK / 8), j = j0 + 8 * (p % (RK / 8));
-        wv[q] = bload128s(rw, c < left && j < r ? (uint32_t)(c * r + j) * 2 : kOOB,
-                          (uint32_t)cb * (kUpCols * 2) * (uint32_t)r);
+        wv[q] = bload128s(rw, c < left && j < r ? (uint32_t)(c * r + j) * 2 : kOOB, at);
       } else {
         const int j = j0 + p / (kUpCols / 8), c = 8 * (p % (kUpCols / 8));
-        wv[q] = bload128s(rw, c < left && j < r ? (uint32_t)j * brow + 2 * c : kOOB,
-                          (uint32_t)cb * (kUpCols * 2));
+        wv[q] = bload128s(rw, c < left && j < r ? (uint32_t)j * brow + 2 * c : kOOB, at);
       }
     }
   };
@@ -468,6 +474,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
   };
   auto finish = [&](int cb, int tgs, const uint4 (&bv)[2][2]) {
     const bool ok = pc < cols - cb * kUpCols;
+    const uint32_t at = (uint32_t)cb * (kUpCols * 2);
 #pragma unroll
     for (int tg = 0; tg < 2; ++tg) {
       if (tg >= tgs) break;
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
         w.y = pack_bf16x2(bf16_to_f32(b.y & 0xffffu) + v[2], bf16_to_f32(b.y >> 16) + v[3]);
         w.z = pack_bf16x2(bf16_to_f32(b.z & 0xffffu) + v[4], bf16_to_f32(b.z >> 16) + v[5]);
         w.w = pack_bf16x2(bf16_to_f32(b.w & 0xffffu) + v[6], bf16_to_f32(b.w >> 16) + v[7]);
-        bstore128s(ro, w, ok ? boff[tg][h] : kOOB, (uint32_t)cb * (kUpCols * 2));
+        bstore128(ro, w, ok && boff[tg][h] != kOOB ? boff[tg][h] + at : kOOB);
       }
     }
   };
@@ -521,10 +528,10 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
           const int n = c + 8 * (i >> 2) + 4 * k + (i & 3);
           const int j = RK == 16 ? 8 * (q4 & 1) : 32 * ch + 8 * q4;
           w[u][ch][k] = bload128s(rw, n < left && j < r ? (uint32_t)(n * r + j) * 2 : kOOB,
-                                  (uint32_t)cb * (kUpCols * 2) * (uint32_t)r);
+                                  block_at(cb, kUpCols * 2 * (uint32_t)r));
         }
       bv[u] = bload128s(rb, noff != kOOB && c + 8 * q4 < left ? noff + 64 * u : kOOB,
-                        (uint32_t)cb * (kUpCols * 2));
+                        block_at(cb, kUpCols * 2));
     }
   };
   if (NARROW && narrow) {
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
           o.y = pack_bf16x2(bf16_to_f32(bv[u].y & 0xffffu) + d[0][2], bf16_to_f32(bv[u].y >> 16) + d[0][3]);
           o.z = pack_bf16x2(bf16_to_f32(bv[u].z & 0xffffu) + d[1][0], bf16_to_f32(bv[u].z >> 16) + d[1][1]);
           o.w = pack_bf16x2(bf16_to_f32(bv[u].w & 0xffffu) + d[1][2], bf16_to_f32(bv[u].w >> 16) + d[1][3]);
-          bstore128s(ro, o, noff != kOOB && c < cols ? noff + 64 * u : kOOB, (uint32_t)cb * (kUpCols * 2));
+          bstore128(ro, o, noff != kOOB && c < cols ? noff + 64 * u + (uint32_t)cb * (kUpCols * 2) : kOOB);
         }
       };
       const int nstep = 2 * step;
@@ -666,19 +673,22 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
 //
 // A workgroup owns a slot, 64 columns of P and up to 64 ranks, and contracts
 // over all of the slot's tokens, gathered through the plan's order: no partial
-// sums in memory, no atomics.  Its eight waves take every eighth 32-token
-// chunk.  Lane (i, q4) loads the 8 columns 32 u + 8 q4 of tokens 16 tg + i, the
-// places of dX that it will write, so that the dropout's words are drawn once
-// for both.  P and the three bf16 planes of Q pass through a slab of LDS per
-// wave and come back as MFMA operands with the transposing read, tokens along
-// the contraction; U's rows of the same slab are the column operand of dX,
-// whose row operand, the slot's A over these columns, stays in LDS.  The
-// waves' sums are added in the order 0, 1, ..., 7.
+// sums in memory, no atomics.  Its NW waves take every NW-th 32-token chunk.
+//  * Lane L holds columns 8 (L % 8) of tokens 8 h + L / 8, h = 0..3: eight whole
+//    128-byte lines per instruction, for P, dX0 and dX alike, so that the
+//    dropout's words of X and of dX are drawn once.
+//  * P and the three bf16 planes of Q pass through a slab of LDS per wave and
+//    come back as MFMA operands with the transposing read, tokens along the
+//    contraction.  Their registers take the next chunk's loads as soon as they
+//    are in the slab.
+//  * U's rows of the slab are the column operand of dX, whose row operand, the
+//    slot's A over these columns, stays in LDS; the products leave through P's
+//    part of the slab (16-byte pieces of row i XOR-swizzled by i).
+//  * The waves' sums are added in the order 0, 1, ..., NW - 1.
 // Bound: HBM, X, dY and dX0 read once, dX and all slots' dA and dB written;
 // Q is read by every column slice, from L2.
 constexpr int kGradRanks = 64;
 constexpr int kGradSlice = 64;
-constexpr int kGradWaves = 8;
 
 struct BatchGradJob {
   const uint16_t* P;   // [M, cols] bf16
@@ -700,12 +710,39 @@ struct BatchGradArgs {
   float keep_scale;
 };
 
-template <int RT, bool DROP, bool DX>
-__global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g) {
+// Where a slab keeps 16-byte piece p of row `row` (rows of PPR pieces): XOR
+// swizzles that keep both reads of the slab free of bank conflicts, four rows
+// of two neighbouring pieces (transposing) and sixteen rows of one piece.  SW
+// off keeps the pieces in place: at 16 ranks the swizzles' addresses cost more
+// registers, and with them a second workgroup per CU, than the conflicts they
+// spare (2048 tokens, 4096 x 4096: 20.1 against 15.6 us).
+template <int PPR, bool SW>
+__device__ __forceinline__ int slab_piece(int row, int p) {
+  if (!SW) return p;
+  if (PPR == 2) return p ^ ((row >> 3) & 1);
+  if (PPR == 4) return p ^ ((row >> 2) & 3);
+  const int x = row >> 1;
+  return p ^ (((x & 1) << 1) | ((x >> 1) & 1) | (x & 4));
+}
+// 16 x 32 operand of a slab of 32 rows: lane (i, q4) gets column 16 band + i of
+// rows 8 q4 .. 8 q4 + 7.
+template <int PPR, bool SW>
+__device__ __forceinline__ bf16x8_t slab_operand(const uint16_t* slab, int band, int lane) {
+  const int i = lane & 15, row = 8 * (lane >> 4) + (i >> 2), p = 2 * band + ((i & 3) >> 1);
+  const v4s_t lo = lds_read_tr16(slab + 8 * (row * PPR + slab_piece<PPR, SW>(row, p)) + 4 * (i & 1));
+  const v4s_t hi =
+      lds_read_tr16(slab + 8 * ((row + 4) * PPR + slab_piece<PPR, SW>(row + 4, p)) + 4 * (i & 1));
+  const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+template <int RT, bool DROP, bool DX, int NW>
+__global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchGradArgs g) {
+  constexpr bool SW = RT > 1;
   constexpr int QW = 16 * RT;
   constexpr int PE = 32 * kGradSlice, CE = PE + 3 * 32 * QW;   // elements of a chunk
   constexpr int AW = 16 * RT + 8;                              // LDS row of a column of A
-  constexpr int SLAB = kGradWaves * CE * 2, RED = kGradWaves * 4 * RT * 64 * 16;
+  constexpr int SLAB = NW * CE * 2, RED = NW * 4 * RT * 64 * 16;
   __shared__ __attribute__((aligned(16))) char smem[SLAB > RED ? SLAB : RED];
   __shared__ __attribute__((aligned(16))) uint16_t as[DX ? kGradSlice * AW : 8];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -713,54 +750,90 @@ __global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g
   const int i = lane & 15, q4 = lane >> 4;
   const bool first = (int)blockIdx.x < g.a.slices;
   const BatchGradJob& job = first ? g.a : g.b;
-  const int64_t cols = job.cols;
-  const int64_t c0 = (int64_t)(first ? (int)blockIdx.x : (int)blockIdx.x - g.a.slices) * kGradSlice;
+  const int cols = (int)job.cols;
+  const int c0 = (first ? (int)blockIdx.x : (int)blockIdx.x - g.a.slices) * kGradSlice;
   const int M = g.M, r = g.r, slot = blockIdx.y;
   const int j0 = (int)blockIdx.z * kGradRanks;
   // The slot's range of the order, cut to M tokens whatever the plan holds.
   const int s0 = min(max(g.start[slot], 0), M), s1 = min(max(g.start[slot + 1], s0), M);
   const int nt = s1 - s0;
+  const int prow = lane >> 3, c = c0 + 8 * (lane & 7);   // this lane's columns
+  const uint32_t prowb = (uint32_t)cols * 2;
+  const __amdgpu_buffer_rsrc_t rx0 =
+      rsrc_whole(g.dX0, DX && g.dX0 ? (uint32_t)M * (uint32_t)g.a.cols * 2 : 0u);
+  const __amdgpu_buffer_rsrc_t rdx =
+      rsrc_whole(g.dX, DX ? (uint32_t)M * (uint32_t)g.a.cols * 2 : 0u);
+  const int nchunks = (nt + 31) / 32;
+  // Tokens of chunk ci (lane L: token L % 32), -1 past the slot's last.
+  auto tokens = [&](int ci) {
+    const int pos = ci * 32 + (lane & 31);
+    const int m = pos < nt ? g.order[s0 + pos] : -1;
+    return (unsigned)m < (unsigned)M ? m : -1;
+  };
+  // Byte offsets of this lane's four pieces of P (dX0, dX).
+  auto places = [&](int tok, uint32_t (&off)[4]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int m = __shfl(tok, 8 * h + prow);
+      off[h] = m >= 0 && c < cols ? (uint32_t)m * prowb + (uint32_t)c * 2 : kOOB;
+    }
+  };
   if (DX && slot == g.slots) {   // tokens without an adapter: dX = dX0
     if (!first || g.dX == g.dX0) return;
-    // Four pieces of a thread are on their way together.
-    const int n = nt * (kGradSlice / 8);
-    for (int e0 = tid; e0 < n; e0 += 4 * 64 * kGradWaves) {
-      int64_t o[4];
+    int tok = tokens(wave);
+    for (int ci = wave; ci < nchunks; ci += NW) {
+      uint32_t off[4];
       uint4 v[4];
+      places(tok, off);
+      tok = tokens(ci + NW);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = e0 + k * 64 * kGradWaves;
-        const int m = e < n ? g.order[s0 + e / (kGradSlice / 8)] : -1;
-        const int64_t c = c0 + 8 * (e % (kGradSlice / 8));
-        o[k] = (unsigned)m < (unsigned)M && c < cols ? (int64_t)m * cols + c : -1;
-      }
+      for (int h = 0; h < 4; ++h) v[h] = bload128s(rx0, off[h], 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (g.dX0 && o[k] >= 0) v[k] = *reinterpret_cast<const uint4*>(g.dX0 + o[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (o[k] >= 0) *reinterpret_cast<uint4*>(g.dX + o[k]) = v[k];
+      for (int h = 0; h < 4; ++h) bstore128(rdx, v[h], off[h]);
     }
     return;
   }
   const bool dx = DX && first, dropped = DROP && first;
-  const __amdgpu_buffer_rsrc_t rp = rsrc_whole(job.P, (uint32_t)((int64_t)M * cols * 2));
-  const __amdgpu_buffer_rsrc_t rq = rsrc_whole(job.Q, (uint32_t)((int64_t)M * r * 6));
+  const __amdgpu_buffer_rsrc_t rp = rsrc_whole(job.P, (uint32_t)M * prowb);
+  const __amdgpu_buffer_rsrc_t rq = rsrc_whole(job.Q, (uint32_t)M * (uint32_t)r * 6);
   const float c_a = g.scale[slot];
+
+  uint4 pv[4], qv[3][RT], xv[4];
+  uint32_t off[4], next[4];
+  auto load = [&](int tok) {
+    places(tok, next);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) pv[h] = bload128s(rp, next[h], 0);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int p = 64 * t + lane;              // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
+      const int m = __shfl(tok, p / (2 * RT));
+      const int j = j0 + 8 * (p % (2 * RT));
+      const uint32_t at = m >= 0 && j < r ? (uint32_t)(m * r + j) * 2 : kOOB;
+#pragma unroll
+      for (int z = 0; z < 3; ++z) qv[z][t] = bload128s(rq, at, (uint32_t)z * M * r * 2);
+    }
+  };
+  auto load_x = [&]() {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) xv[h] = bload128s(rx0, next[h], 0);
+  };
+  int tok = tokens(wave);
+  load(tok);
+  if (dx) load_x();
+  tok = tokens(wave + NW);
   if (dx && nt > 0) {   // as[column][rank] = A, transposed
     const uint16_t* const A = g.A + (int64_t)slot * r * cols;
-    for (int e = tid; e < QW * (kGradSlice / 8); e += 64 * kGradWaves) {
-      const int j = e / (kGradSlice / 8), c = 8 * (e % (kGradSlice / 8));
+    for (int e = tid; e < QW * (kGradSlice / 8); e += 64 * NW) {
+      const int j = e / (kGradSlice / 8), k0 = 8 * (e % (kGradSlice / 8));
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (j < r && c0 + c < cols) v = *reinterpret_cast<const uint4*>(A + j * cols + c0 + c);
+      if (j < r && c0 + k0 < cols) v = *reinterpret_cast<const uint4*>(A + (int64_t)j * cols + c0 + k0);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) as[(c + k) * AW + j] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+      for (int k = 0; k < 8; ++k) as[(k0 + k) * AW + j] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
     }
   }
-  __syncthreads();
+  if (DX) lds_barrier();
 
   uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * CE;
   f32x4_t acc[4][RT];
@@ -768,100 +841,58 @@ __global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g
   for (int h = 0; h < 4; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const float s = dropped ? c_a * g.keep_scale : c_a;
 
-  const int nchunks = (nt + 31) / 32;
-  for (int ci = wave; ci < nchunks; ci += kGradWaves) {
-    const int pos = ci * 32 + (lane & 31);
-    int tok = pos < nt ? g.order[s0 + pos] : -1;
-    if ((unsigned)tok >= (unsigned)M) tok = -1;
-    int mt[2];
-    uint4 pv[2][2], qv[3][RT], xv[2][2];
+  for (int ci = wave; ci < nchunks; ci += NW) {
+    uint32_t keep = 0;   // 8 bits per piece
 #pragma unroll
-    for (int tg = 0; tg < 2; ++tg) {
-      mt[tg] = __shfl(tok, 16 * tg + i);
+    for (int h = 0; h < 4; ++h) off[h] = next[h];
+    if (dropped) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t c = c0 + 32 * u + 8 * q4;
-        const bool ok = mt[tg] >= 0 && c < cols;
-        pv[tg][u] = bload128s(rp, ok ? (uint32_t)(((int64_t)mt[tg] * cols + c) * 2) : kOOB, 0);
+      for (int h = 0; h < 4; ++h)
+        if (off[h] != kOOB) keep |= philox_keep8(off[h] >> 1, g.drop) << (8 * h);
+    }
+    // A wave's LDS operations run in issue order: these stores land after the
+    // last chunk's reads.
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint4 v = pv[h];
+      if (dropped) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] &= ((keep >> (8 * h + 2 * e)) & 1u ? 0xffffu : 0u) |
+                  ((keep >> (8 * h + 2 * e + 1)) & 1u ? 0xffff0000u : 0u);
+        v = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      const int row = 8 * h + prow;
+      *reinterpret_cast<uint4*>(my + 8 * (8 * row + slab_piece<8, SW>(row, lane & 7))) = v;
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int p = 64 * t + lane;              // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
-      const int m = __shfl(tok, p / (2 * RT));
-      const int j = j0 + 8 * (p % (2 * RT));
-      const bool ok = m >= 0 && j < r;
+      const int row = (64 * t + lane) / (2 * RT);
+      const int at = 8 * (2 * RT * row + slab_piece<2 * RT, SW>(row, lane % (2 * RT)));
 #pragma unroll
-      for (int z = 0; z < 3; ++z)
-        qv[z][t] = bload128s(rq, ok ? (uint32_t)((((int64_t)z * M + m) * r + j) * 2) : kOOB, 0);
+      for (int z = 0; z < 3; ++z) *reinterpret_cast<uint4*>(my + PE + z * 32 * QW + at) = qv[z][t];
     }
-    if (dx) {
-#pragma unroll
-      for (int tg = 0; tg < 2; ++tg)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t c = c0 + 32 * u + 8 * q4;
-          xv[tg][u] = make_uint4(0, 0, 0, 0);
-          if (g.dX0 && mt[tg] >= 0 && c < cols)
-            xv[tg][u] = *reinterpret_cast<const uint4*>(g.dX0 + (int64_t)mt[tg] * cols + c);
-        }
-    }
-    uint32_t keep = 0;   // 8 bits per (tg, u)
-    if (dropped) {
-#pragma unroll
-      for (int tg = 0; tg < 2; ++tg)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          keep |= philox_keep8((uint64_t)((int64_t)max(mt[tg], 0) * cols + c0 + 32 * u + 8 * q4),
-                               g.drop) << (8 * (2 * tg + u));
-    }
-#pragma unroll
-    for (int tg = 0; tg < 2; ++tg)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint4 v = pv[tg][u];
-        if (dropped) {
-          const uint32_t k8 = keep >> (8 * (2 * tg + u));
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] &= ((k8 >> (2 * e)) & 1u ? 0xffffu : 0u) | ((k8 >> (2 * e + 1)) & 1u ? 0xffff0000u : 0u);
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4*>(my + (16 * tg + i) * kGradSlice + 32 * u + 8 * q4) = v;
-      }
-#pragma unroll
-    for (int z = 0; z < 3; ++z)
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        *reinterpret_cast<uint4*>(my + PE + z * 32 * QW + 8 * (64 * t + lane)) = qv[z][t];
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): one wave's LDS operations are in order
-    const int rr = 8 * q4 + (i >> 2), cc = 4 * (i & 3);
+    load(tok);
+    tok = tokens(ci + 2 * NW);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     bf16x8_t aop[4];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const v4s_t lo = lds_read_tr16(my + rr * kGradSlice + 16 * h + cc);
-      const v4s_t hi = lds_read_tr16(my + (rr + 4) * kGradSlice + 16 * h + cc);
-      const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      aop[h] = __builtin_bit_cast(bf16x8_t, v);
-    }
+    for (int h = 0; h < 4; ++h) aop[h] = slab_operand<8, SW>(my, h, lane);
 #pragma unroll
     for (int z = 2; z >= 0; --z)          // the small terms first
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const uint16_t* const qs = my + PE + z * 32 * QW + 16 * t + cc;
-        const v4s_t lo = lds_read_tr16(qs + rr * QW);
-        const v4s_t hi = lds_read_tr16(qs + (rr + 4) * QW);
-        const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        const bf16x8_t bop = __builtin_bit_cast(bf16x8_t, v);
+        const bf16x8_t bop = slab_operand<2 * RT, SW>(my + PE + z * 32 * QW, t, lane);
 #pragma unroll
         for (int h = 0; h < 4; ++h) acc[h][t] = mfma_16x16x32(aop[h], bop, acc[h][t]);
       }
     if (dx) {
-      // dX[m][c]: row operand A's column 32 u + 8 (i / 4) + 4 jj + i % 4, ranks
-      // 16 ch + 8 (q4 & 1) ..; column operand U's token 16 tg + i, the hi terms
-      // (q4 < 2) and the mid terms of the same ranks.
+      // dX[m][c]: row operand A's column 16 k + i, ranks 16 ch + 8 (q4 & 1) ..;
+      // column operand U's token 16 tg + i, the hi terms (q4 < 2) and the mid
+      // terms of the same ranks.
       f32x4_t d[2][4];
 #pragma unroll
       for (int tg = 0; tg < 2; ++tg)
@@ -873,71 +904,75 @@ __global__ void __launch_bounds__(64 * kGradWaves) k_batch_grads(BatchGradArgs g
 #pragma unroll
         for (int tg = 0; tg < 2; ++tg)
           uop[tg] = *reinterpret_cast<const bf16x8_t*>(
-              my + PE + (q4 >> 1) * 32 * QW + (16 * tg + i) * QW + 16 * ch + 8 * (q4 & 1));
+              my + PE + (q4 >> 1) * 32 * QW +
+              8 * (2 * RT * (16 * tg + i) + slab_piece<2 * RT, SW>(16 * tg + i, 2 * ch + (q4 & 1))));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int c = 32 * (k >> 1) + 8 * (i >> 2) + 4 * (k & 1) + (i & 3);
           const bf16x8_t wop =
-              *reinterpret_cast<const bf16x8_t*>(as + c * AW + 16 * ch + 8 * (q4 & 1));
+              *reinterpret_cast<const bf16x8_t*>(as + (16 * k + i) * AW + 16 * ch + 8 * (q4 & 1));
 #pragma unroll
           for (int tg = 0; tg < 2; ++tg) d[tg][k] = mfma_16x16x32(wop, uop[tg], d[tg][k]);
         }
       }
-      const float s = DROP ? c_a * g.keep_scale : c_a;
+      float* const e = reinterpret_cast<float*>(my);   // P's part: 16 rows of 64 floats
 #pragma unroll
-      for (int tg = 0; tg < 2; ++tg)
+      for (int tg = 0; tg < 2; ++tg) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t c = c0 + 32 * u + 8 * q4;
-          if (mt[tg] < 0 || c >= cols) continue;
-          const uint32_t bw[4] = {xv[tg][u].x, xv[tg][u].y, xv[tg][u].z, xv[tg][u].w};
-          const uint32_t k8 = keep >> (8 * (2 * tg + u));
-          float v[8];
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<f32x4_t*>(e + 64 * i + 4 * ((4 * k + q4) ^ i)) = d[tg][k];
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = s * d[tg][2 * u + (e >> 2)][e & 3];
-            if (DROP) v[e] = (k8 >> e) & 1u ? v[e] : 0.0f;
+        for (int hh = 0; hh < 2; ++hh) {
+          const int h = 2 * tg + hh, row = 8 * hh + prow, pp = 2 * (lane & 7);
+          const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(e + 64 * row + 4 * (pp ^ row));
+          const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(e + 64 * row + 4 * ((pp + 1) ^ row));
+          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            v[k] *= s;
+            if (DROP) v[k] = (keep >> (8 * h + k)) & 1u ? v[k] : 0.0f;
           }
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(bf16_to_f32(bw[e] & 0xffffu) + v[2 * e],
-                               bf16_to_f32(bw[e] >> 16) + v[2 * e + 1]);
-          *reinterpret_cast<uint4*>(g.dX + (int64_t)mt[tg] * cols + c) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          const uint4 b = xv[h];
+          uint4 w;
+          w.x = pack_bf16x2(bf16_to_f32(b.x & 0xffffu) + v[0], bf16_to_f32(b.x >> 16) + v[1]);
+          w.y = pack_bf16x2(bf16_to_f32(b.y & 0xffffu) + v[2], bf16_to_f32(b.y >> 16) + v[3]);
+          w.z = pack_bf16x2(bf16_to_f32(b.z & 0xffffu) + v[4], bf16_to_f32(b.z >> 16) + v[5]);
+          w.w = pack_bf16x2(bf16_to_f32(b.w & 0xffffu) + v[6], bf16_to_f32(b.w >> 16) + v[7]);
+          bstore128(rdx, w, off[h]);
         }
+      }
+      load_x();
     }
   }
 
   // acc[h][t][v] = O[c0 + 16 h + 4 q4 + v][j0 + 16 t + i]; the unit (h, t) is
-  // added by wave (h RT + t) mod 8.
-  __syncthreads();   // the slabs are free
+  // added by wave (h RT + t) mod NW.
+  lds_barrier();   // the slabs are free
   f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem);
 #pragma unroll
   for (int h = 0; h < 4; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) red[(wave * 4 * RT + h * RT + t) * 64 + lane] = acc[h][t];
-  __syncthreads();
-  const float s = dropped ? c_a * g.keep_scale : c_a;
+  lds_barrier();
   float* const out = job.out + (int64_t)slot * cols * r;
-  for (int unit = wave; unit < 4 * RT; unit += kGradWaves) {
+  for (int unit = wave; unit < 4 * RT; unit += NW) {
     f32x4_t v = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kGradWaves; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const f32x4_t o = red[(w * 4 * RT + unit) * 64 + lane];
       v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
     }
-    const int64_t c = c0 + 16 * (unit / RT) + 4 * q4;   // c .. c + 3 (cols is a multiple of 8)
+    const int cc = c0 + 16 * (unit / RT) + 4 * q4;   // cc .. cc + 3 (cols is a multiple of 8)
     const int j = j0 + 16 * (unit % RT) + i;
-    if (c >= cols || j >= r) continue;
+    if (cc >= cols || j >= r) continue;
     // A slot without tokens has no products: plain zeros, whatever its scale.
     const f32x4_t res = nt > 0 ? f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]}
                                : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     if (job.trans) {
-      *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + c) = res;
+      *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + cc) = res;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[(c + e) * r + j] = res[e];
+      for (int e = 0; e < 4; ++e) out[(int64_t)(cc + e) * r + j] = res[e];
     }
   }
 }
@@ -1054,7 +1089,10 @@ template <int RT, bool DROP, bool DX>
 static void grads(const BatchGradArgs& g, hipStream_t st) {
   const dim3 grid((unsigned)(g.a.slices + g.b.slices), (unsigned)(g.slots + (DX ? 1 : 0)),
                   (unsigned)((g.r + kGradRanks - 1) / kGradRanks));
-  hipLaunchKernelGGL((k_batch_grads<RT, DROP, DX>), grid, dim3(64 * kGradWaves), 0, st, g);
+  // Eight waves per workgroup, two workgroups a CU; four where the planes of
+  // 64 ranks fill the LDS.
+  constexpr int NW = RT == 4 ? 4 : 8;
+  hipLaunchKernelGGL((k_batch_grads<RT, DROP, DX, NW>), grid, dim3(64 * NW), 0, st, g);
 }
 template <bool DROP, bool DX>
 static void grads_rt(const BatchGradArgs& g, hipStream_t st) {
