@@ -90,16 +90,25 @@ struct DownArgs {
   float keep_scale;
 };
 
+// Token groups of 16 per workgroup: 64 tokens, or 32 where the sums and operands
+// of 64 ranks and the slab leave no room for a second wave per SIMD (U at rank
+// 64, 4096 x 11008: 62 against 39 us).
+template <bool WT, int RT>
+constexpr int down_groups() { return WT && RT == 4 ? 2 : 4; }
+
 template <bool WT, bool DROP, int RT>
-__global__ void __launch_bounds__(64 * kDownWaves) k_batch_down(DownArgs g) {
+__global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_batch_down(DownArgs g) {
+  constexpr int TG = down_groups<WT, RT>(), SUBS = 4 / TG;
   constexpr int SW = 16 * RT + 8;   // WT: row of a wave's 64 (c) x 16 RT (j) slab, padded
-  constexpr int SLAB = WT ? kDownWaves * 64 * SW * 2 : 16, RED = 4 * 3 * RT * 64 * 16;
+  constexpr int SLAB = WT ? kDownWaves * 64 * SW * 2 : 16, RED = TG * 3 * RT * 64 * 16;
   __shared__ __attribute__((aligned(16))) char smem[SLAB > RED ? SLAB : RED];
   __shared__ int rows[kPlanTile];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15, grp = lane >> 4;
-  const TileRow t = tile_row(g.tiles, blockIdx.y, g.M, g.slots);
+  TileRow t = tile_row(g.tiles, (int)blockIdx.y / SUBS, g.M, g.slots);
+  t.first += (int)blockIdx.y % SUBS * 16 * TG;
+  t.count = min(t.count - (int)blockIdx.y % SUBS * 16 * TG, 16 * TG);
   if (t.count <= 0 || t.slot < 0) return;
   if (tid < kPlanTile) {
     const int m = tid < t.count ? g.order[t.first + tid] : -1;
@@ -115,112 +124,145 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_batch_down(DownArgs g) {
   // Byte offsets of a lane's pieces at step 0; a step adds 128 bytes (WT: 64
   // rows of B) through the scalar offset.  Lane (row, grp) holds the 16
   // contiguous indices 16 grp .. +15 of the step, MFMA h takes 16 grp + 8 h ..
-  // +7, the same permutation for both operands.
+  // +7, the same permutation for both operands.  WT: piece 64 q + lane of the
+  // step's 64 x 16 RT part of B, row by row.
   const __amdgpu_buffer_rsrc_t rs = rsrc_whole(g.S, (uint32_t)((int64_t)g.M * C * 2));
   const __amdgpu_buffer_rsrc_t rw =
       rsrc_whole(g.W + (int64_t)t.slot * C * r, (uint32_t)((int64_t)C * r * 2));
-  uint32_t xoff[4], woff[2 * RT];
+  constexpr int PR = 2 * RT;              // WT: pieces per row
+  uint32_t xoff[TG];
 #pragma unroll
-  for (int tg = 0; tg < 4; ++tg) {
+  for (int tg = 0; tg < TG; ++tg) {
     const int m = rows[16 * tg + row];
     xoff[tg] = m >= 0 ? (uint32_t)(((int64_t)m * C + 16 * grp) * 2) : kOOB;
   }
+  const uint32_t woff = WT ? (uint32_t)((lane / PR) * r + j0 + 8 * (lane % PR)) * 2
+                           : (uint32_t)(((int64_t)(j0 + row) * C + 16 * grp) * 2);
+  const bool wok = j0 + 8 * (lane % PR) < r;   // WT: the lane's ranks are
+  f32x4_t acc[TG][RT];
 #pragma unroll
-  for (int q = 0; q < 2 * RT; ++q) {
-    if (!WT) {
-      const int j = j0 + 16 * (q >> 1) + row;
-      woff[q] = j < r ? (uint32_t)(((int64_t)j * C + 16 * grp + 8 * (q & 1)) * 2) : kOOB;
-    } else {
-      const int p = 64 * q + lane;          // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
-      const int j = j0 + 8 * (p % (2 * RT));
-      woff[q] = j < r ? (uint32_t)(((p / (2 * RT)) * r + j) * 2) : kOOB;
-    }
-  }
-  f32x4_t acc[4][RT];
-#pragma unroll
-  for (int tg = 0; tg < 4; ++tg)
+  for (int tg = 0; tg < TG; ++tg)
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[tg][q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto load = [&](int st, uint4 (&xv)[4][2], uint4 (&wv)[2 * RT]) {
-    const uint32_t ss = (uint32_t)__builtin_amdgcn_readfirstlane(st);
-    const int left = C - 64 * st;           // indices of this step inside the operand
-#pragma unroll
-    for (int q = 0; q < 2 * RT; ++q) {
-      const int at = WT ? (64 * q + lane) / (2 * RT) : 16 * grp + 8 * (q & 1);
-      wv[q] = bload128s(rw, at < left ? woff[q] : kOOB, WT ? ss * 128u * (uint32_t)r : ss * 128u);
-    }
-#pragma unroll
-    for (int tg = 0; tg < 4; ++tg) {
-      if (tg >= ntg) break;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        xv[tg][h] = bload128s(
-            rs, xoff[tg] != kOOB && 16 * grp + 8 * h < left ? xoff[tg] + 16 * h : kOOB, ss * 128u);
-    }
-  };
   uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + (WT ? wave * 64 * SW : 0);
-  auto mul = [&](int st, uint4 (&xv)[4][2], const uint4 (&wv)[2 * RT]) {
-    bf16x8_t wop[RT][2];
-    if constexpr (!WT) {
-#pragma unroll
-      for (int q = 0; q < 2 * RT; ++q) wop[q >> 1][q & 1] = __builtin_bit_cast(bf16x8_t, wv[q]);
-    } else {
-      // A wave's LDS operations run in issue order: the stores are complete
-      // before the reads, which complete before the next stores.
+  // The wave's steps for NTG token groups (1, or TG with those past the tile at
+  // kOOB).  Loads are issued whether or not there is a step, so that the count
+  // of those in flight is the same on every path: a wait for one step's leaves
+  // the next step's alone.
+  auto steps = [&](auto ntgs) {
+    constexpr int NTG = decltype(ntgs)::value;
+    auto load_w = [&](int st, uint4 (&wv)[2 * RT]) {
+      const int sc = __builtin_amdgcn_readfirstlane(st < s1 ? st : s0);
+      const uint32_t ss = (uint32_t)sc;
+      const int left = st < s1 ? C - 64 * sc : 0;   // indices of this step inside the operand
 #pragma unroll
       for (int q = 0; q < 2 * RT; ++q) {
-        const int p = 64 * q + lane;
-        *reinterpret_cast<uint4*>(my + (p / (2 * RT)) * SW + 8 * (p % (2 * RT))) = wv[q];
+        if constexpr (WT) {
+          const int at = q * (64 / PR) + lane / PR;
+          // rows past the operand: keep the scalar offset inside it
+          const uint32_t so = q * (64 / PR) < left ? (ss * 64 + q * (64 / PR)) * 2 * (uint32_t)r : 0u;
+          wv[q] = bload128s(rw, wok && at < left ? woff : kOOB, so);
+        } else {
+          const int j = j0 + 16 * (q >> 1);
+          const uint32_t so = j < r ? ss * 128u + (uint32_t)(32 * (q >> 1)) * (uint32_t)C : 0u;
+          wv[q] = bload128s(
+              rw, j + row < r && 16 * grp + 8 * (q & 1) < left ? woff + 16 * (q & 1) : kOOB, so);
+        }
       }
-      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    };
+    auto load_x = [&](int st, uint4 (&xv)[NTG][2]) {
+      const int sc = __builtin_amdgcn_readfirstlane(st < s1 ? st : s0);
+      const int left = st < s1 ? C - 64 * sc : 0;
 #pragma unroll
-      for (int q = 0; q < RT; ++q)
+      for (int tg = 0; tg < NTG; ++tg)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          xv[tg][h] = bload128s(
+              rs, xoff[tg] != kOOB && 16 * grp + 8 * h < left ? xoff[tg] + 16 * h : kOOB,
+              (uint32_t)sc * 128u);
+    };
+    // The products of step st; W's registers take the next step's loads as soon
+    // as they are free, X's are two sets.
+    auto mul = [&](int st, uint4 (&xv)[NTG][2], uint4 (&xn)[NTG][2], uint4 (&wv)[2 * RT]) {
+      if constexpr (DROP) {
+#pragma unroll
+        for (int tg = 0; tg < NTG; ++tg) {
+          if (NTG > 1 && tg >= ntg) break;
+          const uint32_t m = (uint32_t)max(rows[16 * tg + row], 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            xv[tg][h] = philox_drop8(
+                xv[tg][h], (uint64_t)m * (uint32_t)C + (uint32_t)(64 * st + 16 * grp + 8 * h), g.drop);
+        }
+      }
+      if constexpr (WT) {
+        // A wave's LDS operations run in issue order: the stores are complete
+        // before the reads, which complete before the next stores.
+#pragma unroll
+        for (int q = 0; q < 2 * RT; ++q)
+          *reinterpret_cast<uint4*>(my + (q * (64 / PR) + lane / PR) * SW + 8 * (lane % PR)) = wv[q];
+        load_w(st + kDownWaves, wv);
+        load_x(st + kDownWaves, xn);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+      }
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        bf16x8_t wop[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint16_t* p = my + (16 * grp + 8 * h + (row >> 2)) * SW + 16 * q + 4 * (row & 3);
-          const v4s_t lo = lds_read_tr16(p);
-          const v4s_t hi = lds_read_tr16(p + 4 * SW);
-          const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          wop[q][h] = __builtin_bit_cast(bf16x8_t, v);
-        }
-    }
-#pragma unroll
-    for (int tg = 0; tg < 4; ++tg) {
-      if (tg >= ntg) break;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 x = xv[tg][h];
-        if constexpr (DROP) {
-          const uint32_t m = (uint32_t)max(rows[16 * tg + row], 0);
-          x = philox_drop8(x, (uint64_t)m * (uint32_t)C + (uint32_t)(64 * st + 16 * grp + 8 * h),
-                           g.drop);
+          if constexpr (!WT) {
+            wop[h] = __builtin_bit_cast(bf16x8_t, wv[2 * q + h]);
+          } else {
+            const uint16_t* p = my + (16 * grp + 8 * h + (row >> 2)) * SW + 16 * q + 4 * (row & 3);
+            const v4s_t lo = lds_read_tr16(p);
+            const v4s_t hi = lds_read_tr16(p + 4 * SW);
+            const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            wop[h] = __builtin_bit_cast(bf16x8_t, v);
+          }
         }
 #pragma unroll
-        for (int q = 0; q < RT; ++q)
-          acc[tg][q] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, x), wop[q][h], acc[tg][q]);
+        for (int tg = 0; tg < NTG; ++tg) {
+          if (NTG > 1 && tg >= ntg) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[tg][q] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xv[tg][h]), wop[h], acc[tg][q]);
+        }
+        if (WT && RT == 4) __builtin_amdgcn_sched_barrier(0);   // one q's operands at a time
       }
+    };
+    uint4 xa[NTG][2], xb[NTG][2], wa[2 * RT];
+    [[maybe_unused]] uint4 wb[2 * RT];
+    int st = s0 + wave;
+    load_w(st, wa);
+    load_x(st, xa);
+    while (st < s1) {
+      if constexpr (!WT) {
+        load_w(st + kDownWaves, wb);
+        load_x(st + kDownWaves, xb);
+      }
+      mul(st, xa, xb, wa);
+      st += kDownWaves;
+      if (st >= s1) break;
+      if constexpr (!WT) {
+        load_w(st + kDownWaves, wa);
+        load_x(st + kDownWaves, xa);
+        mul(st, xb, xa, wb);
+      } else {
+        mul(st, xb, xa, wa);
+      }
+      st += kDownWaves;
     }
   };
-  {
-    uint4 xa[4][2], xb[4][2], wa[2 * RT], wb[2 * RT];
-    int st = s0 + wave;
-    if (st < s1) load(st, xa, wa);
-    for (; st < s1; st += 2 * kDownWaves) {
-      const bool two = st + kDownWaves < s1;
-      if (two) load(st + kDownWaves, xb, wb);
-      mul(st, xa, wa);
-      if (st + 2 * kDownWaves < s1) load(st + 2 * kDownWaves, xa, wa);
-      if (two) mul(st + kDownWaves, xb, wb);
-    }
-  }
+  if (ntg == 1) steps(std::integral_constant<int, 1>());
+  else steps(std::integral_constant<int, TG>());
 
   // acc[tg][q][v]: token 16 tg + 4 grp + v, rank j0 + 16 q + row.  Wave w adds
   // the four waves' sums of token group w in the order 0, 1, 2, 3.
   f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem);
   if (WT) __syncthreads();   // the slabs are free
 #pragma unroll
-  for (int tg = 0; tg < 4; ++tg) {
+  for (int tg = 0; tg < TG; ++tg) {
     if (tg >= ntg || tg == wave) continue;
 #pragma unroll
     for (int q = 0; q < RT; ++q)
@@ -229,7 +271,7 @@ __global__ void __launch_bounds__(64 * kDownWaves) k_batch_down(DownArgs g) {
   __syncthreads();
   float* const out = g.part + (int64_t)z * g.M * r;
 #pragma unroll
-  for (int tg = 0; tg < 4; ++tg) {
+  for (int tg = 0; tg < TG; ++tg) {
     if (tg >= ntg || tg != wave) continue;
     int mo[4];
 #pragma unroll
@@ -264,9 +306,14 @@ __global__ void __launch_bounds__(256) k_batch_split(SplitJob ju, SplitJob jt, i
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int z = 0; z < j.slices; ++z) {
-    const float4 p = reinterpret_cast<const float4*>(j.part)[z * n4 + i];
-    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+  for (int z = 0; z < j.slices; z += 8) {   // eight loads at a time
+    float4 p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      p[k] = reinterpret_cast<const float4*>(j.part)[min(z + k, j.slices - 1) * n4 + i];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (z + k < j.slices) { v.x += p[k].x; v.y += p[k].y; v.z += p[k].z; v.w += p[k].w; }
   }
   const float e[4] = {v.x, v.y, v.z, v.w};
   uint16_t t[3][4];
@@ -541,20 +588,20 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
     load_b(cb, ba);
     load_w(cb, 0, wv);
   }
-  // t of the tile: its slices added in order, four loads at a time.
+  // t of the tile: its slices added in order, eight loads at a time.
   for (int e = tid; e < kPlanTile * NS * RK / 4; e += 64 * kUpWaves) {
     const int tok = e / (NS * RK / 4), j = 4 * (e % (NS * RK / 4));
     const int m = rows[tok];
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (m >= 0 && j < r) {
       const int64_t at = (int64_t)m * r + j, plane = (int64_t)g.M * r;
-      for (int z = 0; z < g.slices; z += 4) {
-        float4 p[4];
+      for (int z = 0; z < g.slices; z += 8) {
+        float4 p[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           p[k] = *reinterpret_cast<const float4*>(g.part + min(z + k, g.slices - 1) * plane + at);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (z + k < g.slices) { v.x += p[k].x; v.y += p[k].y; v.z += p[k].z; v.w += p[k].w; }
       }
       if (g.t_out && blockIdx.x == 0) *reinterpret_cast<float4*>(g.t_out + at) = v;
@@ -736,22 +783,29 @@ __device__ __forceinline__ bf16x8_t slab_operand(const uint16_t* slab, int band,
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+template <int RT, int NW>
+struct GradShape {
+  static constexpr int QW = 16 * RT;
+  static constexpr int PE = 32 * kGradSlice, CE = PE + 3 * 32 * QW;   // elements of a chunk
+  static constexpr int AW = 16 * RT + 8;                              // LDS row of a column of A
+  static constexpr int SLAB = NW * CE * 2, RED = NW * 4 * RT * 64 * 16;
+  static constexpr int SMEM = SLAB > RED ? SLAB : RED;
+};
+
+// One workgroup's share of dA (and, DX, of dX) or of dB: `sl` is its slice.
+// Which of the two is fixed at compile time, so that the count of loads and
+// stores in flight is the same on every path of the loop.
 template <int RT, bool DROP, bool DX, int NW>
-__global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchGradArgs g) {
+__device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchGradJob& job, int sl,
+                                            char* smem, uint16_t* as) {
+  using Sh = GradShape<RT, NW>;
   constexpr bool SW = RT > 1;
-  constexpr int QW = 16 * RT;
-  constexpr int PE = 32 * kGradSlice, CE = PE + 3 * 32 * QW;   // elements of a chunk
-  constexpr int AW = 16 * RT + 8;                              // LDS row of a column of A
-  constexpr int SLAB = NW * CE * 2, RED = NW * 4 * RT * 64 * 16;
-  __shared__ __attribute__((aligned(16))) char smem[SLAB > RED ? SLAB : RED];
-  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? kGradSlice * AW : 8];
+  constexpr int QW = Sh::QW, PE = Sh::PE, CE = Sh::CE, AW = Sh::AW;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, q4 = lane >> 4;
-  const bool first = (int)blockIdx.x < g.a.slices;
-  const BatchGradJob& job = first ? g.a : g.b;
   const int cols = (int)job.cols;
-  const int c0 = (first ? (int)blockIdx.x : (int)blockIdx.x - g.a.slices) * kGradSlice;
+  const int c0 = sl * kGradSlice;
   const int M = g.M, r = g.r, slot = blockIdx.y;
   const int j0 = (int)blockIdx.z * kGradRanks;
   // The slot's range of the order, cut to M tokens whatever the plan holds.
@@ -760,9 +814,9 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
   const int prow = lane >> 3, c = c0 + 8 * (lane & 7);   // this lane's columns
   const uint32_t prowb = (uint32_t)cols * 2;
   const __amdgpu_buffer_rsrc_t rx0 =
-      rsrc_whole(g.dX0, DX && g.dX0 ? (uint32_t)M * (uint32_t)g.a.cols * 2 : 0u);
+      rsrc_whole(g.dX0, DX && g.dX0 ? (uint32_t)M * prowb : 0u);
   const __amdgpu_buffer_rsrc_t rdx =
-      rsrc_whole(g.dX, DX ? (uint32_t)M * (uint32_t)g.a.cols * 2 : 0u);
+      rsrc_whole(g.dX, DX ? (uint32_t)M * prowb : 0u);
   const int nchunks = (nt + 31) / 32;
   // Tokens of chunk ci (lane L: token L % 32), -1 past the slot's last.
   auto tokens = [&](int ci) {
@@ -779,7 +833,7 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
     }
   };
   if (DX && slot == g.slots) {   // tokens without an adapter: dX = dX0
-    if (!first || g.dX == g.dX0) return;
+    if (g.dX == g.dX0) return;
     int tok = tokens(wave);
     for (int ci = wave; ci < nchunks; ci += NW) {
       uint32_t off[4];
@@ -793,7 +847,6 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
     }
     return;
   }
-  const bool dx = DX && first, dropped = DROP && first;
   const __amdgpu_buffer_rsrc_t rp = rsrc_whole(job.P, (uint32_t)M * prowb);
   const __amdgpu_buffer_rsrc_t rq = rsrc_whole(job.Q, (uint32_t)M * (uint32_t)r * 6);
   const float c_a = g.scale[slot];
@@ -820,9 +873,9 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
   };
   int tok = tokens(wave);
   load(tok);
-  if (dx) load_x();
+  if constexpr (DX) load_x();
   tok = tokens(wave + NW);
-  if (dx && nt > 0) {   // as[column][rank] = A, transposed
+  if (DX && nt > 0) {   // as[column][rank] = A, transposed
     const uint16_t* const A = g.A + (int64_t)slot * r * cols;
     for (int e = tid; e < QW * (kGradSlice / 8); e += 64 * NW) {
       const int j = e / (kGradSlice / 8), k0 = 8 * (e % (kGradSlice / 8));
@@ -841,13 +894,13 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
   for (int h = 0; h < 4; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const float s = dropped ? c_a * g.keep_scale : c_a;
+  const float s = DROP ? c_a * g.keep_scale : c_a;
 
   for (int ci = wave; ci < nchunks; ci += NW) {
     uint32_t keep = 0;   // 8 bits per piece
 #pragma unroll
     for (int h = 0; h < 4; ++h) off[h] = next[h];
-    if (dropped) {
+    if constexpr (DROP) {
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         if (off[h] != kOOB) keep |= philox_keep8(off[h] >> 1, g.drop) << (8 * h);
@@ -857,7 +910,7 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       uint4 v = pv[h];
-      if (dropped) {
+      if constexpr (DROP) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -889,7 +942,7 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
 #pragma unroll
         for (int h = 0; h < 4; ++h) acc[h][t] = mfma_16x16x32(aop[h], bop, acc[h][t]);
       }
-    if (dx) {
+    if constexpr (DX) {
       // dX[m][c]: row operand A's column 16 k + i, ranks 16 ch + 8 (q4 & 1) ..;
       // column operand U's token 16 tg + i, the hi terms (q4 < 2) and the mid
       // terms of the same ranks.
@@ -977,6 +1030,17 @@ __global__ void __launch_bounds__(64 * NW, RT == 1 ? 4 : 2) k_batch_grads(BatchG
   }
 }
 
+template <int RT, bool DROP, bool DX, int NW>
+__global__ void __launch_bounds__(64 * NW, RT == 1 ? 3 : 2) k_batch_grads(BatchGradArgs g) {
+  using Sh = GradShape<RT, NW>;
+  __shared__ __attribute__((aligned(16))) char smem[Sh::SMEM];
+  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? kGradSlice * Sh::AW : 8];
+  if ((int)blockIdx.x < g.a.slices)
+    grads_block<RT, DROP, DX, NW>(g, g.a, blockIdx.x, smem, as);
+  else if ((int)blockIdx.y < g.slots)   // the last row is dX's alone
+    grads_block<RT, false, false, NW>(g, g.b, (int)blockIdx.x - g.a.slices, smem, as);
+}
+
 // ------------------------------- launchers ---------------------------------
 
 static inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -993,15 +1057,18 @@ static int64_t expected_tiles(int64_t M, int S) {
 }
 
 // Steps per slice of the down projections' contraction: slices that give about
-// two workgroups per CU, at most kMaxSlices (their sums are read back).
+// two workgroups per CU, at most kMaxSlices (their sums are read back), and a
+// power of two: the slice is the fast grid index, so that an XCD then always
+// meets the same slices and reads only their part of the adapters (4096
+// tokens, 4096 x 11008, rank 64: seven slices 33 us, eight XXX).
 constexpr int kMaxSlices = 16;
+constexpr int kDownGroups = 2;
 static int down_zlen(int64_t M, int S, int64_t C) {
   const int64_t steps = (C + 63) / 64;
-  int64_t want = 2 * kCUs / expected_tiles(M, S);
-  if (want < 1) want = 1;
-  if (want > kMaxSlices) want = kMaxSlices;
-  const int64_t per = (steps + want * kDownWaves - 1) / (want * kDownWaves);   // steps per wave
-  return (int)(per * kDownWaves);
+  const int64_t want = kDownGroups * kCUs / expected_tiles(M, S);
+  int64_t z = 1;
+  while (2 * z <= want && 2 * z <= kMaxSlices && 2 * z * kDownWaves <= steps) z *= 2;
+  return (int)((steps + z - 1) / z);
 }
 static int down_slices(int64_t M, int S, int64_t C) {
   const int64_t steps = (C + 63) / 64;
@@ -1026,8 +1093,9 @@ BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bo
 template <bool WT, bool DROP>
 static hipError_t down(DownArgs g, hipStream_t st) {
   g.zlen = down_zlen(g.M, g.slots, g.C);
+  const unsigned subs = 4 / (g.r <= 32 ? down_groups<WT, 1>() : down_groups<WT, 4>());
   const dim3 grid((unsigned)down_slices(g.M, g.slots, g.C),
-                  (unsigned)adapter_plan_tiles(g.M, g.slots), (unsigned)((g.r + 63) / 64));
+                  subs * (unsigned)adapter_plan_tiles(g.M, g.slots), (unsigned)((g.r + 63) / 64));
   const dim3 block(64 * kDownWaves);
   if (g.r <= 16) hipLaunchKernelGGL((k_batch_down<WT, DROP, 1>), grid, block, 0, st, g);
   else if (g.r <= 32) hipLaunchKernelGGL((k_batch_down<WT, DROP, 2>), grid, block, 0, st, g);
@@ -1044,9 +1112,11 @@ static hipError_t up(const UpArgs& g, hipStream_t st) {
   const int64_t blocks = (g.cols + kUpCols - 1) / kUpCols;
   const int64_t tiles = expected_tiles(g.M, g.slots);
   int64_t gx = (g.M <= 16 * tiles ? 2 : 4) * kCUs / tiles;
-  if (gx >= kXCDs) gx -= gx % kXCDs;
   if (gx < 1) gx = 1;
   if (gx > blocks) gx = blocks;
+  const int64_t per = (blocks + gx - 1) / gx;   // the same number of blocks for each
+  gx = (blocks + per - 1) / per;
+  if (gx >= kXCDs) gx -= gx % kXCDs;
   const dim3 grid((unsigned)gx, (unsigned)adapter_plan_tiles(g.M, g.slots));
   const dim3 block(64 * kUpWaves);
   if constexpr (WT) {

@@ -19,7 +19,7 @@ constexpr int64_t kMaxBufferBytes = (int64_t)1 << 31;
 
 constexpr int kMaxRank = 256;
 constexpr int64_t kMaxBatchDim = (int64_t)1 << 23;   // batched adapters' K and N
-constexpr int64_t kMaxGridRows = 65535;
+constexpr int64_t kMaxTiles = 65535 / 2;   // up to two grid rows each
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -263,7 +263,7 @@ int check_batch_sizes(int64_t M, int64_t K, int64_t N, int r, int S) {
   // tiles of the plan and slots are grid rows
   if (M * K * 2 >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes ||
       (int64_t)r * K * 2 >= kMaxBufferBytes || (int64_t)r * N * 2 >= kMaxBufferBytes ||
-      M * r * 6 >= kMaxBufferBytes || qlk::adapter_plan_tiles(M, S) > kMaxGridRows)
+      M * r * 6 >= kMaxBufferBytes || qlk::adapter_plan_tiles(M, S) > kMaxTiles)
     return QLORA_ERR_SHAPE;
   return QLORA_OK;
 }
