@@ -293,36 +293,98 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
   }
 }
 
-// The sum of the slices of part ([slices][M, r]) and its bf16 terms, for the
-// gradients: four elements per thread, U and T in one launch (two halves of
-// the grid).  Rows without an adapter hold nothing and are not read.
-struct SplitJob {
+// ---------------------------------------------------------------------------
+// U and T as MFMA operands of the gradients' kernel: the slices of part are
+// added, split into three bf16 terms (planes) and written so that a wave loads
+// each operand as 1 KB in a row, lane after lane, with nothing to gather or
+// transpose:
+//   cols  [chunk][plane][rank tile][lane][8]: rank 16 t + i of tokens 8 g ..
+//         8 g + 7 of the chunk, lane = 16 g + i (tokens along the contraction)
+//   rows  [chunk][token group][rank tile][lane][8]: token 16 tg + i, ranks
+//         16 t + 8 (g & 1) .. +7 of plane g / 2 (ranks along the contraction)
+// A chunk is 32 positions of the order of one slot; slot s begins at chunk
+// start[s] / 32 + s.  Ranks past r and tokens past the slot's last are zeros.
+// One workgroup per tile of the plan (two chunks), U or T, and 64 ranks.
+struct PackJob {
   const float* part;
   int slices;
-  uint16_t* planes;   // [3][M, r]
+  uint16_t* cols;
+  uint16_t* rows;     // null: not wanted
 };
-__global__ void __launch_bounds__(256) k_batch_split(SplitJob ju, SplitJob jt, int64_t n4) {
-  const SplitJob& j = blockIdx.y ? jt : ju;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int z = 0; z < j.slices; z += 8) {   // eight loads at a time
-    float4 p[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      p[k] = reinterpret_cast<const float4*>(j.part)[min(z + k, j.slices - 1) * n4 + i];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (z + k < j.slices) { v.x += p[k].x; v.y += p[k].y; v.z += p[k].z; v.w += p[k].w; }
+struct PackArgs {
+  PackJob u, t;
+  int M, r, slots;
+  const int* order;
+  const int* start;
+  const int* tiles;
+  int64_t chunks;     // chunks of one block of 64 ranks
+};
+__host__ __device__ constexpr int64_t pack_chunks(int64_t M, int S) { return M / 32 + S + 1; }
+
+template <int RT>
+__global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
+  constexpr int QW = 16 * RT, LW = QW + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t pl[3][kPlanTile][LW];
+  __shared__ int rows[kPlanTile];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const PackJob& job = blockIdx.y ? g.t : g.u;
+  const TileRow t = tile_row(g.tiles, blockIdx.x, g.M, g.slots);
+  if (t.count <= 0 || t.slot < 0) return;
+  const int in_slot = t.first - g.start[t.slot];   // a multiple of 64
+  const int64_t chunk = g.start[t.slot] / 32 + t.slot + in_slot / 32;
+  if (in_slot < 0 || chunk < 0 || chunk + (t.count > 32) >= g.chunks) return;   // no such plan
+  if (tid < kPlanTile) {
+    const int m = tid < t.count ? g.order[t.first + tid] : -1;
+    rows[tid] = (unsigned)m < (unsigned)g.M ? m : -1;
   }
-  const float e[4] = {v.x, v.y, v.z, v.w};
-  uint16_t t[3][4];
+  __syncthreads();
+  const int r = g.r, j0 = (int)blockIdx.z * 64;
+  for (int e = tid; e < kPlanTile * QW / 4; e += 256) {
+    const int tok = e / (QW / 4), j = 4 * (e % (QW / 4));
+    const int m = rows[tok];
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (m >= 0 && j0 + j < r) {
+      const int64_t at = (int64_t)m * r + j0 + j, plane = (int64_t)g.M * r;
+      for (int z = 0; z < job.slices; z += 8) {   // eight loads at a time
+        float4 p[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) split3(e[k], t[0][k], t[1][k], t[2][k]);
+        for (int k = 0; k < 8; ++k)
+          p[k] = *reinterpret_cast<const float4*>(job.part + min(z + k, job.slices - 1) * plane + at);
 #pragma unroll
-  for (int p = 0; p < 3; ++p)
-    reinterpret_cast<uint2*>(j.planes)[p * n4 + i] =
-        make_uint2(t[p][0] | (uint32_t)t[p][1] << 16, t[p][2] | (uint32_t)t[p][3] << 16);
+        for (int k = 0; k < 8; ++k)
+          if (z + k < job.slices) { v.x += p[k].x; v.y += p[k].y; v.z += p[k].z; v.w += p[k].w; }
+      }
+    }
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint16_t x[3][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split3(f[k], x[0][k], x[1][k], x[2][k]);
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+      *reinterpret_cast<uint2*>(&pl[z][tok][j]) =
+          make_uint2(x[z][0] | (uint32_t)x[z][1] << 16, x[z][2] | (uint32_t)x[z][3] << 16);
+  }
+  __syncthreads();
+  const int i = lane & 15, q4 = lane >> 4;
+  const int64_t block = (int64_t)blockIdx.z * g.chunks + chunk;
+  for (int u = wave; u < 2 * 3 * RT; u += 4) {
+    const int c = u / (3 * RT), z = u / RT % 3, k = u % RT;
+    if (32 * c >= t.count) break;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pl[z][32 * c + 8 * q4 + 2 * e][16 * k + i] |
+             (uint32_t)pl[z][32 * c + 8 * q4 + 2 * e + 1][16 * k + i] << 16;
+    *reinterpret_cast<uint4*>(job.cols + (((block + c) * 3 + z) * RT + k) * 512 + 8 * lane) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (job.rows == nullptr) return;
+  for (int u = wave; u < 2 * 2 * RT; u += 4) {
+    const int c = u / (2 * RT), tg = u / RT % 2, k = u % RT;
+    if (32 * c >= t.count) break;
+    *reinterpret_cast<uint4*>(job.rows + (((block + c) * 2 + tg) * RT + k) * 512 + 8 * lane) =
+        *reinterpret_cast<const uint4*>(&pl[q4 >> 1][32 * c + 16 * tg + i][16 * k + 8 * (q4 & 1)]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -724,13 +786,14 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
 //  * Lane L holds columns 8 (L % 8) of tokens 8 h + L / 8, h = 0..3: eight whole
 //    128-byte lines per instruction, for P, dX0 and dX alike, so that the
 //    dropout's words of X and of dX are drawn once.
-//  * P and the three bf16 planes of Q pass through a slab of LDS per wave and
-//    come back as MFMA operands with the transposing read, tokens along the
-//    contraction.  Their registers take the next chunk's loads as soon as they
-//    are in the slab.
-//  * U's rows of the slab are the column operand of dX, whose row operand, the
-//    slot's A over these columns, stays in LDS; the products leave through P's
-//    part of the slab (16-byte pieces of row i XOR-swizzled by i).
+//  * P passes through a slab of LDS per wave and comes back as MFMA operands
+//    with the transposing read, tokens along the contraction; its registers
+//    take the next chunk's loads as soon as they are in the slab.  Q's operands
+//    (cols, and for dX rows) come packed from memory: passed through the slab
+//    as well, the three planes of 64 ranks bounded the kernel by LDS (4096
+//    tokens, 4096 x 11008: 85 us).
+//  * dX's row operand, the slot's A over these columns, stays in LDS; the
+//    products leave through P's slab (16-byte pieces of row i XOR-swizzled by i).
 //  * The waves' sums are added in the order 0, 1, ..., NW - 1.
 // Bound: HBM, X, dY and dX0 read once, dX and all slots' dA and dB written;
 // Q is read by every column slice, from L2.
@@ -738,57 +801,46 @@ constexpr int kGradRanks = 64;
 constexpr int kGradSlice = 64;
 
 struct BatchGradJob {
-  const uint16_t* P;   // [M, cols] bf16
+  const uint16_t* P;     // [M, cols] bf16
   int64_t cols;
-  const uint16_t* Q;   // [3][M, r] bf16 planes
-  float* out;          // trans: [slots, r, cols] (dA); else [slots, cols, r] (dB)
+  const uint16_t* Q;     // packed cols of U or T
+  float* out;            // trans: [slots, r, cols] (dA); else [slots, cols, r] (dB)
   int trans, slices;
 };
 struct BatchGradArgs {
-  BatchGradJob a, b;   // dA (with dX), dB
+  BatchGradJob a, b;     // dA (with dX), dB
+  const uint16_t* Urows; // packed rows of U, for dX
+  int64_t chunks;        // chunks of one block of 64 ranks
   int M, r, slots;
   const float* scale;
   const int* order;
   const int* start;
-  const uint16_t* A;   // [slots, r, K], for dX
+  const uint16_t* A;     // [slots, r, K], for dX
   const uint16_t* dX0;
   uint16_t* dX;
   DropKey drop;
   float keep_scale;
 };
 
-// Where a slab keeps 16-byte piece p of row `row` (rows of PPR pieces): XOR
-// swizzles that keep both reads of the slab free of bank conflicts, four rows
-// of two neighbouring pieces (transposing) and sixteen rows of one piece.  SW
-// off keeps the pieces in place: at 16 ranks the swizzles' addresses cost more
-// registers, and with them a second workgroup per CU, than the conflicts they
-// spare (2048 tokens, 4096 x 4096: 20.1 against 15.6 us).
-template <int PPR, bool SW>
-__device__ __forceinline__ int slab_piece(int row, int p) {
-  if (!SW) return p;
-  if (PPR == 2) return p ^ ((row >> 3) & 1);
-  if (PPR == 4) return p ^ ((row >> 2) & 3);
-  const int x = row >> 1;
-  return p ^ (((x & 1) << 1) | ((x >> 1) & 1) | (x & 4));
-}
-// 16 x 32 operand of a slab of 32 rows: lane (i, q4) gets column 16 band + i of
-// rows 8 q4 .. 8 q4 + 7.
-template <int PPR, bool SW>
+// 16 x 32 operand of P's slab of 32 rows of 64: lane (i, q4) gets column 16 band
+// + i of rows 8 q4 .. 8 q4 + 7.
 __device__ __forceinline__ bf16x8_t slab_operand(const uint16_t* slab, int band, int lane) {
-  const int i = lane & 15, row = 8 * (lane >> 4) + (i >> 2), p = 2 * band + ((i & 3) >> 1);
-  const v4s_t lo = lds_read_tr16(slab + 8 * (row * PPR + slab_piece<PPR, SW>(row, p)) + 4 * (i & 1));
-  const v4s_t hi =
-      lds_read_tr16(slab + 8 * ((row + 4) * PPR + slab_piece<PPR, SW>(row + 4, p)) + 4 * (i & 1));
+  const int i = lane & 15;
+  const uint16_t* const p =
+      slab + (8 * (lane >> 4) + (i >> 2)) * kGradSlice + 16 * band + 4 * (i & 3);
+  const v4s_t lo = lds_read_tr16(p);
+  const v4s_t hi = lds_read_tr16(p + 4 * kGradSlice);
   const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
 template <int RT, int NW>
 struct GradShape {
-  static constexpr int QW = 16 * RT;
-  static constexpr int PE = 32 * kGradSlice, CE = PE + 3 * 32 * QW;   // elements of a chunk
-  static constexpr int AW = 16 * RT + 8;                              // LDS row of a column of A
-  static constexpr int SLAB = NW * CE * 2, RED = NW * 4 * RT * 64 * 16;
+  static constexpr int PE = 32 * kGradSlice;        // elements of a chunk of P
+  static constexpr int AW = 16 * RT + 8;            // LDS row of a column of A
+  static constexpr int CH = 1;
+  static constexpr int NR = NW / CH;                // waves that share a slice's chunks
+  static constexpr int SLAB = NW * PE * 2, RED = (NR == 2 ? 1 : NR) * CH * 4 * RT * 64 * 16;
   static constexpr int SMEM = SLAB > RED ? SLAB : RED;
 };
 
@@ -797,16 +849,16 @@ struct GradShape {
 // stores in flight is the same on every path of the loop.
 template <int RT, bool DROP, bool DX, int NW>
 __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchGradJob& job, int sl,
-                                            char* smem, uint16_t* as) {
+                                            int slot, char* smem, uint16_t* as) {
   using Sh = GradShape<RT, NW>;
-  constexpr bool SW = RT > 1;
-  constexpr int QW = Sh::QW, PE = Sh::PE, CE = Sh::CE, AW = Sh::AW;
+  constexpr int AW = Sh::AW;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, q4 = lane >> 4;
   const int cols = (int)job.cols;
-  const int c0 = sl * kGradSlice;
-  const int M = g.M, r = g.r, slot = blockIdx.y;
+  const int half = wave % Sh::CH, way = wave / Sh::CH;
+  const int c0 = (sl * Sh::CH + half) * kGradSlice;
+  const int M = g.M, r = g.r;
   const int j0 = (int)blockIdx.z * kGradRanks;
   // The slot's range of the order, cut to M tokens whatever the plan holds.
   const int s0 = min(max(g.start[slot], 0), M), s1 = min(max(g.start[slot + 1], s0), M);
@@ -815,8 +867,7 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   const uint32_t prowb = (uint32_t)cols * 2;
   const __amdgpu_buffer_rsrc_t rx0 =
       rsrc_whole(g.dX0, DX && g.dX0 ? (uint32_t)M * prowb : 0u);
-  const __amdgpu_buffer_rsrc_t rdx =
-      rsrc_whole(g.dX, DX ? (uint32_t)M * prowb : 0u);
+  const __amdgpu_buffer_rsrc_t rdx = rsrc_whole(g.dX, DX ? (uint32_t)M * prowb : 0u);
   const int nchunks = (nt + 31) / 32;
   // Tokens of chunk ci (lane L: token L % 32), -1 past the slot's last.
   auto tokens = [&](int ci) {
@@ -834,12 +885,12 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   };
   if (DX && slot == g.slots) {   // tokens without an adapter: dX = dX0
     if (g.dX == g.dX0) return;
-    int tok = tokens(wave);
-    for (int ci = wave; ci < nchunks; ci += NW) {
+    int tok = tokens(way);
+    for (int ci = way; ci < nchunks; ci += Sh::NR) {
       uint32_t off[4];
       uint4 v[4];
       places(tok, off);
-      tok = tokens(ci + NW);
+      tok = tokens(ci + Sh::NR);
 #pragma unroll
       for (int h = 0; h < 4; ++h) v[h] = bload128s(rx0, off[h], 0);
 #pragma unroll
@@ -847,37 +898,61 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
     }
     return;
   }
+  float* const out = job.out + (int64_t)slot * cols * r;
+  if (nt == 0) {   // a slot without tokens: zeros, whatever its scale
+    for (int e = way * 64 + lane; e < kGradSlice * 16 * RT; e += 64 * Sh::NR) {
+      const int j = job.trans ? e / kGradSlice : e % (16 * RT);
+      const int cc = c0 + (job.trans ? e % kGradSlice : e / (16 * RT));
+      if (cc < cols && j0 + j < r)
+        out[job.trans ? (int64_t)(j0 + j) * cols + cc : (int64_t)cc * r + j0 + j] = 0.0f;
+    }
+    return;
+  }
   const __amdgpu_buffer_rsrc_t rp = rsrc_whole(job.P, (uint32_t)M * prowb);
-  const __amdgpu_buffer_rsrc_t rq = rsrc_whole(job.Q, (uint32_t)M * (uint32_t)r * 6);
   const float c_a = g.scale[slot];
+  // The slot's chunks in the packed operands (a plan that does not fit the
+  // batch must not lead past them).
+  int64_t first = s0 / 32 + slot;
+  if (first + nchunks > g.chunks) first = g.chunks - nchunks;
+  first += (int64_t)blockIdx.z * g.chunks;
+  const uint4* const qcols = reinterpret_cast<const uint4*>(job.Q) + first * (3 * RT * 64) + lane;
+  const uint4* const qrows = reinterpret_cast<const uint4*>(g.Urows) + first * (2 * RT * 64) + lane;
 
-  uint4 pv[4], qv[3][RT], xv[4];
+  uint4 pv[4], qv[3][RT], uv[2][RT], xv[4];
   uint32_t off[4], next[4];
-  auto load = [&](int tok) {
+  auto load_p = [&](int tok) {
     places(tok, next);
 #pragma unroll
     for (int h = 0; h < 4; ++h) pv[h] = bload128s(rp, next[h], 0);
+  };
+  // Past the wave's last chunk these load the slot's last again.
+  auto load_q = [&](int ci, int z) {
+    const uint4* const q = qcols + (int64_t)min(ci, nchunks - 1) * (3 * RT * 64) + z * RT * 64;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int p = 64 * t + lane;              // piece p: row p / (2 RT), ranks 8 (p % (2 RT))
-      const int m = __shfl(tok, p / (2 * RT));
-      const int j = j0 + 8 * (p % (2 * RT));
-      const uint32_t at = m >= 0 && j < r ? (uint32_t)(m * r + j) * 2 : kOOB;
+    for (int t = 0; t < RT; ++t) qv[z][t] = q[64 * t];
+  };
+  auto load_u = [&](int ci) {
+    const uint4* const q = qrows + (int64_t)min(ci, nchunks - 1) * (2 * RT * 64);
 #pragma unroll
-      for (int z = 0; z < 3; ++z) qv[z][t] = bload128s(rq, at, (uint32_t)z * M * r * 2);
-    }
+    for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) uv[tg][t] = q[(tg * RT + t) * 64];
   };
   auto load_x = [&]() {
 #pragma unroll
     for (int h = 0; h < 4; ++h) xv[h] = bload128s(rx0, next[h], 0);
   };
-  int tok = tokens(wave);
-  load(tok);
+  int tok = tokens(way);
+#pragma unroll
+  for (int z = 2; z >= 0; --z) load_q(way, z);
+  if constexpr (DX) load_u(way);
+  load_p(tok);
   if constexpr (DX) load_x();
-  tok = tokens(wave + NW);
-  if (DX && nt > 0) {   // as[column][rank] = A, transposed
+  tok = tokens(way + Sh::NR);
+  if (DX) {   // as[column][rank] = A, transposed
     const uint16_t* const A = g.A + (int64_t)slot * r * cols;
-    for (int e = tid; e < QW * (kGradSlice / 8); e += 64 * NW) {
+    as += half * kGradSlice * AW;
+    for (int e = way * 64 + lane; e < 16 * RT * (kGradSlice / 8); e += 64 * Sh::NR) {
       const int j = e / (kGradSlice / 8), k0 = 8 * (e % (kGradSlice / 8));
       uint4 v = make_uint4(0, 0, 0, 0);
       if (j < r && c0 + k0 < cols) v = *reinterpret_cast<const uint4*>(A + (int64_t)j * cols + c0 + k0);
@@ -885,10 +960,10 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
 #pragma unroll
       for (int k = 0; k < 8; ++k) as[(k0 + k) * AW + j] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
     }
+    lds_barrier();
   }
-  if (DX) lds_barrier();
 
-  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * CE;
+  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * Sh::PE;
   f32x4_t acc[4][RT];
 #pragma unroll
   for (int h = 0; h < 4; ++h)
@@ -896,7 +971,7 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
     for (int t = 0; t < RT; ++t) acc[h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const float s = DROP ? c_a * g.keep_scale : c_a;
 
-  for (int ci = wave; ci < nchunks; ci += NW) {
+  for (int ci = way; ci < nchunks; ci += Sh::NR) {
     uint32_t keep = 0;   // 8 bits per piece
 #pragma unroll
     for (int h = 0; h < 4; ++h) off[h] = next[h];
@@ -918,30 +993,23 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
                   ((keep >> (8 * h + 2 * e + 1)) & 1u ? 0xffff0000u : 0u);
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      const int row = 8 * h + prow;
-      *reinterpret_cast<uint4*>(my + 8 * (8 * row + slab_piece<8, SW>(row, lane & 7))) = v;
+      *reinterpret_cast<uint4*>(my + 8 * (64 * h + lane)) = v;
     }
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = (64 * t + lane) / (2 * RT);
-      const int at = 8 * (2 * RT * row + slab_piece<2 * RT, SW>(row, lane % (2 * RT)));
-#pragma unroll
-      for (int z = 0; z < 3; ++z) *reinterpret_cast<uint4*>(my + PE + z * 32 * QW + at) = qv[z][t];
-    }
-    load(tok);
-    tok = tokens(ci + 2 * NW);
+    load_p(tok);
+    tok = tokens(ci + 2 * Sh::NR);
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     bf16x8_t aop[4];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) aop[h] = slab_operand<8, SW>(my, h, lane);
+    for (int h = 0; h < 4; ++h) aop[h] = slab_operand(my, h, lane);
 #pragma unroll
-    for (int z = 2; z >= 0; --z)          // the small terms first
+    for (int z = 2; z >= 0; --z) {        // the small terms first
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const bf16x8_t bop = slab_operand<2 * RT, SW>(my + PE + z * 32 * QW, t, lane);
+      for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) acc[h][t] = mfma_16x16x32(aop[h], bop, acc[h][t]);
-      }
+        for (int h = 0; h < 4; ++h)
+          acc[h][t] = mfma_16x16x32(aop[h], __builtin_bit_cast(bf16x8_t, qv[z][t]), acc[h][t]);
+      load_q(ci + Sh::NR, z);
+    }
     if constexpr (DX) {
       // dX[m][c]: row operand A's column 16 k + i, ranks 16 ch + 8 (q4 & 1) ..;
       // column operand U's token 16 tg + i, the hi terms (q4 < 2) and the mid
@@ -953,21 +1021,17 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
         for (int k = 0; k < 4; ++k) d[tg][k] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int ch = 0; ch < RT; ++ch) {
-        bf16x8_t uop[2];
-#pragma unroll
-        for (int tg = 0; tg < 2; ++tg)
-          uop[tg] = *reinterpret_cast<const bf16x8_t*>(
-              my + PE + (q4 >> 1) * 32 * QW +
-              8 * (2 * RT * (16 * tg + i) + slab_piece<2 * RT, SW>(16 * tg + i, 2 * ch + (q4 & 1))));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const bf16x8_t wop =
               *reinterpret_cast<const bf16x8_t*>(as + (16 * k + i) * AW + 16 * ch + 8 * (q4 & 1));
 #pragma unroll
-          for (int tg = 0; tg < 2; ++tg) d[tg][k] = mfma_16x16x32(wop, uop[tg], d[tg][k]);
+          for (int tg = 0; tg < 2; ++tg)
+            d[tg][k] = mfma_16x16x32(wop, __builtin_bit_cast(bf16x8_t, uv[tg][ch]), d[tg][k]);
         }
       }
-      float* const e = reinterpret_cast<float*>(my);   // P's part: 16 rows of 64 floats
+      load_u(ci + Sh::NR);
+      float* const e = reinterpret_cast<float*>(my);   // 16 rows of 64 floats
 #pragma unroll
       for (int tg = 0; tg < 2; ++tg) {
 #pragma unroll
@@ -999,46 +1063,77 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   }
 
   // acc[h][t][v] = O[c0 + 16 h + 4 q4 + v][j0 + 16 t + i]; the unit (h, t) is
-  // added by wave (h RT + t) mod NW.
-  lds_barrier();   // the slabs are free
-  f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem);
-#pragma unroll
-  for (int h = 0; h < 4; ++h)
-#pragma unroll
-    for (int t = 0; t < RT; ++t) red[(wave * 4 * RT + h * RT + t) * 64 + lane] = acc[h][t];
-  lds_barrier();
-  float* const out = job.out + (int64_t)slot * cols * r;
-  for (int unit = wave; unit < 4 * RT; unit += NW) {
-    f32x4_t v = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const f32x4_t o = red[(w * 4 * RT + unit) * 64 + lane];
-      v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
-    }
+  // added by wave (h RT + t) mod NR of the slice's.
+  constexpr int NR = Sh::NR;
+  auto finish = [&](int unit, const f32x4_t& v) {
     const int cc = c0 + 16 * (unit / RT) + 4 * q4;   // cc .. cc + 3 (cols is a multiple of 8)
     const int j = j0 + 16 * (unit % RT) + i;
-    if (cc >= cols || j >= r) continue;
-    // A slot without tokens has no products: plain zeros, whatever its scale.
-    const f32x4_t res = nt > 0 ? f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]}
-                               : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (cc >= cols || j >= r) return;
     if (job.trans) {
-      *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + cc) = res;
+      *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + cc) =
+          f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]};
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[(int64_t)(cc + e) * r + j] = res[e];
+      for (int e = 0; e < 4; ++e) out[(int64_t)(cc + e) * r + j] = s * v[e];
+    }
+  };
+  f32x4_t* const red =
+      reinterpret_cast<f32x4_t*>(smem) + half * ((NR == 2 ? 1 : NR) * 4 * RT * 64) + lane;
+  lds_barrier();   // the slabs are free
+  if constexpr (NR == 2) {   // each hands the other half of its sums
+#pragma unroll
+    for (int u = 0; u < 4 * RT; u += 2)
+      red[64 * (u + 1 - way)] = way ? acc[u / RT][u % RT] : acc[(u + 1) / RT][(u + 1) % RT];
+    lds_barrier();
+#pragma unroll
+    for (int u = 0; u < 4 * RT; u += 2) {
+      f32x4_t v = way ? acc[(u + 1) / RT][(u + 1) % RT] : acc[u / RT][u % RT];
+      const f32x4_t o = red[64 * (u + way)];
+      v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
+      finish(u + way, v);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) red[(way * 4 * RT + h * RT + t) * 64] = acc[h][t];
+    lds_barrier();
+    for (int unit = way; unit < 4 * RT; unit += NR) {
+      f32x4_t v = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < NR; ++w) {
+        const f32x4_t o = red[(w * 4 * RT + unit) * 64];
+        v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
+      }
+      finish(unit, v);
     }
   }
+}
+
+// The slot with the n-th most tokens, so that the longest sums start first (up
+// to 64 slots; beyond, slot n).
+__device__ __forceinline__ int slot_by_size(const int* start, int slots, int n) {
+  if (slots > 64) return n;
+  const int lane = threadIdx.x & 63;
+  const int mine = lane < slots ? start[lane + 1] - start[lane] : -1;
+  int before = 0;
+  for (int l = 0; l < slots; ++l) {
+    const int other = __builtin_amdgcn_readlane(mine, l);
+    before += other > mine || (other == mine && l < lane) ? 1 : 0;
+  }
+  return __builtin_ctzll(__ballot(lane < slots && before == n));
 }
 
 template <int RT, bool DROP, bool DX, int NW>
 __global__ void __launch_bounds__(64 * NW, RT == 1 ? 3 : 2) k_batch_grads(BatchGradArgs g) {
   using Sh = GradShape<RT, NW>;
   __shared__ __attribute__((aligned(16))) char smem[Sh::SMEM];
-  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? kGradSlice * Sh::AW : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? Sh::CH * kGradSlice * Sh::AW : 8];
+  const int slot = (int)blockIdx.y < g.slots ? slot_by_size(g.start, g.slots, blockIdx.y) : g.slots;
   if ((int)blockIdx.x < g.a.slices)
-    grads_block<RT, DROP, DX, NW>(g, g.a, blockIdx.x, smem, as);
-  else if ((int)blockIdx.y < g.slots)   // the last row is dX's alone
-    grads_block<RT, false, false, NW>(g, g.b, (int)blockIdx.x - g.a.slices, smem, as);
+    grads_block<RT, DROP, DX, NW>(g, g.a, blockIdx.x, slot, smem, as);
+  else if (slot < g.slots)   // the last row is dX's alone
+    grads_block<RT, false, false, NW>(g, g.b, (int)blockIdx.x - g.a.slices, slot, smem, as);
 }
 
 // ------------------------------- launchers ---------------------------------
@@ -1076,15 +1171,21 @@ static int down_slices(int64_t M, int S, int64_t C) {
   return (int)((steps + zl - 1) / zl);
 }
 
+// Rank tiles of 16 in a workgroup of the gradients' kernel and its packing.
+static int grad_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
+
 BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bool backward) {
   BatchWorkspace w{};
   size_t off = 0;
   w.off_T = off; off += align256((size_t)down_slices(M, S, K) * M * r * 4);
   if (backward) {
-    const size_t planes = align256((size_t)M * r * 6);
+    // packed operands: 1 KB per chunk, plane (or token group) and rank tile
+    const size_t chunks = (size_t)pack_chunks(M, S) * ((r + kGradRanks - 1) / kGradRanks);
+    const size_t cols = chunks * 3 * grad_tiles(r) * 1024, rows = chunks * 2 * grad_tiles(r) * 1024;
     w.off_U = off; off += align256((size_t)down_slices(M, S, N) * M * r * 4);
-    w.off_Up = off; off += planes;
-    w.off_Tp = off; off += planes;
+    w.off_Uc = off; off += cols;
+    w.off_Tc = off; off += cols;
+    w.off_Ur = off; off += rows;
   }
   w.bytes = off;
   return w;
@@ -1178,39 +1279,50 @@ hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, in
   const BatchWorkspace w = batch_workspace(M, K, N, a.r, a.slots, true);
   char* const base = reinterpret_cast<char*>(ws);
   float* const U = reinterpret_cast<float*>(base + w.off_U);
-  uint16_t* const Up = reinterpret_cast<uint16_t*>(base + w.off_Up);
-  uint16_t* const Tp = reinterpret_cast<uint16_t*>(base + w.off_Tp);
-  SplitJob ju{U, down_slices(M, a.slots, N), Up}, jt{T, 1, Tp};
+  uint16_t* const Uc = reinterpret_cast<uint16_t*>(base + w.off_Uc);
+  uint16_t* const Tc = reinterpret_cast<uint16_t*>(base + w.off_Tc);
+  uint16_t* const Ur = reinterpret_cast<uint16_t*>(base + w.off_Ur);
+  // Beyond 64 ranks a workgroup of the gradients' kernel sees only a part of
+  // them: dX has its own launch there.
+  const bool fused = dX != nullptr && a.r <= kGradRanks;
+  PackArgs pk{};
+  pk.u = PackJob{U, down_slices(M, a.slots, N), Uc, fused ? Ur : nullptr};
+  pk.t = PackJob{T, 1, Tc, nullptr};
+  pk.M = (int)M; pk.r = a.r; pk.slots = a.slots; pk.order = a.order; pk.start = a.start;
+  pk.tiles = a.tiles; pk.chunks = pack_chunks(M, a.slots);
   if (!T) {
     float* const part = reinterpret_cast<float*>(base + w.off_T);
     QLK_TRY(batch_T(X, a, M, K, d, part, st));
-    jt.part = part;
-    jt.slices = down_slices(M, a.slots, K);
+    pk.t.part = part;
+    pk.t.slices = down_slices(M, a.slots, K);
   }
   DownArgs g{};
   g.S = dY; g.M = (int)M; g.C = N; g.W = a.B; g.r = a.r; g.slots = a.slots;
   g.order = a.order; g.tiles = a.tiles; g.part = U;
   QLK_TRY((down<true, false>(g, st)));
-  const int64_t n4 = M * a.r / 4;
-  hipLaunchKernelGGL(k_batch_split, dim3((unsigned)((n4 + 255) / 256), 2), dim3(256), 0, st, ju, jt,
-                     n4);
+  const dim3 pgrid((unsigned)adapter_plan_tiles(M, a.slots), 2,
+                   (unsigned)((a.r + kGradRanks - 1) / kGradRanks));
+  switch (grad_tiles(a.r)) {
+    case 1: hipLaunchKernelGGL(k_batch_pack<1>, pgrid, dim3(256), 0, st, pk); break;
+    case 2: hipLaunchKernelGGL(k_batch_pack<2>, pgrid, dim3(256), 0, st, pk); break;
+    default: hipLaunchKernelGGL(k_batch_pack<4>, pgrid, dim3(256), 0, st, pk); break;
+  }
   QLK_TRY(hipGetLastError());
   const DropKey key{d.threshold, d.k0, d.k1};
-  // Beyond 64 ranks a workgroup of the gradients' kernel sees only a part of
-  // them: dX has its own launch there.
-  const bool fused = dX != nullptr && a.r <= kGradRanks;
   if (dX && !fused) {
     UpArgs u{};
-    u.base = dX0; u.out = dX; u.M = (int)M; u.cols = K; u.part = U; u.slices = ju.slices;
+    u.base = dX0; u.out = dX; u.M = (int)M; u.cols = K; u.part = U; u.slices = pk.u.slices;
     u.t_out = nullptr; u.W = a.A; u.scale = a.scale;
     u.r = a.r; u.slots = a.slots; u.order = a.order; u.tiles = a.tiles;
     u.drop = key; u.keep_scale = d.scale;
     QLK_TRY((d.on ? up<true, true>(u, st) : up<true, false>(u, st)));
   }
-  auto slices = [](int64_t cols) { return (int)((cols + kGradSlice - 1) / kGradSlice); };
+  const int64_t wide = kGradSlice;   // columns of a workgroup
+  auto slices = [&](int64_t cols) { return (int)((cols + wide - 1) / wide); };
   BatchGradArgs ga{};
-  ga.a = BatchGradJob{X, K, Up, dA, 1, slices(K)};
-  ga.b = BatchGradJob{dY, N, Tp, dB, 0, slices(N)};
+  ga.a = BatchGradJob{X, K, Uc, dA, 1, slices(K)};
+  ga.b = BatchGradJob{dY, N, Tc, dB, 0, slices(N)};
+  ga.Urows = Ur; ga.chunks = pk.chunks;
   ga.M = (int)M; ga.r = a.r; ga.slots = a.slots; ga.scale = a.scale; ga.order = a.order;
   ga.start = a.start; ga.A = a.A; ga.dX0 = dX0; ga.dX = dX; ga.drop = key; ga.keep_scale = d.scale;
   if (d.on) {

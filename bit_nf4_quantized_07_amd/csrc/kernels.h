@@ -279,7 +279,7 @@ struct BatchDropout {
   float scale;
 };
 struct BatchWorkspace {
-  size_t off_T, off_U, off_Up, off_Tp, bytes;
+  size_t off_T, off_U, off_Uc, off_Tc, off_Ur, bytes;
 };
 BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bool backward);
 // out = Y + c T B^T (Y null: zeros; out may be Y), T = drop(X) A^T to T_out
