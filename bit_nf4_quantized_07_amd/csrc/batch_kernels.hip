@@ -37,8 +37,10 @@ __device__ __forceinline__ void bstore128(__amdgpu_buffer_rsrc_t r, uint4 v, uin
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u_t, v), r, (int)off, 0, 0);
 }
 
-__device__ __forceinline__ uint4 keep_or_zero(bool ok, uint4 v) {
-  return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+// LDS operations done, then the workgroup's barrier; loads from memory into
+// registers stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // x = hi + mid + lo, bf16 terms; an infinity or NaN is hi alone.
@@ -90,15 +92,18 @@ struct DownArgs {
   float keep_scale;
 };
 
-// Token groups of 16 per workgroup: 64 tokens, or 32 where the sums and operands
-// of 64 ranks and the slab leave no room for a second wave per SIMD (U at rank
-// 64, 4096 x 11008: 62 against 39 us).
+// B at 64 ranks: the sums and operands of 64 tokens leave no room for a second
+// wave per SIMD (U, 4096 tokens, 4096 x 11008: 62 us), and 32 tokens per
+// workgroup read B twice (39 us).  So two waves share a step, each with 32 of
+// the 64 tokens: both write half of B's step to one slab, a barrier per step,
+// two slabs in turn (35 us).
 template <bool WT, int RT>
-constexpr int down_groups() { return WT && RT == 4 ? 2 : 4; }
+constexpr bool down_pairs() { return WT && RT == 4; }
 
 template <bool WT, bool DROP, int RT>
 __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_batch_down(DownArgs g) {
-  constexpr int TG = down_groups<WT, RT>(), SUBS = 4 / TG;
+  constexpr bool PAIRS = down_pairs<WT, RT>();
+  constexpr int TG = PAIRS ? 2 : 4;   // token groups of 16 of a wave
   constexpr int SW = 16 * RT + 8;   // WT: row of a wave's 64 (c) x 16 RT (j) slab, padded
   constexpr int SLAB = WT ? kDownWaves * 64 * SW * 2 : 16, RED = TG * 3 * RT * 64 * 16;
   __shared__ __attribute__((aligned(16))) char smem[SLAB > RED ? SLAB : RED];
@@ -106,9 +111,7 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15, grp = lane >> 4;
-  TileRow t = tile_row(g.tiles, (int)blockIdx.y / SUBS, g.M, g.slots);
-  t.first += (int)blockIdx.y % SUBS * 16 * TG;
-  t.count = min(t.count - (int)blockIdx.y % SUBS * 16 * TG, 16 * TG);
+  const TileRow t = tile_row(g.tiles, blockIdx.y, g.M, g.slots);
   if (t.count <= 0 || t.slot < 0) return;
   if (tid < kPlanTile) {
     const int m = tid < t.count ? g.order[t.first + tid] : -1;
@@ -116,6 +119,8 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
   }
   const int z = blockIdx.x, j0 = (int)blockIdx.z * 64;
   const int r = g.r, ntg = (t.count + 15) / 16;
+  const int half = wave & 1, way = wave >> 1;       // of a pair
+  const int tg0 = PAIRS && ntg > 1 ? 2 * half : 0;  // this wave's first token group
   const int C = (int)g.C;
   const int nsteps = (C + 63) / 64;
   const int s0 = z * g.zlen, s1 = min(nsteps, s0 + g.zlen);
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
   uint32_t xoff[TG];
 #pragma unroll
   for (int tg = 0; tg < TG; ++tg) {
-    const int m = rows[16 * tg + row];
+    const int m = rows[16 * (tg0 + tg) + row];
     xoff[tg] = m >= 0 ? (uint32_t)(((int64_t)m * C + 16 * grp) * 2) : kOOB;
   }
   const uint32_t woff = WT ? (uint32_t)((lane / PR) * r + j0 + 8 * (lane % PR)) * 2
@@ -228,7 +233,6 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
           for (int h = 0; h < 2; ++h)
             acc[tg][q] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xv[tg][h]), wop[h], acc[tg][q]);
         }
-        if (WT && RT == 4) __builtin_amdgcn_sched_barrier(0);   // one q's operands at a time
       }
     };
     uint4 xa[NTG][2], xb[NTG][2], wa[2 * RT];
@@ -254,8 +258,86 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
       st += kDownWaves;
     }
   };
-  if (ntg == 1) steps(std::integral_constant<int, 1>());
-  else steps(std::integral_constant<int, TG>());
+  // The steps of a pair of waves.
+  auto pair_steps = [&]() {
+    constexpr int HQ = RT;   // a wave's share of the step's 2 RT pieces of B
+    uint16_t* const slabs = reinterpret_cast<uint16_t*>(smem) + way * 2 * 64 * SW;
+    uint4 wv[HQ], xv[2][TG][2];
+    auto load = [&](int st, uint4 (&xn)[TG][2]) {
+      const int sc = __builtin_amdgcn_readfirstlane(st < s1 ? st : s0);
+      const int left = st < s1 ? C - 64 * sc : 0;
+#pragma unroll
+      for (int q = 0; q < HQ; ++q) {
+        const int from = (half * HQ + q) * (64 / PR), at = from + lane / PR;
+        const uint32_t so = from < left ? (uint32_t)(64 * sc + from) * 2 * (uint32_t)r : 0u;
+        wv[q] = bload128s(rw, wok && at < left ? woff : kOOB, so);
+      }
+#pragma unroll
+      for (int tg = 0; tg < TG; ++tg)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          xn[tg][h] = bload128s(
+              rs, xoff[tg] != kOOB && 16 * grp + 8 * h < left ? xoff[tg] + 16 * h : kOOB,
+              (uint32_t)sc * 128u);
+    };
+    auto mul = [&](int st, uint4 (&xc)[TG][2], uint4 (&xn)[TG][2], uint16_t* slab) {
+#pragma unroll
+      for (int q = 0; q < HQ; ++q)
+        *reinterpret_cast<uint4*>(slab + ((half * HQ + q) * (64 / PR) + lane / PR) * SW +
+                                  8 * (lane % PR)) = wv[q];
+      load(st + kDownWaves / 2, xn);
+      lds_barrier();   // the other slab's reads, of the last step, were before it
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        bf16x8_t wop[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint16_t* p = slab + (16 * grp + 8 * h + (row >> 2)) * SW + 16 * q + 4 * (row & 3);
+          const v4s_t lo = lds_read_tr16(p);
+          const v4s_t hi = lds_read_tr16(p + 4 * SW);
+          const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          wop[h] = __builtin_bit_cast(bf16x8_t, v);
+        }
+#pragma unroll
+        for (int tg = 0; tg < TG; ++tg)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[tg][q] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xc[tg][h]), wop[h], acc[tg][q]);
+      }
+    };
+    load(s0 + way, xv[0]);
+    for (int st = s0; st < s1; st += kDownWaves) {   // every wave meets every barrier
+      mul(st + way, xv[0], xv[1], slabs);
+      mul(st + way + kDownWaves / 2, xv[1], xv[0], slabs + 64 * SW);
+    }
+    // acc[tg][q][v]: token 16 (tg0 + tg) + 4 grp + v, rank j0 + 16 q + row.  Of
+    // a pair's two, way w adds token group tg0 + w.
+    f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem) + half * RT * 2 * 64 + lane;
+    __syncthreads();   // the slabs are free
+#pragma unroll
+    for (int q = 0; q < RT; ++q) red[((1 - way) * RT + q) * 64] = way ? acc[0][q] : acc[1][q];
+    __syncthreads();
+    float* const out = g.part + (int64_t)z * g.M * r;
+    int mo[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) mo[v] = rows[16 * (tg0 + way) + 4 * grp + v];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      const f32x4_t sum = (way ? acc[1][q] : acc[0][q]) + red[(way * RT + q) * 64];
+      const int j = j0 + 16 * q + row;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (mo[v] >= 0 && j < r) out[(int64_t)mo[v] * r + j] = sum[v];
+    }
+  };
+  if (ntg == 1) {
+    steps(std::integral_constant<int, 1>());
+  } else if constexpr (PAIRS) {
+    pair_steps();
+    return;
+  } else {
+    steps(std::integral_constant<int, TG>());
+  }
 
   // acc[tg][q][v]: token 16 tg + 4 grp + v, rank j0 + 16 q + row.  Wave w adds
   // the four waves' sums of token group w in the order 0, 1, 2, 3.
@@ -430,12 +512,6 @@ struct UpArgs {
   DropKey drop;
   float keep_scale;
 };
-
-// LDS operations done, then the workgroup's barrier; loads from memory into
-// registers stay in flight across it.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
 
 // RK ranks of W in LDS at a time, in NS stages (NS = 1: all of them).
 template <bool WT, bool DROP, int RK, int NS>
@@ -1154,22 +1230,26 @@ static int64_t expected_tiles(int64_t M, int S) {
 // Steps per slice of the down projections' contraction: slices that give about
 // two workgroups per CU, at most kMaxSlices (their sums are read back), and a
 // power of two: the slice is the fast grid index, so that an XCD then always
-// meets the same slices and reads only their part of the adapters (4096
-// tokens, 4096 x 11008, rank 64: seven slices 33 us, eight XXX).
+// meets the same slices and reads only their part of the adapters (T, 4096
+// tokens, 4096 columns, rank 64: seven slices 33 us, four 12.9).  Four workgroups
+// per CU for U of more than 32 ranks, whose waves wait for each other at every
+// step (11008 columns, rank 64: 39.9 against 35.1 us; T, whose waves do not:
+// 12.9 against 16.4).
 constexpr int kMaxSlices = 16;
-constexpr int kDownGroups = 2;
-static int down_zlen(int64_t M, int S, int64_t C) {
+static int down_zlen(int64_t M, int S, int64_t C, bool pairs) {
   const int64_t steps = (C + 63) / 64;
-  const int64_t want = kDownGroups * kCUs / expected_tiles(M, S);
+  const int64_t want = (pairs ? 4 : 2) * kCUs / expected_tiles(M, S);
   int64_t z = 1;
   while (2 * z <= want && 2 * z <= kMaxSlices && 2 * z * kDownWaves <= steps) z *= 2;
   return (int)((steps + z - 1) / z);
 }
-static int down_slices(int64_t M, int S, int64_t C) {
+static int down_slices(int64_t M, int S, int64_t C, bool pairs) {
   const int64_t steps = (C + 63) / 64;
-  const int zl = down_zlen(M, S, C);
+  const int zl = down_zlen(M, S, C, pairs);
   return (int)((steps + zl - 1) / zl);
 }
+static int slices_T(int64_t M, int S, int64_t K) { return down_slices(M, S, K, false); }
+static int slices_U(int64_t M, int S, int64_t N, int r) { return down_slices(M, S, N, r > 32); }
 
 // Rank tiles of 16 in a workgroup of the gradients' kernel and its packing.
 static int grad_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
@@ -1177,12 +1257,12 @@ static int grad_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bool backward) {
   BatchWorkspace w{};
   size_t off = 0;
-  w.off_T = off; off += align256((size_t)down_slices(M, S, K) * M * r * 4);
+  w.off_T = off; off += align256((size_t)slices_T(M, S, K) * M * r * 4);
   if (backward) {
     // packed operands: 1 KB per chunk, plane (or token group) and rank tile
     const size_t chunks = (size_t)pack_chunks(M, S) * ((r + kGradRanks - 1) / kGradRanks);
     const size_t cols = chunks * 3 * grad_tiles(r) * 1024, rows = chunks * 2 * grad_tiles(r) * 1024;
-    w.off_U = off; off += align256((size_t)down_slices(M, S, N) * M * r * 4);
+    w.off_U = off; off += align256((size_t)slices_U(M, S, N, r) * M * r * 4);
     w.off_Uc = off; off += cols;
     w.off_Tc = off; off += cols;
     w.off_Ur = off; off += rows;
@@ -1193,10 +1273,10 @@ BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bo
 
 template <bool WT, bool DROP>
 static hipError_t down(DownArgs g, hipStream_t st) {
-  g.zlen = down_zlen(g.M, g.slots, g.C);
-  const unsigned subs = 4 / (g.r <= 32 ? down_groups<WT, 1>() : down_groups<WT, 4>());
-  const dim3 grid((unsigned)down_slices(g.M, g.slots, g.C),
-                  subs * (unsigned)adapter_plan_tiles(g.M, g.slots), (unsigned)((g.r + 63) / 64));
+  const bool pairs = WT && g.r > 32;
+  g.zlen = down_zlen(g.M, g.slots, g.C, pairs);
+  const dim3 grid((unsigned)down_slices(g.M, g.slots, g.C, pairs),
+                  (unsigned)adapter_plan_tiles(g.M, g.slots), (unsigned)((g.r + 63) / 64));
   const dim3 block(64 * kDownWaves);
   if (g.r <= 16) hipLaunchKernelGGL((k_batch_down<WT, DROP, 1>), grid, block, 0, st, g);
   else if (g.r <= 32) hipLaunchKernelGGL((k_batch_down<WT, DROP, 2>), grid, block, 0, st, g);
@@ -1251,7 +1331,7 @@ hipError_t launch_batch_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N,
   QLK_TRY(batch_T(X, a, M, K, d, part, st));
   UpArgs u{};
   u.base = Y; u.out = out; u.M = (int)M; u.cols = N; u.part = part;
-  u.slices = down_slices(M, a.slots, K); u.t_out = T_out; u.W = a.B; u.scale = a.scale;
+  u.slices = slices_T(M, a.slots, K); u.t_out = T_out; u.W = a.B; u.scale = a.scale;
   u.r = a.r; u.slots = a.slots; u.order = a.order; u.tiles = a.tiles;
   return up<false, false>(u, st);
 }
@@ -1286,7 +1366,7 @@ hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, in
   // them: dX has its own launch there.
   const bool fused = dX != nullptr && a.r <= kGradRanks;
   PackArgs pk{};
-  pk.u = PackJob{U, down_slices(M, a.slots, N), Uc, fused ? Ur : nullptr};
+  pk.u = PackJob{U, slices_U(M, a.slots, N, a.r), Uc, fused ? Ur : nullptr};
   pk.t = PackJob{T, 1, Tc, nullptr};
   pk.M = (int)M; pk.r = a.r; pk.slots = a.slots; pk.order = a.order; pk.start = a.start;
   pk.tiles = a.tiles; pk.chunks = pack_chunks(M, a.slots);
@@ -1294,7 +1374,7 @@ hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, in
     float* const part = reinterpret_cast<float*>(base + w.off_T);
     QLK_TRY(batch_T(X, a, M, K, d, part, st));
     pk.t.part = part;
-    pk.t.slices = down_slices(M, a.slots, K);
+    pk.t.slices = slices_T(M, a.slots, K);
   }
   DownArgs g{};
   g.S = dY; g.M = (int)M; g.C = N; g.W = a.B; g.r = a.r; g.slots = a.slots;
