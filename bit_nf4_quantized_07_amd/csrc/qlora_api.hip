@@ -19,7 +19,7 @@ constexpr int64_t kMaxBufferBytes = (int64_t)1 << 31;
 
 constexpr int kMaxRank = 256;
 constexpr int64_t kMaxBatchDim = (int64_t)1 << 23;   // batched adapters' K and N
-constexpr int64_t kMaxTiles = 65535 / 2;   // up to two grid rows each
+constexpr int64_t kMaxTiles = 65535;   // a grid row each
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -259,8 +259,8 @@ int check_batch_sizes(int64_t M, int64_t K, int64_t N, int r, int S) {
   if (M <= 0 || M > kMaxDim || K <= 0 || N <= 0 || K % 8 != 0 || N % 8 != 0) return QLORA_ERR_SHAPE;
   if (K > kMaxBatchDim || N > kMaxBatchDim) return QLORA_ERR_SHAPE;
   if (S < 1 || S > qlk::kMaxSlots || r < 8 || r > kMaxRank || r % 8 != 0) return QLORA_ERR_SHAPE;
-  // 32-bit offsets into X, dY, one slot's A and B, and the bf16 terms of T and U;
-  // tiles of the plan and slots are grid rows
+  // 32-bit offsets into X, dY, and one slot's A and B; the terms of T and U in
+  // the workspace; tiles of the plan are grid rows
   if (M * K * 2 >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes ||
       (int64_t)r * K * 2 >= kMaxBufferBytes || (int64_t)r * N * 2 >= kMaxBufferBytes ||
       M * r * 6 >= kMaxBufferBytes || qlk::adapter_plan_tiles(M, S) > kMaxTiles)

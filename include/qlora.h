@@ -341,7 +341,8 @@ int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, i
  *   T[m] = drop(X[m]) A_a^T,   out[m] = RNE_bf16(Y[m] + scale[a] T[m] B_a^T)
  * and T[m] = 0, out[m] = Y[m] without an adapter.  T is fp32 [M, r] (T_out, or
  * NULL if not wanted); the sum is held in fp32 and rounded once (T enters the
- * product as two bf16 terms, within 2^-17).
+ * product as two bf16 terms, within 2^-17; where one is zero an infinity in B
+ * gives NaN, as in the backward's products).
  * drop() is lora_dropout's mask for (p, seed) -- the same elements are kept --
  * times 1 / (1 - p), regenerated where elements are used: neither the mask nor
  * a dropped copy of X is stored, and X's kept values are not rounded.  p = 0
@@ -351,7 +352,7 @@ int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, i
  *   order, start, tiles: from lora_adapter_plan with the same M and S.
  * Requires r % 8 == 0, 8 <= r <= 256; K % 8 == 0, N % 8 == 0, both at most
  * 2^23; X, Y and one slot's A and B under 2 GiB each; 6 M r < 2^31; at most
- * 32767 tiles; workspace of lora_adapters_workspace_bytes(M, K, N, r, S, 0). */
+ * 65535 tiles; workspace of lora_adapters_workspace_bytes(M, K, N, r, S, 0). */
 int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint16_t* A,
                       const uint16_t* B, const float* scale, int r, int S, const int32_t* order,
                       const int32_t* start, const int32_t* tiles, const uint16_t* Y, double p,
