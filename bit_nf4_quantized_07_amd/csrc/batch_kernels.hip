@@ -910,20 +910,23 @@ __device__ __forceinline__ bf16x8_t slab_operand(const uint16_t* slab, int band,
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// 64-column blocks of a slice: two for dB at 64 ranks, where Q's bytes, read by
+// every slice, are the larger part.
+template <int RT>
+constexpr int grad_blocks_b() { return RT == 4 ? 2 : 1; }
+
 template <int RT, int NW>
 struct GradShape {
   static constexpr int PE = 32 * kGradSlice;        // elements of a chunk of P
   static constexpr int AW = 16 * RT + 8;            // LDS row of a column of A
-  static constexpr int CH = 1;
-  static constexpr int NR = NW / CH;                // waves that share a slice's chunks
-  static constexpr int SLAB = NW * PE * 2, RED = (NR == 2 ? 1 : NR) * CH * 4 * RT * 64 * 16;
+  static constexpr int SLAB = NW * grad_blocks_b<RT>() * PE * 2, RED = NW * 4 * RT * 64 * 16;
   static constexpr int SMEM = SLAB > RED ? SLAB : RED;
 };
 
 // One workgroup's share of dA (and, DX, of dX) or of dB: `sl` is its slice.
 // Which of the two is fixed at compile time, so that the count of loads and
 // stores in flight is the same on every path of the loop.
-template <int RT, bool DROP, bool DX, int NW>
+template <int RT, bool DROP, bool DX, int NW, int CB>
 __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchGradJob& job, int sl,
                                             int slot, char* smem, uint16_t* as) {
   using Sh = GradShape<RT, NW>;
@@ -932,8 +935,7 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, q4 = lane >> 4;
   const int cols = (int)job.cols;
-  const int half = wave % Sh::CH, way = wave / Sh::CH;
-  const int c0 = (sl * Sh::CH + half) * kGradSlice;
+  const int c0 = sl * CB * kGradSlice;
   const int M = g.M, r = g.r;
   const int j0 = (int)blockIdx.z * kGradRanks;
   // The slot's range of the order, cut to M tokens whatever the plan holds.
@@ -961,12 +963,12 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   };
   if (DX && slot == g.slots) {   // tokens without an adapter: dX = dX0
     if (g.dX == g.dX0) return;
-    int tok = tokens(way);
-    for (int ci = way; ci < nchunks; ci += Sh::NR) {
+    int tok = tokens(wave);
+    for (int ci = wave; ci < nchunks; ci += NW) {
       uint32_t off[4];
       uint4 v[4];
       places(tok, off);
-      tok = tokens(ci + Sh::NR);
+      tok = tokens(ci + NW);
 #pragma unroll
       for (int h = 0; h < 4; ++h) v[h] = bload128s(rx0, off[h], 0);
 #pragma unroll
@@ -976,9 +978,10 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   }
   float* const out = job.out + (int64_t)slot * cols * r;
   if (nt == 0) {   // a slot without tokens: zeros, whatever its scale
-    for (int e = way * 64 + lane; e < kGradSlice * 16 * RT; e += 64 * Sh::NR) {
-      const int j = job.trans ? e / kGradSlice : e % (16 * RT);
-      const int cc = c0 + (job.trans ? e % kGradSlice : e / (16 * RT));
+    constexpr int W = CB * kGradSlice;
+    for (int e = tid; e < W * 16 * RT; e += 64 * NW) {
+      const int j = job.trans ? e / W : e % (16 * RT);
+      const int cc = c0 + (job.trans ? e % W : e / (16 * RT));
       if (cc < cols && j0 + j < r)
         out[job.trans ? (int64_t)(j0 + j) * cols + cc : (int64_t)cc * r + j0 + j] = 0.0f;
     }
@@ -994,12 +997,16 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
   const uint4* const qcols = reinterpret_cast<const uint4*>(job.Q) + first * (3 * RT * 64) + lane;
   const uint4* const qrows = reinterpret_cast<const uint4*>(g.Urows) + first * (2 * RT * 64) + lane;
 
-  uint4 pv[4], qv[3][RT], uv[2][RT], xv[4];
+  uint4 pv[CB][4], qv[3][RT], uv[2][RT], xv[4];
   uint32_t off[4], next[4];
   auto load_p = [&](int tok) {
     places(tok, next);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) pv[h] = bload128s(rp, next[h], 0);
+    for (int b = 0; b < CB; ++b)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        pv[b][h] = bload128s(rp, b == 0 || (next[h] != kOOB && c + b * kGradSlice < cols)
+                                     ? next[h] + b * (kGradSlice * 2) : kOOB, 0);
   };
   // Past the wave's last chunk these load the slot's last again.
   auto load_q = [&](int ci, int z) {
@@ -1018,17 +1025,16 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
 #pragma unroll
     for (int h = 0; h < 4; ++h) xv[h] = bload128s(rx0, next[h], 0);
   };
-  int tok = tokens(way);
+  int tok = tokens(wave);
 #pragma unroll
-  for (int z = 2; z >= 0; --z) load_q(way, z);
-  if constexpr (DX) load_u(way);
+  for (int z = 2; z >= 0; --z) load_q(wave, z);
+  if constexpr (DX) load_u(wave);
   load_p(tok);
   if constexpr (DX) load_x();
-  tok = tokens(way + Sh::NR);
+  tok = tokens(wave + NW);
   if (DX) {   // as[column][rank] = A, transposed
     const uint16_t* const A = g.A + (int64_t)slot * r * cols;
-    as += half * kGradSlice * AW;
-    for (int e = way * 64 + lane; e < 16 * RT * (kGradSlice / 8); e += 64 * Sh::NR) {
+    for (int e = tid; e < 16 * RT * (kGradSlice / 8); e += 64 * NW) {
       const int j = e / (kGradSlice / 8), k0 = 8 * (e % (kGradSlice / 8));
       uint4 v = make_uint4(0, 0, 0, 0);
       if (j < r && c0 + k0 < cols) v = *reinterpret_cast<const uint4*>(A + (int64_t)j * cols + c0 + k0);
@@ -1039,15 +1045,17 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
     lds_barrier();
   }
 
-  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * Sh::PE;
-  f32x4_t acc[4][RT];
+  uint16_t* const my = reinterpret_cast<uint16_t*>(smem) + wave * CB * Sh::PE;
+  f32x4_t acc[CB][4][RT];
 #pragma unroll
-  for (int h = 0; h < 4; ++h)
+  for (int b = 0; b < CB; ++b)
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[b][h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const float s = DROP ? c_a * g.keep_scale : c_a;
 
-  for (int ci = way; ci < nchunks; ci += Sh::NR) {
+  for (int ci = wave; ci < nchunks; ci += NW) {
     uint32_t keep = 0;   // 8 bits per piece
 #pragma unroll
     for (int h = 0; h < 4; ++h) off[h] = next[h];
@@ -1059,8 +1067,9 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
     // A wave's LDS operations run in issue order: these stores land after the
     // last chunk's reads.
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint4 v = pv[h];
+    for (int bh = 0; bh < 4 * CB; ++bh) {
+      const int h = bh & 3;
+      uint4 v = pv[bh >> 2][h];
       if constexpr (DROP) {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -1069,22 +1078,26 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
                   ((keep >> (8 * h + 2 * e + 1)) & 1u ? 0xffff0000u : 0u);
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint4*>(my + 8 * (64 * h + lane)) = v;
+      *reinterpret_cast<uint4*>(my + 8 * (64 * bh + lane)) = v;
     }
     load_p(tok);
-    tok = tokens(ci + 2 * Sh::NR);
+    tok = tokens(ci + 2 * NW);
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-    bf16x8_t aop[4];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) aop[h] = slab_operand(my, h, lane);
+    for (int b = 0; b < CB; ++b) {
+      bf16x8_t aop[4];
 #pragma unroll
-    for (int z = 2; z >= 0; --z) {        // the small terms first
+      for (int h = 0; h < 4; ++h) aop[h] = slab_operand(my + b * Sh::PE, h, lane);
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
+      for (int z = 2; z >= 0; --z) {      // the small terms first
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          acc[h][t] = mfma_16x16x32(aop[h], __builtin_bit_cast(bf16x8_t, qv[z][t]), acc[h][t]);
-      load_q(ci + Sh::NR, z);
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            acc[b][h][t] =
+                mfma_16x16x32(aop[h], __builtin_bit_cast(bf16x8_t, qv[z][t]), acc[b][h][t]);
+        if (b == CB - 1) load_q(ci + NW, z);
+      }
     }
     if constexpr (DX) {
       // dX[m][c]: row operand A's column 16 k + i, ranks 16 ch + 8 (q4 & 1) ..;
@@ -1106,7 +1119,7 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
             d[tg][k] = mfma_16x16x32(wop, __builtin_bit_cast(bf16x8_t, uv[tg][ch]), d[tg][k]);
         }
       }
-      load_u(ci + Sh::NR);
+      load_u(ci + NW);
       float* const e = reinterpret_cast<float*>(my);   // 16 rows of 64 floats
 #pragma unroll
       for (int tg = 0; tg < 2; ++tg) {
@@ -1138,50 +1151,35 @@ __device__ __forceinline__ void grads_block(const BatchGradArgs& g, const BatchG
     }
   }
 
-  // acc[h][t][v] = O[c0 + 16 h + 4 q4 + v][j0 + 16 t + i]; the unit (h, t) is
-  // added by wave (h RT + t) mod NR of the slice's.
-  constexpr int NR = Sh::NR;
-  auto finish = [&](int unit, const f32x4_t& v) {
-    const int cc = c0 + 16 * (unit / RT) + 4 * q4;   // cc .. cc + 3 (cols is a multiple of 8)
-    const int j = j0 + 16 * (unit % RT) + i;
-    if (cc >= cols || j >= r) return;
-    if (job.trans) {
-      *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + cc) =
-          f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]};
-    } else {
+  // acc[b][h][t][v] = O[c0 + 64 b + 16 h + 4 q4 + v][j0 + 16 t + i]; the unit
+  // (h, t) is added by wave (h RT + t) mod NW.
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(smem) + lane;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[(int64_t)(cc + e) * r + j] = s * v[e];
-    }
-  };
-  f32x4_t* const red =
-      reinterpret_cast<f32x4_t*>(smem) + half * ((NR == 2 ? 1 : NR) * 4 * RT * 64) + lane;
-  lds_barrier();   // the slabs are free
-  if constexpr (NR == 2) {   // each hands the other half of its sums
-#pragma unroll
-    for (int u = 0; u < 4 * RT; u += 2)
-      red[64 * (u + 1 - way)] = way ? acc[u / RT][u % RT] : acc[(u + 1) / RT][(u + 1) % RT];
-    lds_barrier();
-#pragma unroll
-    for (int u = 0; u < 4 * RT; u += 2) {
-      f32x4_t v = way ? acc[(u + 1) / RT][(u + 1) % RT] : acc[u / RT][u % RT];
-      const f32x4_t o = red[64 * (u + way)];
-      v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
-      finish(u + way, v);
-    }
-  } else {
+  for (int b = 0; b < CB; ++b) {
+    lds_barrier();   // the slabs, or the last block's sums, are free
 #pragma unroll
     for (int h = 0; h < 4; ++h)
 #pragma unroll
-      for (int t = 0; t < RT; ++t) red[(way * 4 * RT + h * RT + t) * 64] = acc[h][t];
+      for (int t = 0; t < RT; ++t) red[(wave * 4 * RT + h * RT + t) * 64] = acc[b][h][t];
     lds_barrier();
-    for (int unit = way; unit < 4 * RT; unit += NR) {
+    for (int unit = wave; unit < 4 * RT; unit += NW) {
       f32x4_t v = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < NR; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const f32x4_t o = red[(w * 4 * RT + unit) * 64];
         v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
       }
-      finish(unit, v);
+      // cc .. cc + 3 (cols is a multiple of 8)
+      const int cc = c0 + b * kGradSlice + 16 * (unit / RT) + 4 * q4;
+      const int j = j0 + 16 * (unit % RT) + i;
+      if (cc >= cols || j >= r) continue;
+      if (job.trans) {
+        *reinterpret_cast<f32x4_t*>(out + (int64_t)j * cols + cc) =
+            f32x4_t{s * v[0], s * v[1], s * v[2], s * v[3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[(int64_t)(cc + e) * r + j] = s * v[e];
+      }
     }
   }
 }
@@ -1204,12 +1202,13 @@ template <int RT, bool DROP, bool DX, int NW>
 __global__ void __launch_bounds__(64 * NW, RT == 1 ? 3 : 2) k_batch_grads(BatchGradArgs g) {
   using Sh = GradShape<RT, NW>;
   __shared__ __attribute__((aligned(16))) char smem[Sh::SMEM];
-  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? Sh::CH * kGradSlice * Sh::AW : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t as[DX ? kGradSlice * Sh::AW : 8];
   const int slot = (int)blockIdx.y < g.slots ? slot_by_size(g.start, g.slots, blockIdx.y) : g.slots;
   if ((int)blockIdx.x < g.a.slices)
-    grads_block<RT, DROP, DX, NW>(g, g.a, blockIdx.x, slot, smem, as);
+    grads_block<RT, DROP, DX, NW, 1>(g, g.a, blockIdx.x, slot, smem, as);
   else if (slot < g.slots)   // the last row is dX's alone
-    grads_block<RT, false, false, NW>(g, g.b, (int)blockIdx.x - g.a.slices, slot, smem, as);
+    grads_block<RT, false, false, NW, grad_blocks_b<RT>()>(g, g.b, (int)blockIdx.x - g.a.slices,
+                                                           slot, smem, as);
 }
 
 // ------------------------------- launchers ---------------------------------
@@ -1397,11 +1396,11 @@ hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, in
     u.drop = key; u.keep_scale = d.scale;
     QLK_TRY((d.on ? up<true, true>(u, st) : up<true, false>(u, st)));
   }
-  const int64_t wide = kGradSlice;   // columns of a workgroup
-  auto slices = [&](int64_t cols) { return (int)((cols + wide - 1) / wide); };
+  auto slices = [](int64_t cols, int64_t wide) { return (int)((cols + wide - 1) / wide); };
+  const int blocks_b = a.r > 32 ? grad_blocks_b<4>() : grad_blocks_b<1>();
   BatchGradArgs ga{};
-  ga.a = BatchGradJob{X, K, Uc, dA, 1, slices(K)};
-  ga.b = BatchGradJob{dY, N, Tc, dB, 0, slices(N)};
+  ga.a = BatchGradJob{X, K, Uc, dA, 1, slices(K, kGradSlice)};
+  ga.b = BatchGradJob{dY, N, Tc, dB, 0, slices(N, kGradSlice * blocks_b)};
   ga.Urows = Ur; ga.chunks = pk.chunks;
   ga.M = (int)M; ga.r = a.r; ga.slots = a.slots; ga.scale = a.scale; ga.order = a.order;
   ga.start = a.start; ga.A = a.A; ga.dX0 = dX0; ga.dX = dX; ga.drop = key; ga.keep_scale = d.scale;
