@@ -76,6 +76,10 @@ __device__ __forceinline__ TileRow tile_row(const int* tiles, int i, int M, int 
 // at least the adapter's (which come from L2) up to rank 64, and slices fill
 // the device where there are few tiles.  A slice is the fast grid index, so
 // that an XCD keeps to its part of the adapters.
+// Measured: T, 2048 tokens x 4096, rank 16: 6.5 us (2.6 TB/s of X); with dropout
+// 12.9, bound by Philox's 32-bit products (10 rounds per four elements); 4096
+// tokens x 4096, rank 64: 13 us.  A single token: 3.2 us, the launch and two
+// trips to memory.
 constexpr int kDownWaves = 4;
 
 struct DownArgs {
@@ -386,7 +390,10 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
 //         16 t + 8 (g & 1) .. +7 of plane g / 2 (ranks along the contraction)
 // A chunk is 32 positions of the order of one slot; slot s begins at chunk
 // start[s] / 32 + s.  Ranks past r and tokens past the slot's last are zeros.
-// One workgroup per tile of the plan (two chunks), U or T, and 64 ranks.
+// One workgroup per chunk (half a tile of the plan), U or T, and 64 ranks.
+// Bound: latency, one round of loads of the slices and one of stores (4096
+// tokens at rank 64: 7.2 us, with a whole tile per workgroup 9.5; 2048 tokens
+// at rank 16: 4.2).
 struct PackJob {
   const float* part;
   int slices;
@@ -406,22 +413,24 @@ __host__ __device__ constexpr int64_t pack_chunks(int64_t M, int S) { return M /
 template <int RT>
 __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
   constexpr int QW = 16 * RT, LW = QW + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t pl[3][kPlanTile][LW];
-  __shared__ int rows[kPlanTile];
+  __shared__ __attribute__((aligned(16))) uint16_t pl[3][32][LW];
+  __shared__ int rows[32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const PackJob& job = blockIdx.y ? g.t : g.u;
-  const TileRow t = tile_row(g.tiles, blockIdx.x, g.M, g.slots);
+  TileRow t = tile_row(g.tiles, (int)blockIdx.x / 2, g.M, g.slots);
+  t.first += (int)blockIdx.x % 2 * 32;
+  t.count = min(t.count - (int)blockIdx.x % 2 * 32, 32);
   if (t.count <= 0 || t.slot < 0) return;
-  const int in_slot = t.first - g.start[t.slot];   // a multiple of 64
+  const int in_slot = t.first - g.start[t.slot];   // a multiple of 32
   const int64_t chunk = g.start[t.slot] / 32 + t.slot + in_slot / 32;
-  if (in_slot < 0 || chunk < 0 || chunk + (t.count > 32) >= g.chunks) return;   // no such plan
-  if (tid < kPlanTile) {
+  if (in_slot < 0 || chunk < 0 || chunk >= g.chunks) return;   // no such plan
+  if (tid < 32) {
     const int m = tid < t.count ? g.order[t.first + tid] : -1;
     rows[tid] = (unsigned)m < (unsigned)g.M ? m : -1;
   }
   __syncthreads();
   const int r = g.r, j0 = (int)blockIdx.z * 64;
-  for (int e = tid; e < kPlanTile * QW / 4; e += 256) {
+  for (int e = tid; e < 32 * QW / 4; e += 256) {
     const int tok = e / (QW / 4), j = 4 * (e % (QW / 4));
     const int m = rows[tok];
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -449,23 +458,21 @@ __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
   __syncthreads();
   const int i = lane & 15, q4 = lane >> 4;
   const int64_t block = (int64_t)blockIdx.z * g.chunks + chunk;
-  for (int u = wave; u < 2 * 3 * RT; u += 4) {
-    const int c = u / (3 * RT), z = u / RT % 3, k = u % RT;
-    if (32 * c >= t.count) break;
+  for (int u = wave; u < 3 * RT; u += 4) {
+    const int z = u / RT, k = u % RT;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      w[e] = pl[z][32 * c + 8 * q4 + 2 * e][16 * k + i] |
-             (uint32_t)pl[z][32 * c + 8 * q4 + 2 * e + 1][16 * k + i] << 16;
-    *reinterpret_cast<uint4*>(job.cols + (((block + c) * 3 + z) * RT + k) * 512 + 8 * lane) =
+      w[e] = pl[z][8 * q4 + 2 * e][16 * k + i] |
+             (uint32_t)pl[z][8 * q4 + 2 * e + 1][16 * k + i] << 16;
+    *reinterpret_cast<uint4*>(job.cols + ((block * 3 + z) * RT + k) * 512 + 8 * lane) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (job.rows == nullptr) return;
-  for (int u = wave; u < 2 * 2 * RT; u += 4) {
-    const int c = u / (2 * RT), tg = u / RT % 2, k = u % RT;
-    if (32 * c >= t.count) break;
-    *reinterpret_cast<uint4*>(job.rows + (((block + c) * 2 + tg) * RT + k) * 512 + 8 * lane) =
-        *reinterpret_cast<const uint4*>(&pl[q4 >> 1][32 * c + 16 * tg + i][16 * k + 8 * (q4 & 1)]);
+  for (int u = wave; u < 2 * RT; u += 4) {
+    const int tg = u / RT, k = u % RT;
+    *reinterpret_cast<uint4*>(job.rows + ((block * 2 + tg) * RT + k) * 512 + 8 * lane) =
+        *reinterpret_cast<const uint4*>(&pl[q4 >> 1][16 * tg + i][16 * k + 8 * (q4 & 1)]);
   }
 }
 
@@ -492,6 +499,9 @@ __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
 //    the first block's while t is gathered from its slices.
 // Bound: HBM, base read and out written once; W comes from L2 once per tile.
 // The column block is the fast grid index: an XCD keeps to its part of W.
+// Measured: 2048 tokens x 4096, rank 16: 9.9 us (33.6 MB, 3.4 TB/s); 4096 x
+// 11008, rank 64: 45 us (180 MB, 4.0 TB/s); 256 single tokens of 48 adapters x
+// 11008, rank 16: 10.2 us.
 constexpr int kUpCols = 128;    // columns per block
 constexpr int kUpWaves = kPlanTile / 16;
 constexpr int kUpSlab = 64 + 4; // row of a wave's 16 x 64 fp32 slab
@@ -856,9 +866,11 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
 // columns, dX = dX0 + drop(c_a U A_a).  Both gradients are O[c][j] = sum P[m][c]
 // Q[m][j], (P, Q) = (X, U) with O = dA^T or (dY, T) with O = dB.
 //
-// A workgroup owns a slot, 64 columns of P and up to 64 ranks, and contracts
-// over all of the slot's tokens, gathered through the plan's order: no partial
-// sums in memory, no atomics.  Its NW waves take every NW-th 32-token chunk.
+// A workgroup owns a slot, 64 columns of P (128 for dB at 64 ranks) and up to
+// 64 ranks, and contracts over all of the slot's tokens, gathered through the
+// plan's order: no partial sums in memory, no atomics.  Its NW waves take every
+// NW-th 32-token chunk.  The slot with the most tokens comes first, so that the
+// longest sums do not start last (78 -> 70 us below).
 //  * Lane L holds columns 8 (L % 8) of tokens 8 h + L / 8, h = 0..3: eight whole
 //    128-byte lines per instruction, for P, dX0 and dX alike, so that the
 //    dropout's words of X and of dX are drawn once.
@@ -867,12 +879,15 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
 //    take the next chunk's loads as soon as they are in the slab.  Q's operands
 //    (cols, and for dX rows) come packed from memory: passed through the slab
 //    as well, the three planes of 64 ranks bounded the kernel by LDS (4096
-//    tokens, 4096 x 11008: 85 us).
+//    tokens, 4096 x 11008: 84 us, packed 78).
 //  * dX's row operand, the slot's A over these columns, stays in LDS; the
 //    products leave through P's slab (16-byte pieces of row i XOR-swizzled by i).
 //  * The waves' sums are added in the order 0, 1, ..., NW - 1.
-// Bound: HBM, X, dY and dX0 read once, dX and all slots' dA and dB written;
-// Q is read by every column slice, from L2.
+// Bound: up to 32 ranks HBM, X, dY and dX0 read once, dX and all slots' dA and
+// dB written (2048 tokens, 4096 x 4096, rank 16: 14.8 us, 67 MB in and out, 4.5
+// TB/s; with dropout 23, Philox); at 64 ranks the L2, since every slice reads Q
+// (4096 tokens, 4096 x 11008, with dropout: 63 us; 641 MB from L2 in 69 us
+// before dB's slices were 128 wide).
 constexpr int kGradRanks = 64;
 constexpr int kGradSlice = 64;
 
@@ -1339,8 +1354,8 @@ template <int RT, bool DROP, bool DX>
 static void grads(const BatchGradArgs& g, hipStream_t st) {
   const dim3 grid((unsigned)(g.a.slices + g.b.slices), (unsigned)(g.slots + (DX ? 1 : 0)),
                   (unsigned)((g.r + kGradRanks - 1) / kGradRanks));
-  // Eight waves per workgroup, two workgroups a CU; four where the planes of
-  // 64 ranks fill the LDS.
+  // Eight waves per workgroup; four where the sums of 64 ranks, added through
+  // the LDS, would fill it.
   constexpr int NW = RT == 4 ? 4 : 8;
   hipLaunchKernelGGL((k_batch_grads<RT, DROP, DX, NW>), grid, dim3(64 * NW), 0, st, g);
 }
@@ -1379,7 +1394,7 @@ hipError_t launch_batch_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, in
   g.S = dY; g.M = (int)M; g.C = N; g.W = a.B; g.r = a.r; g.slots = a.slots;
   g.order = a.order; g.tiles = a.tiles; g.part = U;
   QLK_TRY((down<true, false>(g, st)));
-  const dim3 pgrid((unsigned)adapter_plan_tiles(M, a.slots), 2,
+  const dim3 pgrid(2 * (unsigned)adapter_plan_tiles(M, a.slots), 2,
                    (unsigned)((a.r + kGradRanks - 1) / kGradRanks));
   switch (grad_tiles(a.r)) {
     case 1: hipLaunchKernelGGL(k_batch_pack<1>, pgrid, dim3(256), 0, st, pk); break;
