@@ -104,6 +104,8 @@ struct DownArgs {
 template <bool WT, int RT>
 constexpr bool down_pairs() { return WT && RT == 4; }
 
+// T at 64 ranks: the sums and two steps of X and A take 296 registers, one wave
+// per SIMD.
 template <bool WT, bool DROP, int RT>
 __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_batch_down(DownArgs g) {
   constexpr bool PAIRS = down_pairs<WT, RT>();
