@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
 // Bound: HBM, base read and out written once; W comes from L2 once per tile.
 // The column block is the fast grid index: an XCD keeps to its part of W.
 // Measured: 2048 tokens x 4096, rank 16: 9.9 us (33.6 MB, 3.4 TB/s); 4096 x
-// 11008, rank 64: 45 us (180 MB, 4.0 TB/s); 256 single tokens of 48 adapters x
+// 11008, rank 64: 45 us (180 MB, 4.0 TB/s); 256 single tokens of 64 adapters x
 // 11008, rank 16: 10.2 us.
 constexpr int kUpCols = 128;    // columns per block
 constexpr int kUpWaves = kPlanTile / 16;
