@@ -19,6 +19,7 @@
 // 1024 requests.
 #include "device_common.h"
 #include "kernels.h"
+#include "plan_sum.h"
 
 namespace qlk {
 
@@ -58,8 +59,8 @@ __global__ void __launch_bounds__(NT) k_adapter_plan(PlanArgs g) {
   // One chunk's requests: this thread's class, its first token and number of
   // tokens; returns the chunk's end.  Lengths are clamped to what the M rows
   // hold: a request's tokens are [min(M, sum before), min(M, sum before +
-  // length)).  Sums saturate at M (saturating addition of non-negative numbers
-  // is associative), so no sum leaves 32 bits.
+  // length)).  Every sum is cut at M before it is formed (plan_sum.h): two
+  // requests can hold 2^31 tokens.
   int len = 0, cls = 0, beg = 0;
   auto scan_chunk = [&](int q0, int done) {
     int n = 0;
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(NT) k_adapter_plan(PlanArgs g) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(v, d);
-      if (lane >= d) v = min(g.M, v + o);
+      if (lane >= d) v = cut_sum(v, o, g.M);
     }
     if (lane == 63) part[wave] = v;
     __syncthreads();
@@ -81,11 +82,11 @@ __global__ void __launch_bounds__(NT) k_adapter_plan(PlanArgs g) {
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       if (w == wave) before = all;
-      all = min(g.M, all + part[w]);
+      all = cut_sum(all, part[w], g.M);
     }
     const int prev = __shfl_up(v, 1);
-    beg = lane ? min(g.M, before + prev) : before;
-    len = min(g.M, before + v) - beg;
+    beg = lane ? cut_sum(before, prev, g.M) : before;
+    len = cut_sum(before, v, g.M) - beg;
     __syncthreads();   // part is free again
     return all;
   };
