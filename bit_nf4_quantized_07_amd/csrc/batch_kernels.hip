@@ -15,7 +15,7 @@
 //
 // Sums and the small matrices T and U are fp32.  Where T or U feeds an MFMA
 // it goes in as a sum of bf16 terms, x = hi + mid (+ lo): two terms (within
-// 2^-17 of x) where the result is rounded to bf16, three (2^-25) where it is
+// 2^-16 of x) where the result is rounded to bf16, three (2^-39) where it is
 // kept in fp32.
 #include <type_traits>
 
@@ -43,12 +43,36 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// x = hi + mid + lo, bf16 terms; an infinity or NaN is hi alone.
-__device__ __forceinline__ void split3(float x, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
-  hi = f32_to_bf16(x);
-  const float rest = __builtin_isfinite(x) ? x - bf16_to_f32(hi) : 0.0f;
-  mid = f32_to_bf16(rest);
-  lo = f32_to_bf16(rest - bf16_to_f32(mid));
+// x as two bf16 terms, hi + mid2, and as three, hi + mid3 + lo.  A product with
+// an infinity has to be what x's own would be, so every term has x's sign and is
+// zero only where x is:
+//  * hi and mid3 are cut toward zero, which also keeps them finite where x lies
+//    above bf16's largest value.  Cut, three terms hold all 24 bits of x; of two
+//    the last is rounded (within 2^-16 of x; a first term rounded either way
+//    would save one bit more but leave a rest of either sign).
+//  * a term that would be zero is 2^-40 of hi, far below the others' rounding (a
+//    normal number for |x| down to 2^-86).
+//  * all terms of an infinity or NaN are x.
+__device__ __forceinline__ uint16_t cut_to_bf16(float x) { return (uint16_t)(__float_as_uint(x) >> 16); }
+struct Terms {
+  uint16_t hi, mid2, mid3, lo;
+};
+__device__ __forceinline__ Terms split(float x) {
+  if (!__builtin_isfinite(x)) {
+    const uint16_t v = f32_to_bf16(x);   // a NaN stays one
+    return {v, v, v, v};
+  }
+  Terms t;
+  t.hi = cut_to_bf16(x);
+  const float hi = bf16_to_f32(t.hi), rest = x - hi;
+  t.mid2 = f32_to_bf16(rest);
+  t.mid3 = cut_to_bf16(rest);
+  t.lo = f32_to_bf16(rest - bf16_to_f32(t.mid3));   // exact
+  const uint16_t tiny = f32_to_bf16(hi * 0x1p-40f);
+  if ((t.mid2 & 0x7fffu) == 0) t.mid2 = tiny;
+  if ((t.mid3 & 0x7fffu) == 0) t.mid3 = tiny;
+  if ((t.lo & 0x7fffu) == 0) t.lo = tiny;
+  return t;
 }
 
 // One row of the plan's tiles, its positions checked against M tokens and S
@@ -383,13 +407,14 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
 
 // ---------------------------------------------------------------------------
 // U and T as MFMA operands of the gradients' kernel: the slices of part are
-// added, split into three bf16 terms (planes) and written so that a wave loads
-// each operand as 1 KB in a row, lane after lane, with nothing to gather or
+// added, split into bf16 terms and written so that a wave loads each operand as 1 KB in a row, lane after lane, with nothing to gather or
 // transpose:
-//   cols  [chunk][plane][rank tile][lane][8]: rank 16 t + i of tokens 8 g ..
-//         8 g + 7 of the chunk, lane = 16 g + i (tokens along the contraction)
+//   cols  [chunk][term][rank tile][lane][8]: rank 16 t + i of tokens 8 g ..
+//         8 g + 7 of the chunk, lane = 16 g + i (tokens along the contraction),
+//         three terms
 //   rows  [chunk][token group][rank tile][lane][8]: token 16 tg + i, ranks
-//         16 t + 8 (g & 1) .. +7 of plane g / 2 (ranks along the contraction)
+//         16 t + 8 (g & 1) .. +7 of term g / 2 (ranks along the contraction),
+//         two terms
 // A chunk is 32 positions of the order of one slot; slot s begins at chunk
 // start[s] / 32 + s.  Ranks past r and tokens past the slot's last are zeros.
 // One workgroup per chunk (half a tile of the plan), U or T, and 64 ranks.
@@ -415,7 +440,7 @@ __host__ __device__ constexpr int64_t pack_chunks(int64_t M, int S) { return M /
 template <int RT>
 __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
   constexpr int QW = 16 * RT, LW = QW + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t pl[3][32][LW];
+  __shared__ __attribute__((aligned(16))) uint16_t pl[4][32][LW];   // hi, mid3, lo, mid2
   __shared__ int rows[32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const PackJob& job = blockIdx.y ? g.t : g.u;
@@ -449,11 +474,14 @@ __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
       }
     }
     const float f[4] = {v.x, v.y, v.z, v.w};
-    uint16_t x[3][4];
+    uint16_t x[4][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) split3(f[k], x[0][k], x[1][k], x[2][k]);
+    for (int k = 0; k < 4; ++k) {
+      const Terms q = split(f[k]);
+      x[0][k] = q.hi; x[1][k] = q.mid3; x[2][k] = q.lo; x[3][k] = q.mid2;
+    }
 #pragma unroll
-    for (int z = 0; z < 3; ++z)
+    for (int z = 0; z < 4; ++z)
       *reinterpret_cast<uint2*>(&pl[z][tok][j]) =
           make_uint2(x[z][0] | (uint32_t)x[z][1] << 16, x[z][2] | (uint32_t)x[z][3] << 16);
   }
@@ -474,7 +502,7 @@ __global__ void __launch_bounds__(256) k_batch_pack(PackArgs g) {
   for (int u = wave; u < 2 * RT; u += 4) {
     const int tg = u / RT, k = u % RT;
     *reinterpret_cast<uint4*>(job.rows + ((block * 2 + tg) * RT + k) * 512 + 8 * lane) =
-        *reinterpret_cast<const uint4*>(&pl[q4 >> 1][16 * tg + i][16 * k + 8 * (q4 & 1)]);
+        *reinterpret_cast<const uint4*>(&pl[q4 >> 1 ? 3 : 0][16 * tg + i][16 * k + 8 * (q4 & 1)]);
   }
 }
 
@@ -758,9 +786,12 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
       v.x *= c_a; v.y *= c_a; v.z *= c_a; v.w *= c_a;
     }
     const float f[4] = {v.x, v.y, v.z, v.w};
-    uint16_t hi[4], mid[4], lo;
+    uint16_t hi[4], mid[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) split3(f[k], hi[k], mid[k], lo);
+    for (int k = 0; k < 4; ++k) {
+      const Terms q = split(f[k]);
+      hi[k] = q.hi; mid[k] = q.mid2;
+    }
     uint16_t* const d = tl + tok * LD + (j / RK) * 2 * RK + j % RK;
     *reinterpret_cast<uint2*>(d) =
         make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
@@ -880,7 +911,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
 //    with the transposing read, tokens along the contraction; its registers
 //    take the next chunk's loads as soon as they are in the slab.  Q's operands
 //    (cols, and for dX rows) come packed from memory: passed through the slab
-//    as well, the three planes of 64 ranks bounded the kernel by LDS (4096
+//    as well, the three terms of 64 ranks bounded the kernel by LDS (4096
 //    tokens, 4096 x 11008: 84 us, packed 78).
 //  * dX's row operand, the slot's A over these columns, stays in LDS; the
 //    products leave through P's slab (16-byte pieces of row i XOR-swizzled by i).
@@ -1275,7 +1306,7 @@ BatchWorkspace batch_workspace(int64_t M, int64_t K, int64_t N, int r, int S, bo
   size_t off = 0;
   w.off_T = off; off += align256((size_t)slices_T(M, S, K) * M * r * 4);
   if (backward) {
-    // packed operands: 1 KB per chunk, plane (or token group) and rank tile
+    // packed operands: 1 KB per chunk, term (or token group) and rank tile
     const size_t chunks = (size_t)pack_chunks(M, S) * ((r + kGradRanks - 1) / kGradRanks);
     const size_t cols = chunks * 3 * grad_tiles(r) * 1024, rows = chunks * 2 * grad_tiles(r) * 1024;
     w.off_U = off; off += align256((size_t)slices_U(M, S, N, r) * M * r * 4);

@@ -340,9 +340,9 @@ int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, i
 /* Forward: for a token m of slot a
  *   T[m] = drop(X[m]) A_a^T,   out[m] = RNE_bf16(Y[m] + scale[a] T[m] B_a^T)
  * and T[m] = 0, out[m] = Y[m] without an adapter.  T is fp32 [M, r] (T_out, or
- * NULL if not wanted); the sum is held in fp32 and rounded once (T enters the
- * product as two bf16 terms, within 2^-17; where one is zero an infinity in B
- * gives NaN, as in the backward's products).
+ * NULL if not wanted); the sum is held in fp32 and rounded once.  T enters the
+ * product as two bf16 terms of its own sign, within 2^-16, so that an infinity
+ * in B meets T's sign (for |T| of at least 2^-86; a zero T gives NaN).
  * drop() is lora_dropout's mask for (p, seed) -- the same elements are kept --
  * times 1 / (1 - p), regenerated where elements are used: neither the mask nor
  * a dropped copy of X is stored, and X's kept values are not rounded.  p = 0
@@ -367,8 +367,9 @@ int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const 
  * dX[m] = dX0[m] without an adapter; a slot without tokens gets zeros.
  *   T fp32 [M, r] from the forward (NULL: computed again); dX0 bf16 [M, K]
  *   (NULL: zeros); dX may be dX0, or NULL to skip it.
- * U and T enter dA and dB as three bf16 terms (within 2^-25); the order of
- * every sum is fixed.  Sizes as in the forward; workspace of
+ * U and T enter dA and dB as three bf16 terms (within 2^-39) and U enters dX as
+ * two (2^-16), of their own sign as in the forward; the order of every sum is
+ * fixed.  Sizes as in the forward; workspace of
  * lora_adapters_workspace_bytes(M, K, N, r, S, 1). */
 int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t K, int64_t N,
                       const uint16_t* A, const uint16_t* B, const float* scale, int r, int S,
