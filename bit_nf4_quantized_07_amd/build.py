@@ -1,5 +1,7 @@
 """Build libqlora.so (gfx950) from the HIP sources in csrc/ with hipcc, and
-_calls.so, the C++ marshalling of the batched adapters' calls, with g++.
+_calls.so, the C++ marshalling of the batched adapters' Python calls, with g++
+and torch's headers.  The C library needs hipcc alone: it is built where the
+other cannot be.
 
     python -m bit_nf4_quantized_07_amd.build [--verbose]
 
@@ -60,8 +62,13 @@ def _compile(src: str, verbose: bool) -> str:
 
 def _build_calls(verbose: bool) -> None:
     """csrc/calls.cpp against torch's and Python's headers (host code only; it
-    gets the addresses of libqlora.so's functions when it is loaded)."""
-    import torch
+    gets the addresses of libqlora.so's functions when it is loaded).  Without
+    torch there is nothing it could marshal."""
+    try:
+        import torch
+    except ImportError as e:
+        print(f"_calls.so left out, torch is missing: {e}", file=sys.stderr)
+        return
     root = os.path.dirname(torch.__file__)
     tmp = CALLS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
@@ -79,12 +86,12 @@ def _build_calls(verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link the shared libraries; returns libqlora.so's path."""
+    """Compile every source and link the shared libraries; returns libqlora.so's
+    path.  Raises after libqlora.so is linked where only _calls.so failed."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         calls = ex.submit(_build_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     if verbose:
@@ -93,6 +100,10 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    failed = calls.exception()
+    if failed is not None:
+        raise RuntimeError("libqlora.so is built, _calls.so (the batched adapters' Python calls) "
+                           f"is not: {failed}") from failed
     return LIB
 
 

@@ -1,0 +1,64 @@
+"""The build's two libraries are apart: libqlora.so, the C library, needs hipcc
+alone; the batched adapters' Python binding needs g++ and torch's headers as
+well, and where it cannot be built the C library is built all the same.  Every
+compiler is replaced by a stand-in that writes its output file."""
+import os
+import sys
+import types
+
+import pytest
+
+from bit_nf4_quantized_07_amd import build as b
+
+
+@pytest.fixture
+def compilers(monkeypatch, tmp_path):
+    """Stand-ins for the compilers; `broken` holds the names of those that fail,
+    `missing` of those that are not there."""
+    state = types.SimpleNamespace(broken=set(), missing=set(), ran=[])
+
+    def run(cmd, **kw):
+        name = os.path.basename(cmd[0])
+        if name in state.missing:
+            raise FileNotFoundError(2, "No such file or directory", cmd[0])
+        state.ran.append(name)
+        if name in state.broken:
+            return types.SimpleNamespace(returncode=1, stdout="", stderr=f"{name} is broken")
+        out = cmd[cmd.index("-o") + 1]
+        with open(out, "w") as f:
+            f.write(name)
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(b, "subprocess", types.SimpleNamespace(run=run))
+    monkeypatch.setattr(b, "hipcc", lambda: "/opt/hipcc")
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "obj"))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libqlora.so"))
+    monkeypatch.setattr(b, "CALLS", str(tmp_path / "_calls.so"))
+    return state
+
+
+def test_both_are_built(compilers):
+    assert b.build() == b.LIB
+    assert os.path.exists(b.LIB) and os.path.exists(b.CALLS)
+
+
+@pytest.mark.parametrize("kind", ["broken", "missing"])
+def test_the_c_library_does_not_need_gxx(compilers, kind):
+    getattr(compilers, kind).add("g++")
+    with pytest.raises(RuntimeError, match="libqlora.so is built"):
+        b.build()
+    assert os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
+
+
+def test_the_c_library_does_not_need_torch(compilers, monkeypatch, capsys):
+    monkeypatch.setitem(sys.modules, "torch", None)        # import torch: ImportError
+    assert b.build() == b.LIB
+    assert os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
+    assert "g++" not in compilers.ran and "torch" in capsys.readouterr().err
+
+
+def test_a_failed_hip_source_is_an_error(compilers):
+    compilers.broken.add("hipcc")
+    with pytest.raises(RuntimeError, match="hipcc failed"):
+        b.build()
+    assert not os.path.exists(b.LIB)
