@@ -60,7 +60,7 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _build_calls(verbose: bool) -> None:
+def _build_calls(verbose: bool) -> bool:
     """csrc/calls.cpp against torch's and Python's headers (host code only; it
     gets the addresses of libqlora.so's functions when it is loaded).  Without
     torch there is nothing it could marshal."""
@@ -68,7 +68,7 @@ def _build_calls(verbose: bool) -> None:
         import torch
     except ImportError as e:
         print(f"_calls.so left out, torch is missing: {e}", file=sys.stderr)
-        return
+        return False
     root = os.path.dirname(torch.__file__)
     tmp = CALLS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
@@ -83,6 +83,7 @@ def _build_calls(verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    return True
 
 
 def build(verbose: bool = False) -> str:
@@ -101,6 +102,8 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
     failed = calls.exception()
+    if (failed is not None or not calls.result()) and os.path.exists(CALLS):
+        os.remove(CALLS)   # an older one may call libqlora.so's functions otherwise
     if failed is not None:
         raise RuntimeError("libqlora.so is built, _calls.so (the batched adapters' Python calls) "
                            f"is not: {failed}") from failed

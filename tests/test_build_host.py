@@ -62,3 +62,16 @@ def test_a_failed_hip_source_is_an_error(compilers):
     with pytest.raises(RuntimeError, match="hipcc failed"):
         b.build()
     assert not os.path.exists(b.LIB)
+
+
+@pytest.mark.parametrize("without", ["g++", "torch"])
+def test_no_older_binding_stays_beside_a_new_library(compilers, monkeypatch, without):
+    b.build()
+    if without == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+        b.build()
+    else:
+        compilers.broken.add("g++")
+        with pytest.raises(RuntimeError, match="libqlora.so is built"):
+            b.build()
+    assert os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
