@@ -12,6 +12,7 @@ or no GPU is visible, the compute calls raise.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import NamedTuple, Optional
 
@@ -605,10 +606,10 @@ def adapter_plan(slots, S: int, lengths=None, tokens: Optional[int] = None) -> A
     return AdapterPlan(res[1], res[2], res[3], res[4], S)
 
 
-def _refused_batch(X, A, B, scale, plan, others):
-    """_refused for the tensors that the forward and the backward share;
-    others(M, K, N, r, S) gives the call's own (name, tensor or None, dtype,
-    shape) items."""
+def _refused_batch(fn, X, A, B, scale, plan, ws, others):
+    """_refused for the tensors that the forward and the backward share and the
+    workspace's memory; others(M, K, N, r, S) gives the call's own (name, tensor
+    or None, dtype, shape) items."""
     torch = _torch()
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X: a 2-D tensor")
@@ -621,14 +622,23 @@ def _refused_batch(X, A, B, scale, plan, others):
     M, K = X.shape
     S, r, _ = A.shape
     N = B.shape[1]
-    if plan.S != S:
+    try:
+        slots = operator.index(plan.S)
+    except TypeError:
+        raise ValueError("plan: S, its number of slots, is not a whole number") from None
+    if slots != S:
         raise ValueError(f"plan: built for {plan.S} slots, the adapters have {S}")
     bf, i32 = torch.bfloat16, torch.int32
-    nt = M // PLAN_TILE + min(M, S + 1)
+    nt = load_library().lora_adapter_tiles(M, S)
+    if nt == 0:
+        raise QLoRAError(fn, ERR_SHAPE)
     items = [("X", X, bf, (M, K)), ("A", A, bf, (S, r, K)), ("B", B, bf, (S, N, r)),
              ("scale", scale, torch.float32, (S,)), ("order", plan.order, i32, (M,)),
              ("start", plan.start, i32, (S + 2,)), ("tiles", plan.tiles, i32, (nt, 3))]
-    _refused(items + [it for it in others(M, K, N, r, S) if it[1] is not None])
+    items += [it for it in others(M, K, N, r, S) if it[1] is not None]
+    if ws is not None:
+        items.append(("workspace", ws, torch.uint8, tuple(ws.shape)))
+    _refused(items)
 
 
 def _dropout_args(dropout):
@@ -662,7 +672,7 @@ def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: boo
     if res is None:
         torch = _torch()
         bf = torch.bfloat16
-        _refused_batch(X, A, B, scale, plan, lambda M, K, N, r, S: [
+        _refused_batch("lora_adapters_fwd", X, A, B, scale, plan, ws, lambda M, K, N, r, S: [
             ("Y", Y, bf, (M, N)), ("out", out, bf, (M, N)), ("T_out", T_out, torch.float32, (M, r))])
     if res[0] != OK:
         raise QLoRAError("lora_adapters_fwd", res[0])
@@ -687,7 +697,7 @@ def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout
         bf, f32 = torch.bfloat16, torch.float32
         if dY is None:
             raise ValueError("dY: missing")
-        _refused_batch(X, A, B, scale, plan, lambda M, K, N, r, S: [
+        _refused_batch("lora_adapters_bwd", X, A, B, scale, plan, ws, lambda M, K, N, r, S: [
             ("dY", dY, bf, (M, N)), ("T", T, f32, (M, r)), ("dX", dX, bf, (M, K)),
             ("dX_out", dX_out, bf, (M, K)), ("dA", dA_out, f32, (S, r, K)),
             ("dB", dB_out, f32, (S, N, r))])

@@ -96,8 +96,8 @@ struct Batch {
     scale = c.one(s, at::kFloat, {sa[0]});
     order = c.one(PyTuple_GET_ITEM(plan, 1), at::kInt, {M});
     start = c.one(PyTuple_GET_ITEM(plan, 2), at::kInt, {sa[0] + 2});
-    tiles = c.one(PyTuple_GET_ITEM(plan, 3), at::kInt, {M / 64 + std::min(M, sa[0] + 1), 3});
-    return c.ok;
+    tiles = c.one(PyTuple_GET_ITEM(plan, 3), at::kInt, {g_tiles(M, S), 3});
+    return c.ok && tiles->size(0) > 0;
   }
 };
 

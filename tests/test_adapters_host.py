@@ -159,3 +159,42 @@ def test_plan_binding_refusals():
     _raises("lengths: shape", q.adapter_plan, slots=s, S=2, lengths=s[:3], tokens=8)
     _raises("tokens:", q.adapter_plan, slots=s, S=2, lengths=s)
     _raises("not on a CUDA", q.adapter_plan, slots=s, S=2)
+
+
+def test_every_refusal_names_its_cause():
+    """What the calls' quick check in C++ refuses is named by the binding's."""
+    a = _args()
+    b = dict({k: v for k, v in a.items() if k != "Y"}, dY=a["Y"])
+    for bad in (float(S), str(S)):
+        plan = _plan()._replace(S=bad)
+        _raises("plan: S", q.adapters_fwd, **dict(a, plan=plan))
+        _raises("plan: S", q.adapters_bwd, **dict(b, plan=plan))
+    # sizes that no plan has: the status of the C ABI, not a tensor's
+    big = 1025
+    a = dict(a, A=torch.zeros(big, R, K, dtype=bf), B=torch.zeros(big, N, R, dtype=bf),
+             scale=torch.zeros(big), plan=q.AdapterPlan(*_plan()[:4], big))
+    with pytest.raises(q.QLoRAError) as e:
+        q.adapters_fwd(**a)
+    assert e.value.status == q.ERR_SHAPE
+
+
+def test_a_workspace_elsewhere_is_named(monkeypatch):
+    """A Workspace's memory is among what the refusal checks by name, so that one
+    on another device than the tensors is reported as the workspace."""
+    names = []
+
+    class Named(q._Checker):
+        def __call__(self, name, *rest):
+            names.append(name)
+            return super().__call__(name, *rest)
+
+    monkeypatch.setattr(q, "_Checker", Named)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    monkeypatch.setattr(q, "_batch_workspace", lambda *a: ws)
+    a = _args()
+    _raises("not on a CUDA", q.adapters_fwd, **a, workspace=object())
+    assert names[-1] == "workspace"
+    b = dict({k: v for k, v in a.items() if k != "Y"}, dY=a["Y"])
+    names.clear()
+    _raises("not on a CUDA", q.adapters_bwd, **b, workspace=object())
+    assert names[-1] == "workspace"
