@@ -662,7 +662,8 @@ def adapters_fwd(X, Y, A, B, scale, plan: AdapterPlan, dropout=None, save_T: boo
                  out=None, T_out=None, workspace=None):
     """out = Y + scale (drop(X) A^T) B^T, every token with its slot's A [S, r,
     K], B [S, N, r] and scale [S].  Y bf16 [M, N] is the shared projection's
-    output (None: the adapters' term alone; out may be Y).  dropout: None or
+    output (None: the adapters' term alone; out may be Y, and outputs overlap
+    nothing else).  dropout: None or
     (p, seed), lora_dropout's mask, regenerated where it is needed.  Scratch
     memory is torch's unless a Workspace is given.  Returns (out bf16 [M, N], T
     fp32 [M, r] or None)."""
@@ -683,7 +684,8 @@ def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout
                  need_dX: bool = True, dX_out=None, dA_out=None, dB_out=None, workspace=None):
     """Backward of adapters_fwd: (dX bf16 [M, K] or None, dA fp32 [S, r, K],
     dB fp32 [S, N, r]).  dX, if given, is what the shared projection's backward
-    gave: the adapters' term is added to it (dX_out may be the same tensor).
+    gave: the adapters' term is added to it (dX_out may be the same tensor;
+    outputs overlap nothing else).
     T from the forward (None: computed again); dropout as in the forward.
     Scratch memory is torch's unless a Workspace is given."""
     if not need_dX and (dX is not None or dX_out is not None):

@@ -6,7 +6,8 @@
 //
 // Each call checks its tensors like the binding's checker (type, shape,
 // contiguity, one HIP device) and returns None where one fails, for the
-// checker to name; else (status, outputs...).  Outputs that are not given, and
+// checker to name; else (status, outputs...).  An output that overlaps an input
+// or another output raises ValueError here.  Outputs that are not given, and
 // scratch memory where no workspace is given, come from torch's allocator on
 // the current stream of the tensors' device, on which the call is made.
 #define PY_SSIZE_T_CLEAN
@@ -101,6 +102,35 @@ struct Batch {
   }
 };
 
+struct Named {
+  const char* name;
+  const at::Tensor* t;   // null: not given
+};
+bool overlap(const at::Tensor& a, const at::Tensor& b) {
+  const char* const p = static_cast<const char*>(a.data_ptr());
+  const char* const q = static_cast<const char*>(b.data_ptr());
+  return p < q + b.nbytes() && q < p + a.nbytes();
+}
+// False, with Python's ValueError set, where an output given by the caller
+// shares memory with an input or another output.  The first output may be
+// `base`, the tensor it adds to, itself.
+bool apart(std::initializer_list<Named> outs, std::initializer_list<Named> ins, Named base) {
+  for (const Named* o = outs.begin(); o != outs.end(); ++o) {
+    if (!o->t) continue;
+    const bool adds = o == outs.begin() && base.t && o->t->data_ptr() == base.t->data_ptr();
+    const Named* with = !adds && base.t && overlap(*o->t, *base.t) ? &base : nullptr;
+    for (const Named& i : ins)
+      if (i.t && overlap(*o->t, *i.t)) with = &i;
+    for (const Named* p = outs.begin(); p != o; ++p)
+      if (p->t && overlap(*o->t, *p->t)) with = p;
+    if (with) {
+      PyErr_Format(PyExc_ValueError, "%s: overlaps %s", o->name, with->name);
+      return false;
+    }
+  }
+  return true;
+}
+
 // The given workspace's memory, or fresh scratch of `need` bytes (held by
 // `own`).  A 1-D byte tensor that is too small is the library's to refuse.
 void* scratch(Checked& c, PyObject* o, size_t need, at::Tensor& own, size_t* bytes) {
@@ -181,6 +211,10 @@ PyObject* call_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int save = PyObject_IsTrue(a[8]);
     if (save < 0) return nullptr;
     if (!c.ok) return none();
+    if (!apart({{"out", out}, {"T_out", T}},
+               {{"X", b.X}, {"A", b.A}, {"B", b.B}, {"scale", b.scale}, {"plan", b.order},
+                {"plan", b.start}, {"plan", b.tiles}}, {"Y", Y}))
+      return nullptr;
     const c10::DeviceGuard guard(c.device);
     at::Tensor own_out, own_T, own_ws;
     if (!out) out = &(own_out = fresh(c, at::kBFloat16, {b.M, b.N}));
@@ -217,6 +251,10 @@ PyObject* call_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int need = PyObject_IsTrue(a[10]);
     if (need < 0) return nullptr;
     if (!c.ok) return none();
+    if (!apart({{"dX_out", dX}, {"dA", dA}, {"dB", dB}},
+               {{"dY", dY}, {"X", b.X}, {"A", b.A}, {"B", b.B}, {"scale", b.scale}, {"T", T},
+                {"plan", b.order}, {"plan", b.start}, {"plan", b.tiles}}, {"dX", dX0}))
+      return nullptr;
     const c10::DeviceGuard guard(c.device);
     at::Tensor own_dX, own_dA, own_dB, own_ws;
     if (!dX && need) dX = &(own_dX = fresh(c, at::kBFloat16, {b.M, b.K}));

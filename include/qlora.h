@@ -348,7 +348,7 @@ int lora_adapter_plan(const int32_t* lengths, const int32_t* slots, int64_t Q, i
  * a dropped copy of X is stored, and X's kept values are not rounded.  p = 0
  * drops nothing.  A captured graph repeats the seed it was captured with.
  *   Y bf16 [M, N] (NULL: zeros), out bf16 [M, N]; out may be Y, and otherwise
- *   no output may overlap an input.
+ *   no output may overlap an input or another output.
  *   order, start, tiles: from lora_adapter_plan with the same M and S.
  * Requires r % 8 == 0, 8 <= r <= 256; K % 8 == 0, N % 8 == 0, both at most
  * 2^23; X, Y and one slot's A and B under 2 GiB each; 6 M r < 2^31; at most
@@ -366,7 +366,8 @@ int lora_adapters_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const 
  * over the slot's tokens, drop() as in the forward with the same p and seed.
  * dX[m] = dX0[m] without an adapter; a slot without tokens gets zeros.
  *   T fp32 [M, r] from the forward (NULL: computed again); dX0 bf16 [M, K]
- *   (NULL: zeros); dX may be dX0, or NULL to skip it.
+ *   (NULL: zeros); dX may be dX0, or NULL to skip it.  Otherwise no output may
+ *   overlap an input or another output.
  * U and T enter dA and dB as three bf16 terms (within 2^-39) and U enters dX as
  * two (2^-16), of their own sign as in the forward; the order of every sum is
  * fixed.  Sizes as in the forward; workspace of
