@@ -100,10 +100,15 @@ __device__ __forceinline__ TileRow tile_row(const int* tiles, int i, int M, int 
 // at least the adapter's (which come from L2) up to rank 64, and slices fill
 // the device where there are few tiles.  A slice is the fast grid index, so
 // that an XCD keeps to its part of the adapters.
-// Measured: T, 2048 tokens x 4096, rank 16: 6.5 us (2.6 TB/s of X); with dropout
-// 12.9, bound by Philox's 32-bit products (10 rounds per four elements); 4096
-// tokens x 4096, rank 64: 13 us.  A single token: 3.2 us, the launch and two
-// trips to memory.
+// Measured: T, 2048 tokens x 4096, rank 16: 6.5 us (2.6 TB/s of X); 4096 tokens
+// x 4096, rank 64: 13 us.  A single token: 3.2 us, the launch and two trips to
+// memory.  With dropout the 2048 tokens take 13.4 us, bound by Philox's 32-bit
+// products (10 rounds per four elements) and by the tail: 8 slices of 33 to 36
+// tiles are 264 to 288 equal workgroups, so some of the 256 CUs hold two, which
+// take twice as long side by side.
+// U, 4096 tokens, 4096 x 11008, rank 64: 35 us, 186 MB from L2 at 5.2 TB/s and
+// 109 MB of HBM at 3.1: neither, but the wait at every step's barrier with one
+// step of loads in flight.
 constexpr int kDownWaves = 4;
 
 struct DownArgs {
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(64 * kDownWaves, !WT && RT == 4 ? 1 : 2) k_bat
 // start[s] / 32 + s.  Ranks past r and tokens past the slot's last are zeros.
 // One workgroup per chunk (half a tile of the plan), U or T, and 64 ranks.
 // Bound: latency, one round of loads of the slices and one of stores (4096
-// tokens at rank 64: 7.2 us, with a whole tile per workgroup 9.5; 2048 tokens
+// tokens at rank 64: 7.5 us, with a whole tile per workgroup 9.5; 2048 tokens
 // at rank 16: 4.2).
 struct PackJob {
   const float* part;
@@ -918,9 +923,12 @@ __global__ void __launch_bounds__(64 * kUpWaves) k_batch_up(UpArgs g) {
 //  * The waves' sums are added in the order 0, 1, ..., NW - 1.
 // Bound: up to 32 ranks HBM, X, dY and dX0 read once, dX and all slots' dA and
 // dB written (2048 tokens, 4096 x 4096, rank 16: 14.8 us, 67 MB in and out, 4.5
-// TB/s; with dropout 23, Philox); at 64 ranks the L2, since every slice reads Q
-// (4096 tokens, 4096 x 11008, with dropout: 63 us; 641 MB from L2 in 69 us
-// before dB's slices were 128 wide).
+// TB/s; with dropout 23, Philox); at 64 ranks L2 and HBM together, since every
+// slice reads Q (4096 tokens, 4096 x 11008: 56.6 us, with dropout 62 to 65: 497
+// MB from L2 at 8 TB/s, about 260 MB of HBM at 4.2).
+// The tokens of a slot are not split, so the slots in use times (K + N) / 64
+// workgroups are all there is: one adapter of 4096 x 4096 takes 20.1 us for the
+// same 2048 tokens, of 1024 x 1024 18.7.
 constexpr int kGradRanks = 64;
 constexpr int kGradSlice = 64;
 
@@ -1336,13 +1344,18 @@ static hipError_t up(const UpArgs& g, hipStream_t st) {
   // Workgroups per tile: about four per CU in all, two where most tiles are
   // narrow (a narrow tile takes two blocks at a time; 16 single tokens, 28672
   // columns: 7.8 against 11.0 us; 2048 tokens, 4096 columns: 11.0 against 10.2),
-  // whole multiples of the XCDs where there are that many.
+  // cut to a whole multiple of the XCDs where there are that many.  The same
+  // number of blocks for each, then, only where that number divides them: 15
+  // blocks go to eight workgroups, two to seven of them and one to the last
+  // (2048 tokens, 1920 columns: 7.4 us; 2048 columns, two each: 7.5).  Narrow
+  // tiles' rounds of two blocks may differ by one between workgroups too (28672
+  // columns, 16 tiles: three or four).
   const int64_t blocks = (g.cols + kUpCols - 1) / kUpCols;
   const int64_t tiles = expected_tiles(g.M, g.slots);
   int64_t gx = (g.M <= 16 * tiles ? 2 : 4) * kCUs / tiles;
   if (gx < 1) gx = 1;
   if (gx > blocks) gx = blocks;
-  const int64_t per = (blocks + gx - 1) / gx;   // the same number of blocks for each
+  const int64_t per = (blocks + gx - 1) / gx;   // no workgroup without its share of blocks
   gx = (blocks + per - 1) / per;
   if (gx >= kXCDs) gx -= gx % kXCDs;
   const dim3 grid((unsigned)gx, (unsigned)adapter_plan_tiles(g.M, g.slots));
