@@ -1344,12 +1344,15 @@ static hipError_t up(const UpArgs& g, hipStream_t st) {
   // Workgroups per tile: about four per CU in all, two where most tiles are
   // narrow (a narrow tile takes two blocks at a time; 16 single tokens, 28672
   // columns: 7.8 against 11.0 us; 2048 tokens, 4096 columns: 11.0 against 10.2),
-  // cut to a whole multiple of the XCDs where there are that many.  The same
-  // number of blocks for each, then, only where that number divides them: 15
-  // blocks go to eight workgroups, two to seven of them and one to the last
-  // (2048 tokens, 1920 columns: 7.4 us; 2048 columns, two each: 7.5).  Narrow
-  // tiles' rounds of two blocks may differ by one between workgroups too (28672
-  // columns, 16 tiles: three or four).
+  // cut to a whole multiple of the XCDs where there are that many, so that an XCD
+  // meets the same part of W in every tile (calls, with and without the cut: 4096
+  // tokens, 11008 columns, rank 64: 57 and 65 us).  It undoes equal shares: 15
+  // blocks go to eight workgroups, two to seven of them and one to the last,
+  // which costs at rank 16, where W is small (2048 tokens: 1664 columns 14.2 and
+  // 13.5, 1920 14.0 and 13.8, 11008 25.5 and 24.2, multiples of 1024 level; 256
+  // single tokens, 11008 columns: 15.0 and 14.0).  Narrow tiles' rounds of two
+  // blocks may differ by one between workgroups too (28672 columns, 16 tiles:
+  // three or four).
   const int64_t blocks = (g.cols + kUpCols - 1) / kUpCols;
   const int64_t tiles = expected_tiles(g.M, g.slots);
   int64_t gx = (g.M <= 16 * tiles ? 2 : 4) * kCUs / tiles;
