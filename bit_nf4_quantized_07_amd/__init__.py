@@ -27,6 +27,7 @@ BWD_ACCUMULATE_DX = 1
 BLOCKSIZE = 64
 DQ_BLOCKSIZE = 256
 PLAN_TILE = 64
+BASE_INT8, BASE_NF4, BASE_BF16 = 0, 1, 2
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -106,6 +107,20 @@ SIGNATURES = {
     "lora_adapters_bwd": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P,
                                ctypes.c_double, ctypes.c_uint64, _P, _P, _P, _P, ctypes.c_size_t,
                                _P]),
+    "int8_quantize": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "int8_quantize_fp32": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "int8_dequant": (_I, [_P, _P, _I64, _I64, _I, _P, _P]),
+    "int8_linear_fwd": (_I, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I, _F, _P, _P, _P,
+                             ctypes.c_size_t, _P]),
+    "int8_linear_bwd": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _I, _F, _P, _P, _P, _P,
+                             _I, _P, ctypes.c_size_t, _P]),
+    "qlora_linear_bwd_int8": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _F, _P,
+                                   _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    "qlora_linear_bwd_bf16_int8": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I, _F, _P, _P, _P,
+                                        _P, _I, _P, ctypes.c_size_t, _P]),
+    "int8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I, _I, _I]),
+    "silu_mul_fwd_int8": (_I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "silu_mul_bwd_int8": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _P, _P, _P]),
 }
 
 _lib = None
@@ -565,8 +580,12 @@ def _load_calls():
         try:
             from . import _calls as mod
         except ImportError as e:
-            raise RuntimeError("the batched adapters' binding is missing: build it with "
-                               "`python -m bit_nf4_quantized_07_amd.build`") from e
+            raise RuntimeError("the batched adapters' and 8-bit calls' binding is missing: build it "
+                               "with `python -m bit_nf4_quantized_07_amd.build`") from e
+        mod.bind8(*(ctypes.cast(getattr(lib, n), _P).value for n in (
+            "int8_quantize", "int8_quantize_fp32", "int8_dequant", "int8_linear_workspace_bytes",
+            "int8_linear_fwd", "int8_linear_bwd", "qlora_linear_bwd_int8",
+            "qlora_linear_bwd_bf16_int8", "silu_mul_fwd_int8", "silu_mul_bwd_int8")))
         mod.bind(*(ctypes.cast(getattr(lib, n), _P).value for n in (
             "lora_adapter_tiles", "lora_adapter_plan", "lora_adapters_workspace_bytes",
             "lora_adapters_fwd", "lora_adapters_bwd")))
@@ -706,6 +725,217 @@ def adapters_bwd(dY, X, A, B, scale, plan: AdapterPlan, T=None, dX=None, dropout
     if res[0] != OK:
         raise QLoRAError("lora_adapters_bwd", res[0])
     return res[1], res[2], res[3]
+
+
+# ---------------------------------------------------------------------------
+# activations and weights in 8 bits
+# ---------------------------------------------------------------------------
+
+class Int8Tensor(NamedTuple):
+    """A matrix [rows, cols] in 8 bits: codes times a scale per row (what
+    products read), or per block of 64 columns (what is used element by
+    element)."""
+    codes: "object"   # int8 [rows, cols]
+    scale: "object"   # fp32 [rows] or [rows, cols / 64]
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def _int8_items(name, t, blocks=None):
+    """_refused's items of an Int8Tensor; raises if it is none, or if its scales
+    are not per row (blocks False) or per block (True)."""
+    torch = _torch()
+    if not isinstance(t, Int8Tensor):
+        raise ValueError(f"{name}: an Int8Tensor")
+    for part, x in (("codes", t.codes), ("scale", t.scale)):
+        if not isinstance(x, torch.Tensor):
+            raise ValueError(f"{name}.{part}: not a tensor")
+    if t.codes.dim() != 2:
+        raise ValueError(f"{name}.codes: a 2-D int8 tensor")
+    rows, cols = t.codes.shape
+    if blocks is None:
+        blocks = t.scale.dim() == 2
+    if blocks and cols % BLOCKSIZE:
+        raise ValueError(f"{name}: blocks of {BLOCKSIZE} columns, it has {cols}")
+    return [(f"{name}.codes", t.codes, torch.int8, (rows, cols)),
+            (f"{name}.scale", t.scale, torch.float32, (rows, cols // BLOCKSIZE) if blocks else (rows,))]
+
+
+def _int8_workspace(workspace, X, N, r, base, backward):
+    """The memory of a caller's Workspace for this call (None: none given; the
+    call then takes scratch memory from torch's allocator)."""
+    if workspace is None:
+        return None
+    torch = _torch()
+    if not (isinstance(X, Int8Tensor) and isinstance(X.codes, torch.Tensor) and X.codes.is_cuda
+            and X.codes.dim() == 2):
+        return None                     # refused by the call
+    need = load_library().int8_linear_workspace_bytes(X.codes.shape[0], X.codes.shape[1], N, r, base,
+                                                      1 if backward else 0)
+    return workspace.get(need, torch.cuda.current_stream(X.codes.device))[0]
+
+
+def int8_quantize(X, codes_out=None, scale_out=None) -> Int8Tensor:
+    """X bf16 or fp32 [M, K] (activations by token, a weight by output channel)
+    in rows of 8 bits: scale = max |row| / 127, codes the nearest integers to
+    row / scale.  A row with an infinity or NaN stands for NaN throughout."""
+    res = (_bound_calls or _load_calls()).quantize8(X, codes_out, scale_out)
+    if res is None:
+        torch = _torch()
+        if not isinstance(X, torch.Tensor) or X.dim() != 2:
+            raise ValueError("X: a 2-D tensor")
+        items = [("X", X, torch.float32 if X.dtype == torch.float32 else torch.bfloat16, tuple(X.shape))]
+        if codes_out is not None:
+            items.append(("codes_out", codes_out, torch.int8, tuple(X.shape)))
+        if scale_out is not None:
+            items.append(("scale_out", scale_out, torch.float32, (X.shape[0],)))
+        _refused(items)
+    if res[0] != OK:
+        raise QLoRAError("int8_quantize", res[0])
+    return Int8Tensor(res[1], res[2])
+
+
+def int8_dequant(X: Int8Tensor, out=None):
+    """-> bf16 [rows, cols]: codes times scales, rounded once."""
+    if not isinstance(X, Int8Tensor):
+        raise ValueError("X: an Int8Tensor")
+    res = (_bound_calls or _load_calls()).dequant8(X.codes, X.scale, out)
+    if res is None:
+        items = _int8_items("X", X)
+        if out is not None:
+            items.append(("out", out, _torch().bfloat16, tuple(X.codes.shape)))
+        _refused(items)
+    if res[0] != OK:
+        raise QLoRAError("int8_dequant", res[0])
+    return res[1]
+
+
+def linear_fwd_int8(X: Int8Tensor, W: Int8Tensor, A=None, B=None, alpha: float = 0.0,
+                    save_T: bool = True, out=None, T_out=None, workspace=None):
+    """Y = X W^T + (alpha/r) (X A^T) B^T with X [M, K] and the base W [N, K] in
+    rows of 8 bits (int8_quantize); without A and B the first term alone.
+    Returns (Y bf16 [M, N], T = X A^T fp32 [M, r] or None).  Outputs overlap no
+    input.  Scratch memory is torch's unless a Workspace is given."""
+    torch = _torch()
+    if workspace is not None:
+        known = isinstance(W, Int8Tensor) and isinstance(W.codes, torch.Tensor) and W.codes.dim() == 2
+        r = A.shape[0] if isinstance(A, torch.Tensor) and A.dim() == 2 else 0
+        workspace = _int8_workspace(workspace, X, W.codes.shape[0] if known else 0, r, BASE_INT8, False)
+    res = (_bound_calls or _load_calls()).fwd8(X, W, A, B, alpha, save_T, out, T_out, workspace)
+    if res is None:
+        bf = torch.bfloat16
+        items = _int8_items("X", X, False) + _int8_items("W", W, False)
+        (M, K), (N, KW) = X.codes.shape, W.codes.shape
+        if KW != K:
+            raise ValueError(f"weight has K={KW}, activations K={K}")
+        if A is not None or B is not None:
+            chk = _Checker()
+            r = chk.adapters(A, B, N, K)
+            if r < 1:
+                raise QLoRAError("int8_linear_fwd", ERR_SHAPE)
+            items += [("A", A, bf, (r, K)), ("B", B, bf, (N, r))]
+            if T_out is not None:
+                items.append(("T_out", T_out, torch.float32, (M, r)))
+        elif T_out is not None:
+            raise ValueError("T_out: given, but there is no adapter")
+        if out is not None:
+            items.append(("out", out, bf, (M, N)))
+        if workspace is not None:
+            items.append(("workspace", workspace, torch.uint8, tuple(workspace.shape)))
+        _refused(items)
+    if res[0] != OK:
+        raise QLoRAError("int8_linear_fwd", res[0])
+    return res[1], res[2]
+
+
+def linear_bwd_int8(dY, X: Int8Tensor, qw, A, B, alpha: float, T=None, need_dX: bool = True,
+                    accumulate_into=None, dX_out=None, dA_out=None, dB_out=None, workspace=None):
+    """Backward of a linear whose input was kept in rows of 8 bits: (dX bf16
+    [M, K] or None, dA fp32 [r, K], dB fp32 [N, r]).  `qw` is the base: an
+    Int8Tensor (linear_fwd_int8), a QuantizedWeight or a bf16 tensor [N, K]
+    (linear_fwd); T what its forward returned (None: computed again from X).
+    accumulate_into: a dX to add to.  Outputs overlap no input and not each
+    other.  Scratch memory is torch's unless a Workspace is given."""
+    torch = _torch()
+    if accumulate_into is not None and dX_out is not None:
+        raise ValueError("dX_out: given beside accumulate_into")
+    if not need_dX and (accumulate_into is not None or dX_out is not None):
+        raise ValueError("dX: given, but need_dX is False")
+    kind = (BASE_INT8 if isinstance(qw, Int8Tensor) else
+            BASE_NF4 if isinstance(qw, QuantizedWeight) else BASE_BF16)
+    if workspace is not None:
+        W = qw.codes if kind == BASE_INT8 else qw
+        N = qw.N if kind == BASE_NF4 else (
+            W.shape[0] if isinstance(W, torch.Tensor) and W.dim() == 2 else 0)
+        r = A.shape[0] if isinstance(A, torch.Tensor) and A.dim() == 2 else 0
+        workspace = _int8_workspace(workspace, X, N, r, kind, True)
+    res = (_bound_calls or _load_calls()).bwd8(dY, X, qw, A, B, alpha, T, need_dX, accumulate_into,
+                                               dX_out, dA_out, dB_out, workspace)
+    if res is None:
+        bf, f32 = torch.bfloat16, torch.float32
+        items = _int8_items("X", X, False)
+        M, K = X.codes.shape
+        chk = _Checker()
+        if kind == BASE_INT8:
+            items += _int8_items("base weight", qw, False)
+            N = qw.codes.shape[0]
+            if qw.codes.shape[1] != K:
+                raise ValueError(f"weight has K={qw.codes.shape[1]}, activations K={K}")
+        else:
+            N = chk.base(qw, K)
+        r = chk.adapters(A, B, N, K)
+        if r < 1:
+            raise QLoRAError("int8_linear_bwd", ERR_SHAPE)
+        items += [(n, t, t.dtype, tuple(t.shape)) for n, t in chk.seen]
+        items.append(("dY", dY, bf, (M, N)))
+        items += [it for it in (
+            ("T", T, f32 if kind == BASE_INT8 else bf, (M, r)),
+            ("dX", accumulate_into if accumulate_into is not None else dX_out, bf, (M, K)),
+            ("dA", dA_out, f32, (r, K)), ("dB", dB_out, f32, (N, r))) if it[1] is not None]
+        if workspace is not None:
+            items.append(("workspace", workspace, torch.uint8, tuple(workspace.shape)))
+        _refused(items)
+    if res[0] != OK:
+        raise QLoRAError("int8_linear_bwd", res[0])
+    return res[1], res[2], res[3]
+
+
+def silu_mul_fwd_int8(G, Up, save: bool = True, out=None):
+    """H = silu(G) Up of bf16 [M, I] as rows of 8 bits, the down projection's
+    input, and G and Up as blocks of 8 bits for silu_mul_bwd_int8 (None, None
+    unless save).  `out`: a bf16 [M, I] that gets H as silu_mul_fwd gives it.
+    Returns (H, G, Up) as Int8Tensors."""
+    res = (_bound_calls or _load_calls()).silu8(G, Up, save, out)
+    if res is None:
+        torch = _torch()
+        if not isinstance(G, torch.Tensor) or G.dim() != 2:
+            raise ValueError("G: a 2-D tensor")
+        shape = tuple(G.shape)
+        _refused([("G", G, torch.bfloat16, shape), ("Up", Up, torch.bfloat16, shape)]
+                 + ([("out", out, torch.bfloat16, shape)] if out is not None else []))
+    if res[0] != OK:
+        raise QLoRAError("silu_mul_fwd_int8", res[0])
+    return (Int8Tensor(res[1], res[2]), Int8Tensor(res[3], res[4]) if save else None,
+            Int8Tensor(res[5], res[6]) if save else None)
+
+
+def silu_mul_bwd_int8(dH, G: Int8Tensor, Up: Int8Tensor, dG_out=None, dUp_out=None):
+    """silu_mul_bwd from the blocks that silu_mul_fwd_int8 kept: (dG, dUp)."""
+    res = (_bound_calls or _load_calls()).silu8_bwd(dH, G, Up, dG_out, dUp_out)
+    if res is None:
+        torch = _torch()
+        items = _int8_items("G", G, True) + _int8_items("Up", Up, True)
+        shape = tuple(G.codes.shape)
+        if tuple(Up.codes.shape) != shape:
+            raise ValueError(f"Up: shape {tuple(Up.codes.shape)}, expected {shape}")
+        items += [("dH", dH, torch.bfloat16, shape)]
+        items += [(n, t, torch.bfloat16, shape) for n, t in (("dG_out", dG_out), ("dUp_out", dUp_out))
+                  if t is not None]
+        _refused(items)
+    if res[0] != OK:
+        raise QLoRAError("silu_mul_bwd_int8", res[0])
+    return res[1], res[2]
 
 
 def linear_fwd_dropout(X, Xd, qw: QuantizedWeight, A, B, alpha: float, save_T: bool = True,

@@ -1,5 +1,5 @@
 """Build libqlora.so (gfx950) from the HIP sources in csrc/ with hipcc, and
-_calls.so, the C++ marshalling of the batched adapters' Python calls, with g++
+_calls.so, the C++ marshalling of the batched adapters' and 8-bit Python calls, with g++
 and torch's headers.  The C library needs hipcc alone: it is built where the
 other cannot be.
 
@@ -24,6 +24,7 @@ LIB = os.path.join(HERE, "libqlora.so")
 CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["quant_kernels.hip", "gemm_kernels.hip", "fwd_kernels.hip", "dx_kernels.hip", "adapter_kernels.hip", "gemv_kernels.hip", "elementwise.hip",
            "merge_kernels.hip", "dropout_kernels.hip", "batch_plan_kernels.hip", "batch_kernels.hip",
+           "int8_quant_kernels.hip", "int8_adapter_kernels.hip", "int8_fwd_kernels.hip",
            "qlora_api.hip"]
 ARCH = "gfx950"
 

@@ -190,6 +190,16 @@ __device__ __forceinline__ uint32_t bload8(__amdgpu_buffer_rsrc_t r, uint32_t vo
   return __builtin_amdgcn_raw_buffer_load_b8(r, (int)voff, 0, 0);
 }
 
+typedef unsigned v4u_t __attribute__((ext_vector_type(4)));
+// Store through a buffer resource; a lane at kOOB stores nothing.  The whole
+// offset goes in the lane's: with a scalar offset register the compiler takes
+// a 16-byte store's data registers as free in the next cycle, and a vector
+// instruction that wrote them there has replaced the first word of the last
+// lanes' data (seen as column indices in out).
+__device__ __forceinline__ void bstore128(__amdgpu_buffer_rsrc_t r, uint4 v, uint32_t off) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u_t, v), r, (int)off, 0, 0);
+}
+
 
 // ------------------------- workgroup -> tile order ---------------------------
 

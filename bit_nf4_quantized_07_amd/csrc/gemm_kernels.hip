@@ -798,6 +798,62 @@ hipError_t launch_mlp_fwd(const uint16_t* X, int64_t M, const LoraLinear& gate,
                           G, U, H, st);
 }
 
+hipError_t launch_dx(const uint16_t* dY, int64_t M, const NF4Weight& w, const uint16_t* U,
+                     const uint16_t* A, int r, float s, uint16_t* dX, bool accumulate,
+                     hipStream_t st, const uint32_t* mask, float keep_scale, float* part,
+                     int kz_len, const Timing* tm) {
+  const int64_t K = w.K, N = w.N;
+  GemmArgs g{};
+  g.a1 = opnd(dY, N, (int)M, M);
+  g.b1 = opnd(nullptr, 0, (int)K, 0);
+  g.a2 = opnd(U, r, (int)M, M);
+  g.b2 = opnd(A, K, (int)K, r, s);      // transposed load of A [r, K]: rows k, contraction j
+  g.w = w;
+  g.P = (int)M; g.Q = (int)K;
+  g.c1_len = (int)N; g.c1_split = (int)N; g.c2_len = r;
+  g.out = dX; g.ldo = K; g.accumulate = accumulate ? 1 : 0;
+  hipError_t e;
+  const bool own = dx_nf4_supported(N);   // timed by its launches; the others around them
+  if (!own) timer_begin(tm, TK_DX_GEMM, st);
+  if (own) {
+    e = launch_dx_nf4(dY, M, w, U, A, r, s, dX, accumulate, st, mask, keep_scale,
+                      part, kz_len, span_of(tm, TK_DX_GEMM));
+  } else if (mask) {
+    // Tile engine with a dropout mask: the masked adapter term is written
+    // (or added) first, then dY W_hat is accumulated on top of it.
+    e = launch_dx_adapter_masked(U, A, M, K, r, s, mask, keep_scale, dX, accumulate, st);
+    if (e == hipSuccess) {
+      g.c2_len = 0;
+      g.accumulate = 1;
+      if (w.bf16) {
+        g.b1 = opnd(w.bf16, K, (int)K, N);
+        e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
+                        LdBF16T<kDxBN, kBK, false>, LdBF16K<kDxBM, kBK, false>,
+                        LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
+            g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 2, st);
+      } else {
+        e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
+                        LdNF4T<kDxBN>, LdBF16K<kDxBM, kBK, false>,
+                        LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
+            g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 0.52, st);
+      }
+    }
+  } else if (w.bf16) {
+    g.b1 = opnd(w.bf16, K, (int)K, N);   // transposed load of W [N, K]: rows k, contraction n
+    e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
+                    LdBF16T<kDxBN, kBK, false>, LdBF16K<kDxBM, kBK, false>,
+                    LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
+        g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 2, st);
+  } else {
+    e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
+                    LdNF4T<kDxBN>, LdBF16K<kDxBM, kBK, false>,
+                    LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
+        g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 0.52, st);
+  }
+  if (!own) timer_end(tm, TK_DX_GEMM, st);
+  return e;
+}
+
 hipError_t launch_qlora_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, const NF4Weight& w,
                             const uint16_t* A, const uint16_t* B, int r, float s,
                             const uint16_t* T, uint16_t* dX, float* dA, float* dB,
@@ -829,58 +885,10 @@ hipError_t launch_qlora_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, co
     QLK_TRY(launch_rank16(dY, M, N, B, true, r, U, st));
   }
   // dX = dY W_hat + s U A.
-  if (dX) {
-    GemmArgs g{};
-    g.a1 = opnd(dY, N, (int)M, M);
-    g.b1 = opnd(nullptr, 0, (int)K, 0);
-    g.a2 = opnd(U, r, (int)M, M);
-    g.b2 = opnd(A, K, (int)K, r, s);      // transposed load of A [r, K]: rows k, contraction j
-    g.w = w;
-    g.P = (int)M; g.Q = (int)K;
-    g.c1_len = (int)N; g.c1_split = (int)N; g.c2_len = r;
-    g.out = dX; g.ldo = K; g.accumulate = accumulate_dx ? 1 : 0;
-    hipError_t e;
-    const bool own = dx_nf4_supported(N);   // timed by its launches; the others around them
-    if (!own) timer_begin(tm, TK_DX_GEMM, st);
-    if (own) {
-      e = launch_dx_nf4(dY, M, wx, U, A, r, s, dX, accumulate_dx, st, mask, keep_scale,
-                        plan.dx_kz_len ? reinterpret_cast<float*>(base + plan.off_dxpart) : nullptr,
-                        plan.dx_kz_len, span_of(tm, TK_DX_GEMM));
-    } else if (mask) {
-      // Tile engine with a dropout mask: the masked adapter term is written
-      // (or added) first, then dY W_hat is accumulated on top of it.
-      e = launch_dx_adapter_masked(U, A, M, K, r, s, mask, keep_scale, dX, accumulate_dx, st);
-      if (e == hipSuccess) {
-        g.c2_len = 0;
-        g.accumulate = 1;
-        if (w.bf16) {
-          g.b1 = opnd(w.bf16, K, (int)K, N);
-          e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
-                          LdBF16T<kDxBN, kBK, false>, LdBF16K<kDxBM, kBK, false>,
-                          LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
-              g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 2, st);
-        } else {
-          e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
-                          LdNF4T<kDxBN>, LdBF16K<kDxBM, kBK, false>,
-                          LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
-              g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 0.52, st);
-        }
-      }
-    } else if (w.bf16) {
-      g.b1 = opnd(w.bf16, K, (int)K, N);   // transposed load of W [N, K]: rows k, contraction n
-      e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
-                      LdBF16T<kDxBN, kBK, false>, LdBF16K<kDxBM, kBK, false>,
-                      LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
-          g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 2, st);
-    } else {
-      e = launch_gemm<kDxBM, kDxBN, kBK, LdBF16K<kDxBM, kBK, false>,
-                      LdNF4T<kDxBN>, LdBF16K<kDxBM, kBK, false>,
-                      LdBF16T<kDxBN, kBK, true>, EPI_BF16>(
-          g, 1, (double)kDxBM * N * 2, (double)kDxBN * N * 0.52, st);
-    }
-    if (!own) timer_end(tm, TK_DX_GEMM, st);
-    QLK_TRY(e);
-  }
+  if (dX)
+    QLK_TRY(launch_dx(dY, M, wx, U, A, r, s, dX, accumulate_dx, st, mask, keep_scale,
+                      plan.dx_kz_len ? reinterpret_cast<float*>(base + plan.off_dxpart) : nullptr,
+                      plan.dx_kz_len, tm));
   // dA = s U^T X and dB = s dY^T T, both contracting over m.
   if (plan.one_pass_grads) return launch_adapter_grads(U, X, dY, T, M, K, N, r, s, dA, dB, st);
   // Otherwise the partials of both in one launch (rows j of U^T and columns

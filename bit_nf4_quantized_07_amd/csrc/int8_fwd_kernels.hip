@@ -1,0 +1,495 @@
+// Forward of the linear layer on a base of 8-bit rows, from activations in
+// 8-bit rows:
+//
+//   Y[m][n] = sx[m] sw[n] sum_k Cx[m][k] Cw[n][k] + s sum_j T[m][j] B[n][j]
+//                       (llm-compass "QLoRA", 方法与公式, the equation, with
+//                        8-bit rows for W and x)
+//
+// The first sum is whole numbers, exact in 32 bits for K up to 2^17 (127^2 K <
+// 2^31), so it does not depend on how the contraction is cut.  T comes from the
+// rank-r kernel as two bf16 terms of s T.
+//
+// A workgroup of four waves computes a tile of 64 NI tokens x 64 NJ outputs,
+// each wave a quarter of 32 NI x 32 NJ: NI NJ accumulators of
+// v_mfma_i32_32x32x32_i8, each a 32 (outputs) x 32 (tokens) block of Y^T.
+//  * The contraction advances 64 columns a step (two MFMA steps) through four
+//    LDS stages, filled by buffer loads that write LDS directly, three steps
+//    ahead: rows of 64 bytes whose four 16-byte pieces are XOR-swizzled by
+//    (row >> 2) & 3, so that operand reads are free of bank conflicts.
+//  * The whole sums become fp32, times sx sw, in the accumulators' own
+//    registers, and s T B^T is added by bf16 MFMAs.
+//  * The bf16 tile goes out through the stages, so that every store
+//    instruction writes whole row segments.
+// Where the tiles do not fill the device the contraction is split; a split's
+// fp32 values go to the workspace and are added in a fixed order.
+#include <type_traits>
+
+#include "device_common.h"
+#include "kernels.h"
+#include "terms.h"
+
+namespace qlk {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr int kI8Step = 64;     // columns of the contraction per step
+
+struct Int8FwdArgs {
+  const int8_t* X;      // [M, K]
+  const float* sx;      // [M]
+  const int8_t* W;      // [N, K]
+  const float* sw;      // [N]
+  int M, N, K;
+  const uint16_t* T2;   // [M][2][r]: hi and mid terms of s T
+  const uint16_t* B;    // [N, r]
+  int r;                // 0: no adapter
+  uint16_t* Y;          // [M, N]
+  int tiles_m, tiles_n, group_m;
+  float* part;          // split contraction: fp32 [splits][M, N]
+  int kz_len;           // steps per split; 0: one pass
+};
+
+// s_waitcnt immediates (gfx9 encoding): vmcnt <= vm, lgkmcnt <= lgkm.
+constexpr int i8_wait(int vm, int lgkm) {
+  return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (lgkm << 8);
+}
+
+template <int NI, int NJ>
+__device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
+  constexpr int XB = 64 * NI * kI8Step, WB = 64 * NJ * kI8Step;   // bytes of a stage
+  __shared__ __attribute__((aligned(16))) uint8_t x0[XB];
+  __shared__ __attribute__((aligned(16))) uint8_t x1[XB];
+  __shared__ __attribute__((aligned(16))) uint8_t x2[XB];
+  __shared__ __attribute__((aligned(16))) uint8_t x3[XB];
+  __shared__ __attribute__((aligned(16))) uint8_t w0[WB];
+  __shared__ __attribute__((aligned(16))) uint8_t w1[WB];
+  __shared__ __attribute__((aligned(16))) uint8_t w2[WB];
+  __shared__ __attribute__((aligned(16))) uint8_t w3[WB];
+  uint8_t* const xb[4] = {x0, x1, x2, x3};
+  uint8_t* const wb[4] = {w0, w1, w2, w3};
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int fg = wave & 1, tq = wave >> 1;   // output half, token half
+
+  const int ntiles = g.tiles_m * g.tiles_n;
+  const int z = (int)blockIdx.x / ntiles;
+  int tm, tn;
+  tile_coords((int)blockIdx.x % ntiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
+  const int m0 = tm * 64 * NI, n0 = tn * 64 * NJ;
+  const int nsteps = g.K / kI8Step;
+  const int kz0 = g.kz_len ? z * g.kz_len : 0;
+  const int kz1 = g.kz_len ? min(nsteps, kz0 + g.kz_len) : nsteps;
+
+  // Load i of wave w fills rows 16 (NI w + i) .. +15 of a stage (1 KB); lane L
+  // lands at row L / 4 of them, physical piece L % 4.
+  const __amdgpu_buffer_rsrc_t rx = rsrc_whole(g.X, (uint32_t)((int64_t)g.M * g.K));
+  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K));
+  uint32_t xoff[NI], woff[NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int row = 16 * (NI * wave + i) + (lane >> 2);
+    const int piece = (lane & 3) ^ ((row >> 2) & 3);
+    xoff[i] = m0 + row < g.M ? (uint32_t)((int64_t)(m0 + row) * g.K + piece * 16) : kOOB;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int row = 16 * (NJ * wave + j) + (lane >> 2);
+    const int piece = (lane & 3) ^ ((row >> 2) & 3);
+    woff[j] = n0 + row < g.N ? (uint32_t)((int64_t)(n0 + row) * g.K + piece * 16) : kOOB;
+  }
+  constexpr int kLoads = NI + NJ;
+  auto load_l = [&](int l, int buf, int kb) {
+    const uint32_t soff = (uint32_t)__builtin_amdgcn_readfirstlane(kb) * kI8Step;
+    if (l < NI)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rx, (__attribute__((address_space(3))) void*)(xb[buf] + 1024 * (NI * wave + l)), 16, xoff[l],
+          soff, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rw, (__attribute__((address_space(3))) void*)(wb[buf] + 1024 * (NJ * wave + l - NI)), 16,
+          woff[l - NI], soff, 0, 0);
+  };
+  // Operand of a 32-row block, MFMA step t: row c, logical piece 2 t + h.
+  int rd[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) rd[t] = c * kI8Step + (((2 * t + h) ^ ((c >> 2) & 3)) * 16);
+  auto xfrag = [&](int buf, int i, int t) -> i32x4_t {
+    return *reinterpret_cast<const i32x4_t*>(xb[buf] + 32 * (NI * tq + i) * kI8Step + rd[t]);
+  };
+  auto wfrag = [&](int buf, int j, int t) -> i32x4_t {
+    return *reinterpret_cast<const i32x4_t*>(wb[buf] + 32 * (NJ * fg + j) * kI8Step + rd[t]);
+  };
+
+  i32x16_t acc[NJ][NI];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[j][i][v] = 0;
+
+  i32x4_t a[2][NJ], b[2][NI];   // [MFMA step parity][block]
+#pragma unroll
+  for (int s = 0; s < 3; ++s)
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) load_l(l, s, min(kz0 + s, kz1 - 1));
+  // Steps 0 and 1 in LDS before the barrier (step 2's loads may still be in
+  // flight): the last slots of step 0 read the first operands of step 1.
+  __builtin_amdgcn_s_waitcnt(i8_wait(kLoads, 0));
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) a[0][j] = wfrag(0, j, 0);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) b[0][i] = xfrag(0, i, 0);
+
+  // One step: 2 NI NJ MFMA slots.  The loads of step kb + 3 go out over the
+  // first MFMA step's slots, as do the reads of the second's operands; the
+  // second's slots read the first operands of the next step.
+  auto step = [&](auto Pc, int kb) {
+    constexpr int P = decltype(Pc)::value;
+    constexpr int nxt = (P + 1) % 4, ld = (P + 3) % 4;
+    constexpr int S = NI * NJ;
+    const int kload = min(kb + 3, kz1 - 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < 2 * S; ++u) {
+      const int t = u / S, q = u % S, j = q / NI, i = q % NI;
+      acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[t][j], b[t][i], acc[j][i], 0, 0, 0);
+      // item q of the slot's share: kLoads items over S slots
+#pragma unroll
+      for (int l = q * kLoads / S; l < (q + 1) * kLoads / S; ++l) {
+        if (t == 0) load_l(l, ld, kload);
+      }
+      constexpr int R = S >= kLoads ? kLoads : S;   // reads in the first slots
+      if (q < R) {
+#pragma unroll
+        for (int l = q * kLoads / R; l < (q + 1) * kLoads / R; ++l) {
+          if (l < NI) b[1 - t][l] = xfrag(t ? nxt : P, l, 1 - t);
+          else a[1 - t][l - NI] = wfrag(t ? nxt : P, l - NI, 1 - t);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // Step kb + 2's stages (loaded during step kb - 1) complete in every wave
+    // before step kb + 1, which reads them in its last slots: at most this
+    // step's loads outstanding, then the barrier.
+    __builtin_amdgcn_s_waitcnt(i8_wait(kLoads, 0xF));
+    __builtin_amdgcn_s_barrier();
+  };
+  // Whole groups of four steps without a branch between them: where paths meet
+  // the compiler waits for loads that are not due.
+  int kb = kz0;
+  for (; kb + 4 <= kz1; kb += 4) {
+    step(std::integral_constant<int, 0>(), kb);
+    step(std::integral_constant<int, 1>(), kb + 1);
+    step(std::integral_constant<int, 2>(), kb + 2);
+    step(std::integral_constant<int, 3>(), kb + 3);
+  }
+  if (kb < kz1) {
+    step(std::integral_constant<int, 0>(), kb);
+    if (kb + 1 < kz1) step(std::integral_constant<int, 1>(), kb + 1);
+    if (kb + 2 < kz1) step(std::integral_constant<int, 2>(), kb + 2);
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the loop
+  __syncthreads();                 // every wave's operand reads are done
+
+  // Accumulator [j][i]: lane holds token mw + 32 i + c and outputs
+  // nw + 32 j + 8 (v / 4) + 4 h + (v % 4).  Block column by block column: fp32
+  // values, the adapter's term, then bf16 rows of 128 NJ bytes in LDS: token
+  // block k of 32 rows lies in stage w[k] (k < 4) or x[k - 4], the 16-byte
+  // pieces of a row XOR-swizzled by its number.  N and r are multiples of 8, so
+  // that a piece is wholly inside or wholly outside.
+  constexpr int PR = 8 * NJ;       // pieces of a row
+  auto ob = [&](int k) -> uint8_t* {
+    return k == 0 ? w0 : k == 1 ? w1 : k == 2 ? w2 : k == 3 ? w3 : k == 4 ? x0 : k == 5 ? x1 : k == 6 ? x2 : x3;
+  };
+  const int nw = n0 + 32 * NJ * fg, mw = m0 + 32 * NI * tq;
+  const __amdgpu_buffer_rsrc_t rsx = rsrc_whole(g.sx, (uint32_t)g.M * 4);
+  const __amdgpu_buffer_rsrc_t rsw = rsrc_whole(g.sw, (uint32_t)g.N * 4);
+  const __amdgpu_buffer_rsrc_t rt = rsrc_whole(g.T2, (uint32_t)(g.M * g.r * 4));
+  const __amdgpu_buffer_rsrc_t rb = rsrc_whole(g.B, (uint32_t)(g.N * g.r * 2));
+  const int r = z == 0 ? g.r : 0;
+  float* const part = g.kz_len ? g.part + (int64_t)z * g.M * g.N : nullptr;
+  float sx[NI];
+  uint32_t toff[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int m = mw + 32 * i + c;
+    sx[i] = __uint_as_float(bload32(rsx, m < g.M ? (uint32_t)m * 4 : kOOB));
+    toff[i] = m < g.M ? (uint32_t)((m * 2 * g.r + 8 * h) * 2) : kOOB;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    __builtin_amdgcn_sched_barrier(0);
+    f32x16_t out[NI];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = nw + 32 * j + 8 * q + 4 * h;
+      const uint4 sv = bload128(rsw, n < g.N ? (uint32_t)n * 4 : kOOB);
+      const float s4[4] = {__uint_as_float(sv.x), __uint_as_float(sv.y), __uint_as_float(sv.z),
+                           __uint_as_float(sv.w)};
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[i][4 * q + e] = (float)acc[j][i][4 * q + e] * sx[i] * s4[e];
+    }
+    const int nb = nw + 32 * j + c;
+    for (int r0 = 0; r0 < r; r0 += 16) {
+      const bool rok = r0 + 8 * h < r;
+      const bf16x8_t bop = __builtin_bit_cast(
+          bf16x8_t, bload128(rb, rok && nb < g.N ? (uint32_t)((nb * g.r + r0 + 8 * h) * 2) : kOOB));
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const uint32_t o = rok ? toff[i] : kOOB;
+        const bf16x8_t hi = __builtin_bit_cast(bf16x8_t, bload128s(rt, o, r0 * 2));
+        const bf16x8_t mid = __builtin_bit_cast(bf16x8_t, bload128s(rt, o, (r0 + g.r) * 2));
+        out[i] = mfma_32x32x16(bop, mid, out[i]);
+        out[i] = mfma_32x32x16(bop, hi, out[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int m = mw + 32 * i + c;
+      uint8_t* const row = (tq ? ob(NI + i) : ob(i)) + c * (16 * PR);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (part) {
+          const int n = nw + 32 * j + 8 * q + 4 * h;
+          if (m < g.M && n < g.N)
+            *reinterpret_cast<float4*>(part + (int64_t)m * g.N + n) =
+                make_float4(out[i][4 * q], out[i][4 * q + 1], out[i][4 * q + 2], out[i][4 * q + 3]);
+        } else {
+          const int piece = (4 * NJ * fg + 4 * j + q) ^ (c & (PR - 1));
+          *reinterpret_cast<uint2*>(row + 16 * piece + 8 * h) =
+              make_uint2(pack_bf16x2(out[i][4 * q], out[i][4 * q + 1]),
+                         pack_bf16x2(out[i][4 * q + 2], out[i][4 * q + 3]));
+        }
+      }
+    }
+  }
+  if (part) return;
+  __syncthreads();
+  constexpr int RW = 256 / PR;                     // rows a pass of 256 threads stores
+  const int prow = tid / PR, pp = tid % PR;
+  const __amdgpu_buffer_rsrc_t ry = rsrc_whole(g.Y, (uint32_t)((int64_t)g.M * g.N * 2));
+#pragma unroll
+  for (int e = 0; e < 64 * NI / RW; ++e) {
+    const int row = RW * e + prow, rl = row & 31;  // RW divides 32
+    const uint4 v = *reinterpret_cast<const uint4*>(ob(RW * e / 32) + rl * (16 * PR) +
+                                                    16 * (pp ^ (rl & (PR - 1))));
+    const int m = m0 + row, n = n0 + 8 * pp;
+    bstore128(ry, v, m < g.M && n < g.N ? (uint32_t)(((int64_t)m * g.N + n) * 2) : kOOB);
+  }
+}
+
+// The host pass does not keep a kernel template whose body calls these loads
+// from a lambda: one plain kernel per form.
+__global__ void __launch_bounds__(256) k_int8_fwd_44(Int8FwdArgs g) { int8_tile<4, 4>(g); }
+__global__ void __launch_bounds__(256) k_int8_fwd_24(Int8FwdArgs g) { int8_tile<2, 4>(g); }
+__global__ void __launch_bounds__(256) k_int8_fwd_22(Int8FwdArgs g) { int8_tile<2, 2>(g); }
+__global__ void __launch_bounds__(256) k_int8_fwd_12(Int8FwdArgs g) { int8_tile<1, 2>(g); }
+
+// ---------------------------------------------------------------------------
+// Up to 16 tokens: the weight is streamed once.  A workgroup of kGvWaves waves
+// takes 16 RB outputs; a wave takes every kGvWaves-th run of 256 columns of
+// their weight rows (four loads of 16 rows x 64 bytes) against the tokens'
+// columns with v_mfma_i32_16x16x64_i8, and the waves' whole sums are added
+// through LDS.  T = X A^T arrives as kTSplits partial sums, added in a fixed
+// order by every workgroup (the first one writes T).
+constexpr int kGvWaves = 8;
+constexpr int kGvRun = 256;     // columns per run
+
+template <int RB>
+__device__ __forceinline__ void int8_gemv(const Int8FwdArgs& g, const float* __restrict__ Tpart,
+                                          float s, float* __restrict__ T_out) {
+  __shared__ __attribute__((aligned(16))) i32x4_t red[kGvWaves][RB][64];
+  extern __shared__ float tl[];                    // [M][r]: s T
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i = lane & 15, gq = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16 * RB;
+  const __amdgpu_buffer_rsrc_t rx = rsrc_whole(g.X, (uint32_t)((int64_t)g.M * g.K));
+  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K));
+  const int nruns = (g.K + kGvRun - 1) / kGvRun;
+  uint32_t wrow[RB];
+  bool wok[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int n = n0 + 16 * b + i;
+    wok[b] = n < g.N;
+    wrow[b] = (uint32_t)((int64_t)n * g.K) + 16 * gq;
+  }
+  const uint32_t xrow = (uint32_t)(i * g.K) + 16 * gq;
+  i32x4_t acc[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) acc[b] = i32x4_t{0, 0, 0, 0};
+
+  struct Run { uint4 w[RB][4]; uint4 x[4]; };
+  auto load = [&](Run& R, int run) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = run * kGvRun + 64 * q;
+      const bool kok = run < nruns && k < g.K;     // K % 64 == 0: 64 whole columns or none
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        R.w[b][q] = bload128(rw, kok && wok[b] ? wrow[b] + (uint32_t)k : kOOB);
+      R.x[q] = bload128(rx, kok && i < g.M ? xrow + (uint32_t)k : kOOB);
+    }
+  };
+  auto use = [&](const Run& R) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, R.w[b][q]),
+                                                       __builtin_bit_cast(i32x4_t, R.x[q]), acc[b],
+                                                       0, 0, 0);
+  };
+  Run ra, rb;
+  load(ra, wave);
+  load(rb, wave + kGvWaves);
+  // s T of every token, while the first loads are in flight
+  for (int e = tid; e < g.M * g.r; e += 64 * kGvWaves) {
+    float t = 0.0f;
+    for (int zz = 0; zz < kTSplits; ++zz) t += Tpart[(int64_t)zz * g.M * g.r + e];
+    t *= g.sx[e / g.r];
+    if (T_out && blockIdx.x == 0) T_out[e] = t;
+    tl[e] = s * t;
+  }
+  for (int run = wave; run < nruns; run += 2 * kGvWaves) {
+    use(ra);
+    load(ra, run + 2 * kGvWaves);
+    use(rb);
+    load(rb, run + 3 * kGvWaves);
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b) red[wave][b][lane] = acc[b];
+  __syncthreads();
+  // Output o: token o / (16 RB), output row o % (16 RB); the lane that holds
+  // row 16 b + 4 q + v of token i is 16 q + i, element v.
+  for (int o = tid; o < 16 * RB * g.M; o += 64 * kGvWaves) {
+    const int m = o / (16 * RB), row = o % (16 * RB);
+    const int b = row / 16, q = (row % 16) / 4, v = row % 4;
+    const int n = n0 + row;
+    if (n >= g.N) continue;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kGvWaves; ++w) sum += red[w][b][16 * q + m][v];
+    float y = (float)sum * g.sx[m] * g.sw[n];
+    const uint16_t* const Bn = g.B + (int64_t)n * g.r;
+    for (int j = 0; j < g.r; j += 8) {
+      const uint4 bv = *reinterpret_cast<const uint4*>(Bn + j);
+      const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y = __builtin_fmaf(tl[m * g.r + j + 2 * e], bf16_to_f32(bw[e] & 0xffffu), y);
+        y = __builtin_fmaf(tl[m * g.r + j + 2 * e + 1], bf16_to_f32(bw[e] >> 16), y);
+      }
+    }
+    g.Y[(int64_t)m * g.N + n] = f32_to_bf16(y);
+  }
+}
+__global__ void __launch_bounds__(64 * kGvWaves)
+k_int8_gemv_1(Int8FwdArgs g, const float* Tpart, float s, float* T_out) {
+  int8_gemv<1>(g, Tpart, s, T_out);
+}
+__global__ void __launch_bounds__(64 * kGvWaves)
+k_int8_gemv_2(Int8FwdArgs g, const float* Tpart, float s, float* T_out) {
+  int8_gemv<2>(g, Tpart, s, T_out);
+}
+
+// ------------------------------- launchers ---------------------------------
+
+// Tile and split of the contraction.  A form costs rounds of the device times
+// the time of its tile; `speed` is a form's rate per CU against the largest's.
+struct Int8Form {
+  int ni, nj;
+  double speed;
+  int per_cu;      // workgroups a CU holds (LDS)
+};
+static const Int8Form kForms[] = {{4, 4, 1.0, 1}, {2, 4, 0.85, 1}, {2, 2, 0.7, 2}, {1, 2, 0.5, 3}};
+
+Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  Int8FwdPlan p{};
+  if (M <= kGemvMaxM) {
+    p.gemv = true;
+    p.off_T = 0;
+    p.bytes = up((size_t)kTSplits * M * r * 4);
+    return p;
+  }
+  const int64_t steps = K / kI8Step;
+  double best = 0.0;
+  for (int f = 0; f < 4; ++f) {
+    const Int8Form& F = kForms[f];
+    const int64_t tiles = ((M + 64 * F.ni - 1) / (64 * F.ni)) * ((N + 64 * F.nj - 1) / (64 * F.nj));
+    for (int splits = 1; splits <= 16; ++splits) {
+      if (splits > 1 && (tiles * splits > 512 || steps / splits < 8)) break;
+      const int64_t len = (steps + splits - 1) / splits;
+      const int64_t rounds = (tiles * splits + kCUs - 1) / kCUs;
+      // MFMA cycles of a tile, a fixed start and end, the partial sums' trip
+      double cost = rounds * ((double)len * F.ni * F.nj * 64 / F.speed + 4000.0);
+      if (splits > 1) cost += 6000.0 + (double)M * N * 4 * (2 * splits) / 2500.0;
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        p.form = f;
+        p.kz_len = splits > 1 ? (int)len : 0;
+      }
+    }
+  }
+  p.off_T = 0;
+  p.off_part = up((size_t)M * 2 * r * 2);
+  p.bytes = p.off_part;
+  if (p.kz_len) p.bytes += up((size_t)((steps + p.kz_len - 1) / p.kz_len) * M * N * 4);
+  return p;
+}
+
+hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int64_t N, int64_t K,
+                           const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* Y,
+                           float* T_out, void* ws, const Int8FwdPlan& p, hipStream_t st) {
+  Int8FwdArgs g{};
+  g.X = X.codes; g.sx = X.scale; g.W = W.codes; g.sw = W.scale;
+  g.M = (int)M; g.N = (int)N; g.K = (int)K;
+  g.B = B; g.r = r; g.Y = Y;
+  char* const base = reinterpret_cast<char*>(ws);
+  if (p.gemv) {
+    float* const part = reinterpret_cast<float*>(base + p.off_T);
+    if (r) {
+      const hipError_t e = launch_int8_T_partial(X.codes, M, K, A, r, part, st);
+      if (e != hipSuccess) return e;
+    }
+    const size_t lds = (size_t)M * r * 4;
+    if (N >= 32 * 512)
+      hipLaunchKernelGGL(k_int8_gemv_2, dim3((unsigned)((N + 31) / 32)), dim3(64 * kGvWaves), lds, st,
+                         g, part, s, T_out);
+    else
+      hipLaunchKernelGGL(k_int8_gemv_1, dim3((unsigned)((N + 15) / 16)), dim3(64 * kGvWaves), lds, st,
+                         g, part, s, T_out);
+    return hipGetLastError();
+  }
+  if (r) {
+    uint16_t* const T2 = reinterpret_cast<uint16_t*>(base + p.off_T);
+    const hipError_t e = launch_int8_T(X, M, K, A, r, s, T_out, T2, st);
+    if (e != hipSuccess) return e;
+    g.T2 = T2;
+  }
+  const Int8Form& F = kForms[p.form];
+  g.tiles_m = (int)((M + 64 * F.ni - 1) / (64 * F.ni));
+  g.tiles_n = (int)((N + 64 * F.nj - 1) / (64 * F.nj));
+  g.group_m = group_for(g.tiles_m, g.tiles_n, 64.0 * F.ni * K, 64.0 * F.nj * K);
+  g.kz_len = p.kz_len;
+  const int steps = (int)(K / kI8Step);
+  const int splits = p.kz_len ? (steps + p.kz_len - 1) / p.kz_len : 1;
+  if (p.kz_len) g.part = reinterpret_cast<float*>(base + p.off_part);
+  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * splits)), block(256);
+  if (p.form == 0) hipLaunchKernelGGL(k_int8_fwd_44, grid, block, 0, st, g);
+  else if (p.form == 1) hipLaunchKernelGGL(k_int8_fwd_24, grid, block, 0, st, g);
+  else if (p.form == 2) hipLaunchKernelGGL(k_int8_fwd_22, grid, block, 0, st, g);
+  else hipLaunchKernelGGL(k_int8_fwd_12, grid, block, 0, st, g);
+  if (p.kz_len) return launch_split_reduce(g.part, splits, M * N, Y, false, st);
+  return hipGetLastError();
+}
+
+}  // namespace qlk

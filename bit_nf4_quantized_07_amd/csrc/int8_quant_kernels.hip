@@ -1,0 +1,395 @@
+// Storage in 8 bits: rows of a matrix, or runs of 64 columns of a row, as codes
+// and one fp32 scale each.
+//
+//   a = max |x|,   scale = fp32(a / 127),   code = rne(127 x / a)
+//
+// A row (run) of zeros has scale 0 and codes 0; one that holds an infinity or a
+// NaN has scale NaN and codes 0, so that every value it stands for is NaN.
+//
+// The quotient: with g a power of two that brings a near 1 and R = 127 / (a g)
+// held as two fp32 words (R_hi the rounded quotient, R_lo the rest), n = fma(x g,
+// R_hi, x g R_lo) is 127 x / a rounded once (its error before that is below
+// 2^-40).  For bf16 x this gives the exact code: a tie 127 x / a = k + 1/2 is a
+// representable number and therefore hit, and what is no tie is at least 2^-9
+// of |n| / 254 away from one, since 254 x and (2 k + 1) a are whole multiples
+// of x's last place.  Adding 1.5 2^23 rounds n to the nearest integer, ties to
+// the even one, and leaves the code in the sum's low byte.
+//
+// The gated activation H = silu(G) U in rows of 8 bits, with G and U kept in
+// runs of 64 for the backward, and that backward, read and write these formats
+// in one pass.
+//
+// Bound: HBM.  A row is read once and held in registers (up to 8 pieces of 8
+// values per lane) between its maximum and its codes.
+#include <type_traits>
+
+#include "device_common.h"
+#include "kernels.h"
+
+namespace qlk {
+
+constexpr int kRowPieces = 8;    // pieces of 8 values a lane holds
+
+// 127 x / a for many x of one row or run.
+struct Inverse {
+  float g, hi, lo, scale;
+};
+// a: the largest magnitude (bits of a non-negative fp32; NaN and infinity from
+// 0x7f800000 on).
+__device__ __forceinline__ Inverse inverse_of(uint32_t abits) {
+  Inverse v{0.0f, 0.0f, 0.0f, 0.0f};
+  if (abits == 0) return v;
+  if (abits >= 0x7f800000u) {
+    v.scale = __uint_as_float(0x7fc00000u);
+    return v;
+  }
+  const float a = __uint_as_float(abits);
+  v.scale = a / 127.0f;
+  const int e = min(max((int)(abits >> 23) - 127, -120), 120);
+  v.g = __uint_as_float((uint32_t)(127 - e) << 23);
+  const float as = a * v.g;                       // exact
+  v.hi = 127.0f / as;
+  v.lo = __builtin_fmaf(-v.hi, as, 127.0f) / as;
+  return v;
+}
+// fp32 whose low byte is the code of x.
+__device__ __forceinline__ uint32_t code_of(float x, const Inverse& v) {
+#pragma clang fp contract(off)
+  const float xs = x * v.g;
+  const float t = xs * v.lo;
+  const float n = __builtin_fmaf(xs, v.hi, t);
+  const float s = n + 12582912.0f;
+  return __float_as_uint(s);
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+  return ab | cd;
+}
+// Eight values' codes; all zero where the row has none (a zero or non-finite a:
+// g, hi and lo are zero, and an infinity or NaN times zero must not reach them).
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Inverse& v) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = code_of(x[i], v);
+  const uint32_t keep = v.g > 0.0f ? 0xffffffffu : 0u;
+  return make_uint2(pack4(c[0], c[1], c[2], c[3]) & keep, pack4(c[4], c[5], c[6], c[7]) & keep);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    x[2 * q] = __uint_as_float(w[q] << 16);
+    x[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+// Largest magnitude of eight values as fp32 bits (whole-number maximum: a NaN
+// counts as the largest).
+__device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  return m;
+}
+__device__ __forceinline__ uint32_t max_over_wave(uint32_t m) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+  return m;
+}
+// Over the W waves that share a row (W == 1: a wave's own).
+template <int W>
+__device__ __forceinline__ uint32_t max_over_row(uint32_t m, uint32_t* red) {
+  m = max_over_wave(m);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = max(m, red[w]);
+  }
+  return m;
+}
+
+// Eight values of a piece (piece p holds columns 8 p .. 8 p + 7).
+__device__ __forceinline__ void load8(const uint16_t* row, int64_t p, float (&x)[8]) {
+  unpack8(reinterpret_cast<const uint4*>(row)[p], x);
+}
+__device__ __forceinline__ void load8(const float* row, int64_t p, float (&x)[8]) {
+  const float4 lo = reinterpret_cast<const float4*>(row)[2 * p];
+  const float4 hi = reinterpret_cast<const float4*>(row)[2 * p + 1];
+  x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+  x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+}
+
+// Rows of X [M, K] (8 | K).  W waves share a row; a lane holds P pieces of it.
+// P == 0: rows longer than the registers hold are read a second time.
+template <class T, int W, int P>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
+k_int8_quantize(const T* __restrict__ X, int64_t M, int64_t K, int8_t* __restrict__ codes,
+                float* __restrict__ scale) {
+  __shared__ uint32_t red[W];
+  constexpr int R = W == 1 ? 4 : 1;                     // rows of a workgroup
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = (int64_t)blockIdx.x * R + (W == 1 ? wave : 0);
+  if (W == 1 && m >= M) return;                         // no barrier follows
+  const T* const row = X + m * K;
+  uint2* const out = reinterpret_cast<uint2*>(codes + m * K);
+  const int64_t np = K / 8;
+  const int p0 = W == 1 ? lane : (int)threadIdx.x;
+  constexpr int stride = 64 * W;
+  uint32_t a = 0;
+  if constexpr (P > 0) {
+    float x[P][8];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = p0 + i * stride;
+      if (p < np) load8(row, p, x[i]);
+      else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) a = max(a, amax8(x[i]));
+    const Inverse v = inverse_of(max_over_row<W>(a, red));
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = p0 + i * stride;
+      if (p < np) out[p] = codes8(x[i], v);
+    }
+    if (p0 == 0) scale[m] = v.scale;
+  } else {
+    float x[8];
+    for (int64_t p = p0; p < np; p += stride) {
+      load8(row, p, x);
+      a = max(a, amax8(x));
+    }
+    const Inverse v = inverse_of(max_over_row<W>(a, red));
+    for (int64_t p = p0; p < np; p += stride) {
+      load8(row, p, x);
+      out[p] = codes8(x, v);
+    }
+    if (p0 == 0) scale[m] = v.scale;
+  }
+}
+
+// Waves per row and pieces per lane for np pieces: as few waves as hold the row
+// in registers, so that short rows need no barrier; long rows spread over a
+// workgroup.
+template <class F>
+static void for_row(int64_t np, F f) {
+  auto pieces = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    const int64_t need = (np + 64 * W - 1) / (64 * W);
+    if (need <= 1) f(w, std::integral_constant<int, 1>());
+    else if (need <= 2) f(w, std::integral_constant<int, 2>());
+    else if (need <= 4) f(w, std::integral_constant<int, 4>());
+    else if (need <= 6) f(w, std::integral_constant<int, 6>());
+    else f(w, std::integral_constant<int, kRowPieces>());
+  };
+  if (np <= 64 * 2) pieces(std::integral_constant<int, 1>());
+  else if (np <= 256 * kRowPieces) pieces(std::integral_constant<int, 4>());
+  else if (np <= 1024 * kRowPieces) pieces(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 16>(), std::integral_constant<int, 0>());
+}
+
+template <class T>
+static hipError_t int8_quantize_rows(const T* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                                     hipStream_t st) {
+  for_row(K / 8, [&](auto w, auto p) {
+    constexpr int W = decltype(w)::value, P = decltype(p)::value;
+    const int64_t grid = W == 1 ? (M + 3) / 4 : M;
+    hipLaunchKernelGGL((k_int8_quantize<T, W, P>), dim3((unsigned)grid), dim3(W == 1 ? 256 : 64 * W),
+                       0, st, X, M, K, codes, scale);
+  });
+  return hipGetLastError();
+}
+hipError_t launch_int8_quantize(const uint16_t* X, int64_t M, int64_t K, int8_t* codes,
+                                float* scale, hipStream_t st) {
+  return int8_quantize_rows(X, M, K, codes, scale, st);
+}
+hipError_t launch_int8_quantize(const float* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                                hipStream_t st) {
+  return int8_quantize_rows(X, M, K, codes, scale, st);
+}
+
+__device__ __forceinline__ float code_value(uint32_t w, int i) {
+  return (float)(int8_t)(w >> (8 * i));
+}
+
+// out = bf16(code scale), 16 codes per thread.  block: scales per 64 columns
+// (64 | K), else one per row.
+template <bool BLOCK>
+__global__ void __launch_bounds__(256)
+k_int8_dequant(const int8_t* __restrict__ codes, const float* __restrict__ scale, int64_t n16,
+               uint32_t k16, uint16_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n16) return;
+  const uint4 c = reinterpret_cast<const uint4*>(codes)[i];
+  float s;
+  if constexpr (BLOCK) s = scale[i >> 2];
+  else s = scale[n16 <= 0xffffffffll ? (int64_t)((uint32_t)i / k16) : i / k16];
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = code_value(w[2 * h + e / 4], e % 4) * s;
+    reinterpret_cast<uint4*>(out)[2 * i + h] = pack8(x);
+  }
+}
+
+hipError_t launch_int8_dequant(const int8_t* codes, const float* scale, int64_t M, int64_t K,
+                               bool block, uint16_t* out, hipStream_t st) {
+  const int64_t n16 = M * K / 16;
+  const dim3 grid((unsigned)((n16 + 255) / 256));
+  if (block)
+    hipLaunchKernelGGL(k_int8_dequant<true>, grid, dim3(256), 0, st, codes, scale, n16,
+                       (uint32_t)(K / 16), out);
+  else
+    hipLaunchKernelGGL(k_int8_dequant<false>, grid, dim3(256), 0, st, codes, scale, n16,
+                       (uint32_t)(K / 16), out);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// H = silu(G) U.  The value that is quantised is the fp32 product; where the
+// bf16 H is wanted too, it is that product rounded, the elementwise gating's
+// bits.  The eight lanes of a run of 64 columns hold it whole.
+__device__ __forceinline__ uint32_t max_over_8(uint32_t m) {
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+  return m;
+}
+
+struct GateOut {
+  uint16_t* H;        // bf16 [M, I], or null
+  int8_t* H8;         // rows
+  float* Hs;
+  int8_t* G8;         // runs of 64, or null (then U8 is null too)
+  float* Gs;
+  int8_t* U8;
+  float* Us;
+};
+
+// One piece of G or U kept in 8 bits; every lane of the run calls it.
+__device__ __forceinline__ void keep8(const float (&x)[8], int8_t* codes, float* scale, int64_t row8,
+                                      int64_t p, bool in) {
+  const Inverse v = inverse_of(max_over_8(in ? amax8(x) : 0u));
+  if (!in) return;
+  reinterpret_cast<uint2*>(codes)[row8 + p] = codes8(x, v);
+  if ((p & 7) == 0) scale[(row8 + p) >> 3] = v.scale;
+}
+
+template <int W, int P>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
+k_silu_mul_fwd_int8(const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, int64_t M,
+                    int64_t I, GateOut o) {
+  __shared__ uint32_t red[W];
+  constexpr int R = W == 1 ? 4 : 1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = (int64_t)blockIdx.x * R + (W == 1 ? wave : 0);
+  if (W == 1 && m >= M) return;
+  const int64_t np = I / 8, row8 = m * np;
+  const int p0 = W == 1 ? lane : (int)threadIdx.x;
+  constexpr int stride = 64 * W;
+  const uint16_t* const grow = G + m * I;
+  const uint16_t* const urow = U + m * I;
+  auto gated = [&](int64_t p, bool first, float (&h)[8]) {
+    float g[8], u[8];
+    const bool in = p < np;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
+    if (in) {
+      load8(grow, p, g);
+      load8(urow, p, u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = silu_mul_f32(g[e], u[e]);
+    if (!first) return;
+    if (o.H && in) reinterpret_cast<uint4*>(o.H)[row8 + p] = pack8(h);
+    if (o.G8) {
+      keep8(g, o.G8, o.Gs, row8, p, in);
+      keep8(u, o.U8, o.Us, row8, p, in);
+    }
+  };
+  uint32_t a = 0;
+  uint2* const out = reinterpret_cast<uint2*>(o.H8) + row8;
+  if constexpr (P > 0) {
+    float h[P][8];
+#pragma unroll
+    for (int i = 0; i < P; ++i) gated(p0 + i * stride, true, h[i]);
+#pragma unroll
+    for (int i = 0; i < P; ++i) a = max(a, amax8(h[i]));
+    const Inverse v = inverse_of(max_over_row<W>(a, red));
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = p0 + i * stride;
+      if (p < np) out[p] = codes8(h[i], v);
+    }
+    if (p0 == 0) o.Hs[m] = v.scale;
+  } else {
+    float h[8];
+    for (int64_t q = 0; q < np; q += stride) {
+      gated(q + p0, true, h);
+      a = max(a, amax8(h));
+    }
+    const Inverse v = inverse_of(max_over_row<W>(a, red));
+    for (int64_t p = p0; p < np; p += stride) {
+      gated(p, false, h);
+      out[p] = codes8(h, v);
+    }
+    if (p0 == 0) o.Hs[m] = v.scale;
+  }
+}
+
+hipError_t launch_silu_mul_fwd_int8(const uint16_t* G, const uint16_t* U, int64_t M, int64_t I,
+                                    uint16_t* H, int8_t* H8, float* Hs, int8_t* G8, float* Gs,
+                                    int8_t* U8, float* Us, hipStream_t st) {
+  const GateOut o{H, H8, Hs, G8, Gs, U8, Us};
+  for_row(I / 8, [&](auto w, auto p) {
+    constexpr int W = decltype(w)::value, P = decltype(p)::value;
+    const int64_t grid = W == 1 ? (M + 3) / 4 : M;
+    hipLaunchKernelGGL((k_silu_mul_fwd_int8<W, P>), dim3((unsigned)grid),
+                       dim3(W == 1 ? 256 : 64 * W), 0, st, G, U, M, I, o);
+  });
+  return hipGetLastError();
+}
+
+// dG = dH U sig(G) (1 + G (1 - sig(G))), dU = dH silu(G), from the kept runs.
+__global__ void __launch_bounds__(256)
+k_silu_mul_bwd_int8(const uint16_t* __restrict__ dH, const int8_t* __restrict__ G8,
+                    const float* __restrict__ Gs, const int8_t* __restrict__ U8,
+                    const float* __restrict__ Us, int64_t n8, uint16_t* __restrict__ dG,
+                    uint16_t* __restrict__ dU) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  float d[8], g[8], u[8];
+  unpack8(reinterpret_cast<const uint4*>(dH)[i], d);
+  const uint2 gc = reinterpret_cast<const uint2*>(G8)[i], uc = reinterpret_cast<const uint2*>(U8)[i];
+  const float gs = Gs[i >> 3], us = Us[i >> 3];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float gv = code_value(e < 4 ? gc.x : gc.y, e % 4) * gs;
+    const float uv = code_value(e < 4 ? uc.x : uc.y, e % 4) * us;
+    const float sg = sigmoidf_(gv);
+    g[e] = d[e] * uv * sg * (1.0f + gv * (1.0f - sg));
+    u[e] = d[e] * gv * sg;
+  }
+  reinterpret_cast<uint4*>(dG)[i] = pack8(g);
+  reinterpret_cast<uint4*>(dU)[i] = pack8(u);
+}
+
+hipError_t launch_silu_mul_bwd_int8(const uint16_t* dH, const int8_t* G8, const float* Gs,
+                                    const int8_t* U8, const float* Us, int64_t M, int64_t I,
+                                    uint16_t* dG, uint16_t* dU, hipStream_t st) {
+  const int64_t n8 = M * I / 8;
+  hipLaunchKernelGGL(k_silu_mul_bwd_int8, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, st, dH,
+                     G8, Gs, U8, Us, n8, dG, dU);
+  return hipGetLastError();
+}
+
+}  // namespace qlk

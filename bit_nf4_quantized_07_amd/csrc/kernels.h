@@ -182,6 +182,13 @@ int dx_split_len(int64_t M, int64_t K, int64_t N);
 // split partials, plus out's own values when accumulating; one rounding.
 hipError_t launch_split_reduce(const float* part, int splits, int64_t stride, uint16_t* out,
                                bool accumulate, hipStream_t st, hipEvent_t stop = nullptr);
+// dX (+)= dY W_hat + s U A on the base as w holds it (a bf16 copy if it has one),
+// by the dX kernel or, for other N, the tile engine; part and kz_len as
+// launch_dx_nf4 takes them (used by it alone).
+hipError_t launch_dx(const uint16_t* dY, int64_t M, const NF4Weight& w, const uint16_t* U,
+                     const uint16_t* A, int r, float s, uint16_t* dX, bool accumulate,
+                     hipStream_t st, const uint32_t* mask, float keep_scale, float* part,
+                     int kz_len, const Timing* tm);
 // dX (+)= bf16(mask * keep_scale * s U A): the adapter term alone, for the
 // tile-engine fallback of the dropout backward.
 hipError_t launch_dx_adapter_masked(const uint16_t* U, const uint16_t* A, int64_t M, int64_t K,
@@ -251,6 +258,60 @@ hipError_t launch_silu_mul_fwd(const uint16_t* G, const uint16_t* U, int64_t n, 
                                hipStream_t st);
 hipError_t launch_silu_mul_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
                                int64_t n, uint16_t* dG, uint16_t* dU, hipStream_t st);
+
+// ---- activations and weights in 8 bits --------------------------------------
+
+// Rows of codes [rows, K] and their scales [rows].
+struct Int8Rows {
+  const int8_t* codes;
+  const float* scale;
+};
+hipError_t launch_int8_quantize(const uint16_t* X, int64_t M, int64_t K, int8_t* codes,
+                                float* scale, hipStream_t st);
+hipError_t launch_int8_quantize(const float* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                                hipStream_t st);
+// block: a scale per 64 columns instead of one per row.
+hipError_t launch_int8_dequant(const int8_t* codes, const float* scale, int64_t M, int64_t K,
+                               bool block, uint16_t* out, hipStream_t st);
+// H = silu(G) U in rows (and bf16, if H is not null), G and U in runs of 64 (if
+// G8 is not null).
+hipError_t launch_silu_mul_fwd_int8(const uint16_t* G, const uint16_t* U, int64_t M, int64_t I,
+                                    uint16_t* H, int8_t* H8, float* Hs, int8_t* G8, float* Gs,
+                                    int8_t* U8, float* Us, hipStream_t st);
+hipError_t launch_silu_mul_bwd_int8(const uint16_t* dH, const int8_t* G8, const float* Gs,
+                                    const int8_t* U8, const float* Us, int64_t M, int64_t I,
+                                    uint16_t* dG, uint16_t* dU, hipStream_t st);
+// T = X A^T (fp32 [M, r], if not null) and T2 [M][2][r], the bf16 terms of s T.
+hipError_t launch_int8_T(const Int8Rows& X, int64_t M, int64_t K, const uint16_t* A, int r, float s,
+                         float* T, uint16_t* T2, hipStream_t st);
+// part [kTSplits][M][r]: sums of Cx A^T over slices of the contraction (M <= 16).
+hipError_t launch_int8_T_partial(const int8_t* X, int64_t M, int64_t K, const uint16_t* A, int r,
+                                 float* part, hipStream_t st);
+// Y = X W^T + s (X A^T) B^T (r == 0: no adapter; T_out null: not wanted).
+struct Int8FwdPlan {
+  bool gemv;         // small-M path
+  int form;          // tile
+  int kz_len;        // steps per split of the contraction (0: one pass)
+  size_t off_T, off_part, bytes;
+};
+Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r);
+hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int64_t N, int64_t K,
+                           const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* Y,
+                           float* T_out, void* ws, const Int8FwdPlan& plan, hipStream_t st);
+// Backward from X in 8-bit rows on a base in 8-bit rows (W8 not null), NF4 or
+// bf16 (w).  T in fp32 or bf16, or neither (computed again).
+constexpr int kBaseInt8 = 0, kBaseNF4 = 1, kBaseBF16 = 2;
+struct Int8BwdPlan {
+  bool copy;         // dX on a bf16 copy of the base at off_w
+  int kz_len;
+  size_t off_U, off_up, off_tp, off_w, off_part, bytes;
+};
+Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx);
+hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int64_t K, int64_t N,
+                           const Int8Rows* W8, const NF4Weight& w, const uint16_t* A,
+                           const uint16_t* B, int r, float s, const float* T,
+                           const uint16_t* T_bf16, uint16_t* dX, float* dA, float* dB,
+                           bool accumulate, void* ws, const Int8BwdPlan& plan, hipStream_t st);
 
 // ---- adapters of many requests beside one shared projection ----------------
 

@@ -282,6 +282,113 @@ int check_aligned(std::initializer_list<const void*> ptrs) {
   return QLORA_OK;
 }
 
+// ---- activations and weights in 8 bits ----
+constexpr int64_t kMaxInt8Rows = (int64_t)1 << 22;    // rows are workgroups
+constexpr int64_t kMaxInt8Cols = (int64_t)1 << 24;
+constexpr int64_t kMaxInt8Elems = (int64_t)1 << 35;
+constexpr int64_t kMaxInt8Sum = (int64_t)1 << 17;     // 127^2 K in 32 bits
+
+int check_int8_matrix(int64_t M, int64_t K, int cols) {
+  if (M <= 0 || K <= 0 || K % cols != 0 || M >= kMaxInt8Rows || K > kMaxInt8Cols ||
+      M * K >= kMaxInt8Elems)
+    return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+template <class T>
+int int8_quantize_common(const T* X, int64_t M, int64_t K, int8_t* codes, float* scale, void* stream) {
+  if (!X || !codes || !scale) return QLORA_ERR_NULL;
+  int st = check_int8_matrix(M, K, 16);
+  if (!st) st = check_aligned({X, codes, scale});
+  if (st) return st;
+  return launch_status(qlk::launch_int8_quantize(X, M, K, codes, scale, as_stream(stream)));
+}
+
+// Sizes of the layer on activations in 8-bit rows; base: kBase*.
+int check_int8_sizes(int64_t M, int64_t K, int64_t N, int r, int base, bool bwd) {
+  if (M <= 0 || M > kMaxDim || K > kMaxInt8Sum) return QLORA_ERR_SHAPE;
+  const int st = check_weight_shape(N, K);
+  if (st) return st;
+  if (N % 8 != 0 || r < (bwd ? 1 : 0) || r > kMaxRank) return QLORA_ERR_SHAPE;
+  // 32-bit offsets; out-of-range lanes use offset 2^31
+  const int64_t rp = padded_rank(r);
+  const int64_t weight = base == qlk::kBaseInt8 ? N * K : base == qlk::kBaseNF4 ? N * K / 2 : 2 * N * K;
+  if (M * K >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes || M * rp * 4 >= kMaxBufferBytes ||
+      N * rp * 2 >= kMaxBufferBytes || weight >= kMaxBufferBytes)
+    return QLORA_ERR_SHAPE;
+  // dX, and the bf16 copy of an 8-bit base that it is computed on
+  if (bwd && (M * K * 2 >= kMaxBufferBytes || (base == qlk::kBaseInt8 && 2 * N * K >= kMaxBufferBytes)))
+    return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+// Zero-padded copies for a rank that is no multiple of 8, behind the kernels'
+// own workspace.
+struct Int8Pad {
+  size_t off_A, off_B, off_T, off_dA, off_dB, bytes;
+};
+Int8Pad int8_pad(size_t base, int64_t M, int64_t K, int64_t N, int r, bool bwd) {
+  Int8Pad p{};
+  size_t off = align256(base);
+  const size_t rp = (size_t)padded_rank(r);
+  if (rp != (size_t)r) {
+    p.off_A = off; off += align256(rp * K * 2);
+    p.off_B = off; off += align256((size_t)N * rp * 2);
+    p.off_T = off; off += align256((size_t)M * rp * 4);
+    if (bwd) {
+      p.off_dA = off; off += align256(rp * K * 4);
+      p.off_dB = off; off += align256((size_t)N * rp * 4);
+    }
+  }
+  p.bytes = off;
+  return p;
+}
+
+int int8_bwd_common(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale, int64_t M,
+                    int64_t K, int64_t N, int base, const qlk::Int8Rows* W8, const qlk::NF4Weight& w,
+                    const uint16_t* A, const uint16_t* B, int r, float alpha, const float* T,
+                    const uint16_t* T_bf16, uint16_t* dX, float* dA, float* dB, int flags,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dY || !Xcodes || !Xscale || !A || !B || !dA || !dB) return QLORA_ERR_NULL;
+  int st = check_int8_sizes(M, K, N, r, base, true);
+  if (st) return st;
+  if (!isfinite(alpha) || (flags & ~QLORA_BWD_ACCUMULATE_DX)) return QLORA_ERR_ARG;
+  st = check_aligned({dY, Xcodes, Xscale, A, B, T, T_bf16, dX, dA, dB, workspace});
+  if (st) return st;
+  const int rp = padded_rank(r);
+  const qlk::Int8BwdPlan plan = qlk::plan_int8_bwd(M, K, N, rp, base, dX != nullptr);
+  const Int8Pad pad = int8_pad(plan.bytes, M, K, N, r, true);
+  if (!workspace || workspace_bytes < pad.bytes) return QLORA_ERR_WORKSPACE;
+  const float s = alpha / (float)r;
+  const bool acc = (flags & QLORA_BWD_ACCUMULATE_DX) != 0;
+  const hipStream_t hs = as_stream(stream);
+  const qlk::Int8Rows X{Xcodes, Xscale};
+  if (rp == r)
+    return launch_status(qlk::launch_int8_bwd(dY, X, M, K, N, W8, w, A, B, r, s, T, T_bf16, dX, dA,
+                                              dB, acc, workspace, plan, hs));
+  char* const p = reinterpret_cast<char*>(workspace);
+  uint16_t* const Ap = reinterpret_cast<uint16_t*>(p + pad.off_A);
+  uint16_t* const Bp = reinterpret_cast<uint16_t*>(p + pad.off_B);
+  float* const dAp = reinterpret_cast<float*>(p + pad.off_dA);
+  float* const dBp = reinterpret_cast<float*>(p + pad.off_dB);
+  hipError_t e = qlk::launch_pad2d(A, r, K, Ap, rp, K, hs);
+  if (e == hipSuccess) e = qlk::launch_pad2d(B, N, r, Bp, N, rp, hs);
+  if (e == hipSuccess && T) {
+    float* const Tp = reinterpret_cast<float*>(p + pad.off_T);
+    e = qlk::launch_pad2d(T, M, r, Tp, M, rp, hs);
+    T = Tp;
+  }
+  if (e == hipSuccess && T_bf16) {
+    uint16_t* const Tp = reinterpret_cast<uint16_t*>(p + pad.off_T);
+    e = qlk::launch_pad2d(T_bf16, M, r, Tp, M, rp, hs);
+    T_bf16 = Tp;
+  }
+  if (e == hipSuccess)
+    e = qlk::launch_int8_bwd(dY, X, M, K, N, W8, w, Ap, Bp, rp, s, T, T_bf16, dX, dAp, dBp, acc,
+                             workspace, plan, hs);
+  if (e == hipSuccess) e = qlk::launch_pad2d(dAp, rp, K, dA, r, K, hs);
+  if (e == hipSuccess) e = qlk::launch_pad2d(dBp, N, rp, dB, N, r, hs);
+  return launch_status(e);
+}
+
 int quantize_common(const float* W0, int64_t N, int64_t K, int blocksize, const qlk::Codebook4& cb,
                     uint8_t* packed, float* absmax, void* stream) {
   if (!W0 || !packed || !absmax) return QLORA_ERR_NULL;
@@ -742,6 +849,134 @@ int silu_mul_bwd(const uint16_t* dH, const uint16_t* G, const uint16_t* Up, int6
   if (!aligned16(dH) || !aligned16(G) || !aligned16(Up) || !aligned16(dG) || !aligned16(dUp))
     return QLORA_ERR_ALIGN;
   return launch_status(qlk::launch_silu_mul_bwd(dH, G, Up, n, dG, dUp, as_stream(stream)));
+}
+
+int int8_quantize(const uint16_t* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                  void* stream) {
+  return int8_quantize_common(X, M, K, codes, scale, stream);
+}
+
+int int8_quantize_fp32(const float* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                       void* stream) {
+  return int8_quantize_common(X, M, K, codes, scale, stream);
+}
+
+int int8_dequant(const int8_t* codes, const float* scale, int64_t M, int64_t K, int block,
+                 uint16_t* out, void* stream) {
+  if (!codes || !scale || !out) return QLORA_ERR_NULL;
+  if (block != 0 && block != kBlock) return QLORA_ERR_UNSUPPORTED;
+  int st = check_int8_matrix(M, K, block ? kBlock : 16);
+  if (!st) st = check_aligned({codes, scale, out});
+  if (st) return st;
+  return launch_status(
+      qlk::launch_int8_dequant(codes, scale, M, K, block != 0, out, as_stream(stream)));
+}
+
+int silu_mul_fwd_int8(const uint16_t* G, const uint16_t* Up, int64_t M, int64_t I, uint16_t* H,
+                      int8_t* Hcodes, float* Hscale, int8_t* Gcodes, float* Gscale, int8_t* Ucodes,
+                      float* Uscale, void* stream) {
+  if (!G || !Up || !Hcodes || !Hscale) return QLORA_ERR_NULL;
+  // G and Up are kept both or not at all
+  const bool keep = Gcodes || Gscale || Ucodes || Uscale;
+  if (keep && (!Gcodes || !Gscale || !Ucodes || !Uscale)) return QLORA_ERR_NULL;
+  int st = check_int8_matrix(M, I, kBlock);
+  if (!st) st = check_aligned({G, Up, H, Hcodes, Hscale, Gcodes, Gscale, Ucodes, Uscale});
+  if (st) return st;
+  return launch_status(qlk::launch_silu_mul_fwd_int8(G, Up, M, I, H, Hcodes, Hscale, Gcodes, Gscale,
+                                                     Ucodes, Uscale, as_stream(stream)));
+}
+
+int silu_mul_bwd_int8(const uint16_t* dH, const int8_t* Gcodes, const float* Gscale,
+                      const int8_t* Ucodes, const float* Uscale, int64_t M, int64_t I, uint16_t* dG,
+                      uint16_t* dUp, void* stream) {
+  if (!dH || !Gcodes || !Gscale || !Ucodes || !Uscale || !dG || !dUp) return QLORA_ERR_NULL;
+  int st = check_int8_matrix(M, I, kBlock);
+  if (!st) st = check_aligned({dH, Gcodes, Gscale, Ucodes, Uscale, dG, dUp});
+  if (st) return st;
+  return launch_status(qlk::launch_silu_mul_bwd_int8(dH, Gcodes, Gscale, Ucodes, Uscale, M, I, dG,
+                                                     dUp, as_stream(stream)));
+}
+
+size_t int8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int base, int is_bwd) {
+  if (base < qlk::kBaseInt8 || base > qlk::kBaseBF16 || (!is_bwd && base != qlk::kBaseInt8)) return 0;
+  if (check_int8_sizes(M, K, N, r, base, is_bwd != 0) != QLORA_OK) return 0;
+  const int rp = padded_rank(r);
+  const size_t own = is_bwd ? qlk::plan_int8_bwd(M, K, N, rp, base, true).bytes
+                            : qlk::plan_int8_fwd(M, K, N, rp).bytes;
+  return int8_pad(own, M, K, N, r, is_bwd != 0).bytes;
+}
+
+int int8_linear_fwd(const int8_t* Xcodes, const float* Xscale, int64_t M, int64_t K, int64_t N,
+                    const int8_t* Wcodes, const float* Wscale, const uint16_t* A, const uint16_t* B,
+                    int r, float alpha, uint16_t* Y, float* T_out, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!Xcodes || !Xscale || !Wcodes || !Wscale || !Y) return QLORA_ERR_NULL;
+  if (r != 0 && (!A || !B)) return QLORA_ERR_NULL;
+  int st = check_int8_sizes(M, K, N, r, qlk::kBaseInt8, false);
+  if (st) return st;
+  if (r == 0 ? (A || B || T_out) : !isfinite(alpha)) return QLORA_ERR_ARG;
+  st = check_aligned({Xcodes, Xscale, Wcodes, Wscale, A, B, Y, T_out, workspace});
+  if (st) return st;
+  const int rp = padded_rank(r);
+  const qlk::Int8FwdPlan plan = qlk::plan_int8_fwd(M, K, N, rp);
+  const Int8Pad pad = int8_pad(plan.bytes, M, K, N, r, false);
+  if (workspace_bytes < pad.bytes || (pad.bytes && !workspace)) return QLORA_ERR_WORKSPACE;
+  const float s = r ? alpha / (float)r : 0.0f;
+  const hipStream_t hs = as_stream(stream);
+  const qlk::Int8Rows X{Xcodes, Xscale}, W{Wcodes, Wscale};
+  if (rp == r)
+    return launch_status(
+        qlk::launch_int8_fwd(X, M, W, N, K, A, B, r, s, Y, T_out, workspace, plan, hs));
+  char* const p = reinterpret_cast<char*>(workspace);
+  uint16_t* const Ap = reinterpret_cast<uint16_t*>(p + pad.off_A);
+  uint16_t* const Bp = reinterpret_cast<uint16_t*>(p + pad.off_B);
+  float* const Tp = T_out ? reinterpret_cast<float*>(p + pad.off_T) : nullptr;
+  hipError_t e = qlk::launch_pad2d(A, r, K, Ap, rp, K, hs);
+  if (e == hipSuccess) e = qlk::launch_pad2d(B, N, r, Bp, N, rp, hs);
+  if (e == hipSuccess)
+    e = qlk::launch_int8_fwd(X, M, W, N, K, Ap, Bp, rp, s, Y, Tp, workspace, plan, hs);
+  if (e == hipSuccess && T_out) e = qlk::launch_pad2d(Tp, M, rp, T_out, M, r, hs);
+  return launch_status(e);
+}
+
+int int8_linear_bwd(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale, int64_t M,
+                    int64_t K, int64_t N, const int8_t* Wcodes, const float* Wscale,
+                    const uint16_t* A, const uint16_t* B, int r, float alpha, const float* T,
+                    uint16_t* dX, float* dA, float* dB, int flags, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!Wcodes || !Wscale) return QLORA_ERR_NULL;
+  const int st = check_aligned({Wcodes, Wscale});
+  if (st) return st;
+  const qlk::Int8Rows W{Wcodes, Wscale};
+  return int8_bwd_common(dY, Xcodes, Xscale, M, K, N, qlk::kBaseInt8, &W, weight_bf16(nullptr, N, K),
+                         A, B, r, alpha, T, nullptr, dX, dA, dB, flags, workspace, workspace_bytes,
+                         stream);
+}
+
+int qlora_linear_bwd_int8(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale, int64_t M,
+                          int64_t K, int64_t N, const uint8_t* packed, const uint8_t* codes,
+                          const float* scales, const float* mean, const uint16_t* A,
+                          const uint16_t* B, int r, float alpha, const uint16_t* T, uint16_t* dX,
+                          float* dA, float* dB, int flags, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  if (!packed || !codes || !scales || !mean) return QLORA_ERR_NULL;
+  const int st = check_aligned({packed, codes, scales, mean});
+  if (st) return st;
+  return int8_bwd_common(dY, Xcodes, Xscale, M, K, N, qlk::kBaseNF4, nullptr,
+                         weight(packed, codes, scales, mean, N, K), A, B, r, alpha, nullptr, T, dX,
+                         dA, dB, flags, workspace, workspace_bytes, stream);
+}
+
+int qlora_linear_bwd_bf16_int8(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale,
+                               int64_t M, int64_t K, int64_t N, const uint16_t* W,
+                               const uint16_t* A, const uint16_t* B, int r, float alpha,
+                               const uint16_t* T, uint16_t* dX, float* dA, float* dB, int flags,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!W) return QLORA_ERR_NULL;
+  if (!aligned16(W)) return QLORA_ERR_ALIGN;
+  return int8_bwd_common(dY, Xcodes, Xscale, M, K, N, qlk::kBaseBF16, nullptr, weight_bf16(W, N, K),
+                         A, B, r, alpha, nullptr, T, dX, dA, dB, flags, workspace, workspace_bytes,
+                         stream);
 }
 
 int nf4_codebook(float* out16) {

@@ -382,6 +382,103 @@ int lora_adapters_bwd(const uint16_t* dY, const uint16_t* X, int64_t M, int64_t 
 /* Bytes of workspace of the two calls above; 0 for invalid sizes. */
 size_t lora_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int S, int is_bwd);
 
+/* ---- activations and weights in 8 bits ----------------------------------- */
+
+/* What the layer keeps between forward and backward, and the frozen base where
+ * 4 bits are too few, in 8 bits.  (The pages save the first by gradient
+ * checkpointing, which computes activations again; a row of codes is half the
+ * bytes and computes nothing twice.)  A row x of a matrix is stored as
+ *   codes  int8, in [-127, 127]      scale  fp32, one per row
+ *   a = max |x|,  scale = fp32(a / 127),  code = rne(127 x / a)
+ * and stands for code * scale.  A row of zeros has scale 0 and codes 0; a row
+ * that holds an infinity or a NaN has scale NaN and codes 0, so that all it
+ * stands for is NaN.  "Blocks" are the same rule for runs of 64 columns of a
+ * row (scale [M, K / 64]): for what is used element by element.  Rows are what
+ * products read, because a row's scale leaves the sum. */
+
+/* Rows of X [M, K], bf16 or fp32 (activations by token, weights by output
+ * channel).  From bf16 the codes are exact (ties to the even code); from fp32
+ * the quotient is rounded to fp32 first.
+ * Requires K % 16 == 0, K <= 2^24, 1 <= M < 2^22, M K < 2^35. */
+int int8_quantize(const uint16_t* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                  void* stream);
+int int8_quantize_fp32(const float* X, int64_t M, int64_t K, int8_t* codes, float* scale,
+                       void* stream);
+
+/* out = RNE_bf16(fp32(code * scale)), bf16 [M, K].  block: 0 (a scale per row)
+ * or 64 (per 64 columns; then K % 64 == 0). */
+int int8_dequant(const int8_t* codes, const float* scale, int64_t M, int64_t K, int block,
+                 uint16_t* out, void* stream);
+
+/* Forward on a base in rows of 8 bits W [N, K], from X in rows of 8 bits:
+ *   T = X A^T,   Y = X W^T + s T B^T,   s = fp32(alpha / r)
+ * (the equation of qlora_linear_fwd with 8-bit rows for x and W).  The first
+ * sum is whole numbers, exact; T (fp32 [M, r], T_out NULL: not wanted) is
+ * summed in fp32 from the codes, which bf16 holds exactly, and enters the
+ * second product as two bf16 terms (within 2^-16); Y is rounded once.
+ *   r = 0: no adapter (A, B and T_out NULL)
+ * Requires K % 64 == 0, K <= 2^17, N % 8 == 0, 0 <= r <= 256; M K, N K, 2 M N,
+ * 4 M r and 2 N r under 2^31 (r counted up to a multiple of 8); workspace of
+ * int8_linear_workspace_bytes(M, K, N, r, QLORA_BASE_INT8, 0). */
+int int8_linear_fwd(const int8_t* Xcodes, const float* Xscale, int64_t M, int64_t K, int64_t N,
+                    const int8_t* Wcodes, const float* Wscale, const uint16_t* A, const uint16_t* B,
+                    int r, float alpha, uint16_t* Y, float* T_out, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Backward from an X that was kept in rows of 8 bits, on a base in 8 bits, NF4
+ * or bf16.  With U = dY B:
+ *   dX = dY W_hat + s U A      bf16 [M, K]  (NULL = skip; flags as qlora_linear_bwd)
+ *   dA = s U^T X,   dB = s dY^T T            fp32 [r, K], [N, r]
+ * (straight through the quantiser: the gradient with respect to X's values).
+ *   T  fp32 [M, r] as int8_linear_fwd gives it, or bf16 as the forwards of the
+ *      other two bases do; NULL: computed again from the codes.
+ * dA and dB are fp32 sums of exact products: U and T enter as three bf16 terms
+ * (all 24 bits), the codes as they are, their scale in U's factor.  dX reads an
+ * 8-bit base as a bf16 copy made once per call, each weight rounded once, as
+ * the NF4 base's.  The order of every sum is fixed.
+ * Requires the sizes of int8_linear_fwd with 1 <= r, and 2 M K < 2^31; 2 N K <
+ * 2^31 for an 8-bit or bf16 base; workspace of int8_linear_workspace_bytes(...,
+ * base, 1). */
+int int8_linear_bwd(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale, int64_t M,
+                    int64_t K, int64_t N, const int8_t* Wcodes, const float* Wscale,
+                    const uint16_t* A, const uint16_t* B, int r, float alpha, const float* T,
+                    uint16_t* dX, float* dA, float* dB, int flags, void* workspace,
+                    size_t workspace_bytes, void* stream);
+int qlora_linear_bwd_int8(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale, int64_t M,
+                          int64_t K, int64_t N, const uint8_t* packed, const uint8_t* codes,
+                          const float* scales, const float* mean, const uint16_t* A,
+                          const uint16_t* B, int r, float alpha, const uint16_t* T, uint16_t* dX,
+                          float* dA, float* dB, int flags, void* workspace, size_t workspace_bytes,
+                          void* stream);
+int qlora_linear_bwd_bf16_int8(const uint16_t* dY, const int8_t* Xcodes, const float* Xscale,
+                               int64_t M, int64_t K, int64_t N, const uint16_t* W,
+                               const uint16_t* A, const uint16_t* B, int r, float alpha,
+                               const uint16_t* T, uint16_t* dX, float* dA, float* dB, int flags,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of the calls above for a base (QLORA_BASE_*; the forward
+ * has the 8-bit one alone); 0 where none is needed and for invalid sizes. */
+#define QLORA_BASE_INT8 0
+#define QLORA_BASE_NF4  1
+#define QLORA_BASE_BF16 2
+size_t int8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int base, int is_bwd);
+
+/* The gating of a SiLU-gated MLP between its projections, H = silu(G) Up for
+ * bf16 G, Up [M, I], which leaves H as rows of 8 bits, the down projection's
+ * input (Hcodes [M, I], Hscale [M]), and G and Up as blocks of 8 bits for the
+ * backward (codes [M, I], scale [M, I / 64]; all four pointers NULL: not kept).
+ * H is quantised from its fp32 value; H (bf16 [M, I], may be NULL) is
+ * silu_mul_fwd's.  Requires I % 64 == 0 and the sizes of int8_quantize. */
+int silu_mul_fwd_int8(const uint16_t* G, const uint16_t* Up, int64_t M, int64_t I, uint16_t* H,
+                      int8_t* Hcodes, float* Hscale, int8_t* Gcodes, float* Gscale, int8_t* Ucodes,
+                      float* Uscale, void* stream);
+
+/* silu_mul_bwd from those blocks: dG = dH Up sig(G) (1 + G (1 - sig(G))),
+ * dUp = dH silu(G), bf16 [M, I]. */
+int silu_mul_bwd_int8(const uint16_t* dH, const int8_t* Gcodes, const float* Gscale,
+                      const int8_t* Ucodes, const float* Uscale, int64_t M, int64_t I, uint16_t* dG,
+                      uint16_t* dUp, void* stream);
+
 /* ---- fused gate/up projections of a SiLU-gated MLP ---------------------- */
 
 /* One QLoRA linear of the MLP: NF4 base [I, K] as nf4_quantize + double_quant
