@@ -181,11 +181,12 @@ k_rank16_and_dequant(const uint16_t* __restrict__ S, int M, int64_t C,
                      const uint8_t* __restrict__ codes, const float* __restrict__ scales,
                      const float* __restrict__ mean, int64_t nwords, Codebook4 cb,
                      uint16_t* __restrict__ wout) {
+  __shared__ float q4[16];
   if ((int)blockIdx.x < rank_blocks)
     rank16_block<WT, RT, NW, rank_batch_shared<RT>()>(S, M, C, W, r, rows, out, blockIdx.x);
   else
     nf4_dequant_block(packed, codes, scales, mean, nwords, cb, wout,
-                      (int64_t)blockIdx.x - rank_blocks);
+                      (int64_t)blockIdx.x - rank_blocks, q4);
 }
 
 template <bool WT>

@@ -5,7 +5,8 @@
 // takes word 64 q + L of the wave's range, so every load and store
 // instruction of the wave covers one contiguous range.  The block's waves
 // take consecutive ranges; `blk` is the block's index in the dequant grid.
-// q8: the 8-bit levels as a table in LDS, or null for the linear code.
+// q4: 16 floats of LDS; q8: the 8-bit levels as a table in LDS, or null for the
+// linear code.
 #pragma once
 #include "device_common.h"
 #include "kernels.h"
@@ -20,9 +21,8 @@ __device__ __forceinline__ void nf4_dequant_block(const uint8_t* __restrict__ pa
                                                   const float* __restrict__ scales,
                                                   const float* __restrict__ mean, int64_t nwords,
                                                   const Codebook4& cb, uint16_t* __restrict__ out,
-                                                  int64_t blk_index,
+                                                  int64_t blk_index, float* q4,
                                                   const float* q8 = nullptr) {
-  __shared__ float q4[16];
   if (threadIdx.x < 16) {
     float v = 0.0f;
 #pragma unroll

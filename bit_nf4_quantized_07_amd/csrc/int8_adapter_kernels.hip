@@ -13,6 +13,7 @@
 // is rounded to bf16, three (all 24 bits) where it is kept in fp32.
 #include <type_traits>
 
+#include "dequant_block.h"
 #include "device_common.h"
 #include "kernels.h"
 #include "terms.h"
@@ -33,187 +34,538 @@ __device__ __forceinline__ uint4 zero_unless(bool ok, uint4 v) {
   return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
 }
 
-// What a rank-r product leaves (any may be null).  packed: MFMA operands of the
-// gradients, [chunk][term][rank tile][lane][8]: lane (i, g) holds rank 16 t + i
-// of tokens 8 g .. +7 of the chunk.
+// What a rank-r product leaves (any may be null), as MFMA operands where bf16
+// terms are asked for, 1 KB that a wave loads lane after lane:
+//   two     the forward's [block of 32 tokens][rank tile][term][lane][8]: lane
+//           (c, h) holds ranks 16 t + 8 h .. +7 of token c; hi and mid terms of
+//           s sum; tokens and ranks past the end are zero
+//   packed  the gradients' [chunk][term][rank tile][lane][8]: lane (i, g) holds
+//           rank 16 t + i of tokens 8 g .. +7 of the chunk; three terms of
+//           pscale[m] sum; tokens past the end are zero
 struct RankOut {
   float* sum;              // [M, r]
   uint16_t* bf16;          // [M, r]
-  uint16_t* two;           // [M][2][r]: hi and mid terms of s sum
+  uint16_t* two;
   float s;
-  uint16_t* packed;        // terms of pscale[m] sum
+  uint16_t* packed;
   const float* pscale;     // [M], or null: 1
 };
 
-__device__ __forceinline__ void pack_terms(uint16_t* packed, int ntiles, int m4, int t, int i,
-                                           const float (&x)[4]) {
-  // ranks 16 t + i of tokens m4 .. m4 + 3 (4 | m4)
-  const int64_t chunk = m4 / kChunk;
-  const int lane = 16 * ((m4 % kChunk) / 8) + i;
-  Terms e[4];
+__device__ __forceinline__ uint32_t pair(uint16_t lo, uint16_t hi) { return lo | (uint32_t)hi << 16; }
+__device__ __forceinline__ uint4 eight(const uint16_t (&v)[8]) {
+  return make_uint4(pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7]));
+}
+// Terms of eight tokens m8 .. m8 + 7 (8 | m8) of rank 16 t + i.
+__device__ __forceinline__ void pack_terms(uint16_t* packed, int ntiles, int64_t m8, int t, int i,
+                                           const float (&x)[8]) {
+  uint16_t w[3][8];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) e[v] = split(x[v]);
-  const uint32_t w[3][2] = {{e[0].hi | (uint32_t)e[1].hi << 16, e[2].hi | (uint32_t)e[3].hi << 16},
-                            {e[0].mid3 | (uint32_t)e[1].mid3 << 16, e[2].mid3 | (uint32_t)e[3].mid3 << 16},
-                            {e[0].lo | (uint32_t)e[1].lo << 16, e[2].lo | (uint32_t)e[3].lo << 16}};
+  for (int v = 0; v < 8; ++v) {
+    const Terms e = split(x[v]);
+    w[0][v] = e.hi; w[1][v] = e.mid3; w[2][v] = e.lo;
+  }
+  uint4* const p = reinterpret_cast<uint4*>(packed);
+  const int lane = 16 * (int)((m8 % kChunk) / 8) + i;
 #pragma unroll
-  for (int z = 0; z < 3; ++z)
-    *reinterpret_cast<uint2*>(packed + (((chunk * 3 + z) * ntiles + t) * 64 + lane) * 8 + (m4 % 8)) =
-        make_uint2(w[z][0], w[z][1]);
+  for (int z = 0; z < 3; ++z) p[((m8 / kChunk * 3 + z) * ntiles + t) * 64 + lane] = eight(w[z]);
 }
 
 // out[m][j] = sum_c S[m][c] W(j, c), W(j, c) = A[j][c] or (WT) B[c][j]; S bf16 or,
-// S8, codes whose row scale multiplies the finished sum.  A workgroup owns 16
-// rows and all r columns; its NW waves take every NW-th 64-wide slice of the
-// contraction (v_mfma_f32_16x16x32_bf16) with the loads of kB slices together,
-// and the waves' sums are added through LDS in a fixed order.
-// Rows are counted up to a whole chunk, so that packed terms past M are zero.
-template <bool S8, bool WT, int RT, int NW, int kB>
-__global__ void __launch_bounds__(NW * 64)
-k_int8_rank(const void* __restrict__ Sv, const float* __restrict__ sx, int M, int64_t C,
-            const uint16_t* __restrict__ W, int r, RankOut o) {
-  __shared__ float red[NW - 1][16][RT * 16];
-  __shared__ __attribute__((aligned(16))) uint16_t slab[WT ? NW : 1][64 * 16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// S8, codes whose row scale multiplies the finished sum.  A workgroup owns `rows`
+// rows (16, or 8 where that would leave CUs idle; the MFMA's others are zero) and
+// all r columns; its NW waves take every NW-th 64-wide slice of the contraction
+// (v_mfma_f32_16x16x32_bf16), the next slice in flight.
+//  * A load takes whole lines: eight lanes cover 128 bytes of a row (four 64 of
+//    codes), and a slice of B is one block of memory.  Loaded as the MFMA wants
+//    them, a row per lane, 64 lanes took 60 cycles a load where they take 16 so
+//    (T, 4096 columns: 3 loads a slice, 7.0 us at rank 16; 9, 20 us at rank 64,
+//    from one workgroup to 128).  The pieces go through a slab of LDS per wave,
+//    XOR-swizzled by row so that neither side has bank conflicts.
+//  * Loads cost no address arithmetic: a lane's offsets are fixed, a slice moves
+//    the scalar offset; a slice past the end reads a resource of no bytes, the
+//    last one (where 64 does not divide C) uses offsets of its own.
+//  * The waves' sums are added through LDS in a fixed order, a thread per (row,
+//    column), then leave as terms, a thread per eight of them.
+struct RankJob {
+  const void* S;           // [M, C], bf16 or codes
+  const float* sx;         // the codes' row scales
+  int M, C;
+  const uint16_t* W;       // A [r, C] or B [C, r]
+  int r, rows;             // rows of a workgroup
+  RankOut o;
+};
+template <bool S8, int RT>
+constexpr int rank_slab() { return 1024 * (S8 ? 1 : 2) + 2048 * RT; }   // bytes of a wave's
+
+template <bool S8, bool WT, int RT, int NW>
+__device__ __forceinline__ void rank_block(const RankJob& g, int blk, uint8_t* lds) {
+  constexpr int RK = 16 * RT;
+  constexpr int XN = S8 ? 1 : 2;                   // 1 KB loads of S a slice
+  constexpr int SLAB = rank_slab<S8, RT>();
+  static_assert(16 * RK * 4 + 128 <= SLAB, "a wave's sums, and the scales, take its slab's place");
+  const void* const S = g.S;
+  const float* const sx = g.sx;
+  const uint16_t* const W = g.W;
+  const RankOut& o = g.o;
+  const int M = g.M, C = g.C, r = g.r, rows = g.rows;
+  float* const rowscale = reinterpret_cast<float*>(lds + 16 * RK * 4);   // in wave 0's slab
+  float* const packscale = rowscale + 16;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15, grp = lane >> 4;
-  const int m0 = (int)blockIdx.x * 16, m = m0 + row;
-  const bool mvalid = m < M;
-  const int64_t nsteps = (C + 63) / 64;
-  const int64_t srow = (int64_t)(mvalid ? m : 0) * C;
-  const uint16_t* const S = reinterpret_cast<const uint16_t*>(Sv) + srow;
-  const int8_t* const Q = reinterpret_cast<const int8_t*>(Sv) + srow;
-  const int wrow = lane >> 1, wcol = 8 * (lane & 1);
-  uint16_t* const my = slab[WT ? wave : 0];
-  const int rd = (16 * grp + (row >> 2)) * 16 + 4 * (row & 3);
+  const int m0 = blk * rows;
+  const int nsteps = (C + 63) / 64;
+  const int cut = C % 64 ? nsteps - 1 : -1;        // the slice that C ends in
+  const int left = C - 64 * (nsteps - 1);          // columns of the last slice
+  const uint32_t sbytes = (uint32_t)((int64_t)M * C * (S8 ? 1 : 2));
+  const uint32_t wbytes = (uint32_t)((int64_t)C * r * 2);
+  uint8_t* const xs = lds + wave * SLAB;
+  uint8_t* const ws = xs + 1024 * XN;
+  // S: rows of 64 codes in 4 pieces of 16 bytes, or of 64 bf16 in 8
+  constexpr int XP = S8 ? 4 : 8;
+  auto xswz = [](int i) { return S8 ? (i >> 2) & 3 : (i >> 1) & 7; };
+  auto wswz = [](int i) { return (i >> 1) & 7; };
+  uint32_t xoff[XN], xcut[XN], xput[XN];
+#pragma unroll
+  for (int n = 0; n < XN; ++n) {
+    const int i = (64 / XP) * n + lane / XP, p = lane % XP;
+    xoff[n] = i < rows && m0 + i < M
+                  ? (uint32_t)((int64_t)(m0 + i) * C * (S8 ? 1 : 2) + 16 * p) : kOOB;
+    xcut[n] = p * (S8 ? 16 : 8) < left ? xoff[n] : kOOB;
+    xput[n] = (uint32_t)((i * XP + (p ^ xswz(i))) * 16);
+  }
+  // A: rank 16 t + 8 n + lane / 8 of load (t, n), 8 pieces of 8 values.  B: piece
+  // 64 n + lane of the slice's 64 rows of r8 pieces; the loads past r8 put zeros in
+  // the columns past r.  LDS: [t][64 c][16 ranks] as it is read transposed, rows
+  // XOR-swizzled by 2 t, so that the tiles' pieces of a row fall on different banks,
+  // and in every other 16 by 4, so that the lanes that read two of them do.
+  auto bswz = [](int c, int t) { return c ^ (2 * t) ^ ((c >> 2) & 4); };
+  const int r8 = r / 8;
+  uint32_t woff[2 * RT], wcut[2 * RT], wput[2 * RT];
+#pragma unroll
+  for (int n = 0; n < 2 * RT; ++n) {
+    if constexpr (WT) {
+      const int p = 64 * n + lane;
+      const int c = n < r8 ? p / r8 : lane, oct = n < r8 ? p % r8 : n;
+      woff[n] = n < r8 ? (uint32_t)((c * r + 8 * oct) * 2) : kOOB;
+      wcut[n] = c < left ? woff[n] : kOOB;
+      wput[n] = (uint32_t)((oct >> 1) * 2048 + bswz(c, oct >> 1) * 32 + 16 * (oct & 1));
+    } else {
+      const int i = 8 * (n & 1) + lane / 8, p = lane % 8, j = 16 * (n >> 1) + i;
+      woff[n] = j < r ? (uint32_t)(((int64_t)j * C + 8 * p) * 2) : kOOB;
+      wcut[n] = 8 * p < left ? woff[n] : kOOB;
+      wput[n] = (uint32_t)(((j * 8) + (p ^ wswz(i))) * 16);
+    }
+  }
+  const uint32_t wstep = WT ? (uint32_t)(64 * r * 2) : 128u;
+  float rs = 0.0f, ps = 1.0f;                      // of row tid
+  if (tid < rows && m0 + tid < M) {
+    if (S8) rs = sx[m0 + tid];
+    if (o.pscale) ps = o.pscale[m0 + tid];
+  }
 
   f32x4_t acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int64_t base = wave; base < nsteps; base += (int64_t)NW * kB) {
-    uint4 xv[kB][2], wv[kB][RT][2];
+  struct Batch { uint4 x[XN]; uint4 w[2 * RT]; };
+  auto load = [&](Batch& L, int ks) {
+    const bool sv = ks < nsteps, end = ks == cut;
+    const __amdgpu_buffer_rsrc_t rsr = rsrc_whole(S, sv ? sbytes : 0);
+    const __amdgpu_buffer_rsrc_t rw = rsrc_whole(W, sv ? wbytes : 0);
 #pragma unroll
-    for (int b = 0; b < kB; ++b) {
-      const int64_t ks = base + (int64_t)NW * b;
-      const bool sv = ks < nsteps;
-      if constexpr (S8) {   // 64 | C: a slice's 16 codes of a lane are whole
-        const uint4 v = *reinterpret_cast<const uint4*>(Q + (sv ? ks * 64 + 16 * grp : 0));
-        xv[b][0] = zero_unless(mvalid && sv, v);
-      }
+    for (int n = 0; n < XN; ++n)
+      L.x[n] = bload128s(rsr, end ? xcut[n] : xoff[n], (uint32_t)ks * (S8 ? 64 : 128));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t k = ks * 64 + 16 * grp + 8 * h;
-        const bool kvalid = sv && k < C;
-        if constexpr (!S8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(S + (kvalid ? k : 0));
-          xv[b][h] = zero_unless(mvalid && kvalid, v);
-        }
+    for (int n = 0; n < 2 * RT; ++n)
+      L.w[n] = bload128s(rw, end ? wcut[n] : woff[n], (uint32_t)ks * wstep);
+  };
+  typedef short v8s_t __attribute__((ext_vector_type(8)));
+  auto use = [&](const Batch& L) {
+    // A wave's LDS operations run in issue order: the stores land after the last
+    // slice's reads and before this one's.
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          if (!WT) {
-            const int j = 16 * t + row;
-            const bool ok = kvalid && j < r;
-            const uint4 w = *reinterpret_cast<const uint4*>(W + (ok ? (int64_t)j * C + k : 0));
-            wv[b][t][h] = zero_unless(ok, w);
-          } else {
-            const int64_t c = ks * 64 + 32 * h + wrow;
-            const int j = 16 * t + wcol;
-            const bool ok = sv && c < C && j < r;
-            const uint4 w = *reinterpret_cast<const uint4*>(W + (ok ? c * r + j : 0));
-            wv[b][t][h] = zero_unless(ok, w);
-          }
-        }
-      }
+    for (int n = 0; n < XN; ++n) *reinterpret_cast<uint4*>(xs + xput[n]) = L.x[n];
+#pragma unroll
+    for (int n = 0; n < 2 * RT; ++n) *reinterpret_cast<uint4*>(ws + wput[n]) = L.w[n];
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    uint4 xv[2];                          // columns 16 grp + 8 h of the slice
+    if constexpr (S8) {
+      codes_to_bf16(*reinterpret_cast<const uint4*>(xs + (row * 4 + (grp ^ xswz(row))) * 16), xv);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        xv[h] = *reinterpret_cast<const uint4*>(xs + (row * 8 + ((2 * grp + h) ^ xswz(row))) * 16);
     }
-    __builtin_amdgcn_sched_barrier(0);   // every load of the batch before the first MFMA
-#pragma unroll
-    for (int b = 0; b < kB; ++b) {
-      uint4 xs[2] = {xv[b][0], xv[b][1]};
-      if constexpr (S8) codes_to_bf16(xv[b][0], xs);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        bf16x8_t bop[2];
-        if (!WT) {
-          bop[0] = __builtin_bit_cast(bf16x8_t, wv[b][t][0]);
-          bop[1] = __builtin_bit_cast(bf16x8_t, wv[b][t][1]);
-        } else {
-          // A wave's LDS operations run in issue order: the stores are
-          // complete before the reads, which complete before the next stores.
-          *reinterpret_cast<uint4*>(my + wrow * 16 + wcol) = wv[b][t][0];
-          *reinterpret_cast<uint4*>(my + (32 + wrow) * 16 + wcol) = wv[b][t][1];
-          __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v4s_t lo = lds_read_tr16(my + rd + 8 * h * 16);
-            const v4s_t hi = lds_read_tr16(my + rd + (8 * h + 4) * 16);
-            typedef short v8s_t __attribute__((ext_vector_type(8)));
-            const v8s_t bv = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            bop[h] = __builtin_bit_cast(bf16x8_t, bv);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[t] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xs[h]), bop[h], acc[t]);
-      }
-    }
-  }
-
-  // acc[t][v]: row 4 grp + v, column 16 t + row of the tile.
-  if (wave > 0) {
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave - 1][4 * grp + v][16 * t + row] = acc[t][v];
+      for (int h = 0; h < 2; ++h) {
+        bf16x8_t bop;
+        if constexpr (WT) {
+          const int c = 16 * grp + 8 * h + (row >> 2);
+          const uint16_t* const p = reinterpret_cast<const uint16_t*>(ws + 2048 * t) + 4 * (row & 3);
+          const v4s_t lo = lds_read_tr16(p + bswz(c, t) * 16);
+          const v4s_t hi = lds_read_tr16(p + bswz(c + 4, t) * 16);
+          const v8s_t bv = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          bop = __builtin_bit_cast(bf16x8_t, bv);
+        } else {
+          bop = *reinterpret_cast<const bf16x8_t*>(
+              ws + ((16 * t + row) * 8 + ((2 * grp + h) ^ wswz(row))) * 16);
+        }
+        acc[t] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xv[h]), bop, acc[t]);
+      }
+  };
+  Batch la, lb;
+  load(la, wave);
+  for (int ks = wave; ks < nsteps; ks += 2 * NW) {
+    load(lb, ks + NW);
+    __builtin_amdgcn_sched_barrier(0);   // a slice's loads before the other's MFMAs
+    use(la);
+    load(la, ks + 2 * NW);
+    __builtin_amdgcn_sched_barrier(0);
+    use(lb);
   }
+  if (tid < rows) {
+    rowscale[tid] = rs;
+    packscale[tid] = ps;
+  }
+  auto sums = [&](int q, int i, int j) -> float& {
+    return reinterpret_cast<float*>(lds + q * SLAB)[i * RK + j];
+  };
+
+  // acc[t][v]: row 4 grp + v, column 16 t + row of the tile
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sums(wave, 4 * grp + v, 16 * t + row) = acc[t][v];
   __syncthreads();
-  if (wave != 0) return;
+  for (int e = tid; e < rows * RK; e += NW * 64) {
+    const int i = e / RK, j = e % RK, mm = m0 + i;
+    float sum = 0.0f;
+    if (mm < M && j < r) {
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int j = 16 * t + row;
-    float p[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int mm = m0 + 4 * grp + v;
-      float sum = acc[t][v];
-#pragma unroll
-      for (int q = 0; q < NW - 1; ++q) sum += red[q][4 * grp + v][j];
-      const bool in = mm < M && j < r;
-      if (S8 && in) sum *= sx[mm];
-      p[v] = !in ? 0.0f : o.pscale ? sum * o.pscale[mm] : sum;
-      if (!in) continue;
+      for (int q = 0; q < NW; ++q) sum += sums(q, i, j);
+      if (S8) sum *= rowscale[i];
       if (o.sum) o.sum[(int64_t)mm * r + j] = sum;
       if (o.bf16) o.bf16[(int64_t)mm * r + j] = f32_to_bf16(sum);
-      if (o.two) {
-        const Terms e = split(o.s * sum);
-        o.two[(int64_t)mm * 2 * r + j] = e.hi;
-        o.two[((int64_t)mm * 2 + 1) * r + j] = e.mid2;
-      }
     }
-    if (o.packed && 16 * t < r) pack_terms(o.packed, (r + 15) / 16, m0 + 4 * grp, t, row, p);
+    sums(0, i, j) = sum;                 // this thread's own
   }
+  if (!o.two && !o.packed) return;
+  __syncthreads();
+  const int ntiles = (r + 15) / 16;
+  if (o.two)
+    for (int e = tid; e < rows * 2 * ntiles; e += NW * 64) {
+      const int i = e / (2 * ntiles), oct = e % (2 * ntiles), mm = m0 + i;
+      uint16_t hi[8], mid[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        const Terms x = split(o.s * sums(0, i, 8 * oct + v));
+        hi[v] = x.hi; mid[v] = x.mid2;
+      }
+      uint4* const p = reinterpret_cast<uint4*>(o.two) +
+                       ((int64_t)(mm / 32) * ntiles + oct / 2) * 128 + (mm % 32) + 32 * (oct & 1);
+      p[0] = eight(hi);
+      p[64] = eight(mid);
+    }
+  if (o.packed)
+    for (int e = tid; e < rows / 8 * 16 * ntiles; e += NW * 64) {
+      const int j = e % (16 * ntiles), i8 = 8 * (e / (16 * ntiles));
+      float x[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) x[v] = sums(0, i8 + v, j) * packscale[i8 + v];
+      pack_terms(o.packed, ntiles, m0 + i8, j / 16, j % 16, x);
+    }
 }
 
+// Up to 32 ranks: a workgroup's own sums, no second launch.
+constexpr int kRankOnce = 32;
+template <class F>
+static void rank_form(int r, F f) {
+  using std::integral_constant;
+  if (r <= 16) f(integral_constant<int, 1>());
+  else f(integral_constant<int, 2>());
+}
+constexpr int kRankWaves = 16;
+// rows of a workgroup, and workgroups; operands are whole blocks of tokens
+static int rank_blocks(RankJob& g) {
+  g.rows = (g.M + 15) / 16 < kCUs ? 8 : 16;
+  const int64_t m = g.o.packed || g.o.two ? ((int64_t)g.M + kChunk - 1) / kChunk * kChunk : g.M;
+  return (int)((m + g.rows - 1) / g.rows);
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kRankWaves * 64) k_int8_T(RankJob g) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRankWaves * rank_slab<true, RT>()];
+  rank_block<true, false, RT, kRankWaves>(g, blockIdx.x, lds);
+}
+
+// ---------------------------------------------------------------------------
+// The same products above 32 ranks, where a workgroup that reads all of W for 16
+// rows reads it too often (U, 4001 tokens x 4096, rank 64: 25 us).  A workgroup
+// takes 64 rows, 64 ranks and one of `zs` slices of the contraction; its four waves
+// take 32 rows x 32 ranks each (v_mfma_f32_32x32x16_bf16).  The contraction
+// advances 64 columns a step through four LDS stages that buffer loads fill three
+// steps ahead.  The slices' sums [zs][M][r] go to the workspace; k_int8_finish adds
+// them in their order.  Slices are the fast grid index, so that an XCD keeps to its
+// part of W.
+struct DownJob {
+  const void* S;           // [M, C], bf16 or codes
+  int M, C;
+  const uint16_t* W;       // A [r, C] or B [C, r]
+  int r, groups;           // of 64 ranks
+  int zs, zlen;            // slices, steps in one
+  float* part;
+};
+constexpr int kDownStage = 16 * 1024;
+constexpr int kDownSlices = 4;   // 8 took 1 us off the slices' launch and put 2 on the sums' (4001 tokens)
+
+// s0 .. s3: the stages, arrays of their own (of one array the compiler would wait
+// for every load before each read).
 template <bool S8, bool WT>
-static hipError_t int8_rank(const void* S, const float* sx, int64_t M, int64_t C, const uint16_t* W,
-                            int r, const RankOut& o, hipStream_t st) {
-  int64_t rows = (M + 15) / 16;
-  if (o.packed) rows = (M + kChunk - 1) / kChunk * (kChunk / 16);
-  const dim3 grid((unsigned)rows);
-  const int tiles = (r + 15) / 16;
-  if (tiles <= 1) hipLaunchKernelGGL((k_int8_rank<S8, WT, 1, 16, 4>), grid, dim3(1024), 0, st, S, sx, (int)M, C, W, r, o);
-  else if (tiles <= 2) hipLaunchKernelGGL((k_int8_rank<S8, WT, 2, 16, 2>), grid, dim3(1024), 0, st, S, sx, (int)M, C, W, r, o);
-  else if (tiles <= 4) hipLaunchKernelGGL((k_int8_rank<S8, WT, 4, 8, 1>), grid, dim3(512), 0, st, S, sx, (int)M, C, W, r, o);
-  else if (tiles <= 8) hipLaunchKernelGGL((k_int8_rank<S8, WT, 8, 4, 1>), grid, dim3(256), 0, st, S, sx, (int)M, C, W, r, o);
-  else hipLaunchKernelGGL((k_int8_rank<S8, WT, 16, 4, 1>), grid, dim3(256), 0, st, S, sx, (int)M, C, W, r, o);
-  return hipGetLastError();
+__device__ __forceinline__ void down_block(const DownJob& g, int blk, uint8_t* s0, uint8_t* s1,
+                                           uint8_t* s2, uint8_t* s3) {
+  constexpr int XL = S8 ? 1 : 2, WL = 2, L = XL + WL;      // a wave's loads of a step
+  constexpr int XB = 64 * (S8 ? 64 : 128);                 // bytes of S in a stage
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int z = blk % g.zs, gr = blk / g.zs % g.groups;
+  const int m0 = blk / g.zs / g.groups * 64, j0 = 64 * gr;
+  const int M = g.M, C = g.C, r = g.r;
+  const int nsteps = (C + 63) / 64;
+  const int kz0 = z * g.zlen, kz1 = min(nsteps, kz0 + g.zlen);
+  const int cut = C % 64 ? nsteps - 1 : -1;                // the step that C ends in
+  const int left = C - 64 * (nsteps - 1);
+  // S: load i of wave w fills 1 KB of rows of 64 codes (4 pieces of 16 bytes) or of
+  // 64 bf16 (8 pieces); A: rows of 64 values (8 pieces); B: rows of 64 ranks.
+  constexpr int XP = S8 ? 4 : 8, XR = 64 / XP;
+  auto xswz = [](int i) { return S8 ? (i >> 2) & 3 : (i >> 1) & 7; };
+  auto wswz = [](int i) { return WT ? ((i >> 1) & 1) << 2 : (i >> 1) & 7; };
+  uint32_t xoff[XL], xcut[XL], woff[WL], wcut[WL];
+#pragma unroll
+  for (int n = 0; n < XL; ++n) {
+    const int i = XR * (XL * wave + n) + lane / XP, p = (lane % XP) ^ xswz(i);
+    xoff[n] = m0 + i < M ? (uint32_t)((int64_t)(m0 + i) * C * (S8 ? 1 : 2) + 16 * p) : kOOB;
+    xcut[n] = p * (S8 ? 16 : 8) < left ? xoff[n] : kOOB;
+  }
+#pragma unroll
+  for (int n = 0; n < WL; ++n) {
+    const int i = 8 * (WL * wave + n) + lane / 8, p = (lane % 8) ^ wswz(i);
+    if constexpr (WT) {
+      woff[n] = j0 + 8 * p < r ? (uint32_t)((i * r + j0 + 8 * p) * 2) : kOOB;
+      wcut[n] = i < left ? woff[n] : kOOB;
+    } else {
+      woff[n] = j0 + i < r ? (uint32_t)(((int64_t)(j0 + i) * C + 8 * p) * 2) : kOOB;
+      wcut[n] = 8 * p < left ? woff[n] : kOOB;
+    }
+  }
+  const uint32_t wstep = WT ? (uint32_t)(64 * r * 2) : 128u;
+  const __amdgpu_buffer_rsrc_t rs = rsrc_whole(g.S, (uint32_t)((int64_t)M * C * (S8 ? 1 : 2)));
+  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)C * r * 2));
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  uint8_t* const stage[4] = {s0, s1, s2, s3};
+  auto load = [&](int buf, int kb) {
+    const int k = __builtin_amdgcn_readfirstlane(min(kb, kz1 - 1));
+    uint8_t* const st = stage[buf];
+    const bool end = k == cut;
+#pragma unroll
+    for (int n = 0; n < XL; ++n)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(st + 1024 * (XL * wave + n)), 16,
+                                               end ? xcut[n] : xoff[n], (uint32_t)k * (S8 ? 64 : 128), 0, 0);
+#pragma unroll
+    for (int n = 0; n < WL; ++n)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr)(st + XB + 1024 * (WL * wave + n)), 16,
+                                               end ? wcut[n] : woff[n], (uint32_t)k * wstep, 0, 0);
+  };
+  const int xrow = 32 * (wave >> 1) + c, wblk = 32 * (wave & 1);
+  const int grp = lane >> 4, gi = lane & 15;
+  f32x16_t acc;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 3; ++s) load(s, kz0 + s);
+  auto step = [&](auto Pc, int kb) {
+    constexpr int P = decltype(Pc)::value;
+    // this step has landed in every wave, and nobody reads the stage before it
+    __builtin_amdgcn_s_waitcnt((2 * L & 0xF) | (0x7 << 4) | (0xF << 8));   // vmcnt(2 L)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    load((P + 3) % 4, kb + 3);
+    const uint8_t* const xs = stage[P];
+    const uint8_t* const ws = xs + XB;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      bf16x8_t xop, wop;
+      if constexpr (S8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(xs + (xrow * 4 + (t ^ xswz(xrow))) * 16 + 8 * h);
+        xop = __builtin_bit_cast(bf16x8_t, make_uint4(codes_bf16x2(v.x, 0), codes_bf16x2(v.x, 2),
+                                                      codes_bf16x2(v.y, 0), codes_bf16x2(v.y, 2)));
+      } else {
+        xop = *reinterpret_cast<const bf16x8_t*>(xs + (xrow * 8 + ((2 * t + h) ^ xswz(xrow))) * 16);
+      }
+      if constexpr (WT) {
+        typedef short v8s_t __attribute__((ext_vector_type(8)));
+        const int k = 16 * t + 8 * (grp >> 1) + (gi >> 2), col = wblk + 16 * (grp & 1) + 4 * (gi & 3);
+        auto at = [&](int row) {
+          return reinterpret_cast<const uint16_t*>(ws + row * 128 + ((col >> 3) ^ wswz(row)) * 16) + (col & 7);
+        };
+        const v4s_t lo = lds_read_tr16(at(k)), hi = lds_read_tr16(at(k + 4));
+        const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        wop = __builtin_bit_cast(bf16x8_t, v);
+      } else {
+        const int row = wblk + c;
+        wop = *reinterpret_cast<const bf16x8_t*>(ws + (row * 8 + ((2 * t + h) ^ wswz(row))) * 16);
+      }
+      acc = mfma_32x32x16(wop, xop, acc);
+    }
+  };
+  int kb = kz0;   // whole groups of four without a branch between them
+  for (; kb + 4 <= kz1; kb += 4) {
+    step(std::integral_constant<int, 0>(), kb);
+    step(std::integral_constant<int, 1>(), kb + 1);
+    step(std::integral_constant<int, 2>(), kb + 2);
+    step(std::integral_constant<int, 3>(), kb + 3);
+  }
+  if (kb < kz1) {
+    step(std::integral_constant<int, 0>(), kb);
+    if (kb + 1 < kz1) step(std::integral_constant<int, 1>(), kb + 1);
+    if (kb + 2 < kz1) step(std::integral_constant<int, 2>(), kb + 2);
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the workgroup
+  // lane: row xrow, ranks j0 + wblk + 8 (v / 4) + 4 h + (v % 4)
+  const int m = m0 + xrow;
+  float* const out = g.part + ((int64_t)z * M + m) * r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int j = j0 + wblk + 8 * q + 4 * h;
+    if (m < M && j < r)
+      *reinterpret_cast<f32x4_t*>(out + j) = f32x4_t{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+  }
+}
+// Slices so that two workgroups a CU are in reach, four steps in one at least.
+static int down_blocks(DownJob& g) {
+  g.groups = (g.r + 63) / 64;
+  const int tiles = (g.M + 63) / 64 * g.groups, steps = (g.C + 63) / 64;
+  g.zs = max(1, min(min(2 * kCUs / tiles, steps / 4), kDownSlices));
+  g.zlen = (steps + g.zs - 1) / g.zs;
+  g.zs = (steps + g.zlen - 1) / g.zlen;
+  return tiles * g.zs;
+}
+static size_t down_bytes(int64_t M, int64_t C, int r) {
+  DownJob g{nullptr, (int)M, (int)C, nullptr, r, 0, 0, 0, nullptr};
+  down_blocks(g);
+  return (size_t)g.zs * M * r * 4;
+}
+
+__global__ void __launch_bounds__(256) k_int8_T_down(DownJob g) {
+  __shared__ __attribute__((aligned(16))) uint8_t s0[kDownStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[kDownStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[kDownStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s3[kDownStage];
+  down_block<true, false>(g, blockIdx.x, s0, s1, s2, s3);
+}
+
+// A job's slices added, 32 tokens x 64 ranks a workgroup.
+struct FinishJob {
+  const float* part;
+  int zs, M, r;
+  const float* sx;         // row scales of codes, or null
+  RankOut o;
+};
+__device__ __forceinline__ void finish_block(const FinishJob& g, int blk, float (*val)[33]) {
+  const int groups = (g.r + 63) / 64, ntiles = (g.r + 15) / 16;
+  const int m0 = blk / groups * 32, j0 = blk % groups * 64;
+  const int i = threadIdx.x >> 3, oct = threadIdx.x & 7, m = m0 + i, j = j0 + 8 * oct;
+  const RankOut& o = g.o;
+  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  float ps = 1.0f;
+  if (m < g.M && j < g.r) {
+    const float s = g.sx ? g.sx[m] : 1.0f;
+    if (o.pscale) ps = o.pscale[m];
+    float4 a[kDownSlices], b[kDownSlices];   // every slice's loads before the first sum
+#pragma unroll
+    for (int z = 0; z < kDownSlices; ++z) {
+      const float4* const p =
+          reinterpret_cast<const float4*>(g.part + ((int64_t)min(z, g.zs - 1) * g.M + m) * g.r + j);
+      a[z] = p[0];
+      b[z] = p[1];
+    }
+#pragma unroll
+    for (int z = 0; z < kDownSlices; ++z) {
+      if (z >= g.zs) break;
+      x[0] += a[z].x; x[1] += a[z].y; x[2] += a[z].z; x[3] += a[z].w;
+      x[4] += b[z].x; x[5] += b[z].y; x[6] += b[z].z; x[7] += b[z].w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= s;
+    const int64_t at = (int64_t)m * g.r + j;
+    if (o.sum) {
+      reinterpret_cast<float4*>(o.sum + at)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(o.sum + at)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    if (o.bf16)
+      *reinterpret_cast<uint4*>(o.bf16 + at) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
+  if (o.two && j < 16 * ntiles) {
+    uint16_t hi[8], mid[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const Terms t = split(o.s * x[e]);
+      hi[e] = t.hi; mid[e] = t.mid2;
+    }
+    uint4* const p = reinterpret_cast<uint4*>(o.two) + ((int64_t)(m / 32) * ntiles + j / 16) * 128 + (m % 32) +
+                     32 * (oct & 1);
+    p[0] = eight(hi);
+    p[64] = eight(mid);
+  }
+  if (!o.packed) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) val[8 * oct + e][i] = x[e] * ps;
+  __syncthreads();
+  const int jj = threadIdx.x & 63, i8 = 8 * (threadIdx.x >> 6);
+  if (j0 + jj >= 16 * ntiles) return;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = val[jj][i8 + e];
+  pack_terms(o.packed, ntiles, m0 + i8, (j0 + jj) / 16, jj % 16, v);
+}
+static int finish_blocks(int64_t M, int r) { return (int)((M + 31) / 32 * ((r + 63) / 64)); }
+__global__ void __launch_bounds__(256) k_int8_finish(FinishJob a, int na, FinishJob b) {
+  __shared__ float val[64][33];
+  if ((int)blockIdx.x < na) finish_block(a, blockIdx.x, val);
+  else finish_block(b, (int)blockIdx.x - na, val);
+}
+
+size_t int8_two_bytes(int64_t M, int r) {
+  return (size_t)((M + kChunk - 1) / kChunk) * ((r + 15) / 16) * 2048;
 }
 
 hipError_t launch_int8_T(const Int8Rows& X, int64_t M, int64_t K, const uint16_t* A, int r, float s,
-                         float* T, uint16_t* T2, hipStream_t st) {
+                         float* T, uint16_t* T2, float* part, hipStream_t st) {
   RankOut o{};
   o.sum = T; o.two = T2; o.s = s;
-  return int8_rank<true, false>(X.codes, X.scale, M, K, A, r, o, st);
+  if (r <= kRankOnce) {
+    RankJob g{X.codes, X.scale, (int)M, (int)K, A, r, 0, o};
+    const int blocks = rank_blocks(g);
+    rank_form(r, [&](auto rt) {
+      constexpr int RT = decltype(rt)::value;
+      hipLaunchKernelGGL(k_int8_T<RT>, dim3(blocks), dim3(kRankWaves * 64), 0, st, g);
+    });
+    return hipGetLastError();
+  }
+  DownJob g{X.codes, (int)M, (int)K, A, r, 0, 0, 0, part};
+  const int blocks = down_blocks(g);
+  hipLaunchKernelGGL(k_int8_T_down, dim3(blocks), dim3(256), 0, st, g);
+  const FinishJob f{part, g.zs, (int)M, r, X.scale, o};
+  const int nf = finish_blocks(M, r);
+  hipLaunchKernelGGL(k_int8_finish, dim3(nf), dim3(256), 0, st, f, nf, f);
+  return hipGetLastError();
 }
+// Bytes of fp32 sums that launch_int8_T needs room for.
+size_t int8_T_bytes(int64_t M, int64_t K, int r) { return r <= kRankOnce ? 0 : down_bytes(M, K, r); }
 
 // T = sum over kTSplits slices of the contraction, without the row scale, for up
 // to 16 tokens: a workgroup per (16 ranks, slice), its waves' sums through LDS.
@@ -257,40 +609,107 @@ hipError_t launch_int8_T_partial(const int8_t* X, int64_t M, int64_t K, const ui
   return hipGetLastError();
 }
 
-// T given in fp32 (three terms) or bf16 (its own only term; the others are 2^-40
-// of it, which leaves the sum as it is) as the gradients' operands: a thread per
-// (rank, four tokens).
-template <class E>
-__global__ void __launch_bounds__(256)
-k_int8_pack_T(const E* __restrict__ T, int M, int r, uint16_t* __restrict__ packed) {
-  const int ntiles = (r + 15) / 16, width = 16 * ntiles;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m4 = 4 * (e / width);
+// ---------------------------------------------------------------------------
+// What the backward's products need first, in one launch whose workgroups do one
+// thing each: U = dY B (the dX product's operand, and sx U's terms), T's terms
+// (from T, or T computed again), and the bf16 copy of the base for dX.  U alone
+// waits for memory most of its time and the copy is bound by it: side by side they
+// take little more than the longer one.
+struct PrepArgs {
+  RankJob u;
+  int nu;                    // workgroups of U
+  RankJob t;                 // T computed again (S null: T is given)
+  const float* T;            // [M, r] fp32 (three terms), or
+  const uint16_t* T_bf16;    // bf16 (its own only term; the others are 2^-40 of it,
+                             // which leaves the sum as it is)
+  int nt;                    // workgroups of T
+  const int8_t* wcodes;      // an 8-bit base, or null
+  const float* wscale;
+  NF4Weight w;               // else an NF4 base, if packed is not null
+  int64_t words;             // of 16 codes, or of 8 weights
+  uint32_t k16;              // words of 16 codes in a row
+  uint16_t* copy;
+  Codebook4 cb;
+};
+
+// T's terms, a thread per (rank, eight tokens).
+__device__ __forceinline__ void pack_T(const PrepArgs& g, int64_t e) {
+  const int M = g.t.M, r = g.t.r, ntiles = (r + 15) / 16, width = 16 * ntiles;
+  const int64_t m8 = 8 * (e / width);
   const int j = (int)(e % width);
-  if (m4 >= (int64_t)(M + kChunk - 1) / kChunk * kChunk) return;
-  float x[4];
+  if (m8 >= (int64_t)(M + kChunk - 1) / kChunk * kChunk) return;
+  float x[8];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int64_t m = m4 + v;
+  for (int v = 0; v < 8; ++v) {
+    const int64_t m = m8 + v;
     x[v] = 0.0f;
-    if (m < M && j < r) {
-      if constexpr (sizeof(E) == 4) x[v] = T[m * r + j];
-      else x[v] = bf16_to_f32(T[m * r + j]);
-    }
+    if (m < M && j < r) x[v] = g.T ? g.T[m * r + j] : bf16_to_f32(g.T_bf16[m * r + j]);
   }
-  pack_terms(packed, ntiles, (int)m4, j / 16, j % 16, x);
+  pack_terms(g.t.o.packed, ntiles, m8, j / 16, j % 16, x);
+}
+
+constexpr int kCopyRounds = 4;   // words of 16 codes per thread
+__device__ __forceinline__ void copy_int8(const PrepArgs& g, int64_t blk) {
+  const int64_t w0 = (blk * blockDim.x + (threadIdx.x & ~63)) * kCopyRounds + (threadIdx.x & 63);
+  uint4 c[kCopyRounds];
+  float s[kCopyRounds];
+#pragma unroll
+  for (int q = 0; q < kCopyRounds; ++q) {
+    const int64_t i = min(w0 + 64 * q, g.words - 1);
+    c[q] = reinterpret_cast<const uint4*>(g.wcodes)[i];
+    s[q] = g.wscale[(uint32_t)i / g.k16];
+  }
+#pragma unroll
+  for (int q = 0; q < kCopyRounds; ++q) {
+    const int64_t i = w0 + 64 * q;
+    if (i >= g.words) continue;
+    const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = pack_bf16x2((float)(int8_t)(w[e / 2] >> (16 * (e & 1))) * s[q],
+                         (float)(int8_t)(w[e / 2] >> (16 * (e & 1) + 8)) * s[q]);
+    reinterpret_cast<uint4*>(g.copy)[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(g.copy)[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+__device__ __forceinline__ void prep_copy(const PrepArgs& g, int64_t blk, uint8_t* lds) {
+  if (g.wcodes) copy_int8(g, blk);
+  else nf4_dequant_block(g.w.packed, g.w.codes, g.w.scales, g.w.mean, g.words, g.cb, g.copy, blk,
+                         reinterpret_cast<float*>(lds));
+}
+template <int RT>
+__global__ void __launch_bounds__(kRankWaves * 64) k_int8_prep(PrepArgs g) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRankWaves * rank_slab<false, RT>()];   // T's are smaller
+  const int b = blockIdx.x;
+  if (b < g.nu) rank_block<false, true, RT, kRankWaves>(g.u, b, lds);
+  else if (b >= g.nu + g.nt) prep_copy(g, b - g.nu - g.nt, lds);
+  else if (g.t.S) rank_block<true, false, RT, kRankWaves>(g.t, b - g.nu, lds);
+  else pack_T(g, (int64_t)(b - g.nu) * blockDim.x + threadIdx.x);
+}
+// Above 32 ranks: sums of slices, which k_int8_finish adds.
+__global__ void __launch_bounds__(256) k_int8_prep_down(PrepArgs g, DownJob u, DownJob t) {
+  __shared__ __attribute__((aligned(16))) uint8_t s0[kDownStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[kDownStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[kDownStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s3[kDownStage];
+  const int b = blockIdx.x;
+  if (b < g.nu) down_block<false, true>(u, b, s0, s1, s2, s3);
+  else if (b >= g.nu + g.nt) prep_copy(g, b - g.nu - g.nt, s0);
+  else if (t.S) down_block<true, false>(t, b - g.nu, s0, s1, s2, s3);
+  else pack_T(g, (int64_t)(b - g.nu) * blockDim.x + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
 // O[c][j] = s sum_m P[m][c] Q[m][j] for (P, Q) = (Cx, terms of sx U): dA^T, and
 // (dY, terms of T): dB, in one launch that reads P once.  A workgroup owns 32
-// columns of P and up to 64 ranks and contracts over all tokens itself; its four
+// or 64 columns of P and up to 64 ranks and contracts over all tokens itself; its four
 // waves take every fourth 32-token chunk.  P goes through a slab of LDS per wave
 // (codes as bf16) and comes back transposed as the MFMA operand (v_mfma_f32_16x16x32_bf16);
 // Q is loaded as the operands that it is stored as, 1 KB in a row each.  Each
 // term takes an MFMA on the same P operand, the small terms first.  The waves'
 // sums are added through LDS in a fixed order.
-constexpr int kGradCols8 = 32;
 constexpr int kGradWaves8 = 4;
 
 struct Grad8Job {
@@ -298,86 +717,98 @@ struct Grad8Job {
   int64_t ld;            // its columns (a multiple of 8; of 16 for codes)
   const uint16_t* Q;     // packed terms
   float* out;            // trans: [r, ld], else [ld, r]
-  int slices;            // workgroups: ceil(ld / 32)
+  int slices;            // workgroups: ceil(ld / columns of one)
 };
+
+// CB: bands of 32 columns.  With 64 ranks a workgroup reads 12 KB of Q a chunk, six
+// times a band's P: two bands halve that (4001 tokens, 11008 and 4096 columns: 58 us
+// with one).
+template <int RT>
+constexpr int grad_bands() { return RT == 4 ? 2 : 1; }
 
 template <bool S8, int RT>
 __device__ __forceinline__ void grads8(const Grad8Job& g, int lb, int M, int r, int t0, float s,
-                                       uint16_t (*slab)[kChunk * kGradCols8],
-                                       f32x4_t (*red)[2 * RT][64]) {
+                                       uint8_t* lds) {
+  constexpr int CB = grad_bands<RT>(), CW = 32 * CB;      // columns
+  constexpr int PL = (S8 ? 1 : 2) * CB;                   // 1 KB loads of P a chunk
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, q4 = lane >> 4;
   const int full = (g.slices / kXCDs) * kXCDs;
   const int sl = lb < full ? (lb % kXCDs) * (full / kXCDs) + lb / kXCDs : lb;
-  const int64_t c0 = (int64_t)sl * kGradCols8;
+  const int64_t c0 = (int64_t)sl * CW;
   const int ntiles = (r + 15) / 16;
-  const __amdgpu_buffer_rsrc_t rp = rsrc_whole(g.P, (uint32_t)((int64_t)M * g.ld * (S8 ? 1 : 2)));
-  uint16_t* const my = slab[wave];
+  const uint32_t pbytes = (uint32_t)((int64_t)M * g.ld * (S8 ? 1 : 2));
+  uint16_t* const my = reinterpret_cast<uint16_t*>(lds) + wave * kChunk * CW;
   const int nchunks = (M + kChunk - 1) / kChunk;
-
-  f32x4_t acc[2][RT];
+  const int cut = M % kChunk ? nchunks - 1 : -1;          // the chunk that M ends in
+  // load n: piece 64 n + lane of the chunk's rows of PP pieces of 16 bytes
+  constexpr int PP = CW * (S8 ? 1 : 2) / 16;
+  uint32_t poff[PL], pcut[PL];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int n = 0; n < PL; ++n) {
+    const int m = (64 * n + lane) / PP;
+    const int64_t col = c0 + (64 * n + lane) % PP * (S8 ? 16 : 8);
+    poff[n] = col < g.ld ? (uint32_t)((m * g.ld + col) * (S8 ? 1 : 2)) : kOOB;
+    pcut[n] = (nchunks - 1) * kChunk + m < M ? poff[n] : kOOB;
+  }
+
+  f32x4_t acc[2 * CB][RT];
+#pragma unroll
+  for (int h = 0; h < 2 * CB; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[h][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  struct Chunk { uint4 p[S8 ? 1 : 2]; uint4 q[3][RT]; };
+  struct Chunk { uint4 p[PL]; uint4 q[3][RT]; };
   auto load = [&](Chunk& L, int ch) {
-    const bool cv = ch < nchunks;
-    if constexpr (S8) {
-      const int m = ch * kChunk + (lane >> 1);
-      const int64_t col = c0 + 16 * (lane & 1);
-      L.p[0] = bload128(rp, cv && m < M && col < g.ld ? (uint32_t)(m * g.ld + col) : kOOB);
-    } else {
+    const bool cv = ch < nchunks, end = ch == cut;
+    const __amdgpu_buffer_rsrc_t rp = rsrc_whole(g.P, cv ? pbytes : 0);
+    // a chunk's terms: the resource's base moves, 64 bits wide
+    const int64_t qchunk = (int64_t)ntiles * 3 * 1024;
+    const __amdgpu_buffer_rsrc_t rq =
+        rsrc_whole(reinterpret_cast<const char*>(g.Q) + (cv ? ch * qchunk : 0), cv ? (uint32_t)qchunk : 0);
+    const uint32_t soff = (uint32_t)ch * (uint32_t)(kChunk * g.ld * (S8 ? 1 : 2));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = ch * kChunk + 16 * h + (lane >> 2);
-        const int64_t col = c0 + 8 * (lane & 3);
-        L.p[h] = bload128(rp, cv && m < M && col < g.ld ? (uint32_t)((m * g.ld + col) * 2) : kOOB);
-      }
-    }
+    for (int n = 0; n < PL; ++n) L.p[n] = bload128s(rp, end ? pcut[n] : poff[n], cv ? soff : 0);
 #pragma unroll
     for (int z = 0; z < 3; ++z)
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        L.q[z][t] = make_uint4(0, 0, 0, 0);
-        if (cv && t0 + t < ntiles)
-          L.q[z][t] = *reinterpret_cast<const uint4*>(
-              g.Q + ((((int64_t)ch * 3 + z) * ntiles + t0 + t) * 64 + lane) * 8);
-      }
+      for (int t = 0; t < RT; ++t)   // a rank tile past the last one repeats it (and is not stored)
+        L.q[z][t] = bload128s(rq, 16 * lane, (uint32_t)(((z * ntiles) + min(t0 + t, ntiles - 1)) * 1024));
   };
   auto use = [&](const Chunk& L) {
     // A wave's LDS operations run in issue order: these stores land after the
     // previous chunk's reads and before this one's.
-    if constexpr (S8) {
-      uint4 o[2];
-      codes_to_bf16(L.p[0], o);
-      uint4* const d = reinterpret_cast<uint4*>(my + (lane >> 1) * kGradCols8 + 16 * (lane & 1));
-      d[0] = o[0];
-      d[1] = o[1];
-    } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<uint4*>(my + (16 * h + (lane >> 2)) * kGradCols8 + 8 * (lane & 3)) = L.p[h];
+    for (int n = 0; n < PL; ++n) {
+      const int m = (64 * n + lane) / PP, p = (64 * n + lane) % PP;
+      uint4* const d = reinterpret_cast<uint4*>(my + m * CW + p * (S8 ? 16 : 8));
+      if constexpr (S8) {
+        uint4 o[2];
+        codes_to_bf16(L.p[n], o);
+        d[0] = o[0];
+        d[1] = o[1];
+      } else {
+        d[0] = L.p[n];
+      }
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     typedef short v8s_t __attribute__((ext_vector_type(8)));
     // source lane 4 s + u of a 16-lane group points at row 8 q4 + 4 e + s, column
     // 4 u of a 16-column band: lane i receives column i of the band's four rows
     const int rr = 8 * q4 + (i >> 2), cc = 4 * (i & 3);
-    bf16x8_t aop[2];
+    bf16x8_t aop[2 * CB];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const v4s_t lo = lds_read_tr16(my + rr * kGradCols8 + 16 * h + cc);
-      const v4s_t hi = lds_read_tr16(my + (rr + 4) * kGradCols8 + 16 * h + cc);
+    for (int h = 0; h < 2 * CB; ++h) {
+      const v4s_t lo = lds_read_tr16(my + rr * CW + 16 * h + cc);
+      const v4s_t hi = lds_read_tr16(my + (rr + 4) * CW + 16 * h + cc);
       const v8s_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       aop[h] = __builtin_bit_cast(bf16x8_t, v);
     }
 #pragma unroll
     for (int z = 2; z >= 0; --z)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2 * CB; ++h)
 #pragma unroll
         for (int t = 0; t < RT; ++t)
           acc[h][t] = mfma_16x16x32(aop[h], __builtin_bit_cast(bf16x8_t, L.q[z][t]), acc[h][t]);
@@ -386,25 +817,30 @@ __device__ __forceinline__ void grads8(const Grad8Job& g, int lb, int M, int r, 
   load(a, wave);
   for (int ch = wave; ch < nchunks; ch += 2 * kGradWaves8) {
     load(b, ch + kGradWaves8);
+    __builtin_amdgcn_sched_barrier(0);
     use(a);
     load(a, ch + 2 * kGradWaves8);
+    __builtin_amdgcn_sched_barrier(0);
     use(b);
   }
-  // acc[h][t][v] = O[c0 + 16 h + 4 q4 + v][16 (t0 + t) + i]
+  // acc[h][t][v] = O[c0 + 16 h + 4 q4 + v][16 (t0 + t) + i]; the sums take the
+  // slabs' place once every wave is done with them
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(lds);
+  __syncthreads();
   if (wave > 0)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2 * CB; ++h)
 #pragma unroll
-      for (int t = 0; t < RT; ++t) red[wave - 1][h * RT + t][lane] = acc[h][t];
+      for (int t = 0; t < RT; ++t) red[((wave - 1) * 2 * CB * RT + h * RT + t) * 64 + lane] = acc[h][t];
   __syncthreads();
   if (wave != 0) return;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2 * CB; ++h)
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       f32x4_t v = acc[h][t];
 #pragma unroll
-      for (int w = 0; w < kGradWaves8 - 1; ++w) v += red[w][h * RT + t][lane];
+      for (int w = 0; w < kGradWaves8 - 1; ++w) v += red[(w * 2 * CB * RT + h * RT + t) * 64 + lane];
       v *= s;
       const int64_t c = c0 + 16 * h + 4 * q4;
       const int j = 16 * (t0 + t) + i;
@@ -421,11 +857,12 @@ __device__ __forceinline__ void grads8(const Grad8Job& g, int lb, int M, int r, 
 template <int RT>
 __global__ void __launch_bounds__(64 * kGradWaves8)
 k_int8_grads(Grad8Job ja, Grad8Job jb, int M, int r, float s) {
-  __shared__ __attribute__((aligned(16))) uint16_t slab[kGradWaves8][kChunk * kGradCols8];
-  __shared__ f32x4_t red[kGradWaves8 - 1][2 * RT][64];
+  constexpr int CB = grad_bands<RT>();
+  constexpr int SLABS = kGradWaves8 * kChunk * 32 * CB * 2, RED = (kGradWaves8 - 1) * 2 * CB * RT * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SLABS > RED ? SLABS : RED];
   const int t0 = (int)blockIdx.y * RT;
-  if ((int)blockIdx.x < ja.slices) grads8<true, RT>(ja, blockIdx.x, M, r, t0, s, slab, red);
-  else grads8<false, RT>(jb, (int)blockIdx.x - ja.slices, M, r, t0, s, slab, red);
+  if ((int)blockIdx.x < ja.slices) grads8<true, RT>(ja, blockIdx.x, M, r, t0, s, lds);
+  else grads8<false, RT>(jb, (int)blockIdx.x - ja.slices, M, r, t0, s, lds);
 }
 
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx) {
@@ -435,7 +872,9 @@ Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool
   p.off_U = 0;
   p.off_up = up((size_t)M * r * 2);
   p.off_tp = p.off_up + up(pack);
-  p.bytes = p.off_tp + up(pack);
+  p.off_ds = p.off_tp + up(pack);
+  p.off_dt = p.off_ds + (r <= kRankOnce ? 0 : up(down_bytes(M, N, r)));
+  p.bytes = p.off_dt + (r <= kRankOnce ? 0 : up(down_bytes(M, K, r)));
   // dX on a bf16 copy of the base, made once per call: always of an 8-bit base,
   // of an NF4 base from the token count where its own backward makes one
   p.copy = dx && (base == kBaseInt8 || (base == kBaseNF4 && M >= kDequantDxMinM &&
@@ -457,48 +896,68 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
   uint16_t* const U = reinterpret_cast<uint16_t*>(base + p.off_U);
   uint16_t* const up = reinterpret_cast<uint16_t*>(base + p.off_up);
   uint16_t* const tp = reinterpret_cast<uint16_t*>(base + p.off_tp);
-  hipError_t e = hipSuccess;
-  // T's terms
-  if (!T && !T_bf16) {
-    RankOut o{};
-    o.packed = tp;
-    e = int8_rank<true, false>(X.codes, X.scale, M, K, A, r, o, st);
-  } else {
-    const int64_t n = (M + kChunk - 1) / kChunk * (kChunk / 4) * 16 * ((r + 15) / 16);
-    const dim3 grid((unsigned)((n + 255) / 256));
-    if (T) hipLaunchKernelGGL(k_int8_pack_T<float>, grid, dim3(256), 0, st, T, (int)M, r, tp);
-    else hipLaunchKernelGGL(k_int8_pack_T<uint16_t>, grid, dim3(256), 0, st, T_bf16, (int)M, r, tp);
-    e = hipGetLastError();
+  PrepArgs g{};
+  g.u = RankJob{dY, nullptr, (int)M, (int)N, B, r, 0, RankOut{}};
+  g.u.o.bf16 = dX ? U : nullptr;
+  g.u.o.packed = up;
+  g.u.o.pscale = X.scale;
+  g.t = RankJob{T || T_bf16 ? nullptr : X.codes, X.scale, (int)M, (int)K, A, r, 0, RankOut{}};
+  g.t.o.packed = tp;
+  g.T = T;
+  g.T_bf16 = T_bf16;
+  NF4Weight wx = w;
+  const bool once = r <= kRankOnce;
+  const int threads = once ? kRankWaves * 64 : 256;
+  DownJob du{dY, (int)M, (int)N, B, r, 0, 0, 0, reinterpret_cast<float*>(base + p.off_ds)};
+  DownJob dt{g.t.S, (int)M, (int)K, A, r, 0, 0, 0, reinterpret_cast<float*>(base + p.off_dt)};
+  g.nu = once ? rank_blocks(g.u) : down_blocks(du);
+  g.nt = once ? rank_blocks(g.t) : down_blocks(dt);
+  if (!g.t.S)
+    g.nt = (int)(((M + kChunk - 1) / kChunk * (kChunk / 8) * 16 * ((r + 15) / 16) + threads - 1) / threads);
+  int64_t nc = 0;
+  if (p.copy) {
+    wx.bf16 = g.copy = reinterpret_cast<uint16_t*>(base + p.off_w);
+    int64_t each;
+    if (W8) {
+      g.wcodes = W8->codes; g.wscale = W8->scale;
+      g.words = N * K / 16; g.k16 = (uint32_t)(K / 16);
+      each = threads * kCopyRounds;
+    } else {
+      g.w = w; g.cb = nf4_codebook4();
+      g.words = N * K / 8;
+      each = threads / 64 * kDqWaveWords;
+    }
+    nc = (g.words + each - 1) / each;
   }
-  if (e != hipSuccess) return e;
-  // U as the dX product's operand and as sx U's terms
-  RankOut o{};
-  o.bf16 = dX ? U : nullptr;
-  o.packed = up;
-  o.pscale = X.scale;
-  e = int8_rank<false, true>(dY, nullptr, M, N, B, r, o, st);
+  const dim3 grid((unsigned)(g.nu + g.nt + nc));
+  if (once) {
+    rank_form(r, [&](auto rt) {
+      constexpr int RT = decltype(rt)::value;
+      hipLaunchKernelGGL(k_int8_prep<RT>, grid, dim3(threads), 0, st, g);
+    });
+  } else {
+    hipLaunchKernelGGL(k_int8_prep_down, grid, dim3(threads), 0, st, g, du, dt);
+    const FinishJob fu{du.part, du.zs, (int)M, r, nullptr, g.u.o};
+    const FinishJob ft{dt.part, dt.zs, (int)M, r, X.scale, g.t.o};
+    const int nf = finish_blocks(M, r);
+    hipLaunchKernelGGL(k_int8_finish, dim3(g.t.S ? 2 * nf : nf), dim3(256), 0, st, fu, nf, ft);
+  }
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (dX) {
-    NF4Weight wx = w;
-    if (p.copy) {
-      uint16_t* const wb = reinterpret_cast<uint16_t*>(base + p.off_w);
-      e = W8 ? launch_int8_dequant(W8->codes, W8->scale, N, K, false, wb, st)
-             : launch_nf4_dequant(w.packed, w.codes, w.scales, w.mean, N * K, nf4_codebook4(), wb, st);
-      if (e != hipSuccess) return e;
-      wx.bf16 = wb;
-    }
     e = launch_dx(dY, M, wx, U, A, r, s, dX, accumulate, st, nullptr, 1.0f,
                   p.kz_len ? reinterpret_cast<float*>(base + p.off_part) : nullptr, p.kz_len, nullptr);
     if (e != hipSuccess) return e;
   }
-  const Grad8Job ja{X.codes, K, up, dA, (int)((K + kGradCols8 - 1) / kGradCols8)};
-  const Grad8Job jb{dY, N, tp, dB, (int)((N + kGradCols8 - 1) / kGradCols8)};
-  const int tiles = (r + 15) / 16;
-  const unsigned nx = (unsigned)(ja.slices + jb.slices);
-  const dim3 block(64 * kGradWaves8);
-  if (tiles <= 1) hipLaunchKernelGGL(k_int8_grads<1>, dim3(nx), block, 0, st, ja, jb, (int)M, r, s);
-  else if (tiles <= 2) hipLaunchKernelGGL(k_int8_grads<2>, dim3(nx), block, 0, st, ja, jb, (int)M, r, s);
-  else hipLaunchKernelGGL(k_int8_grads<4>, dim3(nx, (unsigned)((tiles + 3) / 4)), block, 0, st, ja, jb, (int)M, r, s);
+  auto grads = [&](auto rt) {
+    constexpr int RT = decltype(rt)::value, CW = 32 * grad_bands<RT>();
+    const Grad8Job ja{X.codes, K, up, dA, (int)((K + CW - 1) / CW)};
+    const Grad8Job jb{dY, N, tp, dB, (int)((N + CW - 1) / CW)};
+    const dim3 grid((unsigned)(ja.slices + jb.slices), (unsigned)((r + 16 * RT - 1) / (16 * RT)));
+    hipLaunchKernelGGL(k_int8_grads<RT>, grid, dim3(64 * kGradWaves8), 0, st, ja, jb, (int)M, r, s);
+  };
+  if (once) rank_form(r, grads);
+  else grads(std::integral_constant<int, 4>());
   return hipGetLastError();
 }
 

@@ -33,7 +33,7 @@ namespace qlk {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kI8Step = 64;     // columns of the contraction per step
+constexpr int kI8Step = 128;    // columns of the contraction per step
 
 struct Int8FwdArgs {
   const int8_t* X;      // [M, K]
@@ -41,7 +41,7 @@ struct Int8FwdArgs {
   const int8_t* W;      // [N, K]
   const float* sw;      // [N]
   int M, N, K;
-  const uint16_t* T2;   // [M][2][r]: hi and mid terms of s T
+  const uint16_t* T2;   // operands of s T's hi and mid terms (launch_int8_T)
   const uint16_t* B;    // [N, r]
   int r;                // 0: no adapter
   uint16_t* Y;          // [M, N]
@@ -55,66 +55,73 @@ constexpr int i8_wait(int vm, int lgkm) {
   return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (lgkm << 8);
 }
 
-template <int NI, int NJ>
+template <int NI, int NJ, int WM, int WN, int S>
 __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
-  constexpr int XB = 64 * NI * kI8Step, WB = 64 * NJ * kI8Step;   // bytes of a stage
+  constexpr int TM = 32 * NI * WM, TN = 32 * NJ * WN;             // the tile
+  constexpr int XL = 4 * NI / WN, WL = 4 * NJ / WM, L = XL + WL;  // a wave's loads of a stage
+  constexpr int XB = TM * kI8Step, WB = TN * kI8Step;             // bytes of a stage
+  static_assert(S == 2 || S == 3, "stages");
+  static_assert(XL * WN == 4 * NI && WL * WM == 4 * NJ, "whole loads");
   __shared__ __attribute__((aligned(16))) uint8_t x0[XB];
-  __shared__ __attribute__((aligned(16))) uint8_t x1[XB];
-  __shared__ __attribute__((aligned(16))) uint8_t x2[XB];
-  __shared__ __attribute__((aligned(16))) uint8_t x3[XB];
   __shared__ __attribute__((aligned(16))) uint8_t w0[WB];
+  __shared__ __attribute__((aligned(16))) uint8_t x1[XB];
   __shared__ __attribute__((aligned(16))) uint8_t w1[WB];
-  __shared__ __attribute__((aligned(16))) uint8_t w2[WB];
-  __shared__ __attribute__((aligned(16))) uint8_t w3[WB];
-  uint8_t* const xb[4] = {x0, x1, x2, x3};
-  uint8_t* const wb[4] = {w0, w1, w2, w3};
+  __shared__ __attribute__((aligned(16))) uint8_t x2[S == 3 ? XB : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t w2[S == 3 ? WB : 16];
+  uint8_t* const xb[3] = {x0, x1, x2};
+  uint8_t* const wb[3] = {w0, w1, w2};
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
-  const int fg = wave & 1, tq = wave >> 1;   // output half, token half
+  const int fg = wave % WN, tq = wave / WN;   // the wave's outputs and tokens
 
   const int ntiles = g.tiles_m * g.tiles_n;
   const int z = (int)blockIdx.x / ntiles;
   int tm, tn;
   tile_coords((int)blockIdx.x % ntiles, g.tiles_m, g.tiles_n, g.group_m, tm, tn);
-  const int m0 = tm * 64 * NI, n0 = tn * 64 * NJ;
-  const int nsteps = g.K / kI8Step;
+  const int m0 = tm * TM, n0 = tn * TN;
+  const int nsteps = (g.K + kI8Step - 1) / kI8Step;
   const int kz0 = g.kz_len ? z * g.kz_len : 0;
   const int kz1 = g.kz_len ? min(nsteps, kz0 + g.kz_len) : nsteps;
 
-  // Load i of wave w fills rows 16 (NI w + i) .. +15 of a stage (1 KB); lane L
-  // lands at row L / 4 of them, physical piece L % 4.
+  // Load i of wave w fills rows 8 (XL w + i) .. +7 of a stage (1 KB); lane l lands
+  // at row l / 8 of them, physical piece l % 8.  Where K ends inside a step, X's
+  // pieces past it are zero (and what W then holds does not matter).
   const __amdgpu_buffer_rsrc_t rx = rsrc_whole(g.X, (uint32_t)((int64_t)g.M * g.K));
   const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K));
-  uint32_t xoff[NI], woff[NJ];
+  auto swz = [](int row) { return (row >> 1) & 7; };
+  uint32_t xoff[XL], woff[WL];
+  bool xhi[XL];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int row = 16 * (NI * wave + i) + (lane >> 2);
-    const int piece = (lane & 3) ^ ((row >> 2) & 3);
+  for (int i = 0; i < XL; ++i) {
+    const int row = 8 * (XL * wave + i) + (lane >> 3);
+    const int piece = (lane & 7) ^ swz(row);
+    xhi[i] = piece >= 4;
     xoff[i] = m0 + row < g.M ? (uint32_t)((int64_t)(m0 + row) * g.K + piece * 16) : kOOB;
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int row = 16 * (NJ * wave + j) + (lane >> 2);
-    const int piece = (lane & 3) ^ ((row >> 2) & 3);
+  for (int j = 0; j < WL; ++j) {
+    const int row = 8 * (WL * wave + j) + (lane >> 3);
+    const int piece = (lane & 7) ^ swz(row);
     woff[j] = n0 + row < g.N ? (uint32_t)((int64_t)(n0 + row) * g.K + piece * 16) : kOOB;
   }
-  constexpr int kLoads = NI + NJ;
+  const int kcut = g.K % kI8Step ? nsteps - 1 : -1;   // the step that K ends in
   auto load_l = [&](int l, int buf, int kb) {
-    const uint32_t soff = (uint32_t)__builtin_amdgcn_readfirstlane(kb) * kI8Step;
-    if (l < NI)
+    const int k = __builtin_amdgcn_readfirstlane(kb);
+    const uint32_t soff = (uint32_t)k * kI8Step;
+    if (l < XL)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rx, (__attribute__((address_space(3))) void*)(xb[buf] + 1024 * (NI * wave + l)), 16, xoff[l],
-          soff, 0, 0);
+          rx, (__attribute__((address_space(3))) void*)(xb[buf] + 1024 * (XL * wave + l)), 16,
+          k == kcut && xhi[l] ? kOOB : xoff[l], soff, 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (__attribute__((address_space(3))) void*)(wb[buf] + 1024 * (NJ * wave + l - NI)), 16,
-          woff[l - NI], soff, 0, 0);
+          rw, (__attribute__((address_space(3))) void*)(wb[buf] + 1024 * (WL * wave + l - XL)), 16,
+          woff[l - XL], soff, 0, 0);
   };
   // Operand of a 32-row block, MFMA step t: row c, logical piece 2 t + h.
-  int rd[2];
+  int rd[4];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) rd[t] = c * kI8Step + (((2 * t + h) ^ ((c >> 2) & 3)) * 16);
+  for (int t = 0; t < 4; ++t) rd[t] = c * kI8Step + (((2 * t + h) ^ swz(c)) * 16);
   auto xfrag = [&](int buf, int i, int t) -> i32x4_t {
     return *reinterpret_cast<const i32x4_t*>(xb[buf] + 32 * (NI * tq + i) * kI8Step + rd[t]);
   };
@@ -132,98 +139,95 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
 
   i32x4_t a[2][NJ], b[2][NI];   // [MFMA step parity][block]
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
+  for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int l = 0; l < kLoads; ++l) load_l(l, s, min(kz0 + s, kz1 - 1));
-  // Steps 0 and 1 in LDS before the barrier (step 2's loads may still be in
-  // flight): the last slots of step 0 read the first operands of step 1.
-  __builtin_amdgcn_s_waitcnt(i8_wait(kLoads, 0));
+    for (int l = 0; l < L; ++l) load_l(l, s, min(kz0 + s, kz1 - 1));
+  __builtin_amdgcn_s_waitcnt(i8_wait((S - 1) * L, 0));   // the first step has landed
   __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int j = 0; j < NJ; ++j) a[0][j] = wfrag(0, j, 0);
 #pragma unroll
   for (int i = 0; i < NI; ++i) b[0][i] = xfrag(0, i, 0);
 
-  // One step: 2 NI NJ MFMA slots.  The loads of step kb + 3 go out over the
-  // first MFMA step's slots, as do the reads of the second's operands; the
-  // second's slots read the first operands of the next step.
+  // One step: four MFMA steps of NI NJ slots.  Each reads the next one's operands
+  // in its first slots; the last one reads the next step's, which every wave has
+  // waited for before the barrier in front of it.  Behind that barrier nobody
+  // reads this step's stage any more, and the loads of step kb + S go into it.
   auto step = [&](auto Pc, int kb) {
     constexpr int P = decltype(Pc)::value;
-    constexpr int nxt = (P + 1) % 4, ld = (P + 3) % 4;
-    constexpr int S = NI * NJ;
-    const int kload = min(kb + 3, kz1 - 1);
+    constexpr int nxt = (P + 1) % S;
+    constexpr int Q = NI * NJ, F = NI + NJ;
+    constexpr int R = Q >= F ? F : Q;   // slots that read
+    const int kload = min(kb + S, kz1 - 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < 2 * S; ++u) {
-      const int t = u / S, q = u % S, j = q / NI, i = q % NI;
-      acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[t][j], b[t][i], acc[j][i], 0, 0, 0);
-      // item q of the slot's share: kLoads items over S slots
-#pragma unroll
-      for (int l = q * kLoads / S; l < (q + 1) * kLoads / S; ++l) {
-        if (t == 0) load_l(l, ld, kload);
+    for (int t = 0; t < 4; ++t) {
+      if (t == 3) {
+        __builtin_amdgcn_s_waitcnt(i8_wait((S - 2) * L, 0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
       }
-      constexpr int R = S >= kLoads ? kLoads : S;   // reads in the first slots
-      if (q < R) {
 #pragma unroll
-        for (int l = q * kLoads / R; l < (q + 1) * kLoads / R; ++l) {
-          if (l < NI) b[1 - t][l] = xfrag(t ? nxt : P, l, 1 - t);
-          else a[1 - t][l - NI] = wfrag(t ? nxt : P, l - NI, 1 - t);
+      for (int q = 0; q < Q; ++q) {
+        const int j = q / NI, i = q % NI;
+        acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[t & 1][j], b[t & 1][i], acc[j][i], 0, 0, 0);
+        if (q < R) {
+#pragma unroll
+          for (int l = q * F / R; l < (q + 1) * F / R; ++l) {
+            if (l < NI) b[(t + 1) & 1][l] = xfrag(t == 3 ? nxt : P, l, (t + 1) & 3);
+            else a[(t + 1) & 1][l - NI] = wfrag(t == 3 ? nxt : P, l - NI, (t + 1) & 3);
+          }
         }
+        if (t == 3) {
+#pragma unroll
+          for (int l = q * L / Q; l < (q + 1) * L / Q; ++l) load_l(l, P, kload);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-    // Step kb + 2's stages (loaded during step kb - 1) complete in every wave
-    // before step kb + 1, which reads them in its last slots: at most this
-    // step's loads outstanding, then the barrier.
-    __builtin_amdgcn_s_waitcnt(i8_wait(kLoads, 0xF));
-    __builtin_amdgcn_s_barrier();
   };
-  // Whole groups of four steps without a branch between them: where paths meet
-  // the compiler waits for loads that are not due.
+  // Whole groups of S steps without a branch between them: where paths meet the
+  // compiler waits for loads that are not due.
   int kb = kz0;
-  for (; kb + 4 <= kz1; kb += 4) {
+  for (; kb + S <= kz1; kb += S) {
     step(std::integral_constant<int, 0>(), kb);
     step(std::integral_constant<int, 1>(), kb + 1);
-    step(std::integral_constant<int, 2>(), kb + 2);
-    step(std::integral_constant<int, 3>(), kb + 3);
+    if constexpr (S == 3) step(std::integral_constant<int, 2>(), kb + 2);
   }
   if (kb < kz1) {
     step(std::integral_constant<int, 0>(), kb);
-    if (kb + 1 < kz1) step(std::integral_constant<int, 1>(), kb + 1);
-    if (kb + 2 < kz1) step(std::integral_constant<int, 2>(), kb + 2);
+    if (S == 3 && kb + 1 < kz1) step(std::integral_constant<int, 1>(), kb + 1);
   }
   __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the loop
   __syncthreads();                 // every wave's operand reads are done
 
   // Accumulator [j][i]: lane holds token mw + 32 i + c and outputs
   // nw + 32 j + 8 (v / 4) + 4 h + (v % 4).  Block column by block column: fp32
-  // values, the adapter's term, then bf16 rows of 128 NJ bytes in LDS: token
-  // block k of 32 rows lies in stage w[k] (k < 4) or x[k - 4], the 16-byte
+  // values, the adapter's term, then bf16 rows of 2 TN bytes in LDS: two blocks of
+  // 32 token rows lie in each of w0 and w1, the others in x0 and x1, the 16-byte
   // pieces of a row XOR-swizzled by its number.  N and r are multiples of 8, so
   // that a piece is wholly inside or wholly outside.
-  constexpr int PR = 8 * NJ;       // pieces of a row
+  constexpr int PR = TN / 8;       // pieces of a row
+  constexpr int BB = 32 * 16 * PR; // bytes of a block
+  static_assert(NI * WM <= 4 || (NI * WM == 8 && XB >= 2 * BB), "blocks in the stages");
   auto ob = [&](int k) -> uint8_t* {
-    return k == 0 ? w0 : k == 1 ? w1 : k == 2 ? w2 : k == 3 ? w3 : k == 4 ? x0 : k == 5 ? x1 : k == 6 ? x2 : x3;
+    return (k < 2 ? w0 : k < 4 ? w1 : k < 6 ? x0 : x1) + (k & 1) * BB;
   };
   const int nw = n0 + 32 * NJ * fg, mw = m0 + 32 * NI * tq;
   const __amdgpu_buffer_rsrc_t rsx = rsrc_whole(g.sx, (uint32_t)g.M * 4);
   const __amdgpu_buffer_rsrc_t rsw = rsrc_whole(g.sw, (uint32_t)g.N * 4);
-  const __amdgpu_buffer_rsrc_t rt = rsrc_whole(g.T2, (uint32_t)(g.M * g.r * 4));
   const __amdgpu_buffer_rsrc_t rb = rsrc_whole(g.B, (uint32_t)(g.N * g.r * 2));
-  const int r = z == 0 ? g.r : 0;
+  const int r = z == 0 ? g.r : 0, nt = (r + 15) / 16;
   float* const part = g.kz_len ? g.part + (int64_t)z * g.M * g.N : nullptr;
   float sx[NI];
-  uint32_t toff[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int m = mw + 32 * i + c;
     sx[i] = __uint_as_float(bload32(rsx, m < g.M ? (uint32_t)m * 4 : kOOB));
-    toff[i] = m < g.M ? (uint32_t)((m * 2 * g.r + 8 * h) * 2) : kOOB;
   }
+  f32x16_t out[NJ][NI];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    __builtin_amdgcn_sched_barrier(0);
-    f32x16_t out[NI];
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int n = nw + 32 * j + 8 * q + 4 * h;
@@ -233,49 +237,64 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[i][4 * q + e] = (float)acc[j][i][4 * q + e] * sx[i] * s4[e];
+        for (int e = 0; e < 4; ++e)
+          out[j][i][4 * q + e] = (float)acc[j][i][4 * q + e] * sx[i] * s4[e];
     }
-    const int nb = nw + 32 * j + c;
-    for (int r0 = 0; r0 < r; r0 += 16) {
-      const bool rok = r0 + 8 * h < r;
-      const bf16x8_t bop = __builtin_bit_cast(
-          bf16x8_t, bload128(rb, rok && nb < g.N ? (uint32_t)((nb * g.r + r0 + 8 * h) * 2) : kOOB));
+  // A token block's operands are 1 KB in a row; a block past the last token has none.
+  const __amdgpu_buffer_rsrc_t rt =
+      rsrc_whole(g.T2, (uint32_t)((g.M + 31) / 32 * nt * 2048));
+  for (int t = 0; t < nt; ++t) {
+    bf16x8_t top[NI][2], bop[NJ];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const uint32_t o = rok ? toff[i] : kOOB;
-        const bf16x8_t hi = __builtin_bit_cast(bf16x8_t, bload128s(rt, o, r0 * 2));
-        const bf16x8_t mid = __builtin_bit_cast(bf16x8_t, bload128s(rt, o, (r0 + g.r) * 2));
-        out[i] = mfma_32x32x16(bop, mid, out[i]);
-        out[i] = mfma_32x32x16(bop, hi, out[i]);
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int blk = mw / 32 + i;
+        top[i][e] = __builtin_bit_cast(
+            bf16x8_t, bload128(rt, mw + 32 * i < g.M ? (uint32_t)(((blk * nt + t) * 2 + e) * 1024 + 16 * lane)
+                                                     : kOOB));
       }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int nb = nw + 32 * j + c, rr = 16 * t + 8 * h;
+      bop[j] = __builtin_bit_cast(
+          bf16x8_t, bload128(rb, rr < r && nb < g.N ? (uint32_t)((nb * g.r + rr) * 2) : kOOB));
     }
+#pragma unroll
+    for (int e = 1; e >= 0; --e)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) out[j][i] = mfma_32x32x16(bop[j], top[i][e], out[j][i]);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int m = mw + 32 * i + c;
-      uint8_t* const row = (tq ? ob(NI + i) : ob(i)) + c * (16 * PR);
+      uint8_t* const row = ob(NI * tq + i) + c * (16 * PR);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        const f32x16_t& v = out[j][i];
         if (part) {
           const int n = nw + 32 * j + 8 * q + 4 * h;
           if (m < g.M && n < g.N)
             *reinterpret_cast<float4*>(part + (int64_t)m * g.N + n) =
-                make_float4(out[i][4 * q], out[i][4 * q + 1], out[i][4 * q + 2], out[i][4 * q + 3]);
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         } else {
           const int piece = (4 * NJ * fg + 4 * j + q) ^ (c & (PR - 1));
           *reinterpret_cast<uint2*>(row + 16 * piece + 8 * h) =
-              make_uint2(pack_bf16x2(out[i][4 * q], out[i][4 * q + 1]),
-                         pack_bf16x2(out[i][4 * q + 2], out[i][4 * q + 3]));
+              make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
         }
       }
     }
-  }
   if (part) return;
   __syncthreads();
-  constexpr int RW = 256 / PR;                     // rows a pass of 256 threads stores
+  constexpr int RW = 64 * WM * WN / PR;            // rows that a pass of the workgroup stores
   const int prow = tid / PR, pp = tid % PR;
   const __amdgpu_buffer_rsrc_t ry = rsrc_whole(g.Y, (uint32_t)((int64_t)g.M * g.N * 2));
 #pragma unroll
-  for (int e = 0; e < 64 * NI / RW; ++e) {
+  for (int e = 0; e < TM / RW; ++e) {
     const int row = RW * e + prow, rl = row & 31;  // RW divides 32
     const uint4 v = *reinterpret_cast<const uint4*>(ob(RW * e / 32) + rl * (16 * PR) +
                                                     16 * (pp ^ (rl & (PR - 1))));
@@ -286,10 +305,11 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
 
 // The host pass does not keep a kernel template whose body calls these loads
 // from a lambda: one plain kernel per form.
-__global__ void __launch_bounds__(256) k_int8_fwd_44(Int8FwdArgs g) { int8_tile<4, 4>(g); }
-__global__ void __launch_bounds__(256) k_int8_fwd_24(Int8FwdArgs g) { int8_tile<2, 4>(g); }
-__global__ void __launch_bounds__(256) k_int8_fwd_22(Int8FwdArgs g) { int8_tile<2, 2>(g); }
-__global__ void __launch_bounds__(256) k_int8_fwd_12(Int8FwdArgs g) { int8_tile<1, 2>(g); }
+__global__ void __launch_bounds__(512) k_int8_fwd_256x256(Int8FwdArgs g) { int8_tile<4, 2, 2, 4, 2>(g); }
+__global__ void __launch_bounds__(512) k_int8_fwd_128x256(Int8FwdArgs g) { int8_tile<2, 2, 2, 4, 3>(g); }
+__global__ void __launch_bounds__(512) k_int8_fwd_64x256(Int8FwdArgs g) { int8_tile<2, 1, 1, 8, 3>(g); }
+__global__ void __launch_bounds__(256) k_int8_fwd_64x64(Int8FwdArgs g) { int8_tile<1, 1, 2, 2, 3>(g); }
+__global__ void __launch_bounds__(256) k_int8_fwd_64x128(Int8FwdArgs g) { int8_tile<1, 2, 2, 2, 3>(g); }
 
 // ---------------------------------------------------------------------------
 // Up to 16 tokens: the weight is streamed once.  A workgroup of kGvWaves waves
@@ -402,45 +422,56 @@ k_int8_gemv_2(Int8FwdArgs g, const float* Tpart, float s, float* T_out) {
 
 // ------------------------------- launchers ---------------------------------
 
-// Tile and split of the contraction.  A form costs rounds of the device times
-// the time of its tile; `speed` is a form's rate per CU against the largest's.
+// Tile and split of the contraction, by the time each would take.  A step of a
+// tile takes `alone` us where few workgroups run, and `full` for a workgroup on
+// every CU: for the large tiles the power limit's MFMA rate, for the small ones L2
+// (18 TB/s of operands); `per_cu` workgroups share a CU's LDS.  Measured at K =
+// 4096 and 8192 over 32 to 8192 tokens; the model's choice was the fastest or within
+// 5 % of it at 11 of 12 sizes.  A split contraction pays a second launch and its
+// partial sums' trip.
 struct Int8Form {
-  int ni, nj;
-  double speed;
-  int per_cu;      // workgroups a CU holds (LDS)
+  void (*kernel)(Int8FwdArgs);
+  int tm, tn, threads, per_cu;
+  double alone, full;
 };
-static const Int8Form kForms[] = {{4, 4, 1.0, 1}, {2, 4, 0.85, 1}, {2, 2, 0.7, 2}, {1, 2, 0.5, 3}};
+static const Int8Form kForms[] = {{k_int8_fwd_256x256, 256, 256, 512, 1, 0.95, 1.54},
+                                  {k_int8_fwd_128x256, 128, 256, 512, 1, 0.50, 0.85},
+                                  {k_int8_fwd_64x256, 64, 256, 512, 1, 0.33, 0.50},
+                                  {k_int8_fwd_64x128, 64, 128, 256, 2, 0.18, 0.35},
+                                  {k_int8_fwd_64x64, 64, 64, 256, 3, 0.10, 0.22}};
+constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]);
 
 Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Int8FwdPlan p{};
   if (M <= kGemvMaxM) {
     p.gemv = true;
-    p.off_T = 0;
     p.bytes = up((size_t)kTSplits * M * r * 4);
     return p;
   }
-  const int64_t steps = K / kI8Step;
+  const int64_t steps = (K + kI8Step - 1) / kI8Step;
   double best = 0.0;
-  for (int f = 0; f < 4; ++f) {
+  for (int f = 0; f < kNumForms; ++f) {
     const Int8Form& F = kForms[f];
-    const int64_t tiles = ((M + 64 * F.ni - 1) / (64 * F.ni)) * ((N + 64 * F.nj - 1) / (64 * F.nj));
-    for (int splits = 1; splits <= 16; ++splits) {
-      if (splits > 1 && (tiles * splits > 512 || steps / splits < 8)) break;
+    const int64_t tiles = ((M + F.tm - 1) / F.tm) * ((N + F.tn - 1) / F.tn);
+    for (int splits = 1; splits <= 8; ++splits) {
+      if (splits > 1 && (tiles * splits > F.per_cu * kCUs || steps / splits < 8)) break;
       const int64_t len = (steps + splits - 1) / splits;
-      const int64_t rounds = (tiles * splits + kCUs - 1) / kCUs;
-      // MFMA cycles of a tile, a fixed start and end, the partial sums' trip
-      double cost = rounds * ((double)len * F.ni * F.nj * 64 / F.speed + 4000.0);
-      if (splits > 1) cost += 6000.0 + (double)M * N * 4 * (2 * splits) / 2500.0;
-      if (best == 0.0 || cost < best) {
-        best = cost;
+      const int64_t wgs = tiles * splits, round = (int64_t)F.per_cu * kCUs, rest = wgs % round;
+      double step = (double)(wgs / round) * F.per_cu * F.full;
+      if (rest) step += rest * F.full / kCUs > F.alone ? rest * F.full / kCUs : F.alone;
+      double us = len * step;
+      if (splits > 1) us += 2.5 + (double)M * N * splits * 8.0 / 5e6;
+      if (best == 0.0 || us < best) {
+        best = us;
         p.form = f;
         p.kz_len = splits > 1 ? (int)len : 0;
       }
     }
   }
   p.off_T = 0;
-  p.off_part = up((size_t)M * 2 * r * 2);
+  p.off_down = up(int8_two_bytes(M, r));
+  p.off_part = p.off_down + up(int8_T_bytes(M, K, r));
   p.bytes = p.off_part;
   if (p.kz_len) p.bytes += up((size_t)((steps + p.kz_len - 1) / p.kz_len) * M * N * 4);
   return p;
@@ -471,23 +502,21 @@ hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int6
   }
   if (r) {
     uint16_t* const T2 = reinterpret_cast<uint16_t*>(base + p.off_T);
-    const hipError_t e = launch_int8_T(X, M, K, A, r, s, T_out, T2, st);
+    const hipError_t e = launch_int8_T(X, M, K, A, r, s, T_out, T2,
+                                       reinterpret_cast<float*>(base + p.off_down), st);
     if (e != hipSuccess) return e;
     g.T2 = T2;
   }
   const Int8Form& F = kForms[p.form];
-  g.tiles_m = (int)((M + 64 * F.ni - 1) / (64 * F.ni));
-  g.tiles_n = (int)((N + 64 * F.nj - 1) / (64 * F.nj));
-  g.group_m = group_for(g.tiles_m, g.tiles_n, 64.0 * F.ni * K, 64.0 * F.nj * K);
+  g.tiles_m = (int)((M + F.tm - 1) / F.tm);
+  g.tiles_n = (int)((N + F.tn - 1) / F.tn);
+  g.group_m = group_for(g.tiles_m, g.tiles_n, (double)F.tm * K, (double)F.tn * K);
   g.kz_len = p.kz_len;
-  const int steps = (int)(K / kI8Step);
+  const int steps = (int)((K + kI8Step - 1) / kI8Step);
   const int splits = p.kz_len ? (steps + p.kz_len - 1) / p.kz_len : 1;
   if (p.kz_len) g.part = reinterpret_cast<float*>(base + p.off_part);
-  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * splits)), block(256);
-  if (p.form == 0) hipLaunchKernelGGL(k_int8_fwd_44, grid, block, 0, st, g);
-  else if (p.form == 1) hipLaunchKernelGGL(k_int8_fwd_24, grid, block, 0, st, g);
-  else if (p.form == 2) hipLaunchKernelGGL(k_int8_fwd_22, grid, block, 0, st, g);
-  else hipLaunchKernelGGL(k_int8_fwd_12, grid, block, 0, st, g);
+  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n * splits));
+  hipLaunchKernelGGL(F.kernel, grid, dim3(F.threads), 0, st, g);
   if (p.kz_len) return launch_split_reduce(g.part, splits, M * N, Y, false, st);
   return hipGetLastError();
 }

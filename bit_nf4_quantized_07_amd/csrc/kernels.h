@@ -281,9 +281,13 @@ hipError_t launch_silu_mul_fwd_int8(const uint16_t* G, const uint16_t* U, int64_
 hipError_t launch_silu_mul_bwd_int8(const uint16_t* dH, const int8_t* G8, const float* Gs,
                                     const int8_t* U8, const float* Us, int64_t M, int64_t I,
                                     uint16_t* dG, uint16_t* dU, hipStream_t st);
-// T = X A^T (fp32 [M, r], if not null) and T2 [M][2][r], the bf16 terms of s T.
+// T = X A^T (fp32 [M, r], if not null) and T2, the two bf16 terms of s T as the
+// forward's MFMA operands [block of 32 tokens][16 ranks][term][lane][8]
+// (int8_two_bytes of them).
+size_t int8_two_bytes(int64_t M, int r);
 hipError_t launch_int8_T(const Int8Rows& X, int64_t M, int64_t K, const uint16_t* A, int r, float s,
-                         float* T, uint16_t* T2, hipStream_t st);
+                         float* T, uint16_t* T2, float* part, hipStream_t st);
+size_t int8_T_bytes(int64_t M, int64_t K, int r);   // of part
 // part [kTSplits][M][r]: sums of Cx A^T over slices of the contraction (M <= 16).
 hipError_t launch_int8_T_partial(const int8_t* X, int64_t M, int64_t K, const uint16_t* A, int r,
                                  float* part, hipStream_t st);
@@ -292,7 +296,7 @@ struct Int8FwdPlan {
   bool gemv;         // small-M path
   int form;          // tile
   int kz_len;        // steps per split of the contraction (0: one pass)
-  size_t off_T, off_part, bytes;
+  size_t off_T, off_down, off_part, bytes;
 };
 Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r);
 hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int64_t N, int64_t K,
@@ -304,7 +308,7 @@ constexpr int kBaseInt8 = 0, kBaseNF4 = 1, kBaseBF16 = 2;
 struct Int8BwdPlan {
   bool copy;         // dX on a bf16 copy of the base at off_w
   int kz_len;
-  size_t off_U, off_up, off_tp, off_w, off_part, bytes;
+  size_t off_U, off_up, off_tp, off_ds, off_dt, off_w, off_part, bytes;
 };
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx);
 hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int64_t K, int64_t N,

@@ -310,7 +310,7 @@ int check_int8_sizes(int64_t M, int64_t K, int64_t N, int r, int base, bool bwd)
   if (st) return st;
   if (N % 8 != 0 || r < (bwd ? 1 : 0) || r > kMaxRank) return QLORA_ERR_SHAPE;
   // 32-bit offsets; out-of-range lanes use offset 2^31
-  const int64_t rp = padded_rank(r);
+  const int64_t rp = (r + 15) / 16 * 16;   // operands of whole rank tiles
   const int64_t weight = base == qlk::kBaseInt8 ? N * K : base == qlk::kBaseNF4 ? N * K / 2 : 2 * N * K;
   if (M * K >= kMaxBufferBytes || M * N * 2 >= kMaxBufferBytes || M * rp * 4 >= kMaxBufferBytes ||
       N * rp * 2 >= kMaxBufferBytes || weight >= kMaxBufferBytes)

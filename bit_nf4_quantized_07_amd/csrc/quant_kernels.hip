@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(256)
 k_nf4_dequant(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ codes,
               const float* __restrict__ scales, const float* __restrict__ mean,
               int64_t nwords, Codebook4 cb, uint16_t* __restrict__ out) {
-  nf4_dequant_block(packed, codes, scales, mean, nwords, cb, out, blockIdx.x);
+  __shared__ float q4[16];
+  nf4_dequant_block(packed, codes, scales, mean, nwords, cb, out, blockIdx.x, q4);
 }
 
 // The same with the 8-bit levels from a table (staged in LDS).
@@ -242,10 +243,11 @@ __global__ void __launch_bounds__(256)
 k_dequant_tables(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ codes,
                  const float* __restrict__ scales, const float* __restrict__ mean, int64_t nwords,
                  Codebook4 cb, Codebook8 cb8, uint16_t* __restrict__ out) {
+  __shared__ float q4[16];
   __shared__ float q8[256];
   q8[threadIdx.x] = cb8.lv[threadIdx.x];
   __syncthreads();
-  nf4_dequant_block(packed, codes, scales, mean, nwords, cb, out, blockIdx.x, q8);
+  nf4_dequant_block(packed, codes, scales, mean, nwords, cb, out, blockIdx.x, q4, q8);
 }
 
 // ---------------------------------------------------------------------------

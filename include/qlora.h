@@ -418,7 +418,7 @@ int int8_dequant(const int8_t* codes, const float* scale, int64_t M, int64_t K, 
  * second product as two bf16 terms (within 2^-16); Y is rounded once.
  *   r = 0: no adapter (A, B and T_out NULL)
  * Requires K % 64 == 0, K <= 2^17, N % 8 == 0, 0 <= r <= 256; M K, N K, 2 M N,
- * 4 M r and 2 N r under 2^31 (r counted up to a multiple of 8); workspace of
+ * 4 M r and 2 N r under 2^31 (r counted up to a multiple of 16); workspace of
  * int8_linear_workspace_bytes(M, K, N, r, QLORA_BASE_INT8, 0). */
 int int8_linear_fwd(const int8_t* Xcodes, const float* Xscale, int64_t M, int64_t K, int64_t N,
                     const int8_t* Wcodes, const float* Wscale, const uint16_t* A, const uint16_t* B,
