@@ -312,112 +312,166 @@ __global__ void __launch_bounds__(256) k_int8_fwd_64x64(Int8FwdArgs g) { int8_ti
 __global__ void __launch_bounds__(256) k_int8_fwd_64x128(Int8FwdArgs g) { int8_tile<1, 2, 2, 2, 3>(g); }
 
 // ---------------------------------------------------------------------------
-// Up to 16 tokens: the weight is streamed once.  A workgroup of kGvWaves waves
-// takes 16 RB outputs; a wave takes every kGvWaves-th run of 256 columns of
-// their weight rows (four loads of 16 rows x 64 bytes) against the tokens'
-// columns with v_mfma_i32_16x16x64_i8, and the waves' whole sums are added
-// through LDS.  T = X A^T arrives as kTSplits partial sums, added in a fixed
-// order by every workgroup (the first one writes T).
+// Up to 16 tokens: the weight is streamed once.  A workgroup takes up to 8 blocks
+// of 16 outputs, so that one on every CU covers them; its waves take every
+// kGvWaves-th run of 256 columns of a block's rows (four loads of 16 rows x 64
+// bytes, four runs in flight) with v_mfma_i32_16x16x64_i8, and add their whole sums
+// in LDS (integers: in any order the same).
+//  * The tokens' columns lie in LDS, up to kGvCols of them at a time, loaded once
+//    per workgroup by whole lines (rows of 128 bytes, pieces XOR-swizzled by
+//    (token >> 1) & 7).  Read from memory beside the weight, a row per lane, they
+//    took half the address unit's time (16 tokens, 28672 x 8192: 69 us, 3.4 TB/s).
+//    Columns past K are zero there, so that the weight's need no bound.
+//  * T = X A^T arrives as kTSplits partial sums, added in a fixed order by every
+//    workgroup (the first one writes T); s T B^T is summed in fp32 while the first
+//    weights are on their way.
 constexpr int kGvWaves = 8;
-constexpr int kGvRun = 256;     // columns per run
+constexpr int kGvThreads = 64 * kGvWaves;
+constexpr int kGvBlocks = 8;    // blocks of 16 outputs per workgroup
+constexpr int kGvDepth = 4;     // runs in flight per wave
 
-template <int RB>
-__device__ __forceinline__ void int8_gemv(const Int8FwdArgs& g, const float* __restrict__ Tpart,
-                                          float s, float* __restrict__ T_out) {
-  __shared__ __attribute__((aligned(16))) i32x4_t red[kGvWaves][RB][64];
-  extern __shared__ float tl[];                    // [M][r]: s T
+template <int COLS>
+__global__ void __launch_bounds__(kGvThreads)
+k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, float s, float* __restrict__ T_out, int nb) {
+  __shared__ __attribute__((aligned(16))) uint8_t xs[16 * COLS];
+  __shared__ int red[kGvBlocks * 256];             // [block][lane][4]
+  __shared__ float yl[kGvBlocks * 256];            // s T B^T of output o
+  __shared__ float tl[16 * 256];                   // s T
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, gq = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16 * RB;
+  const int n0 = (int)blockIdx.x * 16 * nb;
+  const int outs = 16 * nb * g.M;                  // token o / (16 nb), row o % (16 nb)
   const __amdgpu_buffer_rsrc_t rx = rsrc_whole(g.X, (uint32_t)((int64_t)g.M * g.K));
   const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K));
-  const int nruns = (g.K + kGvRun - 1) / kGvRun;
-  uint32_t wrow[RB];
-  bool wok[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int n = n0 + 16 * b + i;
-    wok[b] = n < g.N;
-    wrow[b] = (uint32_t)((int64_t)n * g.K) + 16 * gq;
-  }
-  const uint32_t xrow = (uint32_t)(i * g.K) + 16 * gq;
-  i32x4_t acc[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) acc[b] = i32x4_t{0, 0, 0, 0};
 
-  struct Run { uint4 w[RB][4]; uint4 x[4]; };
-  auto load = [&](Run& R, int run) {
+  // T's partial sums and what the first output needs, before anything else
+  float t0 = 0.0f, sxt = 0.0f, sx0 = 0.0f, sw0 = 0.0f;
+  uint4 b0 = make_uint4(0, 0, 0, 0), b1 = make_uint4(0, 0, 0, 0);
+  if (tid < g.M * g.r) {
+    float p[kTSplits];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int k = run * kGvRun + 64 * q;
-      const bool kok = run < nruns && k < g.K;     // K % 64 == 0: 64 whole columns or none
+    for (int z = 0; z < kTSplits; ++z) p[z] = Tpart[z * g.M * g.r + tid];
+    sxt = g.sx[tid / g.r];
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-        R.w[b][q] = bload128(rw, kok && wok[b] ? wrow[b] + (uint32_t)k : kOOB);
-      R.x[q] = bload128(rx, kok && i < g.M ? xrow + (uint32_t)k : kOOB);
+    for (int z = 0; z < kTSplits; ++z) t0 += p[z];
+  }
+  const int nfirst = n0 + tid % (16 * nb);
+  if (tid < outs && nfirst < g.N) {
+    sx0 = g.sx[tid / (16 * nb)];
+    sw0 = g.sw[nfirst];
+  }
+  if (g.r && tid < outs && nfirst < g.N) {
+    const uint4* const p = reinterpret_cast<const uint4*>(g.B + (int64_t)nfirst * g.r);
+    b0 = p[0];
+    if (g.r > 8) b1 = p[1];
+  }
+  for (int e = tid; e < nb * 256; e += kGvThreads) red[e] = 0;
+
+  for (int kc = 0; kc < g.K; kc += COLS) {
+    const int cols = min(COLS, g.K - kc), nruns = (cols + 255) / 256;
+    if (kc) __syncthreads();                       // every wave is done with the last columns
+    // X: load u fills tokens 8 (u % 2) .. +7 of columns 128 (u / 2) .. +127
+    for (int u = wave; u < 4 * nruns; u += kGvWaves) {
+      const int m = 8 * (u & 1) + (lane >> 3), col = 128 * (u >> 1) + 16 * ((lane & 7) ^ ((m >> 1) & 7));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rx, (__attribute__((address_space(3))) void*)(xs + 1024 * u), 16,
+          m < g.M && col < cols ? (uint32_t)(m * g.K + kc + col) : kOOB, 0, 0, 0);
     }
-  };
-  auto use = [&](const Run& R) {
+    // Runs wave, wave + kGvWaves, .. of block after block.
+    const int per = (nruns + kGvWaves - 1) / kGvWaves, tasks = per * nb;
+    struct Run { uint4 w[4]; };
+    int lb = 0, lr = 0;                            // the next task to load
+    auto load = [&](Run& R) {
+      const int run = lr * kGvWaves + wave, n = n0 + 16 * lb + i;
+      const bool ok = lb < nb && run < nruns;
+      const __amdgpu_buffer_rsrc_t r = rsrc_whole(g.W, ok ? (uint32_t)((int64_t)g.N * g.K) : 0);
+      const uint32_t off = n < g.N ? (uint32_t)((int64_t)n * g.K) + 16 * gq : kOOB;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) R.w[q] = bload128s(r, off + 64 * q, ok ? (uint32_t)(kc + 256 * run) : 0);
+      if (++lr == per) lr = 0, ++lb;
+    };
+    Run R[kGvDepth];
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-        acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, R.w[b][q]),
-                                                       __builtin_bit_cast(i32x4_t, R.x[q]), acc[b],
-                                                       0, 0, 0);
-  };
-  Run ra, rb;
-  load(ra, wave);
-  load(rb, wave + kGvWaves);
-  // s T of every token, while the first loads are in flight
-  for (int e = tid; e < g.M * g.r; e += 64 * kGvWaves) {
-    float t = 0.0f;
-    for (int zz = 0; zz < kTSplits; ++zz) t += Tpart[(int64_t)zz * g.M * g.r + e];
-    t *= g.sx[e / g.r];
-    if (T_out && blockIdx.x == 0) T_out[e] = t;
-    tl[e] = s * t;
-  }
-  for (int run = wave; run < nruns; run += 2 * kGvWaves) {
-    use(ra);
-    load(ra, run + 2 * kGvWaves);
-    use(rb);
-    load(rb, run + 3 * kGvWaves);
-  }
-#pragma unroll
-  for (int b = 0; b < RB; ++b) red[wave][b][lane] = acc[b];
-  __syncthreads();
-  // Output o: token o / (16 RB), output row o % (16 RB); the lane that holds
-  // row 16 b + 4 q + v of token i is 16 q + i, element v.
-  for (int o = tid; o < 16 * RB * g.M; o += 64 * kGvWaves) {
-    const int m = o / (16 * RB), row = o % (16 * RB);
-    const int b = row / 16, q = (row % 16) / 4, v = row % 4;
-    const int n = n0 + row;
-    if (n >= g.N) continue;
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kGvWaves; ++w) sum += red[w][b][16 * q + m][v];
-    float y = (float)sum * g.sx[m] * g.sw[n];
-    const uint16_t* const Bn = g.B + (int64_t)n * g.r;
-    for (int j = 0; j < g.r; j += 8) {
-      const uint4 bv = *reinterpret_cast<const uint4*>(Bn + j);
-      const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y = __builtin_fmaf(tl[m * g.r + j + 2 * e], bf16_to_f32(bw[e] & 0xffffu), y);
-        y = __builtin_fmaf(tl[m * g.r + j + 2 * e + 1], bf16_to_f32(bw[e] >> 16), y);
+    for (int d = 0; d < kGvDepth; ++d) load(R[d]);
+    if (kc == 0) {
+      if (tid < g.M * g.r) {
+        const float t = t0 * sxt;
+        if (T_out && blockIdx.x == 0) T_out[tid] = t;
+        tl[tid] = s * t;
+      }
+      for (int e = tid + kGvThreads; e < g.M * g.r; e += kGvThreads) {
+        float t = 0.0f;
+        for (int z = 0; z < kTSplits; ++z) t += Tpart[z * g.M * g.r + e];
+        t *= g.sx[e / g.r];
+        if (T_out && blockIdx.x == 0) T_out[e] = t;
+        tl[e] = s * t;
       }
     }
-    g.Y[(int64_t)m * g.N + n] = f32_to_bf16(y);
+    __builtin_amdgcn_s_waitcnt(0x0070 | (4 * kGvDepth & 0xF) | ((4 * kGvDepth >> 4) << 14));   // X has landed, lgkmcnt(0)
+    __syncthreads();
+    if (kc == 0) {
+      for (int o = tid; o < outs; o += kGvThreads) {
+        const int m = o / (16 * nb), n = n0 + o % (16 * nb);
+        float y = 0.0f;
+        auto add = [&](const uint4& bv, int j) {
+          const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y = __builtin_fmaf(tl[m * g.r + j + 2 * e], bf16_to_f32(bw[e] & 0xffffu), y);
+            y = __builtin_fmaf(tl[m * g.r + j + 2 * e + 1], bf16_to_f32(bw[e] >> 16), y);
+          }
+        };
+        if (n < g.N) {
+          int j = 0;
+          if (o == tid && g.r) {
+            add(b0, 0);
+            if (g.r > 8) add(b1, 8);
+            j = 16;
+          }
+          for (; j < g.r; j += 8) add(*reinterpret_cast<const uint4*>(g.B + (int64_t)n * g.r + j), j);
+        }
+        yl[o] = y;
+      }
+    }
+    i32x4_t acc = i32x4_t{0, 0, 0, 0};
+    int ub = 0, ur = 0;                            // the task in use
+    auto use = [&](const Run& R) {
+      const int run = ur * kGvWaves + wave;
+      const uint8_t* const x = xs + 4096 * min(run, nruns - 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 xv = *reinterpret_cast<const uint4*>(
+            x + 2048 * (q >> 1) + 128 * i + 16 * ((4 * (q & 1) + gq) ^ ((i >> 1) & 7)));
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, R.w[q]),
+                                                    __builtin_bit_cast(i32x4_t, xv), acc, 0, 0, 0);
+      }
+      if (++ur == per) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) atomicAdd(&red[ub * 256 + 64 * v + lane], acc[v]);
+        acc = i32x4_t{0, 0, 0, 0};
+        ur = 0;
+        ++ub;
+      }
+    };
+    for (int t = 0; t < tasks; t += kGvDepth) {
+#pragma unroll
+      for (int d = 0; d < kGvDepth; ++d)
+        if (t + d < tasks) {
+          use(R[d]);
+          load(R[d]);
+        }
+    }
   }
-}
-__global__ void __launch_bounds__(64 * kGvWaves)
-k_int8_gemv_1(Int8FwdArgs g, const float* Tpart, float s, float* T_out) {
-  int8_gemv<1>(g, Tpart, s, T_out);
-}
-__global__ void __launch_bounds__(64 * kGvWaves)
-k_int8_gemv_2(Int8FwdArgs g, const float* Tpart, float s, float* T_out) {
-  int8_gemv<2>(g, Tpart, s, T_out);
+  __syncthreads();
+  // The lane that holds row 16 b + 4 q + v of token m is 16 q + m, element v.
+  for (int o = tid; o < outs; o += kGvThreads) {
+    const int m = o / (16 * nb), row = o % (16 * nb), n = n0 + row;
+    if (n >= g.N) continue;
+    const int sum = red[(row >> 4) * 256 + 64 * (row & 3) + 16 * ((row & 15) >> 2) + m];
+    const float fx = o == tid ? sx0 : g.sx[m], fw = o == tid ? sw0 : g.sw[n];
+    g.Y[(int64_t)m * g.N + n] = f32_to_bf16((float)sum * fx * fw + yl[o]);
+  }
 }
 
 // ------------------------------- launchers ---------------------------------
@@ -491,13 +545,11 @@ hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int6
       const hipError_t e = launch_int8_T_partial(X.codes, M, K, A, r, part, st);
       if (e != hipSuccess) return e;
     }
-    const size_t lds = (size_t)M * r * 4;
-    if (N >= 32 * 512)
-      hipLaunchKernelGGL(k_int8_gemv_2, dim3((unsigned)((N + 31) / 32)), dim3(64 * kGvWaves), lds, st,
-                         g, part, s, T_out);
-    else
-      hipLaunchKernelGGL(k_int8_gemv_1, dim3((unsigned)((N + 15) / 16)), dim3(64 * kGvWaves), lds, st,
-                         g, part, s, T_out);
+    const int blocks = (int)((N + 15) / 16);
+    const int nb = min((blocks + kCUs - 1) / kCUs, kGvBlocks);
+    const dim3 grid((unsigned)((blocks + nb - 1) / nb)), block(kGvThreads);
+    if (K <= 4096) hipLaunchKernelGGL(k_int8_gemv<4096>, grid, block, 0, st, g, part, s, T_out, nb);
+    else hipLaunchKernelGGL(k_int8_gemv<8192>, grid, block, 0, st, g, part, s, T_out, nb);
     return hipGetLastError();
   }
   if (r) {

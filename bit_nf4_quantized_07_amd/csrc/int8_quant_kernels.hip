@@ -6,14 +6,14 @@
 // A row (run) of zeros has scale 0 and codes 0; one that holds an infinity or a
 // NaN has scale NaN and codes 0, so that every value it stands for is NaN.
 //
-// The quotient: with g a power of two that brings a near 1 and R = 127 / (a g)
-// held as two fp32 words (R_hi the rounded quotient, R_lo the rest), n = fma(x g,
-// R_hi, x g R_lo) is 127 x / a rounded once (its error before that is below
-// 2^-40).  For bf16 x this gives the exact code: a tie 127 x / a = k + 1/2 is a
+// The quotient: R = 127 / a held as two fp32 words, R_hi near it and R_lo the rest
+// (within 2^-44 of R together), n = fma(x, R_hi, x R_lo) is 127 x / a rounded once.
+// For bf16 x this gives the exact code: a tie 127 x / a = k + 1/2 is a
 // representable number and therefore hit, and what is no tie is at least 2^-9
 // of |n| / 254 away from one, since 254 x and (2 k + 1) a are whole multiples
 // of x's last place.  Adding 1.5 2^23 rounds n to the nearest integer, ties to
-// the even one, and leaves the code in the sum's low byte.
+// the even one, and leaves the code in the sum's low byte.  Where a lies outside
+// [2^-100, 2^100], x and a are scaled by a power of two first.
 //
 // The gated activation H = silu(G) U in rows of 8 bits, with G and U kept in
 // runs of 64 for the backward, and that backward, read and write these formats
@@ -30,34 +30,40 @@ namespace qlk {
 
 constexpr int kRowPieces = 8;    // pieces of 8 values a lane holds
 
-// 127 x / a for many x of one row or run.
+// 127 x / a for many x of one row or run.  g: 1, or the power of two that scales x
+// first; 0 where all codes are 0 (a is zero, infinite or NaN).
 struct Inverse {
   float g, hi, lo, scale;
 };
 // a: the largest magnitude (bits of a non-negative fp32; NaN and infinity from
 // 0x7f800000 on).
 __device__ __forceinline__ Inverse inverse_of(uint32_t abits) {
-  Inverse v{0.0f, 0.0f, 0.0f, 0.0f};
-  if (abits == 0) return v;
-  if (abits >= 0x7f800000u) {
-    v.scale = __uint_as_float(0x7fc00000u);
-    return v;
-  }
+#pragma clang fp contract(off)
+  Inverse v;
   const float a = __uint_as_float(abits);
-  v.scale = a / 127.0f;
-  const int e = min(max((int)(abits >> 23) - 127, -120), 120);
-  v.g = __uint_as_float((uint32_t)(127 - e) << 23);
-  const float as = a * v.g;                       // exact
-  v.hi = 127.0f / as;
-  v.lo = __builtin_fmaf(-v.hi, as, 127.0f) / as;
+  float as = a;
+  v.g = 1.0f;
+  // fp32(a / 127): the product with fl(1/127) and one correction (the rounded
+  // quotient for all 2^23 mantissas, tested against division)
+  const float q = a * (1.0f / 127.0f);
+  v.scale = __builtin_fmaf(__builtin_fmaf(-q, 127.0f, a), 1.0f / 127.0f, q);
+  if (abits - 0x0d800000u > 0x71800000u - 0x0d800000u) {   // outside [2^-100, 2^100]
+    const int e = min(max((int)(abits >> 23) - 127, -120), 120);
+    const bool none = abits == 0 || abits >= 0x7f800000u;
+    v.g = none ? 0.0f : __uint_as_float((uint32_t)(127 - e) << 23);
+    as = none ? 1.0f : a * v.g;                            // exact
+    v.scale = abits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : a / 127.0f;
+  }
+  const float r = __builtin_amdgcn_rcpf(as);
+  v.hi = 127.0f * r;
+  v.lo = __builtin_fmaf(-v.hi, as, 127.0f) * r;
   return v;
 }
 // fp32 whose low byte is the code of x.
 __device__ __forceinline__ uint32_t code_of(float x, const Inverse& v) {
 #pragma clang fp contract(off)
-  const float xs = x * v.g;
-  const float t = xs * v.lo;
-  const float n = __builtin_fmaf(xs, v.hi, t);
+  const float t = x * v.lo;
+  const float n = __builtin_fmaf(x, v.hi, t);
   const float s = n + 12582912.0f;
   return __float_as_uint(s);
 }
@@ -66,16 +72,20 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
   return ab | cd;
 }
-// Eight values' codes; all zero where the row has none (a zero or non-finite a:
-// g, hi and lo are zero, and an infinity or NaN times zero must not reach them).
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Inverse& v) {
   uint32_t c[8];
+  if (__builtin_expect(v.g == 1.0f, 1)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = code_of(x[i], v);
-  const uint32_t keep = v.g > 0.0f ? 0xffffffffu : 0u;
-  return make_uint2(pack4(c[0], c[1], c[2], c[3]) & keep, pack4(c[4], c[5], c[6], c[7]) & keep);
+    for (int i = 0; i < 8; ++i) c[i] = code_of(x[i], v);
+  } else {
+    if (v.g == 0.0f) return make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = code_of(x[i] * v.g, v);
+  }
+  return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
 }
 
+// Eight values as they are stored: bf16 in four words, fp32 in eight.
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -96,6 +106,42 @@ __device__ __forceinline__ uint32_t amax8(const float (&x)[8]) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
   return m;
 }
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t amax8(const uint4& v) {
+  auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2_t, w & 0x7fff7fffu); };
+  const u16x2_t m = __builtin_elementwise_max(__builtin_elementwise_max(mag(v.x), mag(v.y)),
+                                              __builtin_elementwise_max(mag(v.z), mag(v.w)));
+  return (uint32_t)max(m.x, m.y) << 16;
+}
+template <class T>
+struct Piece;
+template <>
+struct Piece<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* row, int64_t p) { v = reinterpret_cast<const uint4*>(row)[p]; }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t amax() const { return amax8(v); }
+  __device__ __forceinline__ void values(float (&x)[8]) const { unpack8(v, x); }
+};
+template <>
+struct Piece<float> {
+  float x8[8];
+  __device__ __forceinline__ void load(const float* row, int64_t p) {
+    const float4 lo = reinterpret_cast<const float4*>(row)[2 * p];
+    const float4 hi = reinterpret_cast<const float4*>(row)[2 * p + 1];
+    x8[0] = lo.x; x8[1] = lo.y; x8[2] = lo.z; x8[3] = lo.w;
+    x8[4] = hi.x; x8[5] = hi.y; x8[6] = hi.z; x8[7] = hi.w;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x8[e] = 0.0f;
+  }
+  __device__ __forceinline__ uint32_t amax() const { return amax8(x8); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x8[e];
+  }
+};
 __device__ __forceinline__ uint32_t max_over_wave(uint32_t m) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
@@ -112,17 +158,6 @@ __device__ __forceinline__ uint32_t max_over_row(uint32_t m, uint32_t* red) {
     for (int w = 0; w < W; ++w) m = max(m, red[w]);
   }
   return m;
-}
-
-// Eight values of a piece (piece p holds columns 8 p .. 8 p + 7).
-__device__ __forceinline__ void load8(const uint16_t* row, int64_t p, float (&x)[8]) {
-  unpack8(reinterpret_cast<const uint4*>(row)[p], x);
-}
-__device__ __forceinline__ void load8(const float* row, int64_t p, float (&x)[8]) {
-  const float4 lo = reinterpret_cast<const float4*>(row)[2 * p];
-  const float4 hi = reinterpret_cast<const float4*>(row)[2 * p + 1];
-  x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-  x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
 }
 
 // Rows of X [M, K] (8 | K).  W waves share a row; a lane holds P pieces of it.
@@ -142,58 +177,61 @@ k_int8_quantize(const T* __restrict__ X, int64_t M, int64_t K, int8_t* __restric
   const int p0 = W == 1 ? lane : (int)threadIdx.x;
   constexpr int stride = 64 * W;
   uint32_t a = 0;
+  float x[8];
   if constexpr (P > 0) {
-    float x[P][8];
+    Piece<T> v[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int p = p0 + i * stride;
-      if (p < np) load8(row, p, x[i]);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+      if (p < np) v[i].load(row, p);
+      else v[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) a = max(a, amax8(x[i]));
-    const Inverse v = inverse_of(max_over_row<W>(a, red));
+    for (int i = 0; i < P; ++i) a = max(a, v[i].amax());
+    const Inverse inv = inverse_of(max_over_row<W>(a, red));
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int p = p0 + i * stride;
-      if (p < np) out[p] = codes8(x[i], v);
+      v[i].values(x);
+      if (p < np) out[p] = codes8(x, inv);
     }
-    if (p0 == 0) scale[m] = v.scale;
+    if (p0 == 0) scale[m] = inv.scale;
   } else {
-    float x[8];
+    Piece<T> v;
     for (int64_t p = p0; p < np; p += stride) {
-      load8(row, p, x);
-      a = max(a, amax8(x));
+      v.load(row, p);
+      a = max(a, v.amax());
     }
-    const Inverse v = inverse_of(max_over_row<W>(a, red));
+    const Inverse inv = inverse_of(max_over_row<W>(a, red));
     for (int64_t p = p0; p < np; p += stride) {
-      load8(row, p, x);
-      out[p] = codes8(x, v);
+      v.load(row, p);
+      v.values(x);
+      out[p] = codes8(x, inv);
     }
-    if (p0 == 0) scale[m] = v.scale;
+    if (p0 == 0) scale[m] = inv.scale;
   }
 }
 
-// Waves per row and pieces per lane for np pieces: as few waves as hold the row
-// in registers, so that short rows need no barrier; long rows spread over a
-// workgroup.
+// Waves per row and pieces per lane for np pieces: a wave holds a short row alone
+// and needs no barrier; long rows spread over a workgroup, up to kRowPieces pieces a
+// lane, and what that does not hold is read twice.
 template <class F>
 static void for_row(int64_t np, F f) {
+  using std::integral_constant;
   auto pieces = [&](auto w) {
     constexpr int W = decltype(w)::value;
     const int64_t need = (np + 64 * W - 1) / (64 * W);
-    if (need <= 1) f(w, std::integral_constant<int, 1>());
-    else if (need <= 2) f(w, std::integral_constant<int, 2>());
-    else if (need <= 4) f(w, std::integral_constant<int, 4>());
-    else if (need <= 6) f(w, std::integral_constant<int, 6>());
-    else f(w, std::integral_constant<int, kRowPieces>());
+    if (need <= 1) f(w, integral_constant<int, 1>());
+    else if (need <= 2) f(w, integral_constant<int, 2>());
+    else if (need <= 4) f(w, integral_constant<int, 4>());
+    else if (need <= 6) f(w, integral_constant<int, 6>());
+    else f(w, integral_constant<int, kRowPieces>());
   };
-  if (np <= 64 * 2) pieces(std::integral_constant<int, 1>());
-  else if (np <= 256 * kRowPieces) pieces(std::integral_constant<int, 4>());
-  else if (np <= 1024 * kRowPieces) pieces(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 16>(), std::integral_constant<int, 0>());
+  if (np <= 64 * 2) pieces(integral_constant<int, 1>());
+  else if (np <= 256 * kRowPieces) pieces(integral_constant<int, 4>());
+  else if (np <= 1024 * 4) f(integral_constant<int, 16>(), integral_constant<int, 4>());
+  else if (np <= 1024 * kRowPieces) f(integral_constant<int, 16>(), integral_constant<int, kRowPieces>());
+  else f(integral_constant<int, 16>(), integral_constant<int, 0>());
 }
 
 template <class T>
@@ -257,8 +295,7 @@ hipError_t launch_int8_dequant(const int8_t* codes, const float* scale, int64_t 
 
 // ---------------------------------------------------------------------------
 // H = silu(G) U.  The value that is quantised is the fp32 product; where the
-// bf16 H is wanted too, it is that product rounded, the elementwise gating's
-// bits.  The eight lanes of a run of 64 columns hold it whole.
+// bf16 H is wanted too, it has the elementwise gating's bits.  The eight lanes of a run of 64 columns hold it whole.
 __device__ __forceinline__ uint32_t max_over_8(uint32_t m) {
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
@@ -276,86 +313,110 @@ struct GateOut {
 };
 
 // One piece of G or U kept in 8 bits; every lane of the run calls it.
-__device__ __forceinline__ void keep8(const float (&x)[8], int8_t* codes, float* scale, int64_t row8,
-                                      int64_t p, bool in) {
-  const Inverse v = inverse_of(max_over_8(in ? amax8(x) : 0u));
+__device__ __forceinline__ void keep8(const uint4& v, const float (&x)[8], int8_t* codes, float* scale,
+                                      int64_t row8, int64_t p, bool in) {
+  const Inverse inv = inverse_of(max_over_8(amax8(v)));
   if (!in) return;
-  reinterpret_cast<uint2*>(codes)[row8 + p] = codes8(x, v);
-  if ((p & 7) == 0) scale[(row8 + p) >> 3] = v.scale;
+  reinterpret_cast<uint2*>(codes)[row8 + p] = codes8(x, inv);
+  if ((p & 7) == 0) scale[(row8 + p) >> 3] = inv.scale;
+}
+// silu(g) u for eight values.  The reciprocal is the instruction's, within an ulp;
+// where it would be subnormal (g below -87) the value is 0.
+__device__ __forceinline__ void silu_mul8(const float (&g)[8], const float (&u)[8], float (&h)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = g[e] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[e])) * u[e];
 }
 
-template <int W, int P>
-__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
-k_silu_mul_fwd_int8(const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, int64_t M,
-                    int64_t I, GateOut o) {
+struct GateIn {
+  uint4 g, u;
+};
+__device__ __forceinline__ void gate_load(GateIn& v, const uint16_t* grow, const uint16_t* urow, int64_t p,
+                                          int64_t np) {
+  v.g = v.u = make_uint4(0, 0, 0, 0);
+  if (p < np) {
+    v.g = reinterpret_cast<const uint4*>(grow)[p];
+    v.u = reinterpret_cast<const uint4*>(urow)[p];
+  }
+}
+// H of a piece; `first`: G and U (and the bf16 H) leave as well.
+__device__ __forceinline__ void gate_piece(const GateOut& o, const GateIn& v, int64_t row8, int64_t p,
+                                           int64_t np, bool first, float (&h)[8]) {
+  float g[8], u[8];
+  unpack8(v.g, g);
+  unpack8(v.u, u);
+  silu_mul8(g, u, h);
+  if (!first) return;
+  const bool in = p < np;
+  if (o.H && in) {
+    float b[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = silu_mul_f32(g[e], u[e]);
+    reinterpret_cast<uint4*>(o.H)[row8 + p] = pack8(b);
+  }
+  if (o.G8) {
+    keep8(v.g, g, o.G8, o.Gs, row8, p, in);
+    keep8(v.u, u, o.U8, o.Us, row8, p, in);
+  }
+}
+
+// A row per workgroup of W waves.  LDS: its H stays there in fp32 between the
+// maximum and the codes, the next piece's loads in flight; otherwise (a row longer
+// than LDS) G and U are read a second time.  (In registers H, G and U took 24 for
+// each piece of a lane, and two waves a SIMD did not cover the loads: 4096 x 11008,
+// 92 us.)
+template <int W, bool LDS>
+__global__ void __launch_bounds__(64 * W)
+k_silu_mul_fwd_int8(const uint16_t* __restrict__ G, const uint16_t* __restrict__ U, int64_t I, GateOut o) {
   __shared__ uint32_t red[W];
-  constexpr int R = W == 1 ? 4 : 1;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = (int64_t)blockIdx.x * R + (W == 1 ? wave : 0);
-  if (W == 1 && m >= M) return;
+  extern __shared__ float4 hl[];
+  const int64_t m = blockIdx.x;
   const int64_t np = I / 8, row8 = m * np;
-  const int p0 = W == 1 ? lane : (int)threadIdx.x;
   constexpr int stride = 64 * W;
+  const int tid = threadIdx.x;
   const uint16_t* const grow = G + m * I;
   const uint16_t* const urow = U + m * I;
-  auto gated = [&](int64_t p, bool first, float (&h)[8]) {
-    float g[8], u[8];
-    const bool in = p < np;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
-    if (in) {
-      load8(grow, p, g);
-      load8(urow, p, u);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = silu_mul_f32(g[e], u[e]);
-    if (!first) return;
-    if (o.H && in) reinterpret_cast<uint4*>(o.H)[row8 + p] = pack8(h);
-    if (o.G8) {
-      keep8(g, o.G8, o.Gs, row8, p, in);
-      keep8(u, o.U8, o.Us, row8, p, in);
-    }
-  };
-  uint32_t a = 0;
   uint2* const out = reinterpret_cast<uint2*>(o.H8) + row8;
-  if constexpr (P > 0) {
-    float h[P][8];
-#pragma unroll
-    for (int i = 0; i < P; ++i) gated(p0 + i * stride, true, h[i]);
-#pragma unroll
-    for (int i = 0; i < P; ++i) a = max(a, amax8(h[i]));
-    const Inverse v = inverse_of(max_over_row<W>(a, red));
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int p = p0 + i * stride;
-      if (p < np) out[p] = codes8(h[i], v);
+  uint32_t a = 0;
+  float h[8];
+  GateIn v, next;
+  gate_load(v, grow, urow, tid, np);
+  for (int64_t q = 0; q < np; q += stride) {       // whole waves: a run's lanes work together
+    const int64_t p = q + tid;
+    gate_load(next, grow, urow, p + stride, np);
+    gate_piece(o, v, row8, p, np, true, h);
+    a = max(a, amax8(h));
+    if (LDS && p < np) {
+      hl[p] = make_float4(h[0], h[1], h[2], h[3]);
+      hl[np + p] = make_float4(h[4], h[5], h[6], h[7]);
     }
-    if (p0 == 0) o.Hs[m] = v.scale;
-  } else {
-    float h[8];
-    for (int64_t q = 0; q < np; q += stride) {
-      gated(q + p0, true, h);
-      a = max(a, amax8(h));
-    }
-    const Inverse v = inverse_of(max_over_row<W>(a, red));
-    for (int64_t p = p0; p < np; p += stride) {
-      gated(p, false, h);
-      out[p] = codes8(h, v);
-    }
-    if (p0 == 0) o.Hs[m] = v.scale;
+    v = next;
   }
+  const Inverse inv = inverse_of(max_over_row<W>(a, red));
+  for (int64_t p = tid; p < np; p += stride) {
+    if constexpr (LDS) {                           // this thread's own
+      const float4 x = hl[p], y = hl[np + p];
+      const float hv[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      out[p] = codes8(hv, inv);
+    } else {
+      gate_load(v, grow, urow, p, np);
+      gate_piece(o, v, row8, p, np, false, h);
+      out[p] = codes8(h, inv);
+    }
+  }
+  if (tid == 0) o.Hs[m] = inv.scale;
 }
 
 hipError_t launch_silu_mul_fwd_int8(const uint16_t* G, const uint16_t* U, int64_t M, int64_t I,
                                     uint16_t* H, int8_t* H8, float* Hs, int8_t* G8, float* Gs,
                                     int8_t* U8, float* Us, hipStream_t st) {
   const GateOut o{H, H8, Hs, G8, Gs, U8, Us};
-  for_row(I / 8, [&](auto w, auto p) {
-    constexpr int W = decltype(w)::value, P = decltype(p)::value;
-    const int64_t grid = W == 1 ? (M + 3) / 4 : M;
-    hipLaunchKernelGGL((k_silu_mul_fwd_int8<W, P>), dim3((unsigned)grid),
-                       dim3(W == 1 ? 256 : 64 * W), 0, st, G, U, M, I, o);
-  });
+  const dim3 grid((unsigned)M);
+  const size_t lds = (size_t)I * 4;
+  if (I <= 512) hipLaunchKernelGGL((k_silu_mul_fwd_int8<1, true>), grid, dim3(64), lds, st, G, U, I, o);
+  else if (I <= 8192) hipLaunchKernelGGL((k_silu_mul_fwd_int8<4, true>), grid, dim3(256), lds, st, G, U, I, o);
+  else if (I <= 14336) hipLaunchKernelGGL((k_silu_mul_fwd_int8<8, true>), grid, dim3(512), lds, st, G, U, I, o);
+  else if (I <= 40000) hipLaunchKernelGGL((k_silu_mul_fwd_int8<16, true>), grid, dim3(1024), lds, st, G, U, I, o);
+  else hipLaunchKernelGGL((k_silu_mul_fwd_int8<16, false>), grid, dim3(1024), 0, st, G, U, I, o);
   return hipGetLastError();
 }
 
