@@ -25,6 +25,7 @@ CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["quant_kernels.hip", "gemm_kernels.hip", "fwd_kernels.hip", "dx_kernels.hip", "adapter_kernels.hip", "gemv_kernels.hip", "elementwise.hip",
            "merge_kernels.hip", "dropout_kernels.hip", "batch_plan_kernels.hip", "batch_kernels.hip",
            "int8_quant_kernels.hip", "int8_adapter_kernels.hip", "int8_fwd_kernels.hip",
+           "int8_dx_kernels.hip",
            "qlora_api.hip"]
 ARCH = "gfx950"
 

@@ -865,6 +865,10 @@ k_int8_grads(Grad8Job ja, Grad8Job jb, int M, int r, float s) {
   else grads8<false, RT>(jb, (int)blockIdx.x - ja.slices, M, r, t0, s, lds);
 }
 
+// Token count up to which dX reads an 8-bit base as it is stored.  The whole backward
+// at 4096 x 4096, r = 16, read as stored and on a copy: 16 tokens 24 and 35 us, 300
+// tokens 41 and 46, 512 tokens 49 and 51.
+constexpr int64_t kCodesMaxM = 512;
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Int8BwdPlan p{};
@@ -875,15 +879,24 @@ Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool
   p.off_ds = p.off_tp + up(pack);
   p.off_dt = p.off_ds + (r <= kRankOnce ? 0 : up(down_bytes(M, N, r)));
   p.bytes = p.off_dt + (r <= kRankOnce ? 0 : up(down_bytes(M, K, r)));
-  // dX on a bf16 copy of the base, made once per call: always of an 8-bit base,
-  // of an NF4 base from the token count where its own backward makes one
-  p.copy = dx && (base == kBaseInt8 || (base == kBaseNF4 && M >= kDequantDxMinM &&
-                                        dx_nf4_supported(N) && N * K * 2 < ((int64_t)1 << 31)));
+  // An 8-bit base is read as it is stored up to kCodesMaxM tokens, and above on a
+  // bf16 copy made once per call; an NF4 base is copied where its own backward does
+  // and where that has no kernel for N (256 does not divide it).
+  const bool whole = dx_nf4_supported(N);
+  const bool room = N * K * 2 < ((int64_t)1 << 31);
+  if (dx && base == kBaseInt8) p.copy = M > kCodesMaxM && room;
+  if (dx && base == kBaseNF4) p.copy = room && (!whole || M >= kDequantDxMinM);
   p.off_w = p.bytes;
   if (p.copy) p.bytes += up((size_t)N * K * 2);
-  p.kz_len = dx && dx_nf4_supported(N) ? dx_split_len(M, K, N) : 0;
   p.off_part = p.bytes;
-  if (p.kz_len) p.bytes += up((size_t)((N / 64 + p.kz_len - 1) / p.kz_len) * M * K * 4);
+  p.any = dx && (base == kBaseInt8 ? !p.copy || !whole : !whole && (p.copy || base == kBaseBF16));
+  if (p.any) {
+    p.dx8 = plan_dx8(M, K, N, base == kBaseInt8 && !p.copy);
+    p.bytes += up(p.dx8.bytes);
+  } else if (dx && whole) {
+    p.kz_len = dx_split_len(M, K, N);
+    if (p.kz_len) p.bytes += up((size_t)((N / 64 + p.kz_len - 1) / p.kz_len) * M * K * 4);
+  }
   return p;
 }
 
@@ -945,8 +958,11 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (dX) {
-    e = launch_dx(dY, M, wx, U, A, r, s, dX, accumulate, st, nullptr, 1.0f,
-                  p.kz_len ? reinterpret_cast<float*>(base + p.off_part) : nullptr, p.kz_len, nullptr);
+    float* const part = reinterpret_cast<float*>(base + p.off_part);
+    e = p.any ? launch_dx8(dY, M, K, N, p.copy ? nullptr : W8, wx.bf16, U, A, r, s, dX, accumulate, part,
+                           p.dx8, st)
+              : launch_dx(dY, M, wx, U, A, r, s, dX, accumulate, st, nullptr, 1.0f,
+                          p.kz_len ? part : nullptr, p.kz_len, nullptr);
     if (e != hipSuccess) return e;
   }
   auto grads = [&](auto rt) {

@@ -302,12 +302,24 @@ Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r);
 hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int64_t N, int64_t K,
                            const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* Y,
                            float* T_out, void* ws, const Int8FwdPlan& plan, hipStream_t st);
+// dX (+)= dY W_hat + s U A for any N (8 | N) on a base in 8-bit rows (W8) or a bf16
+// one (W); part: plan.bytes of room.
+struct Dx8Plan {
+  int form, kz_len, splits;
+  size_t bytes;
+};
+Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes);
+hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Int8Rows* W8,
+                      const uint16_t* W, const uint16_t* U, const uint16_t* A, int r, float s,
+                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& plan, hipStream_t st);
 // Backward from X in 8-bit rows on a base in 8-bit rows (W8 not null), NF4 or
 // bf16 (w).  T in fp32 or bf16, or neither (computed again).
 constexpr int kBaseInt8 = 0, kBaseNF4 = 1, kBaseBF16 = 2;
 struct Int8BwdPlan {
   bool copy;         // dX on a bf16 copy of the base at off_w
-  int kz_len;
+  bool any;          // by launch_dx8, else by launch_dx
+  Dx8Plan dx8;
+  int kz_len;        // launch_dx's split
   size_t off_U, off_up, off_tp, off_ds, off_dt, off_w, off_part, bytes;
 };
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx);

@@ -373,6 +373,45 @@ def test_backward_nf4_and_bf16_base(M, K, N, r):
     _assert_within(h.host_bf16_f64(dX), ref, np.abs(ref) * BF + tol * (1 + BF), "bf16: dX")
 
 
+DX = [(1, 64, 8), (3, 4096, 4104), (16, 8192, 1000), (40, 320, 72), (100, 2048, 2056), (130, 4160, 520),
+      (257, 1088, 4096), (300, 4096, 1544), (512, 11008, 264), (511, 576, 8200), (513, 320, 72), (700, 2112, 776),
+      (1100, 4096, 1032), (2100, 4160, 328), (4100, 4096, 200)]
+
+
+@pytest.mark.parametrize("M,K,N", DX)
+def test_input_gradient(M, K, N):
+    """dX on every base at few and many tokens, with outputs that end inside a step
+    and features that end inside a tile, alone and added to what is there."""
+    q, t = _q(), h.torch()
+    g = t.Generator("cuda")
+    g.manual_seed(M + K + N)
+    rnd = lambda *s: t.randn(*s, device="cuda", generator=g)
+    r = 8
+    X, W0 = q.int8_quantize(rnd(M, K).bfloat16()), 0.02 * rnd(N, K)
+    A, B, dY = (rnd(r, K) / 32).bfloat16(), (rnd(N, r) / 16).bfloat16(), rnd(M, N).bfloat16()
+    dX0 = rnd(M, K).bfloat16()
+    W8, W4 = q.int8_quantize(W0), q.quantize(W0)
+    # NF4 decodes to a bf16 value; codes are rounded to one (within half a step)
+    for W, v, wtol in ((W8, W8.codes.double() * W8.scale.double()[:, None], BF),
+                       (W4, q.nf4_dequant(W4).double(), BF), (W0.bfloat16(), W0.bfloat16().double(), 0.0)):
+        T = rnd(M, r)
+        T = T if W is W8 else T.bfloat16()
+        dX = q.linear_bwd_int8(dY, X, W, A, B, 2.0 * r, T=T)[0]
+        U, absU = dY.double() @ B.double(), dY.double().abs() @ B.double().abs()
+        ref = dY.double() @ v + 2.0 * U @ A.double()
+        # the weight's rounding; U and 2 A in bf16; the sums in fp32, the splits' too
+        tol = dY.double().abs() @ v.abs() * (wtol + (N + 40) * 2 * F32) + 2.0 * (
+            absU * ((N + 16) * 2 * F32 + 2 * BF + BF * BF + 4 * r * F32)) @ A.double().abs()
+        err = (dX.double() - ref).abs() - ref.abs() * BF - tol * (1 + BF)
+        assert float(err.max()) <= 0.0, (type(W).__name__, float(err.max()))
+        acc = dX0.clone()
+        q.linear_bwd_int8(dY, X, W, A, B, 2.0 * r, T=T, accumulate_into=acc)
+        ref = ref + dX0.double()
+        tol = tol + dX0.double().abs() * 2 * F32
+        err = (acc.double() - ref).abs() - ref.abs() * BF - tol * (1 + BF)
+        assert float(err.max()) <= 0.0, (type(W).__name__, "added", float(err.max()))
+
+
 def test_gradient_against_differences():
     """dA and dB of L = sum(dY Y) against differences of the forward's formula in
     64 bits (L is linear in A and in B alone, so a difference is exact)."""
