@@ -52,6 +52,8 @@
 // bf16 results through LDS to the gate waves, which write
 // H = silu(G) U (the elementwise kernel's arithmetic on the same bf16 G and
 // U); G and U are written too, for the backward.
+#include <type_traits>
+
 #include "device_common.h"
 #include "kernels.h"
 
@@ -483,12 +485,26 @@ k_split_reduce(const float* __restrict__ part, int splits, int64_t stride, int64
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n8) return;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int z = 0; z < splits; ++z) {
-    const float4* p = reinterpret_cast<const float4*>(part + (int64_t)z * stride) + 2 * i;
-    const float4 a = p[0], b = p[1];
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-  }
+  // eight splits' loads, then four's, in flight together
+  auto add = [&](int z, auto nc) {
+    constexpr int NZ = decltype(nc)::value;
+    float4 a[NZ], b[NZ];
+#pragma unroll
+    for (int u = 0; u < NZ; ++u) {
+      const float4* p = reinterpret_cast<const float4*>(part + (int64_t)(z + u) * stride) + 2 * i;
+      a[u] = p[0];
+      b[u] = p[1];
+    }
+#pragma unroll
+    for (int u = 0; u < NZ; ++u) {
+      v[0] += a[u].x; v[1] += a[u].y; v[2] += a[u].z; v[3] += a[u].w;
+      v[4] += b[u].x; v[5] += b[u].y; v[6] += b[u].z; v[7] += b[u].w;
+    }
+  };
+  int z = 0;
+  for (; z + 8 <= splits; z += 8) add(z, std::integral_constant<int, 8>());
+  for (; z + 4 <= splits; z += 4) add(z, std::integral_constant<int, 4>());
+  for (; z < splits; ++z) add(z, std::integral_constant<int, 1>());
   uint4* const o = reinterpret_cast<uint4*>(out) + i;
   if (accumulate) {
     const uint4 old = *o;

@@ -319,7 +319,10 @@ struct DownJob {
   float* part;
 };
 constexpr int kDownStage = 16 * 1024;
-constexpr int kDownSlices = 4;   // 8 took 1 us off the slices' launch and put 2 on the sums' (4001 tokens)
+// Most slices of the contraction: at 4001 tokens 8 took 1 us off the slices' launch and
+// put 2 on the sums'; where few tiles leave CUs idle they
+// take 9 us off 24 (2 tokens, 28576 columns, r = 64).
+constexpr int kDownSlices = 4, kDownSlicesFew = 8, kDownFewTiles = 16;
 
 // s0 .. s3: the stages, arrays of their own (of one array the compiler would wait
 // for every load before each read).
@@ -448,7 +451,8 @@ __device__ __forceinline__ void down_block(const DownJob& g, int blk, uint8_t* s
 static int down_blocks(DownJob& g) {
   g.groups = (g.r + 63) / 64;
   const int tiles = (g.M + 63) / 64 * g.groups, steps = (g.C + 63) / 64;
-  g.zs = max(1, min(min(2 * kCUs / tiles, steps / 4), kDownSlices));
+  g.zs = max(1, min(min(2 * kCUs / tiles, steps / 4),
+                    tiles <= kDownFewTiles ? kDownSlicesFew : kDownSlices));
   g.zlen = (steps + g.zs - 1) / g.zs;
   g.zs = (steps + g.zlen - 1) / g.zlen;
   return tiles * g.zs;
@@ -484,20 +488,26 @@ __device__ __forceinline__ void finish_block(const FinishJob& g, int blk, float 
   if (m < g.M && j < g.r) {
     const float s = g.sx ? g.sx[m] : 1.0f;
     if (o.pscale) ps = o.pscale[m];
-    float4 a[kDownSlices], b[kDownSlices];   // every slice's loads before the first sum
+    // four slices' loads, or all eight's, before the first sum
+    auto add = [&](auto nc) {
+      constexpr int NZ = decltype(nc)::value;
+      float4 a[NZ], b[NZ];
 #pragma unroll
-    for (int z = 0; z < kDownSlices; ++z) {
-      const float4* const p =
-          reinterpret_cast<const float4*>(g.part + ((int64_t)min(z, g.zs - 1) * g.M + m) * g.r + j);
-      a[z] = p[0];
-      b[z] = p[1];
-    }
+      for (int z = 0; z < NZ; ++z) {
+        const float4* const p =
+            reinterpret_cast<const float4*>(g.part + ((int64_t)min(z, g.zs - 1) * g.M + m) * g.r + j);
+        a[z] = p[0];
+        b[z] = p[1];
+      }
 #pragma unroll
-    for (int z = 0; z < kDownSlices; ++z) {
-      if (z >= g.zs) break;
-      x[0] += a[z].x; x[1] += a[z].y; x[2] += a[z].z; x[3] += a[z].w;
-      x[4] += b[z].x; x[5] += b[z].y; x[6] += b[z].z; x[7] += b[z].w;
-    }
+      for (int z = 0; z < NZ; ++z) {
+        if (z >= g.zs) break;
+        x[0] += a[z].x; x[1] += a[z].y; x[2] += a[z].z; x[3] += a[z].w;
+        x[4] += b[z].x; x[5] += b[z].y; x[6] += b[z].z; x[7] += b[z].w;
+      }
+    };
+    if (g.zs <= kDownSlices) add(std::integral_constant<int, kDownSlices>());
+    else add(std::integral_constant<int, kDownSlicesFew>());
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= s;
     const int64_t at = (int64_t)m * g.r + j;
@@ -869,6 +879,10 @@ k_int8_grads(Grad8Job ja, Grad8Job jb, int M, int r, float s) {
 // at 4096 x 4096, r = 16, read as stored and on a copy: 16 tokens 24 and 35 us, 300
 // tokens 41 and 46, 512 tokens 49 and 51.
 constexpr int64_t kCodesMaxM = 512;
+// And up to which dX decodes an NF4 base on the way, a tile of 256 tokens: 200 tokens
+// x 4096 x 4096 40 us and 41 on a copy, 4096 x 11008 63 and 71; 300 tokens 50 and 45,
+// 90 and 80; 1000 tokens 95 and 65, 228 and 150.
+constexpr int64_t kNF4MaxM = 256;
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Int8BwdPlan p{};
@@ -880,12 +894,12 @@ Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool
   p.off_dt = p.off_ds + (r <= kRankOnce ? 0 : up(down_bytes(M, N, r)));
   p.bytes = p.off_dt + (r <= kRankOnce ? 0 : up(down_bytes(M, K, r)));
   // An 8-bit base is read as it is stored up to kCodesMaxM tokens, and above on a
-  // bf16 copy made once per call; an NF4 base is copied where its own backward does
-  // and where that has no kernel for N (256 does not divide it).
+  // bf16 copy made once per call; an NF4 base is copied above kNF4MaxM tokens and
+  // where no kernel decodes it on the way (256 does not divide N).
   const bool whole = dx_nf4_supported(N);
   const bool room = N * K * 2 < ((int64_t)1 << 31);
   if (dx && base == kBaseInt8) p.copy = M > kCodesMaxM && room;
-  if (dx && base == kBaseNF4) p.copy = room && (!whole || M >= kDequantDxMinM);
+  if (dx && base == kBaseNF4) p.copy = room && (!whole || M > kNF4MaxM);
   p.off_w = p.bytes;
   if (p.copy) p.bytes += up((size_t)N * K * 2);
   p.off_part = p.bytes;

@@ -479,20 +479,22 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, float s, float* __re
 // Tile and split of the contraction, by the time each would take.  A step of a
 // tile takes `alone` us where few workgroups run, and `full` for a workgroup on
 // every CU: for the large tiles the power limit's MFMA rate, for the small ones L2
-// (18 TB/s of operands); `per_cu` workgroups share a CU's LDS.  Measured at K =
-// 4096 and 8192 over 32 to 8192 tokens; the model's choice was the fastest or within
-// 5 % of it at 11 of 12 sizes.  A split contraction pays a second launch and its
-// partial sums' trip.
+// (18 TB/s of operands); `per_cu` workgroups share a CU's LDS.  A split contraction
+// pays a second launch and its partial sums' trip.  Fitted to all forms at one to
+// eight splits; the choice against the fastest at twelve sizes of 64 to 4000 tokens
+// and 192 to 11072 columns: equal or within 2 us, but for 647 x 9152 x 3288 (42 us,
+// with a third split 38).
 struct Int8Form {
   void (*kernel)(Int8FwdArgs);
   int tm, tn, threads, per_cu;
-  double alone, full;
+  double alone, full;          // rows of whole 128-byte lines
+  double alone_cut, full_cut;  // 128 does not divide K: a row's load touches two lines
 };
-static const Int8Form kForms[] = {{k_int8_fwd_256x256, 256, 256, 512, 1, 0.95, 1.54},
-                                  {k_int8_fwd_128x256, 128, 256, 512, 1, 0.50, 0.85},
-                                  {k_int8_fwd_64x256, 64, 256, 512, 1, 0.33, 0.50},
-                                  {k_int8_fwd_64x128, 64, 128, 256, 2, 0.18, 0.35},
-                                  {k_int8_fwd_64x64, 64, 64, 256, 3, 0.10, 0.22}};
+static const Int8Form kForms[] = {{k_int8_fwd_256x256, 256, 256, 512, 1, 0.95, 1.54, 1.12, 1.80},
+                                  {k_int8_fwd_128x256, 128, 256, 512, 1, 0.50, 0.85, 0.68, 1.03},
+                                  {k_int8_fwd_64x256, 64, 256, 512, 1, 0.33, 0.50, 0.57, 0.66},
+                                  {k_int8_fwd_64x128, 64, 128, 256, 2, 0.18, 0.35, 0.31, 0.37},
+                                  {k_int8_fwd_64x64, 64, 64, 256, 3, 0.10, 0.22, 0.20, 0.23}};
 constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]);
 
 Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r) {
@@ -512,8 +514,10 @@ Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r) {
       if (splits > 1 && (tiles * splits > F.per_cu * kCUs || steps / splits < 8)) break;
       const int64_t len = (steps + splits - 1) / splits;
       const int64_t wgs = tiles * splits, round = (int64_t)F.per_cu * kCUs, rest = wgs % round;
-      double step = (double)(wgs / round) * F.per_cu * F.full;
-      if (rest) step += rest * F.full / kCUs > F.alone ? rest * F.full / kCUs : F.alone;
+      const double alone = K % kI8Step ? F.alone_cut : F.alone, full = K % kI8Step ? F.full_cut : F.full;
+      double step = (double)(wgs / round) * F.per_cu * full;
+      if (rest > kCUs) step += full * ((rest + kCUs - 1) / kCUs);
+      else if (rest) step += rest * full / kCUs > alone ? rest * full / kCUs : alone;
       double us = len * step;
       if (splits > 1) us += 2.5 + (double)M * N * splits * 8.0 / 5e6;
       if (best == 0.0 || us < best) {
