@@ -97,6 +97,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// Sixteen codes as two operands' worth of bf16.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w, int i) {   // codes i, i + 1
+  return pack_bf16x2((float)(int8_t)(w >> (8 * i)), (float)(int8_t)(w >> (8 * i + 8)));
+}
+__device__ __forceinline__ void codes_to_bf16(const uint4& v, uint4 (&o)[2]) {
+  o[0] = make_uint4(codes_bf16x2(v.x, 0), codes_bf16x2(v.x, 2), codes_bf16x2(v.y, 0), codes_bf16x2(v.y, 2));
+  o[1] = make_uint4(codes_bf16x2(v.z, 0), codes_bf16x2(v.z, 2), codes_bf16x2(v.w, 0), codes_bf16x2(v.w, 2));
+}
+
 __device__ __forceinline__ uint16_t f32_to_bf16(float x) {
   return __builtin_bit_cast(uint16_t, (__bf16)x);
 }

@@ -22,14 +22,6 @@ namespace qlk {
 
 constexpr int kChunk = 32;       // tokens of an MFMA step of the gradients
 
-// Sixteen codes as two operands' worth of bf16.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w, int i) {   // codes i, i + 1
-  return pack_bf16x2((float)(int8_t)(w >> (8 * i)), (float)(int8_t)(w >> (8 * i + 8)));
-}
-__device__ __forceinline__ void codes_to_bf16(const uint4& v, uint4 (&o)[2]) {
-  o[0] = make_uint4(codes_bf16x2(v.x, 0), codes_bf16x2(v.x, 2), codes_bf16x2(v.y, 0), codes_bf16x2(v.y, 2));
-  o[1] = make_uint4(codes_bf16x2(v.z, 0), codes_bf16x2(v.z, 2), codes_bf16x2(v.w, 0), codes_bf16x2(v.w, 2));
-}
 __device__ __forceinline__ uint4 zero_unless(bool ok, uint4 v) {
   return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
 }

@@ -330,13 +330,21 @@ constexpr int kGvThreads = 64 * kGvWaves;
 constexpr int kGvBlocks = 8;    // blocks of 16 outputs per workgroup
 constexpr int kGvDepth = 4;     // runs in flight per wave
 
-template <int COLS>
+// RT = 0: T's partial sums come from a launch of their own.  RT = 1, 2: every
+// workgroup computes T for up to 16 RT ranks from A [r, K], K <= COLS / RT, and its
+// tokens in LDS; wave w takes the slices w, w + 8, .. of 64 columns with
+// v_mfma_f32_16x16x32_bf16, and the waves' sums are added in order.
+template <int COLS, int RT>
 __global__ void __launch_bounds__(kGvThreads)
-k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, float s, float* __restrict__ T_out, int nb) {
+k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, const uint16_t* __restrict__ A, float s,
+            float* __restrict__ T_out, int nb) {
+  constexpr int TU = RT ? COLS / 64 / kGvWaves / RT : 1;   // a wave's slices
+  constexpr int TL = 2 * TU * RT;                          // its loads of A
   __shared__ __attribute__((aligned(16))) uint8_t xs[16 * COLS];
   __shared__ int red[kGvBlocks * 256];             // [block][lane][4]
   __shared__ float yl[kGvBlocks * 256];            // s T B^T of output o
-  __shared__ float tl[16 * 256];                   // s T
+  __shared__ float tl[16 * (RT ? 16 * RT : 256)];  // s T
+  __shared__ f32x4_t tw[RT ? kGvWaves * RT : 1][64];   // a wave's sums for T
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, gq = lane >> 4;
@@ -348,7 +356,20 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, float s, float* __re
   // T's partial sums and what the first output needs, before anything else
   float t0 = 0.0f, sxt = 0.0f, sx0 = 0.0f, sw0 = 0.0f;
   uint4 b0 = make_uint4(0, 0, 0, 0), b1 = make_uint4(0, 0, 0, 0);
-  if (tid < g.M * g.r) {
+  uint4 aw[TU][RT ? 2 * RT : 1];
+  if constexpr (RT > 0) {
+    const __amdgpu_buffer_rsrc_t ra = rsrc_whole(A, (uint32_t)(g.r * g.K * 2));
+#pragma unroll
+    for (int u = 0; u < TU; ++u)
+#pragma unroll
+      for (int e = 0; e < 2 * RT; ++e) {
+        const int j = 16 * (e >> 1) + i, sl = wave + kGvWaves * u;
+        aw[u][e] = bload128(ra, j < g.r && 64 * sl < g.K
+                                    ? (uint32_t)((j * g.K + 64 * sl + 16 * gq + 8 * (e & 1)) * 2) : kOOB);
+      }
+    if (tid < g.M * g.r) sxt = g.sx[tid / g.r];
+  }
+  if (RT == 0 && tid < g.M * g.r) {
     float p[kTSplits];
 #pragma unroll
     for (int z = 0; z < kTSplits; ++z) p[z] = Tpart[z * g.M * g.r + tid];
@@ -394,7 +415,7 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, float s, float* __re
     Run R[kGvDepth];
 #pragma unroll
     for (int d = 0; d < kGvDepth; ++d) load(R[d]);
-    if (kc == 0) {
+    if (RT == 0 && kc == 0) {
       if (tid < g.M * g.r) {
         const float t = t0 * sxt;
         if (T_out && blockIdx.x == 0) T_out[tid] = t;
@@ -410,6 +431,36 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, float s, float* __re
     }
     __builtin_amdgcn_s_waitcnt(0x0070 | (4 * kGvDepth & 0xF) | ((4 * kGvDepth >> 4) << 14));   // X has landed, lgkmcnt(0)
     __syncthreads();
+    if constexpr (RT > 0) {
+      f32x4_t ta[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) ta[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < TU; ++u) {
+        const int sl = wave + kGvWaves * u;
+        if (64 * sl >= g.K) break;
+        uint4 xv[2];
+        codes_to_bf16(*reinterpret_cast<const uint4*>(
+                          xs + 2048 * (sl >> 1) + 128 * i + 16 * ((4 * (sl & 1) + gq) ^ ((i >> 1) & 7))), xv);
+#pragma unroll
+        for (int e = 0; e < 2 * RT; ++e)
+          ta[e >> 1] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, xv[e & 1]),
+                                     __builtin_bit_cast(bf16x8_t, aw[u][e]), ta[e >> 1]);
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) tw[wave * RT + t][lane] = ta[t];
+      __syncthreads();
+      if (tid < g.M * g.r) {                       // 16 RT ranks of 16 tokens at most
+        const int m = tid / g.r, j = tid % g.r;
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kGvWaves; ++w) t += tw[w * RT + (j >> 4)][16 * (m >> 2) + (j & 15)][m & 3];
+        t *= sxt;
+        if (T_out && blockIdx.x == 0) T_out[tid] = t;
+        tl[tid] = s * t;
+      }
+      __syncthreads();
+    }
     if (kc == 0) {
       for (int o = tid; o < outs; o += kGvThreads) {
         const int m = o / (16 * nb), n = n0 + o % (16 * nb);
@@ -497,12 +548,20 @@ static const Int8Form kForms[] = {{k_int8_fwd_256x256, 256, 256, 512, 1, 0.95, 1
                                   {k_int8_fwd_64x64, 64, 64, 256, 3, 0.10, 0.22, 0.20, 0.23}};
 constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]);
 
+// Sixteens of ranks that the single-token forward multiplies itself; 0: none.  It
+// saves a launch, and every workgroup reads A: 1024 x 1024 at r = 16 8.4 -> 5.2 us
+// (replayed in a graph 5.9 -> 5.3), 4096 x 4096 at r = 16 7.8 -> 9.7 in a graph.
+static int int8_gemv_ranks(int64_t K, int r) {
+  const int rt = (r + 15) / 16;
+  return rt <= 2 && K * rt <= 2048 && K * r <= 16384 ? rt : 0;
+}
+
 Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Int8FwdPlan p{};
   if (M <= kGemvMaxM) {
     p.gemv = true;
-    p.bytes = up((size_t)kTSplits * M * r * 4);
+    p.bytes = r && !int8_gemv_ranks(K, r) ? up((size_t)kTSplits * M * r * 4) : 0;
     return p;
   }
   const int64_t steps = (K + kI8Step - 1) / kI8Step;
@@ -545,15 +604,21 @@ hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int6
   char* const base = reinterpret_cast<char*>(ws);
   if (p.gemv) {
     float* const part = reinterpret_cast<float*>(base + p.off_T);
-    if (r) {
+    const int rt = r ? int8_gemv_ranks(K, r) : 0;
+    if (r && !rt) {
       const hipError_t e = launch_int8_T_partial(X.codes, M, K, A, r, part, st);
       if (e != hipSuccess) return e;
     }
     const int blocks = (int)((N + 15) / 16);
     const int nb = min((blocks + kCUs - 1) / kCUs, kGvBlocks);
     const dim3 grid((unsigned)((blocks + nb - 1) / nb)), block(kGvThreads);
-    if (K <= 4096) hipLaunchKernelGGL(k_int8_gemv<4096>, grid, block, 0, st, g, part, s, T_out, nb);
-    else hipLaunchKernelGGL(k_int8_gemv<8192>, grid, block, 0, st, g, part, s, T_out, nb);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, st, g, part, A, s, T_out, nb);
+    };
+    if (rt == 1) launch(k_int8_gemv<2048, 1>);
+    else if (rt == 2) launch(k_int8_gemv<2048, 2>);
+    else if (K <= 4096) launch(k_int8_gemv<4096, 0>);
+    else launch(k_int8_gemv<8192, 0>);
     return hipGetLastError();
   }
   if (r) {
