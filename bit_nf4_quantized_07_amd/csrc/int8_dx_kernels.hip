@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "int8_grads.h"
 #include "kernels.h"
 
 namespace qlk {
@@ -51,6 +52,7 @@ struct Dx8Args {
   int tiles_m, tiles_k, group_m;
   float* part;          // split contraction: fp32 [splits][M, K]
   int kz_len;           // steps per split; 0: one pass
+  int blocks;           // workgroups of dX; the rest are the gradients'
 };
 
 constexpr int dx8_wait(int vm, int lgkm) {
@@ -70,8 +72,17 @@ __device__ __forceinline__ bf16x8_t scaled_codes(i32x2_t v, const float (&s)[8])
   return __builtin_bit_cast(bf16x8_t, make_uint4(o[0], o[1], o[2], o[3]));
 }
 
+// The stages are arrays of their own (of one array the compiler would wait for every
+// load before each read).
 template <bool W8, int NI, int WM, int WN, int S>
-__device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
+struct Dx8Lds {
+  static constexpr int Y = 32 * NI * WM * 128, W = 64 * 64 * WN * (W8 ? 1 : 2), C = W8 ? 64 : 4;
+  static constexpr int Y2 = S == 3 ? Y : 16, W2 = S == 3 ? W : 16;
+};
+
+template <bool W8, int NI, int WM, int WN, int S>
+__device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t* w0, float* s0, uint8_t* y1,
+                                         uint8_t* w1, float* s1, uint8_t* y2, uint8_t* w2, float* s2) {
   constexpr int NJ = 2, TM = 32 * NI * WM, TF = 64 * WN, NW = WM * WN;
   constexpr int RB = TF * (W8 ? 1 : 2), RP = RB / 16;      // bytes and pieces of a weight row
   constexpr int YL = TM / 8 / NW, WL = RB / 16 / NW;       // a wave's loads of a step (1 KB each)
@@ -79,18 +90,10 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
   constexpr int YB = TM * 128, WB = 64 * RB;
   static_assert(YL * NW * 8 == TM && WL * NW * 16 == RB, "whole loads");
   static_assert(S == 2 || S == 3, "stages");
-  __shared__ __attribute__((aligned(16))) uint8_t y0[YB];
-  __shared__ __attribute__((aligned(16))) uint8_t w0[WB];
-  __shared__ __attribute__((aligned(16))) uint8_t y1[YB];
-  __shared__ __attribute__((aligned(16))) uint8_t w1[WB];
-  __shared__ __attribute__((aligned(16))) uint8_t y2[S == 3 ? YB : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t w2[S == 3 ? WB : 16];
-  __shared__ __attribute__((aligned(16))) float s0[W8 ? 64 : 4];
-  __shared__ __attribute__((aligned(16))) float s1[W8 ? 64 : 4];
-  __shared__ __attribute__((aligned(16))) float s2[W8 ? 64 : 4];
-  uint8_t* const yb[3] = {y0, y1, y2};
-  uint8_t* const wb[3] = {w0, w1, w2};
-  float* const sb[3] = {s0, s1, s2};
+  // (+: values, not a choice of variables, which would keep them in memory)
+  auto yb = [&](int b) { return b == 0 ? +y0 : b == 1 ? +y1 : +y2; };
+  auto wb = [&](int b) { return b == 0 ? +w0 : b == 1 ? +w1 : +w2; };
+  auto sb = [&](int b) { return b == 0 ? +s0 : b == 1 ? +s1 : +s2; };
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5, grp = lane >> 4, gi = lane & 15;
@@ -137,19 +140,19 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
     const uint32_t k = (uint32_t)__builtin_amdgcn_readfirstlane(kb);
     const bool end = (int)k == cut;
     if (l < YL)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ry, (lds_ptr)(yb[buf] + 1024 * (YL * wave + l)), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ry, (lds_ptr)(yb(buf) + 1024 * (YL * wave + l)), 16,
                                                end ? ycut[l] : yoff[l], k * 128, 0, 0);
     else if (l < YL + WL)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr)(wb[buf] + 1024 * (WL * wave + l - YL)), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr)(wb(buf) + 1024 * (WL * wave + l - YL)), 16,
                                                end ? wcut[l - YL] : woff[l - YL], k * wstep, 0, 0);
     else   // every wave the same 64
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_ptr)sb[buf], 4, end ? scut : soff, k * 256, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_ptr)sb(buf), 4, end ? scut : soff, k * 256, 0, 0);
   };
   int yrd[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) yrd[t] = c * 128 + (((2 * t + h) ^ yswz(c)) * 16);
   auto yfrag = [&](int buf, int i, int t) -> bf16x8_t {
-    return *reinterpret_cast<const bf16x8_t*>(yb[buf] + 32 * (NI * tq + i) * 128 + yrd[t]);
+    return *reinterpret_cast<const bf16x8_t*>(yb(buf) + 32 * (NI * tq + i) * 128 + yrd[t]);
   };
   // Features 64 fg + 32 j + c, rows 16 t + 8 h + 0..7.  j sets a bit of the piece that
   // the swizzle XORs: its place is that of j = 0 XOR 32 features.
@@ -162,10 +165,10 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
   }
   auto wraw = [&](int buf, int j, int t) -> i32x2_t {
     return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-        (lds_i32x2_ptr)(wb[buf] + 16 * RB * t + (wrd[0] ^ (32 * j))));
+        (lds_i32x2_ptr)(wb(buf) + 16 * RB * t + (wrd[0] ^ (32 * j))));
   };
   auto wfrag = [&](int buf, int j, int t) -> bf16x8_t {
-    const uint16_t* const base = reinterpret_cast<const uint16_t*>(wb[buf] + 16 * RB * t);
+    const uint16_t* const base = reinterpret_cast<const uint16_t*>(wb(buf) + 16 * RB * t);
     const v4s_t lo = lds_read_tr16(base + ((wrd[0] ^ (64 * j)) >> 1));
     const v4s_t hi = lds_read_tr16(base + ((wrd[1] ^ (64 * j)) >> 1));
     typedef short v8s_t __attribute__((ext_vector_type(8)));
@@ -193,8 +196,8 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
       else a[t & 1][j] = wfrag(buf, j, t);
     }
     if constexpr (W8) {
-      const float4 lo = *reinterpret_cast<const float4*>(sb[buf] + 16 * t + 8 * h);
-      const float4 hi = *reinterpret_cast<const float4*>(sb[buf] + 16 * t + 8 * h + 4);
+      const float4 lo = *reinterpret_cast<const float4*>(sb(buf) + 16 * t + 8 * h);
+      const float4 hi = *reinterpret_cast<const float4*>(sb(buf) + 16 * t + 8 * h + 4);
       sv[0] = lo.x; sv[1] = lo.y; sv[2] = lo.z; sv[3] = lo.w;
       sv[4] = hi.x; sv[5] = hi.y; sv[6] = hi.z; sv[7] = hi.w;
     }
@@ -312,9 +315,9 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
   static_assert(WBL >= 1 && BLOCKS <= S * (WBL + YB / BB), "blocks");
   auto ob = [&](int k) -> uint8_t* {
     const int n = k / WBL;
-    if (n < S) return (n == 0 ? w0 : n == 1 ? w1 : w2) + (k % WBL) * BB;
+    if (n < S) return wb(n) + (k % WBL) * BB;
     const int y = k - S * WBL, per = YB / BB > 0 ? YB / BB : 1;
-    return (y / per == 0 ? y0 : y / per == 1 ? y1 : y2) + (y % per) * BB;
+    return yb(y / per) + (y % per) * BB;
   };
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -354,16 +357,41 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g) {
 }
 
 // The host pass does not keep a kernel template whose body calls these loads from a
-// lambda: one plain kernel per form.
-__global__ void __launch_bounds__(256) k_dx8_codes_32(Dx8Args g) { dx8_tile<true, 1, 1, 4, 3>(g); }
-__global__ void __launch_bounds__(256) k_dx8_codes_64(Dx8Args g) { dx8_tile<true, 2, 1, 4, 3>(g); }
-__global__ void __launch_bounds__(256) k_dx8_codes_128(Dx8Args g) { dx8_tile<true, 4, 1, 4, 3>(g); }
-__global__ void __launch_bounds__(256) k_dx8_bf16_64(Dx8Args g) { dx8_tile<false, 2, 1, 4, 3>(g); }
-__global__ void __launch_bounds__(512) k_dx8_bf16_128(Dx8Args g) { dx8_tile<false, 2, 2, 4, 3>(g); }
-__global__ void __launch_bounds__(512) k_dx8_bf16_256(Dx8Args g) { dx8_tile<false, 4, 2, 4, 2>(g); }
+// lambda: one plain kernel per form.  Where the workgroups are of four waves, those of
+// the gradients follow in the same grid, on LDS of a weight stage: a launch less, and
+// the gradients' loads run beside the tiles (16 x 256 x 256, r = 8: 13.8 -> 9.5 us).
+#define QLK_DX8_LDS(...)                                                                 \
+  typedef Dx8Lds<__VA_ARGS__> L;                                                         \
+  __shared__ __attribute__((aligned(16))) uint8_t y0[L::Y], w0[L::W], y1[L::Y], w1[L::W]; \
+  __shared__ __attribute__((aligned(16))) uint8_t y2[L::Y2], w2[L::W2];                  \
+  __shared__ __attribute__((aligned(16))) float s0[L::C], s1[L::C], s2[L::C]
+#define QLK_DX8_KERNEL(name, threads, ...)                                               \
+  __global__ void __launch_bounds__(threads) name(Dx8Args g) {                           \
+    QLK_DX8_LDS(__VA_ARGS__);                                                            \
+    dx8_tile<__VA_ARGS__>(g, y0, w0, s0, y1, w1, s1, y2, w2, s2);                        \
+  }
+#define QLK_DX8_GRADS_KERNEL(name, RT, ...)                                              \
+  __global__ void __launch_bounds__(256) name(Dx8Args g, Grad8Args ga) {                 \
+    QLK_DX8_LDS(__VA_ARGS__);                                                            \
+    static_assert(grads8_lds<RT>() <= L::W && kGradWaves8 == 4, "room");                 \
+    if ((int)blockIdx.x < g.blocks) dx8_tile<__VA_ARGS__>(g, y0, w0, s0, y1, w1, s1, y2, w2, s2); \
+    else grads8_block<RT>(ga, (int)blockIdx.x - g.blocks, w0);                           \
+  }
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_32_r16, 1, true, 1, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_32_r32, 2, true, 1, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_64_r16, 1, true, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_64_r32, 2, true, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_128_r16, 1, true, 4, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_128_r32, 2, true, 4, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_bf16_64_r16, 1, false, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_bf16_64_r32, 2, false, 2, 1, 4, 3)
+QLK_DX8_KERNEL(k_dx8_bf16_128, 512, false, 2, 2, 4, 3)
+QLK_DX8_KERNEL(k_dx8_bf16_256, 512, false, 4, 2, 4, 2)
 
 struct Dx8Form {
-  void (*kernel)(Dx8Args);
+  void (*kernel)(Dx8Args);                      // or, with the gradients,
+  void (*r16)(Dx8Args, Grad8Args);              // of up to 16 ranks,
+  void (*r32)(Dx8Args, Grad8Args);              // of 32 at a time
   bool codes;
   int tm, threads, per_cu;
   double alone, full;      // us of a step: in one workgroup; with one on every CU
@@ -372,12 +400,12 @@ struct Dx8Form {
 // fit is within 3 us of what was measured).  Fewer tokens a tile: the weight is
 // decoded or staged again for each tile row (512 tokens on codes unsplit: 48, 49 and
 // 66 us at 32, 64 and 128); more: too few workgroups (16 tokens: 40, 43, 61).
-static const Dx8Form kDx8Forms[] = {{k_dx8_codes_32, true, 32, 256, 2, 0.53, 0.58},
-                                    {k_dx8_codes_64, true, 64, 256, 2, 0.58, 0.83},
-                                    {k_dx8_codes_128, true, 128, 256, 1, 0.86, 1.45},
-                                    {k_dx8_bf16_64, false, 64, 256, 1, 0.45, 0.63},
-                                    {k_dx8_bf16_128, false, 128, 512, 1, 0.55, 0.93},
-                                    {k_dx8_bf16_256, false, 256, 512, 1, 1.08, 1.72}};
+static const Dx8Form kDx8Forms[] = {{nullptr, k_dx8_codes_32_r16, k_dx8_codes_32_r32, true, 32, 256, 2, 0.53, 0.58},
+                                    {nullptr, k_dx8_codes_64_r16, k_dx8_codes_64_r32, true, 64, 256, 2, 0.58, 0.83},
+                                    {nullptr, k_dx8_codes_128_r16, k_dx8_codes_128_r32, true, 128, 256, 1, 0.86, 1.45},
+                                    {nullptr, k_dx8_bf16_64_r16, k_dx8_bf16_64_r32, false, 64, 256, 1, 0.45, 0.63},
+                                    {k_dx8_bf16_128, nullptr, nullptr, false, 128, 512, 1, 0.55, 0.93},
+                                    {k_dx8_bf16_256, nullptr, nullptr, false, 256, 512, 1, 1.08, 1.72}};
 constexpr int kDx8MaxSplits = 16;
 
 // The form and split of the contraction with the least expected time: whole rounds of
@@ -407,13 +435,15 @@ Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes) {
     }
   }
   p.splits = p.kz_len ? (int)((steps + p.kz_len - 1) / p.kz_len) : 1;
+  p.grads = !kDx8Forms[p.form].kernel;
   p.bytes = p.kz_len ? (size_t)p.splits * M * K * 4 : 0;
   return p;
 }
 
 hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Int8Rows* W8,
                       const uint16_t* W, const uint16_t* U, const uint16_t* A, int r, float s,
-                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& p, hipStream_t st) {
+                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& p, Grad8Args& ga,
+                      hipStream_t st) {
   const Dx8Form& F = kDx8Forms[p.form];
   Dx8Args g{};
   g.dY = dY; g.M = (int)M; g.N = (int)N; g.K = (int)K;
@@ -426,8 +456,14 @@ hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const
   g.group_m = group_for(g.tiles_m, g.tiles_k, F.tm * N * 2.0, 256.0 * N * (W8 ? 1 : 2));
   g.part = part;
   g.kz_len = p.kz_len;
-  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_k * p.splits));
-  hipLaunchKernelGGL(F.kernel, grid, dim3(F.threads), 0, st, g);
+  g.blocks = (int)((int64_t)g.tiles_m * g.tiles_k * p.splits);
+  const dim3 block(F.threads);
+  if (F.kernel)
+    hipLaunchKernelGGL(F.kernel, dim3(g.blocks), block, 0, st, g);
+  else if (r <= 16)
+    hipLaunchKernelGGL(F.r16, dim3(g.blocks + grads8_blocks<1>(ga)), block, 0, st, g, ga);
+  else
+    hipLaunchKernelGGL(F.r32, dim3(g.blocks + grads8_blocks<2>(ga)), block, 0, st, g, ga);
   if (p.kz_len) return launch_split_reduce(part, p.splits, M * K, dX, accumulate, st);
   return hipGetLastError();
 }

@@ -306,12 +306,15 @@ hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int6
 // one (W); part: plan.bytes of room.
 struct Dx8Plan {
   int form, kz_len, splits;
+  bool grads;        // the launch computes dA and dB too
   size_t bytes;
 };
+struct Grad8Args;
 Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes);
 hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Int8Rows* W8,
                       const uint16_t* W, const uint16_t* U, const uint16_t* A, int r, float s,
-                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& plan, hipStream_t st);
+                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& plan, Grad8Args& grads,
+                      hipStream_t st);
 // Backward from X in 8-bit rows on a base in 8-bit rows (W8 not null), NF4 or
 // bf16 (w).  T in fp32 or bf16, or neither (computed again).
 constexpr int kBaseInt8 = 0, kBaseNF4 = 1, kBaseBF16 = 2;
