@@ -311,8 +311,8 @@ struct DownJob {
 };
 constexpr int kDownStage = 16 * 1024;
 // Most slices of the contraction: at 4001 tokens 8 took 1 us off the slices' launch and
-// put 2 on the sums'; where few tiles leave CUs idle they
-// take 9 us off 24 (2 tokens, 28576 columns, r = 64).
+// put 2 on the sums'; where few tiles leave CUs idle they take 6 us off 25 (2 tokens,
+// 28576 columns, r = 64; 16 slices another 3, and 2 more on the sums').
 constexpr int kDownSlices = 4, kDownSlicesFew = 8, kDownFewTiles = 16;
 
 // s0 .. s3: the stages, arrays of their own (of one array the compiler would wait
@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(64 * kGradWaves8) k_int8_grads(Grad8Args g) {
 }
 
 // Token count up to which dX reads an 8-bit base as it is stored.  The whole backward
-// at 4096 x 4096, r = 16, read as stored and on a copy: 16 tokens 24 and 35 us, 300
-// tokens 41 and 46, 512 tokens 49 and 51.
+// at 4096 x 4096, r = 16, read as stored and on a copy: 16 tokens 18 and 35 us, 300
+// tokens 36 and 46, 512 tokens 44 and 51; 700 tokens on a copy 58.
 constexpr int64_t kCodesMaxM = 512;
 // And up to which dX decodes an NF4 base on the way, a tile of 256 tokens: 200 tokens
 // x 4096 x 4096 40 us and 41 on a copy, 4096 x 11008 63 and 71; 300 tokens 50 and 45,
@@ -732,7 +732,7 @@ Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool
   // where no kernel decodes it on the way (256 does not divide N).
   const bool whole = dx_nf4_supported(N);
   const bool room = N * K * 2 < ((int64_t)1 << 31);
-  if (dx && base == kBaseInt8) p.copy = M > kCodesMaxM && room;
+  if (dx && base == kBaseInt8) p.copy = M > kCodesMaxM;
   if (dx && base == kBaseNF4) p.copy = room && (!whole || M > kNF4MaxM);
   p.off_w = p.bytes;
   if (p.copy) p.bytes += up((size_t)N * K * 2);

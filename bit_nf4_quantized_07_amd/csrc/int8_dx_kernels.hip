@@ -14,20 +14,20 @@
 //    operand is two transposing reads of four rows.
 //  * 8-bit weight: rows n of 64 WN bytes, pieces XOR-swizzled by 2 (n & 7); an
 //    operand is one transposing read of eight rows' codes, which become bf16(code
-//    scale[n]), the value a bf16 copy of the base would hold.  For few tokens that copy
-//    is most of the work: without it the backward of 16 tokens x 4096 x 4096 takes 24
-//    us, with it 35.  From 512 tokens on decoding once for all of them costs less
-//    (kCodesMaxM).
+//    scale[n]), the value a bf16 copy of the base would hold.  For few tokens that
+//    copy is most of the work: without it the backward of 16 tokens x 4096 x 4096
+//    takes 18 us, with it 35.  Above 512 tokens decoding once for all of them costs
+//    less (kCodesMaxM).
 // Where N ends inside a step, both operands past it are zero.  A split contraction's
 // fp32 sums go to the workspace and are added in a fixed order.
 //
 // What bounds it: few tokens, the start of a workgroup and the steps' latency (16 x
-// 4096 x 4096 in 16 splits 8 us, 4.6 us of which are the loads of a 17 MB weight);
+// 4096 x 4096 in 16 splits 8 us; its 17 MB of weight are 3.4 at a copy's rate);
 // many, the matrix units at the clock that power leaves (4000 x 4096 x 4104 bf16 115
-// us, 1.17 PFLOP/s).  The tile engine that took such N before: 52 us for 300 tokens
-// (here 22 and 5 for the split's reduction), 84 for 1200.  Where 256 divides N the bf16 base
-// stays with launch_dx, whose largest tile keeps its operands in registers longer
-// (4001 x 4096 x 11008: 282 us; here, at 11000 outputs, 319).
+// us, 1.17 PFLOP/s).  The tile engine that takes such N in linear_bwd: 52 us for 300
+// tokens (here 22 and 5 for the split's reduction), 84 for 1200.  Where 256 divides N
+// a bf16 base stays with launch_dx, whose largest tile keeps its operands in registers
+// longer (4001 x 4096 x 11008: 282 us; here, at 11000 outputs, 319).
 #include <type_traits>
 
 #include "device_common.h"
@@ -359,7 +359,8 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
 // The host pass does not keep a kernel template whose body calls these loads from a
 // lambda: one plain kernel per form.  Where the workgroups are of four waves, those of
 // the gradients follow in the same grid, on LDS of a weight stage: a launch less, and
-// the gradients' loads run beside the tiles (16 x 256 x 256, r = 8: 13.8 -> 9.5 us).
+// the gradients' loads run beside the tiles (the whole backward, 16 x 256 x 256: 13.8
+// -> 11.0 us; 16 x 4096 x 4096: 24 -> 18).
 #define QLK_DX8_LDS(...)                                                                 \
   typedef Dx8Lds<__VA_ARGS__> L;                                                         \
   __shared__ __attribute__((aligned(16))) uint8_t y0[L::Y], w0[L::W], y1[L::Y], w1[L::W]; \

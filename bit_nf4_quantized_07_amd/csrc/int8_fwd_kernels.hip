@@ -9,19 +9,30 @@
 // 2^31), so it does not depend on how the contraction is cut.  T comes from the
 // rank-r kernel as two bf16 terms of s T.
 //
-// A workgroup of four waves computes a tile of 64 NI tokens x 64 NJ outputs,
-// each wave a quarter of 32 NI x 32 NJ: NI NJ accumulators of
-// v_mfma_i32_32x32x32_i8, each a 32 (outputs) x 32 (tokens) block of Y^T.
-//  * The contraction advances 64 columns a step (two MFMA steps) through four
-//    LDS stages, filled by buffer loads that write LDS directly, three steps
-//    ahead: rows of 64 bytes whose four 16-byte pieces are XOR-swizzled by
-//    (row >> 2) & 3, so that operand reads are free of bank conflicts.
+// A workgroup of WM x WN waves computes 32 NI WM tokens x 32 NJ WN outputs, each
+// wave 32 NI x 32 NJ: NI NJ accumulators of v_mfma_i32_32x32x32_i8, each a 32
+// (outputs) x 32 (tokens) block of Y^T.
+//  * The contraction advances 128 columns a step (four MFMA steps) through S LDS
+//    stages that buffer loads fill directly, S steps ahead: rows of 128 bytes, whole
+//    cache lines, whose eight 16-byte pieces are XOR-swizzled by (row >> 1) & 7, so
+//    that operand reads are free of bank conflicts.  Rows of 64 bytes asked L2 twice
+//    as often (8192^3: 31 million requests and 269 us of a 256 x 256 form, here 13
+//    and 187).
+//  * One barrier a step, in front of its last MFMA step: what that one reads is the
+//    next step's, and the loads of S steps on go into the stage that is done.
+//    Eight waves: with two on a SIMD one multiplies while the other reads (four
+//    waves of 128 x 64 took 1.2 times as long).
 //  * The whole sums become fp32, times sx sw, in the accumulators' own
 //    registers, and s T B^T is added by bf16 MFMAs.
 //  * The bf16 tile goes out through the stages, so that every store
 //    instruction writes whole row segments.
 // Where the tiles do not fill the device the contraction is split; a split's
 // fp32 values go to the workspace and are added in a fixed order.
+//
+// What bounds it: the large tiles the clock that power leaves (8192^3 437 us, 2.5
+// PTOP/s, 62 % of the cycles in MFMAs at 1.8 GHz; 4096 x 4096 x 11008 190 us); at
+// 2048 x 4096 x 4096 (36 us) one round of 256 workgroups, a fifth of which is its
+// start and epilogue; at few tokens the weight (one token: 5.2 TB/s of it).
 #include <type_traits>
 
 #include "device_common.h"
@@ -323,8 +334,10 @@ __global__ void __launch_bounds__(256) k_int8_fwd_64x128(Int8FwdArgs g) { int8_t
 //    took half the address unit's time (16 tokens, 28672 x 8192: 69 us, 3.4 TB/s).
 //    Columns past K are zero there, so that the weight's need no bound.
 //  * T = X A^T arrives as kTSplits partial sums, added in a fixed order by every
-//    workgroup (the first one writes T); s T B^T is summed in fp32 while the first
-//    weights are on their way.
+//    workgroup (the first one writes T), or is computed here; s T B^T is summed in
+//    fp32 while the first weights are on their way.
+// Measured: 16 tokens, 28672 x 8192 45 us (5.2 TB/s of weight; a copy reads and
+// writes 5.0), one token, 4096 x 4096 7 us, two of which are a launch's.
 constexpr int kGvWaves = 8;
 constexpr int kGvThreads = 64 * kGvWaves;
 constexpr int kGvBlocks = 8;    // blocks of 16 outputs per workgroup
@@ -339,7 +352,6 @@ __global__ void __launch_bounds__(kGvThreads)
 k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, const uint16_t* __restrict__ A, float s,
             float* __restrict__ T_out, int nb) {
   constexpr int TU = RT ? COLS / 64 / kGvWaves / RT : 1;   // a wave's slices
-  constexpr int TL = 2 * TU * RT;                          // its loads of A
   __shared__ __attribute__((aligned(16))) uint8_t xs[16 * COLS];
   __shared__ int red[kGvBlocks * 256];             // [block][lane][4]
   __shared__ float yl[kGvBlocks * 256];            // s T B^T of output o
@@ -351,7 +363,6 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, const uint16_t* __re
   const int n0 = (int)blockIdx.x * 16 * nb;
   const int outs = 16 * nb * g.M;                  // token o / (16 nb), row o % (16 nb)
   const __amdgpu_buffer_rsrc_t rx = rsrc_whole(g.X, (uint32_t)((int64_t)g.M * g.K));
-  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K));
 
   // T's partial sums and what the first output needs, before anything else
   float t0 = 0.0f, sxt = 0.0f, sx0 = 0.0f, sw0 = 0.0f;

@@ -20,7 +20,10 @@
 // in one pass.
 //
 // Bound: HBM.  A row is read once and held in registers (up to 8 pieces of 8
-// values per lane) between its maximum and its codes.
+// values per lane) between its maximum and its codes.  Measured: codes of bf16 rows,
+// 2048 x 4096 6.3 us and 4001 x 11008 25 us (5.3 TB/s), values of them 6.7 and 22.5
+// (5.9); 4096 x 11008 of the gating 75 us (4.3 TB/s; two rows of sigmoids a CU beside
+// the loads), its backward 65 (5.6).  A copy of 1 GiB: 5.0 TB/s.
 #include <type_traits>
 
 #include "device_common.h"
@@ -222,10 +225,12 @@ static void for_row(int64_t np, F f) {
     constexpr int W = decltype(w)::value;
     const int64_t need = (np + 64 * W - 1) / (64 * W);
     if (need <= 1) f(w, integral_constant<int, 1>());
-    else if (need <= 2) f(w, integral_constant<int, 2>());
-    else if (need <= 4) f(w, integral_constant<int, 4>());
-    else if (need <= 6) f(w, integral_constant<int, 6>());
-    else f(w, integral_constant<int, kRowPieces>());
+    else if (W == 1 || need <= 2) f(w, integral_constant<int, 2>());
+    else if constexpr (W > 1) {
+      if (need <= 4) f(w, integral_constant<int, 4>());
+      else if (need <= 6) f(w, integral_constant<int, 6>());
+      else f(w, integral_constant<int, kRowPieces>());
+    }
   };
   if (np <= 64 * 2) pieces(integral_constant<int, 1>());
   else if (np <= 256 * kRowPieces) pieces(integral_constant<int, 4>());
