@@ -285,7 +285,7 @@ int check_aligned(std::initializer_list<const void*> ptrs) {
 // ---- activations and weights in 8 bits ----
 constexpr int64_t kMaxInt8Rows = (int64_t)1 << 22;    // rows are workgroups
 constexpr int64_t kMaxInt8Cols = (int64_t)1 << 24;
-constexpr int64_t kMaxInt8Elems = (int64_t)1 << 35;
+constexpr int64_t kMaxInt8Elems = (int64_t)1 << 34;   // an eighth in threads, below 2^32
 constexpr int64_t kMaxInt8Sum = (int64_t)1 << 17;     // 127^2 K in 32 bits
 
 int check_int8_matrix(int64_t M, int64_t K, int cols) {

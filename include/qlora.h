@@ -399,7 +399,7 @@ size_t lora_adapters_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int
 /* Rows of X [M, K], bf16 or fp32 (activations by token, weights by output
  * channel).  From bf16 the codes are exact (ties to the even code); from fp32
  * the quotient is rounded to fp32 first.
- * Requires K % 16 == 0, K <= 2^24, 1 <= M < 2^22, M K < 2^35. */
+ * Requires K % 16 == 0, K <= 2^24, 1 <= M < 2^22, M K < 2^34. */
 int int8_quantize(const uint16_t* X, int64_t M, int64_t K, int8_t* codes, float* scale,
                   void* stream);
 int int8_quantize_fp32(const float* X, int64_t M, int64_t K, int8_t* codes, float* scale,

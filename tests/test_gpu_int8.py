@@ -412,6 +412,32 @@ def test_input_gradient(M, K, N):
         assert float(err.max()) <= 0.0, (type(W).__name__, "added", float(err.max()))
 
 
+@pytest.mark.parametrize("M,N", [(3, 136), (40, 264), (600, 264), (600, 256)])
+def test_backward_non_finite_rows(M, N):
+    """An infinity in a token's dY reaches that token's dX alone, a token kept as NaN
+    dA alone (T is given), a base row of NaN dX alone."""
+    q, t = _q(), h.torch()
+    L = _Layer(M, 256, N, 8)
+    _, T = q.linear_fwd_int8(L.X, L.W, L.dA, L.dB, L.alpha)
+    run = lambda dY, X, W: q.linear_bwd_int8(dY, X, W, L.dA, L.dB, L.alpha, T=T)
+    dX, dA, dB = run(L.ddY, L.X, L.W)
+    dY = L.ddY.clone()
+    dY[1, 9] = float("inf")
+    gX, gA, gB = run(dY, L.X, L.W)
+    keep = [m for m in range(M) if m != 1]
+    cols = [n for n in range(N) if n != 9]
+    assert t.equal(gX[keep], dX[keep]) and not bool(gX[1].isfinite().any())
+    assert not bool(gA.isfinite().any()) and t.equal(gB[cols], dB[cols]) and not bool(gB[9].isfinite().any())
+    xs = L.X.scale.clone()
+    xs[1] = float("nan")
+    gX, gA, gB = run(L.ddY, q.Int8Tensor(L.X.codes, xs), L.W)
+    assert t.equal(gX, dX) and t.equal(gB, dB) and bool(gA.isnan().all())
+    ws = L.W.scale.clone()
+    ws[N - 1] = float("nan")
+    gX, gA, gB = run(L.ddY, L.X, q.Int8Tensor(L.W.codes, ws))
+    assert bool(gX.isnan().all()) and t.equal(gA, dA) and t.equal(gB, dB)
+
+
 def test_gradient_against_differences():
     """dA and dB of L = sum(dY Y) against differences of the forward's formula in
     64 bits (L is linear in A and in B alone, so a difference is exact)."""
@@ -528,6 +554,33 @@ def test_mlp_block_captured_and_replayed(M):
         replayed = [v.clone() for v in held]
         for a, b in zip(replayed, step()):
             assert t.equal(a, b)
+
+
+def test_rows_past_32_bit_offsets():
+    """Elementwise calls on more than 2^31 elements: sampled rows equal the same
+    rows by themselves."""
+    q, t = _q(), h.torch()
+    M, I = 66000, 32768                              # 2.16e9 elements
+    if t.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GiB of free memory")
+    g = t.Generator("cuda")
+    g.manual_seed(5)
+    rows = [0, 65534, 65535, 65536, 65537, M - 1]
+    rnd = lambda: t.empty(M, I, dtype=t.bfloat16, device="cuda").normal_(generator=g)
+    G, U = rnd(), rnd()
+    H, G8, U8 = q.silu_mul_fwd_int8(G, U)
+    want = q.silu_mul_fwd_int8(G[rows].contiguous(), U[rows].contiguous())
+    for a, b in zip((H, G8, U8), want):
+        assert t.equal(a.codes[rows], b.codes) and t.equal(a.scale[rows], b.scale)
+    del H
+    dG, dU = q.silu_mul_bwd_int8(G, G8, U8)
+    wG, wU = q.silu_mul_bwd_int8(G[rows].contiguous(), want[1], want[2])
+    assert t.equal(dG[rows], wG) and t.equal(dU[rows], wU)
+    del dG, dU, G8, U8, U
+    X = q.int8_quantize(G)
+    one = q.int8_quantize(G[rows].contiguous())
+    assert t.equal(X.codes[rows], one.codes) and t.equal(X.scale[rows], one.scale)
+    assert t.equal(q.int8_dequant(X, out=G)[rows], q.int8_dequant(one))
 
 
 def test_two_streams_at_once():
