@@ -270,8 +270,13 @@ __device__ __forceinline__ void rank_block(const RankJob& g, int blk, uint8_t* l
     }
 }
 
-// Up to 32 ranks: a workgroup's own sums, no second launch.
+// Up to 32 ranks: a workgroup's own sums, no second launch.  Where a row of `bytes`
+// is long its one workgroup takes longer than slices of it and a launch that adds
+// them (4 to 700 tokens): U at 16 ranks 8192 columns 8 to 11 us against 9 to 12 and a
+// launch, 28672 columns 19 to 22 against 14 to 19; at 32 ranks 4096 columns level,
+// 8192 11 to 13 against 9 to 11.
 constexpr int kRankOnce = 32;
+static bool rank_once(int64_t bytes, int r) { return r <= kRankOnce && bytes * ((r + 15) / 16) < 32768; }
 template <class F>
 static void rank_form(int r, F f) {
   using std::integral_constant;
@@ -548,7 +553,7 @@ hipError_t launch_int8_T(const Int8Rows& X, int64_t M, int64_t K, const uint16_t
                          float* T, uint16_t* T2, float* part, hipStream_t st) {
   RankOut o{};
   o.sum = T; o.two = T2; o.s = s;
-  if (r <= kRankOnce) {
+  if (rank_once(K, r)) {
     RankJob g{X.codes, X.scale, (int)M, (int)K, A, r, 0, o};
     const int blocks = rank_blocks(g);
     rank_form(r, [&](auto rt) {
@@ -566,7 +571,7 @@ hipError_t launch_int8_T(const Int8Rows& X, int64_t M, int64_t K, const uint16_t
   return hipGetLastError();
 }
 // Bytes of fp32 sums that launch_int8_T needs room for.
-size_t int8_T_bytes(int64_t M, int64_t K, int r) { return r <= kRankOnce ? 0 : down_bytes(M, K, r); }
+size_t int8_T_bytes(int64_t M, int64_t K, int r) { return rank_once(K, r) ? 0 : down_bytes(M, K, r); }
 
 // T = sum over kTSplits slices of the contraction, without the row scale, for up
 // to 16 tokens: a workgroup per (16 ranks, slice), its waves' sums through LDS.
@@ -725,8 +730,9 @@ Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool
   p.off_up = up((size_t)M * r * 2);
   p.off_tp = p.off_up + up(pack);
   p.off_ds = p.off_tp + up(pack);
-  p.off_dt = p.off_ds + (r <= kRankOnce ? 0 : up(down_bytes(M, N, r)));
-  p.bytes = p.off_dt + (r <= kRankOnce ? 0 : up(down_bytes(M, K, r)));
+  p.once = rank_once(2 * N, r);
+  p.off_dt = p.off_ds + (p.once ? 0 : up(down_bytes(M, N, r)));
+  p.bytes = p.off_dt + (p.once ? 0 : up(down_bytes(M, K, r)));
   // An 8-bit base is read as it is stored up to kCodesMaxM tokens, and above on a
   // bf16 copy made once per call; an NF4 base is copied above kNF4MaxM tokens and
   // where no kernel decodes it on the way (256 does not divide N).
@@ -767,7 +773,7 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
   g.T = T;
   g.T_bf16 = T_bf16;
   NF4Weight wx = w;
-  const bool once = r <= kRankOnce;
+  const bool once = p.once;
   const int threads = once ? kRankWaves * 64 : 256;
   DownJob du{dY, (int)M, (int)N, B, r, 0, 0, 0, reinterpret_cast<float*>(base + p.off_ds)};
   DownJob dt{g.t.S, (int)M, (int)K, A, r, 0, 0, 0, reinterpret_cast<float*>(base + p.off_dt)};
@@ -821,7 +827,7 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
     constexpr int RT = decltype(rt)::value;
     hipLaunchKernelGGL(k_int8_grads<RT>, dim3(grads8_blocks<RT>(ga)), dim3(64 * kGradWaves8), 0, st, ga);
   };
-  if (once) rank_form(r, grads);
+  if (r <= kRankOnce) rank_form(r, grads);
   else grads(std::integral_constant<int, 4>());
   return hipGetLastError();
 }

@@ -398,7 +398,8 @@ struct Dx8Form {
   double alone, full;      // us of a step: in one workgroup; with one on every CU
 };
 // Fitted to 16 to 4000 tokens x 4096 x 4104, one to sixteen splits (all forms; the
-// fit is within 3 us of what was measured).  Fewer tokens a tile: the weight is
+// fit is within 3 us of what was measured); 32 splits for a few tokens of a long
+// contraction (4 x 128 x 22744: 19 us with 16, 11 with 32).  Fewer tokens a tile: the weight is
 // decoded or staged again for each tile row (512 tokens on codes unsplit: 48, 49 and
 // 66 us at 32, 64 and 128); more: too few workgroups (16 tokens: 40, 43, 61).
 static const Dx8Form kDx8Forms[] = {{nullptr, k_dx8_codes_32_r16, k_dx8_codes_32_r32, true, 32, 256, 2, 0.53, 0.58},
@@ -407,7 +408,7 @@ static const Dx8Form kDx8Forms[] = {{nullptr, k_dx8_codes_32_r16, k_dx8_codes_32
                                     {nullptr, k_dx8_bf16_64_r16, k_dx8_bf16_64_r32, false, 64, 256, 1, 0.45, 0.63},
                                     {k_dx8_bf16_128, nullptr, nullptr, false, 128, 512, 1, 0.55, 0.93},
                                     {k_dx8_bf16_256, nullptr, nullptr, false, 256, 512, 1, 1.08, 1.72}};
-constexpr int kDx8MaxSplits = 16;
+constexpr int kDx8MaxSplits = 32;
 
 // The form and split of the contraction with the least expected time: whole rounds of
 // workgroups and a last one whose steps take longer the more CUs it fills, and for a
@@ -427,7 +428,7 @@ Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes) {
       const int64_t wgs = tiles * splits, whole = wgs / kCUs, rest = wgs % kCUs;
       double us = 6.0 + len * (whole * F.full +
                                (rest ? F.alone + (F.full - F.alone) * rest / kCUs : 0.0));
-      if (splits > 1) us += 3.5 + (double)M * K * splits * 8.0 / 8e6;
+      if (splits > 1) us += 3.5 + 0.1 * splits + (double)M * K * splits * 8.0 / 8e6;
       if (p.form < 0 || us < best) {
         best = us;
         p.form = f;

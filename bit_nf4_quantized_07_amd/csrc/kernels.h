@@ -319,6 +319,7 @@ hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const
 // bf16 (w).  T in fp32 or bf16, or neither (computed again).
 constexpr int kBaseInt8 = 0, kBaseNF4 = 1, kBaseBF16 = 2;
 struct Int8BwdPlan {
+  bool once;         // U and T in one launch, without slices of the contraction
   bool copy;         // dX on a bf16 copy of the base at off_w
   bool any;          // by launch_dx8, else by launch_dx
   Dx8Plan dx8;

@@ -247,7 +247,7 @@ class _Layer:
         _assert_within(h.host(dB), refB, self.s * (np.abs(dY).T @ np.abs(T)) * n, what + "dB")
 
 
-LAYERS = [(1, 64, 8, 8), (1, 4096, 512, 16), (3, 2048, 136, 8), (16, 1024, 264, 16), (16, 512, 4104, 32), (7, 640, 72, 24), (2, 128, 24, 0), (5, 192, 40, 3), (16, 256, 256, 8),
+LAYERS = [(1, 64, 8, 8), (20, 32768, 40, 8), (40, 16448, 72, 32), (1, 4096, 512, 16), (3, 2048, 136, 8), (16, 1024, 264, 16), (16, 512, 4104, 32), (7, 640, 72, 24), (2, 128, 24, 0), (5, 192, 40, 3), (16, 256, 256, 8),
           (16, 832, 1000, 64), (16, 320, 4104, 256), (17, 64, 8, 8), (17, 256, 136, 16), (33, 448, 72, 24),
           (64, 1024, 520, 0), (100, 4096, 264, 12), (129, 512, 1032, 128), (257, 320, 776, 16),
           (300, 2048, 2056, 256), (700, 576, 1304, 40), (1030, 1152, 2824, 8)]
@@ -316,7 +316,7 @@ def test_forward_non_finite_rows():
         assert bool(Y[:, 6].isfinite().all())
 
 
-BWD = [(1, 64, 8, 8), (5, 192, 40, 3), (16, 256, 256, 8), (33, 448, 72, 24), (100, 1024, 264, 16),
+BWD = [(1, 64, 8, 8), (4, 128, 16648, 16), (70, 64, 8200, 24), (5, 192, 40, 3), (16, 256, 256, 8), (33, 448, 72, 24), (100, 1024, 264, 16),
        (129, 512, 1032, 128), (300, 320, 776, 256), (1030, 576, 512, 12)]
 
 
