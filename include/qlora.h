@@ -433,9 +433,9 @@ int int8_linear_fwd(const int8_t* Xcodes, const float* Xscale, int64_t M, int64_
  *   T  fp32 [M, r] as int8_linear_fwd gives it, or bf16 as the forwards of the
  *      other two bases do; NULL: computed again from the codes.
  * dA and dB are fp32 sums of exact products: U and T enter as three bf16 terms
- * (all 24 bits), the codes as they are, their scale in U's factor.  dX reads an
- * 8-bit base as a bf16 copy made once per call, each weight rounded once, as
- * the NF4 base's.  The order of every sum is fixed.
+ * (all 24 bits), the codes as they are, their scale in U's factor.  dX takes
+ * each weight of an 8-bit base rounded to bf16 once, as an NF4 base's.  The
+ * order of every sum is fixed.
  * Requires the sizes of int8_linear_fwd with 1 <= r, and 2 M K < 2^31; 2 N K <
  * 2^31 for an 8-bit or bf16 base; workspace of int8_linear_workspace_bytes(...,
  * base, 1). */

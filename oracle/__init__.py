@@ -49,6 +49,9 @@ Functions and what pins them (tests/test_oracle_*.py):
   adapters          one slot reduces to the single-adapter layer without its
                     base; differences of a scalar of the output against every
                     gradient; the plan's invariants
+  int8              nearest codes with ties to the even one against exact
+                    rational arithmetic; zero and non-finite rows; half a step;
+                    the gating's gradient against differences
 No function is "parity unpinned".
 """
 from .nf4 import (  # noqa: F401
