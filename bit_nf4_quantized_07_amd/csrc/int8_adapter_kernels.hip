@@ -634,9 +634,24 @@ struct PrepArgs {
   NF4Weight w;               // else an NF4 base, if packed is not null
   int64_t words;             // of 16 codes, or of 8 weights
   uint32_t k16;              // words of 16 codes in a row
-  uint16_t* copy;
+  uint16_t* copy;            // of the base, or
+  float* consts;             // an NF4 base's block constants [K / 64, N]
   Codebook4 cb;
 };
+
+// Block constants decoded, a thread per (block of a row, row), rows fastest.
+constexpr int kConstRounds = 4;
+__device__ __forceinline__ void prep_consts(const PrepArgs& g, int64_t blk) {
+  const float mean = g.w.mean[0];
+  const int64_t N = g.w.N, blocks = g.w.K / kBlock, i0 = blk * (blockDim.x * kConstRounds) + threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < kConstRounds; ++q) {
+    const int64_t i = i0 + q * blockDim.x;
+    if (i >= g.words) break;
+    const int64_t b = (i % N) * blocks + i / N;
+    g.consts[i] = absmax_decode(g.w.codes[b], g.w.scales[b / kDQBlock], mean);
+  }
+}
 
 // T's terms, a thread per (rank, eight tokens).
 __device__ __forceinline__ void pack_T(const PrepArgs& g, int64_t e) {
@@ -681,7 +696,8 @@ __device__ __forceinline__ void copy_int8(const PrepArgs& g, int64_t blk) {
 }
 
 __device__ __forceinline__ void prep_copy(const PrepArgs& g, int64_t blk, uint8_t* lds) {
-  if (g.wcodes) copy_int8(g, blk);
+  if (g.consts) prep_consts(g, blk);
+  else if (g.wcodes) copy_int8(g, blk);
   else nf4_dequant_block(g.w.packed, g.w.codes, g.w.scales, g.w.mean, g.words, g.cb, g.copy, blk,
                          reinterpret_cast<float*>(lds));
 }
@@ -718,10 +734,14 @@ __global__ void __launch_bounds__(64 * kGradWaves8) k_int8_grads(Grad8Args g) {
 // at 4096 x 4096, r = 16, read as stored and on a copy: 16 tokens 18 and 35 us, 300
 // tokens 36 and 46, 512 tokens 44 and 51; 700 tokens on a copy 58.
 constexpr int64_t kCodesMaxM = 512;
-// And up to which dX decodes an NF4 base on the way, a tile of 256 tokens: 200 tokens
-// x 4096 x 4096 40 us and 41 on a copy, 4096 x 11008 63 and 71; 300 tokens 50 and 45,
-// 90 and 80; 1000 tokens 95 and 65, 228 and 150.
+// And up to which launch_dx decodes an NF4 base on the way, a tile of 256 tokens: 200
+// tokens x 4096 x 4096 40 us and 41 on a copy, 4096 x 11008 63 and 71; 300 tokens 50
+// and 45, 90 and 80; 1000 tokens 95 and 65, 228 and 150.
 constexpr int64_t kNF4MaxM = 256;
+// And up to which launch_dx8 does (its tile against launch_dx's, 4096 x 4096: 16
+// tokens 22 and 32 us, 64 tokens 28 and 35, 200 tokens 39 and 39; against a copy, 4096
+// x 4104: 22 and 32, 29 and 31, 40 and 36).
+constexpr int64_t kNibblesMaxM = 128;
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Int8BwdPlan p{};
@@ -734,18 +754,24 @@ Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool
   p.off_dt = p.off_ds + (p.once ? 0 : up(down_bytes(M, N, r)));
   p.bytes = p.off_dt + (p.once ? 0 : up(down_bytes(M, K, r)));
   // An 8-bit base is read as it is stored up to kCodesMaxM tokens, and above on a
-  // bf16 copy made once per call; an NF4 base is copied above kNF4MaxM tokens and
-  // where no kernel decodes it on the way (256 does not divide N).
+  // bf16 copy made once per call.  An NF4 base is decoded by launch_dx8's tile up to
+  // kNibblesMaxM tokens, by launch_dx's up to kNF4MaxM where that has one (256
+  // divides N), and else read on a copy.
   const bool whole = dx_nf4_supported(N);
   const bool room = N * K * 2 < ((int64_t)1 << 31);
   if (dx && base == kBaseInt8) p.copy = M > kCodesMaxM;
-  if (dx && base == kBaseNF4) p.copy = room && (!whole || M > kNF4MaxM);
+  if (dx && base == kBaseNF4) {
+    p.consts = M <= kNibblesMaxM;
+    p.copy = !p.consts && room && (!whole || M > kNF4MaxM);
+  }
   p.off_w = p.bytes;
   if (p.copy) p.bytes += up((size_t)N * K * 2);
+  if (p.consts) p.bytes += up((size_t)N * (K / kBlock) * 4);
   p.off_part = p.bytes;
-  p.any = dx && (base == kBaseInt8 ? !p.copy || !whole : !whole && (p.copy || base == kBaseBF16));
+  p.any = dx && (base == kBaseInt8 ? !p.copy || !whole
+                                   : p.consts || (!whole && (p.copy || base == kBaseBF16)));
   if (p.any) {
-    p.dx8 = plan_dx8(M, K, N, base == kBaseInt8 && !p.copy);
+    p.dx8 = plan_dx8(M, K, N, p.consts ? kDxNF4 : base == kBaseInt8 && !p.copy ? kDxCodes : kDxBf16);
     p.bytes += up(p.dx8.bytes);
   } else if (dx && whole) {
     p.kz_len = dx_split_len(M, K, N);
@@ -796,6 +822,12 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
     }
     nc = (g.words + each - 1) / each;
   }
+  if (p.consts) {
+    g.w = w;
+    g.consts = reinterpret_cast<float*>(base + p.off_w);
+    g.words = N * (K / kBlock);
+    nc = (g.words + threads * kConstRounds - 1) / (threads * kConstRounds);
+  }
   const dim3 grid((unsigned)(g.nu + g.nt + nc));
   if (once) {
     rank_form(r, [&](auto rt) {
@@ -817,8 +849,11 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
   ga.M = (int)M; ga.r = r; ga.s = s;
   if (dX) {
     float* const part = reinterpret_cast<float*>(base + p.off_part);
-    e = p.any ? launch_dx8(dY, M, K, N, p.copy ? nullptr : W8, wx.bf16, U, A, r, s, dX, accumulate, part,
-                           p.dx8, ga, st)
+    const Codebook4 cb = nf4_codebook4();
+    const Dx8Base b8 = p.consts ? Dx8Base{w.packed, g.consts, cb.lv}
+                       : W8 && !p.copy ? Dx8Base{W8->codes, W8->scale, nullptr}
+                                       : Dx8Base{wx.bf16, nullptr, nullptr};
+    e = p.any ? launch_dx8(dY, M, K, N, b8, U, A, r, s, dX, accumulate, part, p.dx8, ga, st)
               : launch_dx(dY, M, wx, U, A, r, s, dX, accumulate, st, nullptr, 1.0f,
                           p.kz_len ? part : nullptr, p.kz_len, nullptr);
     if (e != hipSuccess || (p.any && p.dx8.grads)) return e;

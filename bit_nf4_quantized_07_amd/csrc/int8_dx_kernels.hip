@@ -1,5 +1,5 @@
 // Input gradient of the linear layer for any number of outputs (8 | N), on a base in
-// 8-bit rows as it is stored or on a bf16 one:
+// 8-bit rows or NF4 as it is stored or on a bf16 one:
 //
 //   dX[m][k] = sum_n dY[m][n] w_hat[n][k] + s sum_j U[m][j] A[j][k]
 //                       (llm-compass "QLoRA", 方法与公式, the equation,
@@ -18,6 +18,13 @@
 //    copy is most of the work: without it the backward of 16 tokens x 4096 x 4096
 //    takes 18 us, with it 35.  Above 512 tokens decoding once for all of them costs
 //    less (kCodesMaxM).
+//  * NF4 weight: rows n of 32 WN bytes, pieces XOR-swizzled by n & 6; one transposing
+//    read gives eight rows of 32 bytes' columns, whose high nibbles are the operand of
+//    the even features and whose low ones that of the odd (so a lane's sums are eight
+//    features in a row).  A weight is bf16(level[nibble] constant), the value of the
+//    base's own backward; levels from LDS (16 of them, in different banks), the block
+//    constants [K / 64, N] decoded in the launch before.  That lookup, a read per
+//    weight, is what the step waits for (1.3 us, codes 0.8).
 // Where N ends inside a step, both operands past it are zero.  A split contraction's
 // fp32 sums go to the workspace and are added in a fixed order.
 //
@@ -41,8 +48,9 @@ constexpr int kDxStep = 64;     // outputs per step
 struct Dx8Args {
   const uint16_t* dY;   // [M, N]
   int M, N, K;
-  const void* W;        // [N, K] codes or bf16
-  const float* sw;      // codes' row scales
+  const void* W;        // [N, K] bf16, codes or packed nibbles
+  const float* sw;      // codes' row scales, or the nibbles' block constants [K / 64, N]
+  float lv[16];         // the nibbles' levels
   const uint16_t* U;    // [M, r] bf16
   const uint16_t* A;    // [r, K]
   int r;
@@ -74,19 +82,24 @@ __device__ __forceinline__ bf16x8_t scaled_codes(i32x2_t v, const float (&s)[8])
 
 // The stages are arrays of their own (of one array the compiler would wait for every
 // load before each read).
-template <bool W8, int NI, int WM, int WN, int S>
+constexpr int dx8_row(int base, int features) {   // bytes of a weight row's features
+  return base == kDxBf16 ? 2 * features : base == kDxCodes ? features : features / 2;
+}
+template <int BASE, int NI, int WM, int WN, int S>
 struct Dx8Lds {
-  static constexpr int Y = 32 * NI * WM * 128, W = 64 * 64 * WN * (W8 ? 1 : 2), C = W8 ? 64 : 4;
+  static constexpr int Y = 32 * NI * WM * 128, W = 64 * dx8_row(BASE, 64 * WN);
+  static constexpr int C = BASE == kDxNF4 ? 64 * WN : BASE == kDxCodes ? 64 : 4;
   static constexpr int Y2 = S == 3 ? Y : 16, W2 = S == 3 ? W : 16;
 };
 
-template <bool W8, int NI, int WM, int WN, int S>
+template <int BASE, int NI, int WM, int WN, int S>
 __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t* w0, float* s0, uint8_t* y1,
-                                         uint8_t* w1, float* s1, uint8_t* y2, uint8_t* w2, float* s2) {
+                                         uint8_t* w1, float* s1, uint8_t* y2, uint8_t* w2, float* s2, float* lv) {
   constexpr int NJ = 2, TM = 32 * NI * WM, TF = 64 * WN, NW = WM * WN;
-  constexpr int RB = TF * (W8 ? 1 : 2), RP = RB / 16;      // bytes and pieces of a weight row
+  constexpr bool W8 = BASE == kDxCodes, W4 = BASE == kDxNF4;
+  constexpr int RB = dx8_row(BASE, TF), RP = RB / 16;      // bytes and pieces of a weight row
   constexpr int YL = TM / 8 / NW, WL = RB / 16 / NW;       // a wave's loads of a step (1 KB each)
-  constexpr int L = YL + WL + (W8 ? 1 : 0);                // and its 64 scales
+  constexpr int L = YL + WL + (W8 || W4 ? 1 : 0);          // and 64 scales
   constexpr int YB = TM * 128, WB = 64 * RB;
   static_assert(YL * NW * 8 == TM && WL * NW * 16 == RB, "whole loads");
   static_assert(S == 2 || S == 3, "stages");
@@ -114,10 +127,10 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
   // physical piece l % 8.  Weight: load i of wave w fills the rows of pieces
   // 64 (WL w + i) .. +63.
   const __amdgpu_buffer_rsrc_t ry = rsrc_whole(g.dY, (uint32_t)((int64_t)g.M * g.N * 2));
-  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K * (W8 ? 1 : 2)));
-  const __amdgpu_buffer_rsrc_t rsw = rsrc_whole(g.sw, W8 ? (uint32_t)g.N * 4 : 0);
+  const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * dx8_row(BASE, g.K)));
+  const __amdgpu_buffer_rsrc_t rsw = rsrc_whole(g.sw, W8 ? (uint32_t)g.N * 4 : W4 ? (uint32_t)g.N * (g.K / 64) * 4 : 0);
   auto yswz = [](int row) { return (row >> 1) & 7; };
-  auto wswz = [](int row) { return W8 ? 2 * (row & 7) : 4 * (row & 3); };
+  auto wswz = [](int row) { return W4 ? row & 6 : W8 ? 2 * (row & 7) : 4 * (row & 3); };
   uint32_t yoff[YL], ycut[YL], woff[WL], wcut[WL];
 #pragma unroll
   for (int i = 0; i < YL; ++i) {
@@ -129,12 +142,14 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
 #pragma unroll
   for (int i = 0; i < WL; ++i) {
     const int p = 64 * (WL * wave + i) + lane, row = p / RP;
-    const int col = k0 + ((p % RP) ^ wswz(row)) * (W8 ? 16 : 8);
-    woff[i] = col < g.K ? (uint32_t)(((int64_t)row * g.K + col) * (W8 ? 1 : 2)) : kOOB;
+    const int col = k0 + ((p % RP) ^ wswz(row)) * (W4 ? 32 : W8 ? 16 : 8);
+    woff[i] = col < g.K ? (uint32_t)((int64_t)row * dx8_row(BASE, g.K) + dx8_row(BASE, col)) : kOOB;
     wcut[i] = row < left ? woff[i] : kOOB;
   }
-  const uint32_t soff = 4 * lane, scut = lane < left ? 4 * lane : kOOB;
-  const uint32_t wstep = (uint32_t)kDxStep * g.K * (W8 ? 1 : 2);
+  const int kblk = k0 / 64 + wave;                         // W4: the wave's blocks
+  const uint32_t soff = !W4 ? 4 * lane : kblk < g.K / 64 ? (uint32_t)(kblk * g.N + lane) * 4 : kOOB;
+  const uint32_t scut = lane < left ? soff : kOOB;
+  const uint32_t wstep = (uint32_t)kDxStep * dx8_row(BASE, g.K);
   typedef __attribute__((address_space(3))) void* lds_ptr;
   auto load_l = [&](int l, int buf, int kb) {
     const uint32_t k = (uint32_t)__builtin_amdgcn_readfirstlane(kb);
@@ -145,8 +160,9 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
     else if (l < YL + WL)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr)(wb(buf) + 1024 * (WL * wave + l - YL)), 16,
                                                end ? wcut[l - YL] : woff[l - YL], k * wstep, 0, 0);
-    else   // every wave the same 64
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_ptr)sb(buf), 4, end ? scut : soff, k * 256, 0, 0);
+    else   // codes: every wave the same 64
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (lds_ptr)(sb(buf) + (W4 ? 64 * wave : 0)), 4,
+                                               end ? scut : soff, k * 256, 0, 0);
   };
   int yrd[4];
 #pragma unroll
@@ -159,13 +175,13 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
   int wrd[2];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const int n = W8 ? 8 * (grp >> 1) + (gi >> 1) : 8 * (grp >> 1) + 4 * half + (gi >> 2);
-    const int p = W8 ? 4 * fg + (grp & 1) : 8 * fg + 2 * (grp & 1) + ((gi & 3) >> 1);
+    const int n = W8 || W4 ? 8 * (grp >> 1) + (gi >> 1) : 8 * (grp >> 1) + 4 * half + (gi >> 2);
+    const int p = W4 ? 2 * fg + (grp & 1) : W8 ? 4 * fg + (grp & 1) : 8 * fg + 2 * (grp & 1) + ((gi & 3) >> 1);
     wrd[half] = n * RB + ((p ^ wswz(n)) * 16) + 8 * (gi & 1);
   }
   auto wraw = [&](int buf, int j, int t) -> i32x2_t {
     return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-        (lds_i32x2_ptr)(wb(buf) + 16 * RB * t + (wrd[0] ^ (32 * j))));
+        (lds_i32x2_ptr)(wb(buf) + 16 * RB * t + (W4 ? wrd[0] : wrd[0] ^ (32 * j))));
   };
   auto wfrag = [&](int buf, int j, int t) -> bf16x8_t {
     const uint16_t* const base = reinterpret_cast<const uint16_t*>(wb(buf) + 16 * RB * t);
@@ -193,11 +209,13 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       if constexpr (W8) q[j] = wraw(buf, j, t);
-      else a[t & 1][j] = wfrag(buf, j, t);
+      else if constexpr (!W4) a[t & 1][j] = wfrag(buf, j, t);
     }
-    if constexpr (W8) {
-      const float4 lo = *reinterpret_cast<const float4*>(sb(buf) + 16 * t + 8 * h);
-      const float4 hi = *reinterpret_cast<const float4*>(sb(buf) + 16 * t + 8 * h + 4);
+    if constexpr (W4) q[0] = wraw(buf, 0, t);
+    if constexpr (W8 || W4) {
+      const float* const s = sb(buf) + (W4 ? 64 * fg : 0) + 16 * t + 8 * h;
+      const float4 lo = *reinterpret_cast<const float4*>(s);
+      const float4 hi = *reinterpret_cast<const float4*>(s + 4);
       sv[0] = lo.x; sv[1] = lo.y; sv[2] = lo.z; sv[3] = lo.w;
       sv[4] = hi.x; sv[5] = hi.y; sv[6] = hi.z; sv[7] = hi.w;
     }
@@ -206,7 +224,28 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
     if constexpr (W8)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) a[t & 1][j] = scaled_codes(q[j], sv);
+    if constexpr (W4) {
+      uint32_t o[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {                        // rows 2 e and 2 e + 1
+        const uint32_t b = (uint32_t)q[0][e >> 1] >> (16 * (e & 1));
+        o[0][e] = pack_bf16x2(lv[b >> 4 & 15] * sv[2 * e], lv[b >> 12 & 15] * sv[2 * e + 1]);
+        o[1][e] = pack_bf16x2(lv[b & 15] * sv[2 * e], lv[b >> 8 & 15] * sv[2 * e + 1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        a[t & 1][j] = __builtin_bit_cast(bf16x8_t, make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
+    }
   };
+  if constexpr (W4) {
+    if (tid < 16) {
+      float v = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v = tid == e ? g.lv[e] : v;   // no dynamic index
+      lv[tid] = v;
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -273,7 +312,7 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int kf = kw + 32 * j + c;
+        const int kf = W4 ? kw + 2 * c + j : kw + 32 * j + c;
         float av[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -289,70 +328,105 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
 
   // Accumulator [j][i]: lane holds token mw + 32 i + c and features
   // kw + 32 j + 8 (v / 4) + 4 h + (v % 4).
-  if (g.kz_len) {
-    float* const part = g.part + (int64_t)z * g.M * g.K;
+  // (W4: blocks j = 0, 1 are the even and the odd features: 16 (v / 4) + 8 h + 2 (v % 4) + j.)
+  if constexpr (W4) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int m = mw + 32 * i + c;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int v = 0; v < 4; ++v) {
+        const int k = kw + 16 * v + 8 * h;
+        if (m >= g.M || k >= g.K) continue;
+        float x[8];
 #pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = acc[e & 1][i][4 * v + (e >> 1)];
+        const int64_t at = (int64_t)m * g.K + k;
+        if (g.kz_len) {
+          float4* const part = reinterpret_cast<float4*>(g.part + (int64_t)z * g.M * g.K + at);
+          part[0] = make_float4(x[0], x[1], x[2], x[3]);
+          part[1] = make_float4(x[4], x[5], x[6], x[7]);
+          continue;
+        }
+        uint4* const out = reinterpret_cast<uint4*>(g.dX + at);
+        if (g.accumulate) {
+          const uint4 old = *out;
+          const uint32_t ow[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] += bf16_to_f32(ow[e] & 0xffffu);
+            x[2 * e + 1] += bf16_to_f32(ow[e] >> 16);
+          }
+        }
+        *out = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                          pack_bf16x2(x[6], x[7]));
+      }
+    }
+  } else {
+    if (g.kz_len) {
+      float* const part = g.part + (int64_t)z * g.M * g.K;
+  #pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int m = mw + 32 * i + c;
+  #pragma unroll
+        for (int j = 0; j < NJ; ++j)
+  #pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int k = kw + 32 * j + 8 * v + 4 * h;
+            if (m < g.M && k < g.K)
+              *reinterpret_cast<float4*>(part + (int64_t)m * g.K + k) =
+                  make_float4(acc[j][i][4 * v], acc[j][i][4 * v + 1], acc[j][i][4 * v + 2],
+                              acc[j][i][4 * v + 3]);
+          }
+      }
+      return;
+    }
+    // Old values are added here, then the tile goes out as bf16 rows of 2 TF bytes
+    // through the stages, 32 tokens (a block) at a time in place of whole stages, the
+    // 16-byte pieces of a row XOR-swizzled by its number.
+    constexpr int BB = 32 * 2 * TF, PR = TF / 8;             // bytes of a block, pieces of a row
+    constexpr int WBL = WB / BB, BLOCKS = NI * WM;           // blocks in a weight stage
+    static_assert(WBL >= 1 && BLOCKS <= S * (WBL + YB / BB), "blocks");
+    auto ob = [&](int k) -> uint8_t* {
+      const int n = k / WBL;
+      if (n < S) return wb(n) + (k % WBL) * BB;
+      const int y = k - S * WBL, per = YB / BB > 0 ? YB / BB : 1;
+      return yb(y / per) + (y % per) * BB;
+    };
+  #pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      uint8_t* const row = ob(NI * tq + i) + c * (2 * TF);
+      const int m = mw + 32 * i + c;
+  #pragma unroll
+      for (int j = 0; j < NJ; ++j)
+  #pragma unroll
         for (int v = 0; v < 4; ++v) {
+          float x[4];
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = acc[j][i][4 * v + e];
           const int k = kw + 32 * j + 8 * v + 4 * h;
-          if (m < g.M && k < g.K)
-            *reinterpret_cast<float4*>(part + (int64_t)m * g.K + k) =
-                make_float4(acc[j][i][4 * v], acc[j][i][4 * v + 1], acc[j][i][4 * v + 2],
-                            acc[j][i][4 * v + 3]);
+          if (g.accumulate && m < g.M && k < g.K) {
+            const uint2 old = *reinterpret_cast<const uint2*>(g.dX + (int64_t)m * g.K + k);
+            x[0] += bf16_to_f32(old.x & 0xffffu);
+            x[1] += bf16_to_f32(old.x >> 16);
+            x[2] += bf16_to_f32(old.y & 0xffffu);
+            x[3] += bf16_to_f32(old.y >> 16);
+          }
+          const int piece = (8 * fg + 4 * j + v) ^ (c & (PR - 1));
+          *reinterpret_cast<uint2*>(row + 16 * piece + 8 * h) =
+              make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         }
     }
-    return;
-  }
-  // Old values are added here, then the tile goes out as bf16 rows of 2 TF bytes
-  // through the stages, 32 tokens (a block) at a time in place of whole stages, the
-  // 16-byte pieces of a row XOR-swizzled by its number.
-  constexpr int BB = 32 * 2 * TF, PR = TF / 8;             // bytes of a block, pieces of a row
-  constexpr int WBL = WB / BB, BLOCKS = NI * WM;           // blocks in a weight stage
-  static_assert(WBL >= 1 && BLOCKS <= S * (WBL + YB / BB), "blocks");
-  auto ob = [&](int k) -> uint8_t* {
-    const int n = k / WBL;
-    if (n < S) return wb(n) + (k % WBL) * BB;
-    const int y = k - S * WBL, per = YB / BB > 0 ? YB / BB : 1;
-    return yb(y / per) + (y % per) * BB;
-  };
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    uint8_t* const row = ob(NI * tq + i) + c * (2 * TF);
-    const int m = mw + 32 * i + c;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = acc[j][i][4 * v + e];
-        const int k = kw + 32 * j + 8 * v + 4 * h;
-        if (g.accumulate && m < g.M && k < g.K) {
-          const uint2 old = *reinterpret_cast<const uint2*>(g.dX + (int64_t)m * g.K + k);
-          x[0] += bf16_to_f32(old.x & 0xffffu);
-          x[1] += bf16_to_f32(old.x >> 16);
-          x[2] += bf16_to_f32(old.y & 0xffffu);
-          x[3] += bf16_to_f32(old.y >> 16);
-        }
-        const int piece = (8 * fg + 4 * j + v) ^ (c & (PR - 1));
-        *reinterpret_cast<uint2*>(row + 16 * piece + 8 * h) =
-            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-      }
-  }
-  __syncthreads();
-  constexpr int RW = 64 * NW / PR;                         // rows that a pass stores
-  const int prow = tid / PR, pp = tid % PR;
-#pragma unroll
-  for (int e = 0; e < TM / RW; ++e) {
-    const int row = RW * e + prow, rl = row & 31;          // RW divides 32
-    const uint4 v = *reinterpret_cast<const uint4*>(ob(RW * e / 32) + rl * (2 * TF) +
-                                                    16 * (pp ^ (rl & (PR - 1))));
-    const int m = m0 + row, k = k0 + 8 * pp;
-    if (m < g.M && k < g.K) *reinterpret_cast<uint4*>(g.dX + (int64_t)m * g.K + k) = v;
+    __syncthreads();
+    constexpr int RW = 64 * NW / PR;                         // rows that a pass stores
+    const int prow = tid / PR, pp = tid % PR;
+  #pragma unroll
+    for (int e = 0; e < TM / RW; ++e) {
+      const int row = RW * e + prow, rl = row & 31;          // RW divides 32
+      const uint4 v = *reinterpret_cast<const uint4*>(ob(RW * e / 32) + rl * (2 * TF) +
+                                                      16 * (pp ^ (rl & (PR - 1))));
+      const int m = m0 + row, k = k0 + 8 * pp;
+      if (m < g.M && k < g.K) *reinterpret_cast<uint4*>(g.dX + (int64_t)m * g.K + k) = v;
+    }
   }
 }
 
@@ -365,35 +439,40 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
   typedef Dx8Lds<__VA_ARGS__> L;                                                         \
   __shared__ __attribute__((aligned(16))) uint8_t y0[L::Y], w0[L::W], y1[L::Y], w1[L::W]; \
   __shared__ __attribute__((aligned(16))) uint8_t y2[L::Y2], w2[L::W2];                  \
-  __shared__ __attribute__((aligned(16))) float s0[L::C], s1[L::C], s2[L::C]
+  __shared__ __attribute__((aligned(16))) float s0[L::C], s1[L::C], s2[L::C], lv[16]
 #define QLK_DX8_KERNEL(name, threads, ...)                                               \
   __global__ void __launch_bounds__(threads) name(Dx8Args g) {                           \
     QLK_DX8_LDS(__VA_ARGS__);                                                            \
-    dx8_tile<__VA_ARGS__>(g, y0, w0, s0, y1, w1, s1, y2, w2, s2);                        \
+    dx8_tile<__VA_ARGS__>(g, y0, w0, s0, y1, w1, s1, y2, w2, s2, lv);                        \
   }
 #define QLK_DX8_GRADS_KERNEL(name, RT, ...)                                              \
   __global__ void __launch_bounds__(256) name(Dx8Args g, Grad8Args ga) {                 \
     QLK_DX8_LDS(__VA_ARGS__);                                                            \
-    static_assert(grads8_lds<RT>() <= L::W && kGradWaves8 == 4, "room");                 \
-    if ((int)blockIdx.x < g.blocks) dx8_tile<__VA_ARGS__>(g, y0, w0, s0, y1, w1, s1, y2, w2, s2); \
-    else grads8_block<RT>(ga, (int)blockIdx.x - g.blocks, w0);                           \
+    __shared__ __attribute__((aligned(16))) uint8_t gl[grads8_lds<RT>() <= L::W ? 16 : grads8_lds<RT>()]; \
+    static_assert(kGradWaves8 == 4, "waves");                 \
+    if ((int)blockIdx.x < g.blocks) dx8_tile<__VA_ARGS__>(g, y0, w0, s0, y1, w1, s1, y2, w2, s2, lv); \
+    else grads8_block<RT>(ga, (int)blockIdx.x - g.blocks, grads8_lds<RT>() <= L::W ? w0 : gl);                           \
   }
-QLK_DX8_GRADS_KERNEL(k_dx8_codes_32_r16, 1, true, 1, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_codes_32_r32, 2, true, 1, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_codes_64_r16, 1, true, 2, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_codes_64_r32, 2, true, 2, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_codes_128_r16, 1, true, 4, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_codes_128_r32, 2, true, 4, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_bf16_64_r16, 1, false, 2, 1, 4, 3)
-QLK_DX8_GRADS_KERNEL(k_dx8_bf16_64_r32, 2, false, 2, 1, 4, 3)
-QLK_DX8_KERNEL(k_dx8_bf16_128, 512, false, 2, 2, 4, 3)
-QLK_DX8_KERNEL(k_dx8_bf16_256, 512, false, 4, 2, 4, 2)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_32_r16, 1, kDxCodes, 1, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_32_r32, 2, kDxCodes, 1, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_64_r16, 1, kDxCodes, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_64_r32, 2, kDxCodes, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_128_r16, 1, kDxCodes, 4, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_codes_128_r32, 2, kDxCodes, 4, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_bf16_64_r16, 1, kDxBf16, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_bf16_64_r32, 2, kDxBf16, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_nf4_32_r16, 1, kDxNF4, 1, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_nf4_32_r32, 2, kDxNF4, 1, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_nf4_64_r16, 1, kDxNF4, 2, 1, 4, 3)
+QLK_DX8_GRADS_KERNEL(k_dx8_nf4_64_r32, 2, kDxNF4, 2, 1, 4, 3)
+QLK_DX8_KERNEL(k_dx8_bf16_128, 512, kDxBf16, 2, 2, 4, 3)
+QLK_DX8_KERNEL(k_dx8_bf16_256, 512, kDxBf16, 4, 2, 4, 2)
 
 struct Dx8Form {
   void (*kernel)(Dx8Args);                      // or, with the gradients,
   void (*r16)(Dx8Args, Grad8Args);              // of up to 16 ranks,
   void (*r32)(Dx8Args, Grad8Args);              // of 32 at a time
-  bool codes;
+  int base;
   int tm, threads, per_cu;
   double alone, full;      // us of a step: in one workgroup; with one on every CU
 };
@@ -402,25 +481,27 @@ struct Dx8Form {
 // contraction (4 x 128 x 22744: 19 us with 16, 11 with 32).  Fewer tokens a tile: the weight is
 // decoded or staged again for each tile row (512 tokens on codes unsplit: 48, 49 and
 // 66 us at 32, 64 and 128); more: too few workgroups (16 tokens: 40, 43, 61).
-static const Dx8Form kDx8Forms[] = {{nullptr, k_dx8_codes_32_r16, k_dx8_codes_32_r32, true, 32, 256, 2, 0.53, 0.58},
-                                    {nullptr, k_dx8_codes_64_r16, k_dx8_codes_64_r32, true, 64, 256, 2, 0.58, 0.83},
-                                    {nullptr, k_dx8_codes_128_r16, k_dx8_codes_128_r32, true, 128, 256, 1, 0.86, 1.45},
-                                    {nullptr, k_dx8_bf16_64_r16, k_dx8_bf16_64_r32, false, 64, 256, 1, 0.45, 0.63},
-                                    {k_dx8_bf16_128, nullptr, nullptr, false, 128, 512, 1, 0.55, 0.93},
-                                    {k_dx8_bf16_256, nullptr, nullptr, false, 256, 512, 1, 1.08, 1.72}};
+static const Dx8Form kDx8Forms[] = {{nullptr, k_dx8_codes_32_r16, k_dx8_codes_32_r32, kDxCodes, 32, 256, 2, 0.53, 0.58},
+                                    {nullptr, k_dx8_codes_64_r16, k_dx8_codes_64_r32, kDxCodes, 64, 256, 2, 0.58, 0.83},
+                                    {nullptr, k_dx8_codes_128_r16, k_dx8_codes_128_r32, kDxCodes, 128, 256, 1, 0.86, 1.45},
+                                    {nullptr, k_dx8_bf16_64_r16, k_dx8_bf16_64_r32, kDxBf16, 64, 256, 1, 0.45, 0.63},
+                                    {nullptr, k_dx8_nf4_32_r16, k_dx8_nf4_32_r32, kDxNF4, 32, 256, 2, 0.90, 1.30},
+                                    {nullptr, k_dx8_nf4_64_r16, k_dx8_nf4_64_r32, kDxNF4, 64, 256, 2, 0.90, 1.30},
+                                    {k_dx8_bf16_128, nullptr, nullptr, kDxBf16, 128, 512, 1, 0.55, 0.93},
+                                    {k_dx8_bf16_256, nullptr, nullptr, kDxBf16, 256, 512, 1, 1.08, 1.72}};
 constexpr int kDx8MaxSplits = 32;
 
 // The form and split of the contraction with the least expected time: whole rounds of
 // workgroups and a last one whose steps take longer the more CUs it fills, and for a
 // split the partial sums' way out and back and the reduction's launch.
-Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes) {
+Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, int base) {
   Dx8Plan p{};
   p.form = -1;
   const int64_t steps = (N + kDxStep - 1) / kDxStep;
   double best = 0.0;
   for (int f = 0; f < (int)(sizeof(kDx8Forms) / sizeof(kDx8Forms[0])); ++f) {
     const Dx8Form& F = kDx8Forms[f];
-    if (F.codes != codes) continue;
+    if (F.base != base) continue;
     const int64_t tiles = ((M + F.tm - 1) / F.tm) * ((K + 255) / 256);
     for (int splits = 1; splits <= kDx8MaxSplits; ++splits) {
       if (splits > 1 && (tiles * splits > F.per_cu * kCUs || steps / splits < 3)) break;
@@ -442,20 +523,22 @@ Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes) {
   return p;
 }
 
-hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Int8Rows* W8,
-                      const uint16_t* W, const uint16_t* U, const uint16_t* A, int r, float s,
+hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Dx8Base& W,
+                      const uint16_t* U, const uint16_t* A, int r, float s,
                       uint16_t* dX, bool accumulate, float* part, const Dx8Plan& p, Grad8Args& ga,
                       hipStream_t st) {
   const Dx8Form& F = kDx8Forms[p.form];
   Dx8Args g{};
   g.dY = dY; g.M = (int)M; g.N = (int)N; g.K = (int)K;
-  g.W = W8 ? (const void*)W8->codes : (const void*)W;
-  g.sw = W8 ? W8->scale : nullptr;
+  g.W = W.weight;
+  g.sw = W.scale;
+  if (F.base == kDxNF4)
+    for (int i = 0; i < 16; ++i) g.lv[i] = W.levels[i];
   g.U = U; g.A = A; g.r = r; g.s = s; g.dX = dX;
   g.accumulate = accumulate ? 1 : 0;
   g.tiles_m = (int)((M + F.tm - 1) / F.tm);
   g.tiles_k = (int)((K + 255) / 256);
-  g.group_m = group_for(g.tiles_m, g.tiles_k, F.tm * N * 2.0, 256.0 * N * (W8 ? 1 : 2));
+  g.group_m = group_for(g.tiles_m, g.tiles_k, F.tm * N * 2.0, (double)N * dx8_row(F.base, 256));
   g.part = part;
   g.kz_len = p.kz_len;
   g.blocks = (int)((int64_t)g.tiles_m * g.tiles_k * p.splits);

@@ -302,17 +302,23 @@ Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r);
 hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int64_t N, int64_t K,
                            const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* Y,
                            float* T_out, void* ws, const Int8FwdPlan& plan, hipStream_t st);
-// dX (+)= dY W_hat + s U A for any N (8 | N) on a base in 8-bit rows (W8) or a bf16
-// one (W); part: plan.bytes of room.
+// dX (+)= dY W_hat + s U A for any N (8 | N) on a bf16 base, one in 8-bit rows or an
+// NF4 one (its block constants decoded, [K / 64, N]); part: plan.bytes of room.
+constexpr int kDxBf16 = 0, kDxCodes = 1, kDxNF4 = 2;
+struct Dx8Base {
+  const void* weight;
+  const float* scale;
+  const float* levels;   // NF4's
+};
 struct Dx8Plan {
   int form, kz_len, splits;
   bool grads;        // the launch computes dA and dB too
   size_t bytes;
 };
 struct Grad8Args;
-Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, bool codes);
-hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Int8Rows* W8,
-                      const uint16_t* W, const uint16_t* U, const uint16_t* A, int r, float s,
+Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, int base);
+hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Dx8Base& W,
+                      const uint16_t* U, const uint16_t* A, int r, float s,
                       uint16_t* dX, bool accumulate, float* part, const Dx8Plan& plan, Grad8Args& grads,
                       hipStream_t st);
 // Backward from X in 8-bit rows on a base in 8-bit rows (W8 not null), NF4 or
@@ -321,6 +327,7 @@ constexpr int kBaseInt8 = 0, kBaseNF4 = 1, kBaseBF16 = 2;
 struct Int8BwdPlan {
   bool once;         // U and T in one launch, without slices of the contraction
   bool copy;         // dX on a bf16 copy of the base at off_w
+  bool consts;       // dX on an NF4 base with its block constants decoded at off_w
   bool any;          // by launch_dx8, else by launch_dx
   Dx8Plan dx8;
   int kz_len;        // launch_dx's split

@@ -373,7 +373,7 @@ def test_backward_nf4_and_bf16_base(M, K, N, r):
     _assert_within(h.host_bf16_f64(dX), ref, np.abs(ref) * BF + tol * (1 + BF), "bf16: dX")
 
 
-DX = [(1, 64, 8), (3, 4096, 4104), (16, 8192, 1000), (40, 320, 72), (100, 2048, 2056), (130, 4160, 520),
+DX = [(1, 64, 8), (3, 4096, 4104), (16, 8192, 1000), (40, 320, 72), (100, 2048, 2056), (130, 4160, 520), (7, 1088, 4096), (100, 2112, 512), (128, 64, 768),
       (257, 1088, 4096), (300, 4096, 1544), (512, 11008, 264), (511, 576, 8200), (513, 320, 72), (700, 2112, 776),
       (1100, 4096, 1032), (2100, 4160, 328), (4100, 4096, 200)]
 
