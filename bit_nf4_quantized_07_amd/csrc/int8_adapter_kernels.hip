@@ -739,8 +739,8 @@ constexpr int64_t kCodesMaxM = 512;
 // and 45, 90 and 80; 1000 tokens 95 and 65, 228 and 150.
 constexpr int64_t kNF4MaxM = 256;
 // And up to which launch_dx8 does (its tile against launch_dx's, 4096 x 4096: 16
-// tokens 22 and 32 us, 64 tokens 28 and 35, 200 tokens 39 and 39; against a copy, 4096
-// x 4104: 22 and 32, 29 and 31, 40 and 36).
+// tokens 20 and 32 us, 64 tokens 28 and 35, 200 tokens 39 and 39; against a copy, 4096
+// x 4104: 21 and 32, 29 and 31, 40 and 36).
 constexpr int64_t kNibblesMaxM = 128;
 Int8BwdPlan plan_int8_bwd(int64_t M, int64_t K, int64_t N, int r, int base, bool dx) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
