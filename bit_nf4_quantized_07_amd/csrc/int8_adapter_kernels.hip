@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(kRankWaves * 64) k_int8_T(RankJob g) {
 
 // ---------------------------------------------------------------------------
 // The same products above 32 ranks, where a workgroup that reads all of W for 16
-// rows reads it too often (U, 4001 tokens x 4096, rank 64: 25 us).  A workgroup
+// rows reads it too often (U, 4001 tokens x 4096, rank 64: 25 us), and for long rows
+// at fewer (rank_once).  A workgroup
 // takes 64 rows, 64 ranks and one of `zs` slices of the contraction; its four waves
 // take 32 rows x 32 ranks each (v_mfma_f32_32x32x16_bf16).  The contraction
 // advances 64 columns a step through four LDS stages that buffer loads fill three
@@ -618,8 +619,8 @@ hipError_t launch_int8_T_partial(const int8_t* X, int64_t M, int64_t K, const ui
 // ---------------------------------------------------------------------------
 // What the backward's products need first, in one launch whose workgroups do one
 // thing each: U = dY B (the dX product's operand, and sx U's terms), T's terms
-// (from T, or T computed again), and the bf16 copy of the base for dX.  U alone
-// waits for memory most of its time and the copy is bound by it: side by side they
+// (from T, or T computed again), and the bf16 copy of the base for dX, or an NF4
+// base's block constants.  U alone waits for memory most of its time and the copy is bound by it: side by side they
 // take little more than the longer one.
 struct PrepArgs {
   RankJob u;
@@ -632,7 +633,7 @@ struct PrepArgs {
   const int8_t* wcodes;      // an 8-bit base, or null
   const float* wscale;
   NF4Weight w;               // else an NF4 base, if packed is not null
-  int64_t words;             // of 16 codes, or of 8 weights
+  int64_t words;             // of 16 codes, or of 8 weights, or block constants
   uint32_t k16;              // words of 16 codes in a row
   uint16_t* copy;            // of the base, or
   float* consts;             // an NF4 base's block constants [K / 64, N]

@@ -80,11 +80,11 @@ __device__ __forceinline__ bf16x8_t scaled_codes(i32x2_t v, const float (&s)[8])
   return __builtin_bit_cast(bf16x8_t, make_uint4(o[0], o[1], o[2], o[3]));
 }
 
-// The stages are arrays of their own (of one array the compiler would wait for every
-// load before each read).
 constexpr int dx8_row(int base, int features) {   // bytes of a weight row's features
   return base == kDxBf16 ? 2 * features : base == kDxCodes ? features : features / 2;
 }
+// The stages are arrays of their own (of one array the compiler would wait for every
+// load before each read).
 template <int BASE, int NI, int WM, int WN, int S>
 struct Dx8Lds {
   static constexpr int Y = 32 * NI * WM * 128, W = 64 * dx8_row(BASE, 64 * WN);

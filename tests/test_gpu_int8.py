@@ -438,6 +438,36 @@ def test_backward_non_finite_rows(M, N):
     assert bool(gX.isnan().all()) and t.equal(gA, dA) and t.equal(gB, dB)
 
 
+@pytest.mark.parametrize("base,K,N", [("int8", 32768, 32760), ("nf4", 65536, 65528)])
+def test_input_gradient_of_the_largest_bases(base, K, N):
+    """Weights just under the size limits, against sampled features."""
+    q, t = _q(), h.torch()
+    if t.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of free memory")
+    M, r = 9, 8
+    g = t.Generator("cuda")
+    g.manual_seed(K)
+    W0 = t.empty(N, K, device="cuda").normal_(std=0.02, generator=g)
+    cols = [0, 63, 64, 257, K // 2 + 5, K - 1]
+    W = q.int8_quantize(W0) if base == "int8" else q.quantize(W0)
+    del W0
+    rnd = lambda *s: t.randn(*s, device="cuda", generator=g)
+    X, A, B = q.int8_quantize(rnd(M, K).bfloat16()), (rnd(r, K) / 32).bfloat16(), (rnd(N, r) / 16).bfloat16()
+    dY, T = rnd(M, N).bfloat16(), rnd(M, r)
+    dX = q.linear_bwd_int8(dY, X, W, A, B, 2.0 * r, T=T if base == "int8" else T.bfloat16())[0]
+    v = W.codes[:, cols].double() * W.scale.double()[:, None] if base == "int8" else q.nf4_dequant(W)[:, cols].double()
+    U, absU = dY.double() @ B.double(), dY.double().abs() @ B.double().abs()
+    a = A[:, cols].double()
+    ref = dY.double() @ v + 2.0 * U @ a
+    # the bound of test_input_gradient
+    tol = dY.double().abs() @ v.abs() * (BF + (N + 40) * 2 * F32) + 2.0 * (
+        absU * ((N + 16) * 2 * F32 + 2 * BF + BF * BF + 4 * r * F32)) @ a.abs()
+    err = (dX[:, cols].double() - ref).abs() - ref.abs() * BF - tol * (1 + BF)
+    assert float(err.max()) <= 0.0, float(err.max())
+    # and not only within the bound: the errors are independent roundings
+    assert float((dX[:, cols].double() - ref).norm() / ref.norm()) <= 2 * BF
+
+
 def test_gradient_against_differences():
     """dA and dB of L = sum(dY Y) against differences of the forward's formula in
     64 bits (L is linear in A and in B alone, so a difference is exact)."""
