@@ -358,12 +358,15 @@ class Workspace:
     Every buffer it hands out is marked as used by the stream of the call
     (`record_stream`), so that when it grows, the caching allocator does not
     hand the old memory to anyone before the work queued on that stream is
-    done.  Calls that share one Workspace must still be ordered (one stream,
-    or events): the library writes scratch data into it."""
+    done.  A buffer that a captured graph writes into lives as long as the
+    Workspace, also after a larger one has taken its place.  Calls that share
+    one Workspace must still be ordered (one stream, or events): the library
+    writes scratch data into it."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self._captured = []
 
     def get(self, nbytes: int, stream=None):
         torch = _torch()
@@ -373,6 +376,9 @@ class Workspace:
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         if stream is not None:
             self.buf.record_stream(stream)
+        if (not self._captured or self._captured[-1] is not self.buf) and self.buf.is_cuda \
+                and torch.cuda.is_current_stream_capturing():
+            self._captured.append(self.buf)
         return self.buf, self.buf.numel()
 
 

@@ -586,6 +586,74 @@ def test_mlp_block_captured_and_replayed(M):
             assert t.equal(a, b)
 
 
+@pytest.mark.parametrize("M,N", [(20, 264), (20, 512), (200, 512), (300, 264)])
+def test_backward_on_other_bases_captured_and_replayed(M, N):
+    """An NF4 and a bf16 base at token counts that decode it in dX's tile and that
+    copy it, captured in two graphs that share a Workspace and are replayed in turn."""
+    q, t = _q(), h.torch()
+    K, r = 320, 8
+    g = t.Generator("cuda")
+    g.manual_seed(M + N)
+    rnd = lambda *s: t.randn(*s, device="cuda", generator=g)
+    W0 = 0.05 * rnd(N, K)
+    A, B = (0.06 * rnd(r, K)).bfloat16(), (0.1 * rnd(N, r)).bfloat16()
+    x, dY, T, dX0 = rnd(M, K).bfloat16(), rnd(M, N).bfloat16(), rnd(M, r).bfloat16(), rnd(M, K).bfloat16()
+    X, ws = q.int8_quantize(x), q.Workspace()
+
+    def step(W, acc):
+        return q.linear_bwd_int8(dY, X, W, A, B, 16.0, T=T, accumulate_into=acc, workspace=ws)
+
+    graphs = []
+    for W in (q.quantize(W0), W0.bfloat16()):
+        acc = dX0.clone()
+        side = t.cuda.Stream()
+        side.wait_stream(t.cuda.current_stream())
+        with t.cuda.stream(side):
+            step(W, acc.clone())
+        t.cuda.current_stream().wait_stream(side)
+        graph = t.cuda.CUDAGraph()
+        with t.cuda.graph(graph):
+            held = step(W, acc)
+        graphs.append((W, acc, graph, held))
+    for k in range(3):
+        dY.copy_(rnd(M, N).bfloat16())
+        T.copy_(rnd(M, r).bfloat16())
+        q.int8_quantize(rnd(M, K).bfloat16(), codes_out=X.codes, scale_out=X.scale)
+        for W, acc, graph, held in graphs:
+            acc.copy_(dX0)
+            graph.replay()
+            got = [v.clone() for v in held]
+            for a, b in zip(got, q.linear_bwd_int8(dY, X, W, A, B, 16.0, T=T, accumulate_into=dX0.clone())):
+                assert t.equal(a, b)
+
+
+def test_workspace_that_grows_after_a_capture():
+    """The graph's scratch memory stays its own when a later call needs more."""
+    q, t = _q(), h.torch()
+    L, big = _Layer(24, 256, 136, 8), _Layer(600, 512, 264, 64)
+    ws = q.Workspace()
+    run = lambda: q.linear_bwd_int8(L.ddY, L.X, L.W, L.dA, L.dB, L.alpha, workspace=ws)
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        run()
+    t.cuda.current_stream().wait_stream(side)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        held = run()
+    n, at = ws.buf.numel(), ws.buf.data_ptr()
+    q.linear_bwd_int8(big.ddY, big.X, big.W, big.dA, big.dB, big.alpha, workspace=ws)
+    t.cuda.synchronize()
+    assert ws.buf.numel() > n
+    others = [t.full((n,), 77, dtype=t.uint8, device="cuda") for _ in range(8)]
+    assert all(o.data_ptr() != at for o in others)
+    graph.replay()
+    t.cuda.synchronize()
+    assert all(bool((o == 77).all()) for o in others)
+    for a, b in zip(held, q.linear_bwd_int8(L.ddY, L.X, L.W, L.dA, L.dB, L.alpha)):
+        assert t.equal(a, b)
+
+
 def test_rows_past_32_bit_offsets():
     """Elementwise calls on more than 2^31 elements: sampled rows equal the same
     rows by themselves."""
