@@ -388,8 +388,11 @@ __device__ __forceinline__ void down_block(const DownJob& g, int blk, uint8_t* s
   for (int s = 0; s < 3; ++s) load(s, kz0 + s);
   auto step = [&](auto Pc, int kb) {
     constexpr int P = decltype(Pc)::value;
-    // this step has landed in every wave, and nobody reads the stage before it
-    __builtin_amdgcn_s_waitcnt((2 * L & 0xF) | (0x7 << 4) | (0xF << 8));   // vmcnt(2 L)
+    // vmcnt(2 L), lgkmcnt(0): this step has landed, and the operand reads of the step
+    // before have ended, in every wave that is past the barrier: the loads below go
+    // into that step's stage.
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((2 * L & 0xF) | (0x7 << 4));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     load((P + 3) % 4, kb + 3);
