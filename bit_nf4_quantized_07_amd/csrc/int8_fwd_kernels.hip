@@ -36,6 +36,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "int8_loads.h"
 #include "kernels.h"
 #include "terms.h"
 
@@ -45,6 +46,7 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kI8Step = 128;    // columns of the contraction per step
+static_assert(kPast == kOOB, "the tiles' resources leave this offset out");
 
 struct Int8FwdArgs {
   const int8_t* X;      // [M, K]
@@ -96,26 +98,16 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
   const int kz1 = g.kz_len ? min(nsteps, kz0 + g.kz_len) : nsteps;
 
   // Load i of wave w fills rows 8 (XL w + i) .. +7 of a stage (1 KB); lane l lands
-  // at row l / 8 of them, physical piece l % 8.  Where K ends inside a step, X's
-  // pieces past it are zero (and what W then holds does not matter).
+  // at row l / 8 of them, physical piece l % 8.  Where K ends inside a step, the
+  // pieces past it are zero.
   const __amdgpu_buffer_rsrc_t rx = rsrc_whole(g.X, (uint32_t)((int64_t)g.M * g.K));
   const __amdgpu_buffer_rsrc_t rw = rsrc_whole(g.W, (uint32_t)((int64_t)g.N * g.K));
   auto swz = [](int row) { return (row >> 1) & 7; };
-  uint32_t xoff[XL], woff[WL];
-  bool xhi[XL];
+  LinePiece xp[XL], wp[WL];
 #pragma unroll
-  for (int i = 0; i < XL; ++i) {
-    const int row = 8 * (XL * wave + i) + (lane >> 3);
-    const int piece = (lane & 7) ^ swz(row);
-    xhi[i] = piece >= 4;
-    xoff[i] = m0 + row < g.M ? (uint32_t)((int64_t)(m0 + row) * g.K + piece * 16) : kOOB;
-  }
+  for (int i = 0; i < XL; ++i) xp[i] = line_piece(8 * (XL * wave + i) + (lane >> 3), lane, m0, g.M, g.K);
 #pragma unroll
-  for (int j = 0; j < WL; ++j) {
-    const int row = 8 * (WL * wave + j) + (lane >> 3);
-    const int piece = (lane & 7) ^ swz(row);
-    woff[j] = n0 + row < g.N ? (uint32_t)((int64_t)(n0 + row) * g.K + piece * 16) : kOOB;
-  }
+  for (int j = 0; j < WL; ++j) wp[j] = line_piece(8 * (WL * wave + j) + (lane >> 3), lane, n0, g.N, g.K);
   const int kcut = g.K % kI8Step ? nsteps - 1 : -1;   // the step that K ends in
   auto load_l = [&](int l, int buf, int kb) {
     const int k = __builtin_amdgcn_readfirstlane(kb);
@@ -123,11 +115,11 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
     if (l < XL)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rx, (__attribute__((address_space(3))) void*)(xb[buf] + 1024 * (XL * wave + l)), 16,
-          k == kcut && xhi[l] ? kOOB : xoff[l], soff, 0, 0);
+          line_at(xp[l], k == kcut), soff, 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rw, (__attribute__((address_space(3))) void*)(wb[buf] + 1024 * (WL * wave + l - XL)), 16,
-          woff[l - XL], soff, 0, 0);
+          line_at(wp[l - XL], k == kcut), soff, 0, 0);
   };
   // Operand of a 32-row block, MFMA step t: row c, logical piece 2 t + h.
   int rd[4];
@@ -332,7 +324,8 @@ __global__ void __launch_bounds__(256) k_int8_fwd_64x128(Int8FwdArgs g) { int8_t
 //    per workgroup by whole lines (rows of 128 bytes, pieces XOR-swizzled by
 //    (token >> 1) & 7).  Read from memory beside the weight, a row per lane, they
 //    took half the address unit's time (16 tokens, 28672 x 8192: 69 us, 3.4 TB/s).
-//    Columns past K are zero there, so that the weight's need no bound.
+//    Columns past K are zero there, so that it does not matter which the weight's
+//    loads then bring.
 //  * T = X A^T arrives as kTSplits partial sums, added in a fixed order by every
 //    workgroup (the first one writes T), or is computed here; s T B^T is summed in
 //    fp32 while the first weights are on their way.
@@ -420,7 +413,7 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, const uint16_t* __re
       const __amdgpu_buffer_rsrc_t r = rsrc_whole(g.W, ok ? (uint32_t)((int64_t)g.N * g.K) : 0);
       const uint32_t off = n < g.N ? (uint32_t)((int64_t)n * g.K) + 16 * gq : kOOB;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) R.w[q] = bload128s(r, off + 64 * q, ok ? (uint32_t)(kc + 256 * run) : 0);
+      for (int q = 0; q < 4; ++q) R.w[q] = bload128s(r, off, ok ? run_at(q, run, cols, kc) : 0);
       if (++lr == per) lr = 0, ++lb;
     };
     Run R[kGvDepth];
