@@ -35,7 +35,7 @@ __device__ __forceinline__ uint4 zero_unless(bool ok, uint4 v) {
 //           pscale[m] sum; tokens past the end are zero
 struct RankOut {
   float* sum;              // [M, r]
-  uint16_t* bf16;          // [M, r]
+  uint16_t* bf16;          // [M, r], of s sum
   uint16_t* two;
   float s;
   uint16_t* packed;
@@ -239,7 +239,7 @@ __device__ __forceinline__ void rank_block(const RankJob& g, int blk, uint8_t* l
       for (int q = 0; q < NW; ++q) sum += sums(q, i, j);
       if (S8) sum *= rowscale[i];
       if (o.sum) o.sum[(int64_t)mm * r + j] = sum;
-      if (o.bf16) o.bf16[(int64_t)mm * r + j] = f32_to_bf16(sum);
+      if (o.bf16) o.bf16[(int64_t)mm * r + j] = f32_to_bf16(o.s * sum);
     }
     sums(0, i, j) = sum;                 // this thread's own
   }
@@ -516,8 +516,9 @@ __device__ __forceinline__ void finish_block(const FinishJob& g, int blk, float 
       reinterpret_cast<float4*>(o.sum + at)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
     if (o.bf16)
-      *reinterpret_cast<uint4*>(o.bf16 + at) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      *reinterpret_cast<uint4*>(o.bf16 + at) =
+          make_uint4(pack_bf16x2(o.s * x[0], o.s * x[1]), pack_bf16x2(o.s * x[2], o.s * x[3]),
+                     pack_bf16x2(o.s * x[4], o.s * x[5]), pack_bf16x2(o.s * x[6], o.s * x[7]));
   }
   if (o.two && j < 16 * ntiles) {
     uint16_t hi[8], mid[8];
@@ -795,7 +796,8 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
   uint16_t* const tp = reinterpret_cast<uint16_t*>(base + p.off_tp);
   PrepArgs g{};
   g.u = RankJob{dY, nullptr, (int)M, (int)N, B, r, 0, RankOut{}};
-  g.u.o.bf16 = dX ? U : nullptr;
+  g.u.o.bf16 = dX ? U : nullptr;   // s U rounded once; A is bf16 as it is
+  g.u.o.s = s;
   g.u.o.packed = up;
   g.u.o.pscale = X.scale;
   g.t = RankJob{T || T_bf16 ? nullptr : X.codes, X.scale, (int)M, (int)K, A, r, 0, RankOut{}};
@@ -857,8 +859,8 @@ hipError_t launch_int8_bwd(const uint16_t* dY, const Int8Rows& X, int64_t M, int
     const Dx8Base b8 = p.consts ? Dx8Base{w.packed, g.consts, cb.lv}
                        : W8 && !p.copy ? Dx8Base{W8->codes, W8->scale, nullptr}
                                        : Dx8Base{wx.bf16, nullptr, nullptr};
-    e = p.any ? launch_dx8(dY, M, K, N, b8, U, A, r, s, dX, accumulate, part, p.dx8, ga, st)
-              : launch_dx(dY, M, wx, U, A, r, s, dX, accumulate, st, nullptr, 1.0f,
+    e = p.any ? launch_dx8(dY, M, K, N, b8, U, A, r, dX, accumulate, part, p.dx8, ga, st)
+              : launch_dx(dY, M, wx, U, A, r, 1.0f, dX, accumulate, st, nullptr, 1.0f,
                           p.kz_len ? part : nullptr, p.kz_len, nullptr);
     if (e != hipSuccess || (p.any && p.dx8.grads)) return e;
   }

@@ -1,9 +1,14 @@
 // Input gradient of the linear layer for any number of outputs (8 | N), on a base in
 // 8-bit rows or NF4 as it is stored or on a bf16 one:
 //
-//   dX[m][k] = sum_n dY[m][n] w_hat[n][k] + s sum_j U[m][j] A[j][k]
+//   dX[m][k] = sum_n dY[m][n] w_hat[n][k] + sum_j U[m][j] A[j][k],   U = s dY B
 //                       (llm-compass "QLoRA", 方法与公式, the equation,
 //                        differentiated with respect to x)
+//
+// Rounded to bf16 on the way, once each: a weight that is not bf16 as it is stored (a
+// second term would double the MFMAs), and U, which holds s already so that A goes in
+// as it is.  From 64 bits dX is 2.33e-3 at s = 1.7 where the adapter's term is most of
+// it (8-bit base; 1.66e-3 of that its own rounding), with s A rounded as well 2.64e-3.
 //
 // A workgroup computes 32 NI WM tokens x 64 WN features with WM x WN waves, each
 // 32 NI tokens x 64 features: 2 NI accumulators of v_mfma_f32_32x32x16_bf16, each a
@@ -51,10 +56,9 @@ struct Dx8Args {
   const void* W;        // [N, K] bf16, codes or packed nibbles
   const float* sw;      // codes' row scales, or the nibbles' block constants [K / 64, N]
   float lv[16];         // the nibbles' levels
-  const uint16_t* U;    // [M, r] bf16
+  const uint16_t* U;    // [M, r] bf16, of s U
   const uint16_t* A;    // [r, K]
   int r;
-  float s;
   uint16_t* dX;         // [M, K]
   int accumulate;
   int tiles_m, tiles_k, group_m;
@@ -309,7 +313,7 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
   __builtin_amdgcn_s_waitcnt(0);   // no load into LDS outlives the loop
   __syncthreads();                 // every wave's operand reads are done
 
-  // Adapter term: (s A)^T U^T over r in steps of 16 into the accumulators.
+  // Adapter term: A^T U^T over r in steps of 16 into the accumulators.
   const int kw = k0 + 64 * fg;               // first feature of this wave
   const int mw = m0 + 32 * NI * tq;          // first token
   const __amdgpu_buffer_rsrc_t ru = rsrc_whole(g.U, (uint32_t)(g.M * g.r * 2));
@@ -327,14 +331,14 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int kf = W4 ? kw + 2 * c + j : kw + 32 * j + c;
-        float av[8];
+        uint32_t av[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          av[e] = bf16_to_f32((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(
-                      ra, kf < g.K && rr < g.r ? ((rr + e) * g.K + kf) * 2 : (int)kOOB, 0, 0)) * g.s;
+          av[e] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+              ra, kf < g.K && rr < g.r ? ((rr + e) * g.K + kf) * 2 : (int)kOOB, 0, 0);
         const bf16x8_t afr = __builtin_bit_cast(
-            bf16x8_t, make_uint4(pack_bf16x2(av[0], av[1]), pack_bf16x2(av[2], av[3]),
-                                 pack_bf16x2(av[4], av[5]), pack_bf16x2(av[6], av[7])));
+            bf16x8_t, make_uint4(av[0] | av[1] << 16, av[2] | av[3] << 16, av[4] | av[5] << 16,
+                                 av[6] | av[7] << 16));
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[j][i] = mfma_32x32x16(afr, uop[i], acc[j][i]);
       }
@@ -538,8 +542,7 @@ Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, int base) {
 }
 
 hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Dx8Base& W,
-                      const uint16_t* U, const uint16_t* A, int r, float s,
-                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& p, Grad8Args& ga,
+                      const uint16_t* U, const uint16_t* A, int r, uint16_t* dX, bool accumulate, float* part, const Dx8Plan& p, Grad8Args& ga,
                       hipStream_t st) {
   const Dx8Form& F = kDx8Forms[p.form];
   Dx8Args g{};
@@ -548,7 +551,7 @@ hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const
   g.sw = W.scale;
   if (F.base == kDxNF4)
     for (int i = 0; i < 16; ++i) g.lv[i] = W.levels[i];
-  g.U = U; g.A = A; g.r = r; g.s = s; g.dX = dX;
+  g.U = U; g.A = A; g.r = r; g.dX = dX;
   g.accumulate = accumulate ? 1 : 0;
   g.tiles_m = (int)((M + F.tm - 1) / F.tm);
   g.tiles_k = (int)((K + 255) / 256);

@@ -302,8 +302,9 @@ Int8FwdPlan plan_int8_fwd(int64_t M, int64_t K, int64_t N, int r);
 hipError_t launch_int8_fwd(const Int8Rows& X, int64_t M, const Int8Rows& W, int64_t N, int64_t K,
                            const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* Y,
                            float* T_out, void* ws, const Int8FwdPlan& plan, hipStream_t st);
-// dX (+)= dY W_hat + s U A for any N (8 | N) on a bf16 base, one in 8-bit rows or an
-// NF4 one (its block constants decoded, [K / 64, N]); part: plan.bytes of room.
+// dX (+)= dY W_hat + U A for any N (8 | N) on a bf16 base, one in 8-bit rows or an
+// NF4 one (its block constants decoded, [K / 64, N]), from U that holds s already;
+// part: plan.bytes of room.
 constexpr int kDxBf16 = 0, kDxCodes = 1, kDxNF4 = 2;
 struct Dx8Base {
   const void* weight;
@@ -318,8 +319,7 @@ struct Dx8Plan {
 struct Grad8Args;
 Dx8Plan plan_dx8(int64_t M, int64_t K, int64_t N, int base);
 hipError_t launch_dx8(const uint16_t* dY, int64_t M, int64_t K, int64_t N, const Dx8Base& W,
-                      const uint16_t* U, const uint16_t* A, int r, float s,
-                      uint16_t* dX, bool accumulate, float* part, const Dx8Plan& plan, Grad8Args& grads,
+                      const uint16_t* U, const uint16_t* A, int r, uint16_t* dX, bool accumulate, float* part, const Dx8Plan& plan, Grad8Args& grads,
                       hipStream_t st);
 // Backward from X in 8-bit rows on a base in 8-bit rows (W8 not null), NF4 or
 // bf16 (w).  T in fp32 or bf16, or neither (computed again).

@@ -434,8 +434,9 @@ int int8_linear_fwd(const int8_t* Xcodes, const float* Xscale, int64_t M, int64_
  *      other two bases do; NULL: computed again from the codes.
  * dA and dB are fp32 sums of exact products: U and T enter as three bf16 terms
  * (all 24 bits), the codes as they are, their scale in U's factor.  dX takes
- * each weight of an 8-bit base rounded to bf16 once, as an NF4 base's.  The
- * order of every sum is fixed.
+ * each weight of an 8-bit base rounded to bf16 once, as an NF4 base's, and s U
+ * rounded to bf16 once, on all bases; both products are exact, summed in fp32.
+ * The order of every sum is fixed.
  * Requires the sizes of int8_linear_fwd with 1 <= r, and 2 M K < 2^31; 2 N K <
  * 2^31 for an 8-bit or bf16 base; workspace of int8_linear_workspace_bytes(...,
  * base, 1). */
