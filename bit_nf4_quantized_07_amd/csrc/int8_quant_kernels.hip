@@ -332,11 +332,13 @@ __device__ __forceinline__ void keep8(const uint4& v, const float (&x)[8], int8_
   reinterpret_cast<uint2*>(codes)[row8 + p] = codes8(x, inv);
   if ((p & 7) == 0) scale[(row8 + p) >> 3] = inv.scale;
 }
-// silu(g) u for eight values.  The reciprocal is the instruction's, within an ulp;
-// where it would be subnormal (g below -87) the value is 0.
+// silu(g) u for eight values.  The reciprocal is the instruction's, within an ulp, and
+// would be 0 where it is subnormal (1 + exp(-g) above 2^126, g below -87.3): it is
+// taken of a quarter of that sum, against a quarter of g.
 __device__ __forceinline__ void silu_mul8(const float (&g)[8], const float (&u)[8], float (&h)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = g[e] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[e])) * u[e];
+  for (int e = 0; e < 8; ++e)
+    h[e] = 0.25f * g[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, __expf(-g[e]), 0.25f)) * u[e];
 }
 
 struct GateIn {
