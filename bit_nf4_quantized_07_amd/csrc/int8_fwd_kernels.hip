@@ -245,7 +245,7 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
     }
   // A token block's operands are 1 KB in a row; a block past the last token has none.
   const __amdgpu_buffer_rsrc_t rt =
-      rsrc_whole(g.T2, (uint32_t)((g.M + 31) / 32 * nt * 2048));
+      rsrc_whole(g.T2, (uint32_t)((g.M + 31) / 32 * nt) * 2048u);   // up to 2^31
   for (int t = 0; t < nt; ++t) {
     bf16x8_t top[NI][2], bop[NJ];
 #pragma unroll
