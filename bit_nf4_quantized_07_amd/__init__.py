@@ -352,6 +352,16 @@ def workspace_bytes(M: int, K: int, N: int, r: int, backward: bool) -> int:
     return int(load_library().qlora_workspace_bytes(M, K, N, r, 1 if backward else 0))
 
 
+def _capturing(device) -> bool:
+    """Whether the current stream of `device`, on which the calls are made, is
+    being captured; it need not be the current device."""
+    cuda = _torch().cuda
+    if device.index == cuda.current_device():
+        return cuda.is_current_stream_capturing()
+    with cuda.device(device):
+        return cuda.is_current_stream_capturing()
+
+
 class Workspace:
     """A reusable device workspace that grows on demand.
 
@@ -377,7 +387,7 @@ class Workspace:
         if stream is not None:
             self.buf.record_stream(stream)
         if (not self._captured or self._captured[-1] is not self.buf) and self.buf.is_cuda \
-                and torch.cuda.is_current_stream_capturing():
+                and _capturing(self.buf.device):
             self._captured.append(self.buf)
         return self.buf, self.buf.numel()
 
