@@ -157,6 +157,12 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(bf16x8_t a, bf16x8_t b, f32x4_t
 }
 
 
+// s_waitcnt immediate (gfx9 encoding): vmcnt <= vm, lgkmcnt <= lgkm (15: not waited
+// on), expcnt not waited on.
+constexpr int wait_for(int vm, int lgkm) {
+  return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (lgkm << 8);
+}
+
 // ----------------------------- buffer loads ---------------------------------
 //
 // Loads go through raw buffer resources.  Each loader fixes its per-lane byte

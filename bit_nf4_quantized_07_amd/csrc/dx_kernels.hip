@@ -62,9 +62,6 @@ constexpr int kDxStepN = 64;               // contraction (weight rows) per step
 constexpr int kDyTile = kDxBM * kDxStepN;  // elements per dY buffer
 constexpr int kWTile = kDxStepN * kDxBK;   // elements per weight buffer
 constexpr int kDxUnroll = 4;
-// s_waitcnt immediates (gfx9 encoding), expcnt not waited on:
-// vmcnt <= 7, lgkmcnt <= 4 (end of a step); vmcnt <= 14, lgkmcnt = 0 (prologue).
-constexpr int dx_wait(int vm, int lgkm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (lgkm << 8); }
 
 struct DxArgs {
   const uint16_t* dY;   // [M, N] bf16
@@ -295,7 +292,7 @@ __global__ void __launch_bounds__(64 * kDxWaves) k_dx_nf4(DxArgs g) {
     // W(0), dY(0) and dY(1) arrived (dY(2) may still be in flight): the last
     // slot of step 0 reads the first operands of step 1, which other waves
     // loaded.
-    __builtin_amdgcn_s_waitcnt(dx_wait(4, 0));
+    __builtin_amdgcn_s_waitcnt(wait_for(4, 0));
   } else {
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -306,9 +303,9 @@ __global__ void __launch_bounds__(64 * kDxWaves) k_dx_nf4(DxArgs g) {
     // steps 0 and 1 (step 2's loads may still be in flight) before the
     // barrier publishes dY(0), dY(1) and W(0): the last slot of step 0 reads
     // the first operands of step 1, which other waves loaded.
-    __builtin_amdgcn_s_waitcnt(dx_wait(14, 0));
+    __builtin_amdgcn_s_waitcnt(wait_for(14, 0));
     decode_all(wr[0], wtb[0]);
-    __builtin_amdgcn_s_waitcnt(dx_wait(7, 0));
+    __builtin_amdgcn_s_waitcnt(wait_for(7, 0));
   }
   __builtin_amdgcn_s_barrier();
 #pragma unroll
@@ -389,7 +386,7 @@ __global__ void __launch_bounds__(64 * kDxWaves) k_dx_nf4(DxArgs g) {
     // weight, at most this step's 4 dY loads, so that W(kb+1) has arrived)
     // and this wave's decoded weight stores done (at most the 2 operand
     // reads of slot 15, issued after them, outstanding), then the barrier.
-    __builtin_amdgcn_s_waitcnt(BF16W ? dx_wait(4, 2) : dx_wait(7, 2));
+    __builtin_amdgcn_s_waitcnt(BF16W ? wait_for(4, 2) : wait_for(7, 2));
     __builtin_amdgcn_s_barrier();
   };
   for (int kb = kz0; kb < kz1; kb += kDxUnroll) {
@@ -697,7 +694,7 @@ __device__ __forceinline__ void dx_wide_tile(const DxArgs& g) {
     for (int j = 0; j < kWdLoads; ++j) load_j(j, s, min(s, nsteps - 1));
   // Steps 0 and 1 in LDS (step 2's loads may still be in flight) before the
   // barrier: the last slots of step 0 read the first operands of step 1.
-  __builtin_amdgcn_s_waitcnt(dx_wait(kWdLoads, 0));
+  __builtin_amdgcn_s_waitcnt(wait_for(kWdLoads, 0));
   __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int j = 0; j < 4; ++j) a[0][j] = wfrag(0, j, 0);
@@ -727,7 +724,7 @@ __device__ __forceinline__ void dx_wide_tile(const DxArgs& g) {
     // Step kb+2's stages (loaded during step kb-1) complete in every wave
     // before step kb+1, which reads them in its last slots: at most this
     // step's loads outstanding, then the barrier.
-    __builtin_amdgcn_s_waitcnt(dx_wait(kWdLoads, 0xF));
+    __builtin_amdgcn_s_waitcnt(wait_for(kWdLoads, 0xF));
     __builtin_amdgcn_s_barrier();
   };
   for (int kb = 0; kb < nsteps; kb += kWdUnroll) {

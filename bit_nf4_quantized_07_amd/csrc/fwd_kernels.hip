@@ -65,10 +65,6 @@ constexpr int kFwdBN = 4 * kFwdWaveN;          // weight rows per tile
 constexpr int kXRow = kBlock;                  // LDS row of the X tile (elements, swizzled)
 constexpr int kXTile = kFwdBM * kXRow;         // elements per X buffer
 constexpr int kXBufs = 4;
-// s_waitcnt immediates (gfx9 encoding), expcnt not waited on: vmcnt <= the
-// loads of one step, lgkmcnt not waited on (end of a step); vmcnt <= the
-// loads of two steps, lgkmcnt = 0 (end of the prologue).
-constexpr int wait_vm(int n, int lgkm) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (lgkm << 8); }
 constexpr int kFwdUnroll = 4;                  // K-steps per loop iteration (register sets)
 
 struct FwdArgs {
@@ -259,7 +255,7 @@ __global__ void __launch_bounds__(256) k_fwd_nf4(FwdArgs g) {
   // flight) before the barrier publishes X(0) and X(1): the last slots of
   // step 0 read the first operands of step 1, which other waves loaded.
   decode_all(wr[0], bf[0], crun_cur & 0xffu, srun_cur);
-  __builtin_amdgcn_s_waitcnt(wait_vm(kLoads, 0));
+  __builtin_amdgcn_s_waitcnt(wait_for(kLoads, 0));
   __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[0][i] = xfrag(xbuf[0], i, 0);
@@ -325,7 +321,7 @@ __global__ void __launch_bounds__(256) k_fwd_nf4(FwdArgs g) {
     // X(kb+2) (loaded during step kb-1) must be in LDS, from every wave,
     // before step kb+1 reads it: wait until at most this step's loads are
     // outstanding, then barrier.
-    __builtin_amdgcn_s_waitcnt(wait_vm(kStepLoads, 0xF));
+    __builtin_amdgcn_s_waitcnt(wait_for(kStepLoads, 0xF));
     __builtin_amdgcn_s_barrier();
     if constexpr (P == 3) {
       crun_cur = crun_next;

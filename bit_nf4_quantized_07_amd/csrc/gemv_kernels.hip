@@ -213,8 +213,6 @@ k_gemv_nf4(const uint16_t* __restrict__ X, int M, NF4Weight w, const float* __re
 // into registers; the 8-bit codes (4 per row) and the scale come with them.
 constexpr int kGemvSS = 4;                      // blocks per super-step
 constexpr int kGemvStage = 64 * 128;            // bytes per wave and stage
-// s_waitcnt immediate (gfx9 encoding): vmcnt <= 28, expcnt and lgkmcnt not waited on.
-constexpr int kGemvWaitVm28 = (28 & 0xF) | ((28 >> 4) << 14) | (0x7 << 4) | (0xF << 8);
 
 struct GemvSSRegs {
   uint4 x[kGemvSS][4];    // activations: block b, MFMA step t
@@ -358,7 +356,7 @@ k_gemv_dma(const uint16_t* __restrict__ X, int M, NF4Weight w, const float* __re
       load_w(nxt, ss + 1);
       load_r(rg[(P + 1) % 2], ss + 1);
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(kGemvWaitVm28);
+      __builtin_amdgcn_s_waitcnt(wait_for(28, 15));
     } else {
       __builtin_amdgcn_s_waitcnt(0);
     }

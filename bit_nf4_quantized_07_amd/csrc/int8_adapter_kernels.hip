@@ -392,7 +392,7 @@ __device__ __forceinline__ void down_block(const DownJob& g, int blk, uint8_t* s
     // before have ended, in every wave that is past the barrier: the loads below go
     // into that step's stage.
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((2 * L & 0xF) | (0x7 << 4));
+    __builtin_amdgcn_s_waitcnt(wait_for(2 * L, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     load((P + 3) % 4, kb + 3);
@@ -622,10 +622,10 @@ hipError_t launch_int8_T_partial(const int8_t* X, int64_t M, int64_t K, const ui
 
 // ---------------------------------------------------------------------------
 // What the backward's products need first, in one launch whose workgroups do one
-// thing each: U = dY B (the dX product's operand, and sx U's terms), T's terms
+// thing each: U = dY B (s U, the dX product's operand, and sx U's terms), T's terms
 // (from T, or T computed again), and the bf16 copy of the base for dX, or an NF4
-// base's block constants.  U alone waits for memory most of its time and the copy is bound by it: side by side they
-// take little more than the longer one.
+// base's block constants.  U alone waits for memory most of its time and the copy is
+// bound by it: side by side they take little more than the longer one.
 struct PrepArgs {
   RankJob u;
   int nu;                    // workgroups of U

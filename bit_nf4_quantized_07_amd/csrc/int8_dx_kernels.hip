@@ -34,9 +34,9 @@
 // fp32 sums go to the workspace and are added in a fixed order.
 //
 // What bounds it: few tokens, the start of a workgroup and the steps' latency (16 x
-// 4096 x 4096 in 16 splits 8 us; its 17 MB of weight are 3.4 at a copy's rate);
-// many, the matrix units at the clock that power leaves (4000 x 4096 x 4104 bf16 115
-// us, 1.17 PFLOP/s).  The tile engine that takes such N in linear_bwd: 52 us for 300
+// 4096 x 4096 in 16 splits 10 us; its 17 MB of weight are 3.4 at a copy's rate);
+// many, the matrix units at the clock that power leaves (4000 x 4096 x 4104 bf16 126
+// us, 1.07 PFLOP/s).  The tile engine that takes such N in linear_bwd: 52 us for 300
 // tokens (here 22 and 5 for the split's reduction), 84 for 1200.  Where 256 divides N
 // a bf16 base stays with launch_dx, whose largest tile keeps its operands in registers
 // longer (4001 x 4096 x 11008: 282 us; here, at 11000 outputs, 319).
@@ -67,9 +67,6 @@ struct Dx8Args {
   int blocks;           // workgroups of dX; the rest are the gradients'
 };
 
-constexpr int dx8_wait(int vm, int lgkm) {
-  return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (lgkm << 8);
-}
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2_t* lds_i32x2_ptr;
 
@@ -265,7 +262,7 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int l = 0; l < L; ++l) load_l(l, s, min(kz0 + s, kz1 - 1));
-  __builtin_amdgcn_s_waitcnt(dx8_wait((S - 1) * L, 0));   // the first step has landed
+  __builtin_amdgcn_s_waitcnt(wait_for((S - 1) * L, 0));   // the first step has landed
   __builtin_amdgcn_s_barrier();
   read(0, 0);
   look(0);
@@ -273,8 +270,9 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
 
   // One step: four MFMA steps; each reads the next one's operands first and converts
   // them last.  The last one reads the next step's, which every wave has waited for
-  // before the barrier in front of it; behind it the finished stage takes the loads of
-  // step kb + S.
+  // before the barrier in front of it (vmcnt).  Before the same barrier every wave's
+  // reads of this step's stage, scales and nibbles too, have ended (lgkmcnt): the loads
+  // of step kb + S go into it.
   auto step = [&](auto Pc, int kb) {
     constexpr int P = decltype(Pc)::value, nxt = (P + 1) % S;
     constexpr int Q = NI * NJ;
@@ -283,7 +281,7 @@ __device__ __forceinline__ void dx8_tile(const Dx8Args& g, uint8_t* y0, uint8_t*
     for (int t = 0; t < 4; ++t) {
       __builtin_amdgcn_sched_barrier(0);
       if (t == 3) {
-        __builtin_amdgcn_s_waitcnt(dx8_wait((S - 2) * L, 0));
+        __builtin_amdgcn_s_waitcnt(wait_for((S - 2) * L, 0));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }

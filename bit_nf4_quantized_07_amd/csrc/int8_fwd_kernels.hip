@@ -15,9 +15,9 @@
 //  * The contraction advances 128 columns a step (four MFMA steps) through S LDS
 //    stages that buffer loads fill directly, S steps ahead: rows of 128 bytes, whole
 //    cache lines, whose eight 16-byte pieces are XOR-swizzled by (row >> 1) & 7, so
-//    that operand reads are free of bank conflicts.  Rows of 64 bytes asked L2 twice
-//    as often (8192^3: 31 million requests and 269 us of a 256 x 256 form, here 13
-//    and 187).
+//    that operand reads are free of bank conflicts.  Rows of 64 bytes asked L2 more than
+//    twice as often (4096 x 4096 x 11008 without an adapter: 31 million requests and
+//    269 us of a 256 x 256 form, here 13 million and 179).
 //  * One barrier a step, in front of its last MFMA step: what that one reads is the
 //    next step's, and the loads of S steps on go into the stage that is done.
 //    Eight waves: with two on a SIMD one multiplies while the other reads (four
@@ -29,10 +29,12 @@
 // Where the tiles do not fill the device the contraction is split; a split's
 // fp32 values go to the workspace and are added in a fixed order.
 //
-// What bounds it: the large tiles the clock that power leaves (8192^3 437 us, 2.5
-// PTOP/s, 62 % of the cycles in MFMAs at 1.8 GHz; 4096 x 4096 x 11008 190 us); at
-// 2048 x 4096 x 4096 (36 us) one round of 256 workgroups, a fifth of which is its
-// start and epilogue; at few tokens the weight (one token: 5.2 TB/s of it).
+// What bounds it: the large tiles the clock that power leaves (8192^3 450 us, 2.45
+// POP/s, level with the library's product on the same codes, 62 % of the cycles in
+// MFMAs at 1.8 GHz; 4096 x 4096 x 11008, r = 64, 205); at 2048 x 4096 x 4096 (37 us;
+// the library 42) one round of 256 workgroups, a quarter of which is its start and
+// epilogue; at 16 tokens the weight (28672 x 8192: 5.2 TB/s of it); at one token the
+// latency of what is loaded before the weight.
 #include <type_traits>
 
 #include "device_common.h"
@@ -62,11 +64,6 @@ struct Int8FwdArgs {
   float* part;          // split contraction: fp32 [splits][M, N]
   int kz_len;           // steps per split; 0: one pass
 };
-
-// s_waitcnt immediates (gfx9 encoding): vmcnt <= vm, lgkmcnt <= lgkm.
-constexpr int i8_wait(int vm, int lgkm) {
-  return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (lgkm << 8);
-}
 
 template <int NI, int NJ, int WM, int WN, int S>
 __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
@@ -145,7 +142,7 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int l = 0; l < L; ++l) load_l(l, s, min(kz0 + s, kz1 - 1));
-  __builtin_amdgcn_s_waitcnt(i8_wait((S - 1) * L, 0));   // the first step has landed
+  __builtin_amdgcn_s_waitcnt(wait_for((S - 1) * L, 0));   // the first step has landed
   __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int j = 0; j < NJ; ++j) a[0][j] = wfrag(0, j, 0);
@@ -154,8 +151,9 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
 
   // One step: four MFMA steps of NI NJ slots.  Each reads the next one's operands
   // in its first slots; the last one reads the next step's, which every wave has
-  // waited for before the barrier in front of it.  Behind that barrier nobody
-  // reads this step's stage any more, and the loads of step kb + S go into it.
+  // waited for before the barrier in front of it (vmcnt).  Before the same barrier
+  // every wave's reads of this step's stage, the last of them for MFMA step 3, have
+  // ended (lgkmcnt): the loads of step kb + S go into it.
   auto step = [&](auto Pc, int kb) {
     constexpr int P = decltype(Pc)::value;
     constexpr int nxt = (P + 1) % S;
@@ -166,7 +164,7 @@ __device__ __forceinline__ void int8_tile(const Int8FwdArgs& g) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (t == 3) {
-        __builtin_amdgcn_s_waitcnt(i8_wait((S - 2) * L, 0));
+        __builtin_amdgcn_s_waitcnt(wait_for((S - 2) * L, 0));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -327,10 +325,12 @@ __global__ void __launch_bounds__(256) k_int8_fwd_64x128(Int8FwdArgs g) { int8_t
 //    Columns past K are zero there, so that it does not matter which the weight's
 //    loads then bring.
 //  * T = X A^T arrives as kTSplits partial sums, added in a fixed order by every
-//    workgroup (the first one writes T), or is computed here; s T B^T is summed in
-//    fp32 while the first weights are on their way.
+//    workgroup (the first one writes T), or is computed here.  The partial sums, the
+//    first output's scales and its B are waited for before X and the weight are asked
+//    for; s T B^T is summed in fp32 while the first weights are on their way.
 // Measured: 16 tokens, 28672 x 8192 45 us (5.2 TB/s of weight; a copy reads and
-// writes 5.0), one token, 4096 x 4096 7 us, two of which are a launch's.
+// writes 5.1), one token, 4096 x 4096 7.0 us: 17 MB of weight behind a launch's start and
+// the loads above.
 constexpr int kGvWaves = 8;
 constexpr int kGvThreads = 64 * kGvWaves;
 constexpr int kGvBlocks = 8;    // blocks of 16 outputs per workgroup
@@ -433,7 +433,8 @@ k_int8_gemv(Int8FwdArgs g, const float* __restrict__ Tpart, const uint16_t* __re
         tl[e] = s * t;
       }
     }
-    __builtin_amdgcn_s_waitcnt(0x0070 | (4 * kGvDepth & 0xF) | ((4 * kGvDepth >> 4) << 14));   // X has landed, lgkmcnt(0)
+    // X has landed: its loads are in front of the weight's 4 kGvDepth
+    __builtin_amdgcn_s_waitcnt(wait_for(4 * kGvDepth, 0));
     __syncthreads();
     if constexpr (RT > 0) {
       f32x4_t ta[RT];

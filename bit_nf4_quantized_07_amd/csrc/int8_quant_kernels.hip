@@ -20,10 +20,11 @@
 // in one pass.
 //
 // Bound: HBM.  A row is read once and held in registers (up to 8 pieces of 8
-// values per lane) between its maximum and its codes.  Measured: codes of bf16 rows,
-// 2048 x 4096 6.3 us and 4001 x 11008 25 us (5.3 TB/s), values of them 6.7 and 22.5
-// (5.9); 4096 x 11008 of the gating 75 us (4.3 TB/s; two rows of sigmoids a CU beside
-// the loads), its backward 65 (5.6).  A copy of 1 GiB: 5.0 TB/s.
+// values per lane) between its maximum and its codes.  Measured (launches in a kernel
+// trace): codes of bf16 rows, 2048 x 4096 6.4 us and 4001 x 11008 25.6 (5.2 TB/s), of
+// fp32 rows 8.2 and 39 (5.6), values 6.0 and 20.6 (6.4: the codes partly from the
+// last-level cache); 4096 x 11008 of the gating 77 us (4.2; three rows a CU, whose
+// sigmoids run beside the loads), its backward 64 (5.7).  A copy of 1 GiB: 5.07 TB/s.
 #include <type_traits>
 
 #include "device_common.h"
@@ -280,7 +281,7 @@ k_int8_dequant(const int8_t* __restrict__ codes, const float* __restrict__ scale
     const int64_t i = min(i0 + 256 * e, n8 - 1);
     c[e] = reinterpret_cast<const uint2*>(codes)[i];
     if constexpr (BLOCK) s[e] = scale[i >> 3];
-    else s[e] = scale[n8 <= 0xffffffffll ? (int64_t)((uint32_t)i / k8) : i / k8];
+    else s[e] = scale[(uint32_t)i / k8];   // M K < 2^34: i < 2^31
   }
 #pragma unroll
   for (int e = 0; e < kDqPieces; ++e) {
