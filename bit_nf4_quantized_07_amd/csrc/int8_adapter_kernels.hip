@@ -674,6 +674,9 @@ __device__ __forceinline__ void pack_T(const PrepArgs& g, int64_t e) {
   pack_terms(g.t.o.packed, ntiles, m8, j / 16, j % 16, x);
 }
 
+// The base's values rounded to bf16, as dX's own tile rounds them: the forward takes
+// codes and scales as they are, dX weights up to half a step of bf16 from them, since
+// its products would cost twice as much on two terms.
 constexpr int kCopyRounds = 4;   // words of 16 codes per thread
 __device__ __forceinline__ void copy_int8(const PrepArgs& g, int64_t blk) {
   const int64_t w0 = (blk * blockDim.x + (threadIdx.x & ~63)) * kCopyRounds + (threadIdx.x & 63);
